@@ -1,0 +1,287 @@
+// Top-k router: expert ids and probabilities from the router's logits, and the
+// gradient of the logits from that of the probabilities.
+//
+// Scores of a row: s_e = softmax(l)_e or sigmoid(l_e). Both rise with the
+// logit, so the k experts are the k largest logits (ties to the lower id).
+//   p_j = scale s_j                    or, renormalised, scale s_j / S,  S = sum of the selected s
+// Backward, d_j = dprobs_j, all sums over the selected experts:
+//   softmax:               dl_e = s_e (G_e - sum_i s_i G_i),  G_e = scale d_j at the selected, 0 elsewhere
+//   softmax, renormalised: dl_j = scale q_j (d_j - sum_i q_i d_i),  q = softmax over the selected
+//   sigmoid:               dl_j = scale d_j s_j (1 - s_j)
+//   sigmoid, renormalised: dl_j = scale / S (d_j - sum_i d_i s_i / S) s_j (1 - s_j)
+//
+// One warp takes one row and holds it in registers (V values a lane). Each of
+// the k rounds finds the largest ordered key with one integer warp reduction
+// and the lowest id that has it with a second one; no memory is touched
+// between the load of the logits and the store of the k results, so the
+// kernels are bound by the logits' traffic (or, for few rows, by latency).
+#include "mgq_internal.h"
+#include "device_common.cuh"
+
+namespace mgq {
+namespace {
+
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kMaxTopK = 8;
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+  const float v = BF16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << 16)
+                       : __ldg(static_cast<const float*>(p) + i);
+  return v != v ? -INFINITY : v + 0.0f;   // NaN ranks with the masked experts; -0 becomes +0
+}
+// unsigned key with the order of the floats; 0 is below every float's key
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float from_key(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+// sigmoid without overflow; 0 for -infinity
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  const float e = expf(-fabsf(x));
+  return x >= 0.0f ? 1.0f / (1.0f + e) : e / (1.0f + e);
+}
+// exp(x - m) of a softmax whose largest logit is m; a row with nothing but
+// masked experts (m = -infinity) has no mass
+__device__ __forceinline__ float softmax_term(float x, float m) { return m == -INFINITY ? 0.0f : expf(x - m); }
+
+struct RouterArgs {
+  const void* logits;
+  int64_t T;
+  int E, k;
+  float scale;
+  int32_t* idx;
+  float* probs;
+  // backward
+  const int32_t* sel;
+  const float* dprobs;
+  void* dlogits;
+  int* err;
+};
+
+template <int V, bool BF16, bool SIGMOID, bool RENORM>
+__global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  for (int64_t r = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); r < a.T; r += nw) {
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane + 32 * i;
+      key[i] = e < a.E ? order_key(load_logit<BF16>(a.logits, r * a.E + e)) : 0u;
+    }
+    float l_sel = 0.0f;   // lane j: the j-th selected logit and its expert
+    int e_sel = 0;
+    float top = 0.0f;
+    float all = 0.0f;
+    uint32_t best = 0;
+    int bi = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i] > best) best = key[i], bi = i;
+    for (int j = 0; j < a.k; ++j) {
+      const uint32_t m = __reduce_max_sync(kFull, best);
+      const uint32_t mine = best == m ? static_cast<uint32_t>(lane + 32 * bi) : kFull;
+      const uint32_t e = __reduce_min_sync(kFull, mine);
+      if (lane == j) l_sel = from_key(m), e_sel = static_cast<int>(e);
+      if (j == 0) {
+        top = from_key(m);
+        if (!SIGMOID && !RENORM) {   // the whole row's softmax denominator, before keys are taken out
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (key[i]) all += softmax_term(from_key(key[i]), top);
+          all = warp_sum(all);
+        }
+      }
+      if (mine == e) {   // the owner takes it out and finds its next best
+        best = 0;
+        const int taken = bi;
+        bi = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (i == taken) key[i] = 0;
+          if (key[i] > best) best = key[i], bi = i;
+        }
+      }
+    }
+    const bool on = lane < a.k;
+    const float s = !on ? 0.0f : SIGMOID ? sigmoid_f32(l_sel) : softmax_term(l_sel, top);
+    const float S = RENORM ? warp_sum(s) : SIGMOID ? 1.0f : all;
+    if (on) {
+      a.idx[r * a.k + lane] = e_sel;
+      a.probs[r * a.k + lane] = S == 0.0f ? 0.0f : a.scale * (s / S);
+    }
+  }
+}
+
+template <int V, bool BF16, bool SIGMOID, bool RENORM>
+__global__ void __launch_bounds__(256) router_bwd_kernel(RouterArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  for (int64_t r = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); r < a.T; r += nw) {
+    int e = -1;
+    float d = 0.0f;
+    if (lane < a.k) {
+      e = __ldg(a.sel + r * a.k + lane);
+      d = __ldg(a.dprobs + r * a.k + lane);
+      if (e < 0 || e >= a.E) {
+        report(a.err, MGQ_ERR_DEVICE_INDEX);
+        e = -1;
+      }
+    }
+    const bool on = e >= 0;
+    const float l = on ? load_logit<BF16>(a.logits, r * a.E + e) : -INFINITY;
+    float g = 0.0f;         // lane j: the selected logit's own gradient
+    float back = 0.0f;      // softmax over the row: what every expert's score loses
+    float top = 0.0f, inv = 0.0f, v[V];
+    if (SIGMOID) {
+      const float s = on ? sigmoid_f32(l) : 0.0f;
+      if (RENORM) {
+        const float S = warp_sum(s);
+        const float q = S == 0.0f ? 0.0f : s / S;
+        const float c = warp_sum(q > 0.0f ? d * q : 0.0f);
+        g = q > 0.0f ? a.scale * (d - c) * q * sigmoid_f32(-l) : 0.0f;
+      } else {
+        g = s > 0.0f ? a.scale * d * s * sigmoid_f32(-l) : 0.0f;
+      }
+    } else if (RENORM) {
+      const float m = from_key(__reduce_max_sync(kFull, order_key(l)));
+      const float s = on ? softmax_term(l, m) : 0.0f;
+      const float S = warp_sum(s);
+      const float q = S == 0.0f ? 0.0f : s / S;
+      const float c = warp_sum(q > 0.0f ? d * q : 0.0f);
+      g = q > 0.0f ? a.scale * q * (d - c) : 0.0f;
+    } else {
+      uint32_t km = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int x = lane + 32 * i;
+        v[i] = x < a.E ? load_logit<BF16>(a.logits, r * a.E + x) : -INFINITY;
+        km = max(km, order_key(v[i]));
+      }
+      top = from_key(__reduce_max_sync(kFull, km));
+      float all = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) all += softmax_term(v[i], top);
+      all = warp_sum(all);
+      inv = all == 0.0f ? 0.0f : 1.0f / all;
+      const float s = on ? softmax_term(l, top) * inv : 0.0f;
+      back = a.scale * warp_sum(s > 0.0f ? s * d : 0.0f);
+      g = s > 0.0f ? a.scale * s * d : 0.0f;
+    }
+    // dense row: the selected experts' gradients by id
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int x = lane + 32 * i;
+      float o = 0.0f;
+      if (!SIGMOID && !RENORM) o = -softmax_term(v[i], top) * inv * back;
+      for (int j = 0; j < a.k; ++j) {
+        const int ej = __shfl_sync(kFull, e, j);
+        const float gj = __shfl_sync(kFull, g, j);
+        if (ej == x) o += gj;
+      }
+      if (x < a.E) {
+        if (BF16)
+          static_cast<__nv_bfloat16*>(a.dlogits)[r * a.E + x] = __float2bfloat16_rn(o);
+        else
+          static_cast<float*>(a.dlogits)[r * a.E + x] = o;
+      }
+    }
+  }
+}
+
+template <int V, bool BF16>
+void launch_mode(const RouterArgs& a, bool bwd, bool sigmoid, bool renorm, int grid, cudaStream_t s) {
+  if (bwd) {
+    if (sigmoid && renorm) router_bwd_kernel<V, BF16, true, true><<<grid, 256, 0, s>>>(a);
+    else if (sigmoid) router_bwd_kernel<V, BF16, true, false><<<grid, 256, 0, s>>>(a);
+    else if (renorm) router_bwd_kernel<V, BF16, false, true><<<grid, 256, 0, s>>>(a);
+    else router_bwd_kernel<V, BF16, false, false><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (sigmoid && renorm) router_topk_kernel<V, BF16, true, true><<<grid, 256, 0, s>>>(a);
+    else if (sigmoid) router_topk_kernel<V, BF16, true, false><<<grid, 256, 0, s>>>(a);
+    else if (renorm) router_topk_kernel<V, BF16, false, true><<<grid, 256, 0, s>>>(a);
+    else router_topk_kernel<V, BF16, false, false><<<grid, 256, 0, s>>>(a);
+  }
+}
+
+template <bool BF16>
+void launch_router(const RouterArgs& a, bool bwd, bool sigmoid, bool renorm, cudaStream_t s) {
+  const int64_t ctas = (a.T + 7) / 8, most = static_cast<int64_t>(num_sms()) * 8;
+  const int grid = static_cast<int>(ctas < most ? ctas : most);
+  if (a.E <= 32) launch_mode<1, BF16>(a, bwd, sigmoid, renorm, grid, s);
+  else if (a.E <= 64) launch_mode<2, BF16>(a, bwd, sigmoid, renorm, grid, s);
+  else if (a.E <= 128) launch_mode<4, BF16>(a, bwd, sigmoid, renorm, grid, s);
+  else if (a.E <= 256) launch_mode<8, BF16>(a, bwd, sigmoid, renorm, grid, s);
+  else launch_mode<32, BF16>(a, bwd, sigmoid, renorm, grid, s);
+}
+
+int check_router(const void* logits, int dtype, int64_t T, int E, int k, int score, int renorm) {
+  MGQ_CHECK_ARG(dtype == MGQ_OUT_BF16 || dtype == MGQ_OUT_F32);
+  MGQ_CHECK_ARG(score == MGQ_SCORE_SOFTMAX || score == MGQ_SCORE_SIGMOID);
+  MGQ_CHECK_ARG(renorm == 0 || renorm == 1);
+  MGQ_CHECK_ARG(T >= 0 && T <= (int64_t(1) << 40) && E >= 1 && E <= 1024 && k >= 1 && k <= kMaxTopK && k <= E);
+  MGQ_CHECK_ARG(T == 0 || logits);
+  const uintptr_t size = dtype == MGQ_OUT_BF16 ? 2 : 4;
+  MGQ_CHECK_ARG((reinterpret_cast<uintptr_t>(logits) & (size - 1)) == 0);
+  return MGQ_OK;
+}
+
+}  // namespace
+}  // namespace mgq
+
+using namespace mgq;
+
+extern "C" int mgq_router_topk(const void* logits, int dtype, int64_t T, int E, int k, int score, int renorm,
+                               float scale, int32_t* topk_idx, float* probs, void* stream) {
+  const int rc = check_router(logits, dtype, T, E, k, score, renorm);
+  if (rc != MGQ_OK) return rc;
+  if (T == 0) return MGQ_OK;
+  MGQ_CHECK_ARG(topk_idx && probs);
+  RouterArgs a{};
+  a.logits = logits;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.scale = scale;
+  a.idx = topk_idx;
+  a.probs = probs;
+  if (dtype == MGQ_OUT_BF16)
+    launch_router<true>(a, false, score == MGQ_SCORE_SIGMOID, renorm != 0, as_stream(stream));
+  else
+    launch_router<false>(a, false, score == MGQ_SCORE_SIGMOID, renorm != 0, as_stream(stream));
+  MGQ_LAUNCH_CHECK();
+  return MGQ_OK;
+}
+
+extern "C" int mgq_router_topk_bwd(const void* logits, int dtype, const int32_t* topk_idx, const float* dprobs,
+                                   int64_t T, int E, int k, int score, int renorm, float scale, void* dlogits,
+                                   void* stream) {
+  const int rc = check_router(logits, dtype, T, E, k, score, renorm);
+  if (rc != MGQ_OK) return rc;
+  if (T == 0) return MGQ_OK;
+  MGQ_CHECK_ARG(topk_idx && dprobs && dlogits);
+  RouterArgs a{};
+  a.logits = logits;
+  a.T = T;
+  a.E = E;
+  a.k = k;
+  a.scale = scale;
+  a.sel = topk_idx;
+  a.dprobs = dprobs;
+  a.dlogits = dlogits;
+  a.err = error_word();
+  if (dtype == MGQ_OUT_BF16)
+    launch_router<true>(a, true, score == MGQ_SCORE_SIGMOID, renorm != 0, as_stream(stream));
+  else
+    launch_router<false>(a, true, score == MGQ_SCORE_SIGMOID, renorm != 0, as_stream(stream));
+  MGQ_LAUNCH_CHECK();
+  return MGQ_OK;
+}

@@ -27,6 +27,8 @@ LAYOUT_K, LAYOUT_MN = 0, 1
 (GEMM_OPT_FORCE_1CTA, GEMM_OPT_MX_PAIR, GEMM_OPT_NV_PAIR, GEMM_OPT_DIRECT_STORE, GEMM_OPT_DEBUG_STALL,
  GEMM_OPT_WAIT_MS) = range(6)
 
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+
 FMAX = {E4M3: 448.0, E5M2: 57344.0}
 
 # every symbol include/mgq.h declares
@@ -38,7 +40,8 @@ EXPORTS = (
     "mgq_grouped_gemm_wgrad", "mgq_grouped_gemm_fwd_swiglu",
     "mgq_grouped_gemm_dgrad_dswiglu", "mgq_swiglu_quantize", "mgq_dswiglu_quantize", "mgq_moe_unpermute",
     "mgq_moe_unpermute_bwd", "mgq_moe_permute_bwd", "mgq_amax_history_update", "mgq_set_gemm_option",
-    "mgq_get_gemm_option", "mgq_nv_scale_image",
+    "mgq_get_gemm_option", "mgq_nv_scale_image", "mgq_add_rmsnorm_quantize", "mgq_add_rmsnorm_bwd_workspace_size",
+    "mgq_add_rmsnorm_bwd", "mgq_router_topk", "mgq_router_topk_bwd",
 )
 
 
@@ -105,8 +108,15 @@ def load() -> ctypes.CDLL:
         lib.mgq_amax_history_update.argtypes = [vp, vp, vp, vp, i32, i32, ctypes.c_float, vp]
         lib.mgq_set_gemm_option.argtypes = [i32, i64]
         lib.mgq_get_gemm_option.argtypes = [i32, P(i64)]
+        f32 = ctypes.c_float
+        lib.mgq_add_rmsnorm_quantize.argtypes = [vp, vp, vp, i32, i64, i64, f32, vp, vp, P(QDesc), vp, vp]
+        lib.mgq_add_rmsnorm_bwd_workspace_size.restype = sz
+        lib.mgq_add_rmsnorm_bwd_workspace_size.argtypes = [i64, i64]
+        lib.mgq_add_rmsnorm_bwd.argtypes = [vp, vp, vp, i32, vp, vp, i64, i64, vp, vp, f32, vp, sz, vp]
+        lib.mgq_router_topk.argtypes = [vp, i32, i64, i32, i32, i32, i32, f32, vp, vp, vp]
+        lib.mgq_router_topk_bwd.argtypes = [vp, i32, vp, vp, i64, i32, i32, i32, i32, f32, vp, vp]
         for name in EXPORTS:
-            if name not in ("mgq_status_string", "mgq_permute_workspace_size"):
+            if name != "mgq_status_string" and not name.endswith("_workspace_size"):
                 getattr(lib, name).restype = i32
         if lib.mgq_version() != INTERFACE_VERSION:   # the struct layouts below are this version's
             raise RuntimeError(f"{LIB_PATH}: interface version {lib.mgq_version()}, expected {INTERFACE_VERSION}")
@@ -327,3 +337,84 @@ def amax_history_update(history, head, amax, scale, fmax, stream=None):
     n, L = history.shape
     _check(load().mgq_amax_history_update(_p(history), _p(head), _p(amax), _p(scale), n, L,
                                           ctypes.c_float(fmax), _s(stream)), "mgq_amax_history_update")
+
+
+def _dense(where, *tensors):
+    """The row-major tensors these calls read and write: contiguous, on the GPU."""
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.is_contiguous()):
+            raise MGQError(ERR_INVALID_ARG, where)
+
+
+_OUT_DTYPE = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+
+
+def _typed(where, t):
+    dt = _OUT_DTYPE.get(t.dtype)
+    if dt is None:
+        raise MGQError(ERR_UNSUPPORTED, where)
+    return dt
+
+
+def _of(where, dtype, shape, *tensors):
+    """Tensors (or None) of one dtype and shape."""
+    for t in tensors:
+        if t is not None and (t.dtype != dtype or t.shape != shape):
+            raise MGQError(ERR_INVALID_ARG, where)
+
+
+def add_rmsnorm_quantize(x, w, eps, q: QDesc | None = None, residual=None, sum_out=None, y=None, rstd=None,
+                         stream=None):
+    """s = x + residual; y = s / rms(s) * w, quantised row-wise into q (x, residual,
+    sum_out, y: bf16 [T, H]; w [H] bf16 or float32; rstd float32 [T])."""
+    fn = "mgq_add_rmsnorm_quantize"
+    T, H = x.shape
+    _dense(fn, x, w, residual, sum_out, y, rstd)
+    _of(fn, torch.bfloat16, x.shape, x, residual, sum_out, y)
+    _of(fn, torch.float32, (T,), rstd)
+    _of(fn, w.dtype, (H,), w)
+    _check(load().mgq_add_rmsnorm_quantize(_p(x), _p(residual), _p(w), _typed(fn, w), T, H, eps, _p(sum_out), _p(y),
+                                           ctypes.byref(q) if q is not None else None, _p(rstd), _s(stream)), fn)
+
+
+def add_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
+    return int(load().mgq_add_rmsnorm_bwd_workspace_size(T, H))
+
+
+def add_rmsnorm_bwd(dy, s, w, rstd, dx, dw, workspace, dsum=None, beta=0.0, stream=None):
+    """Gradients of add_rmsnorm_quantize: dx bf16 [T, H] (+ dsum), dw float32 [H] (beta dw + ...)."""
+    fn = "mgq_add_rmsnorm_bwd"
+    T, H = dy.shape
+    _dense(fn, dy, s, w, rstd, dx, dw, workspace, dsum)
+    _of(fn, torch.bfloat16, dy.shape, dy, s, dx, dsum)
+    _of(fn, torch.float32, (T,), rstd)
+    _of(fn, torch.float32, (H,), dw)
+    _of(fn, w.dtype, (H,), w)
+    _check(load().mgq_add_rmsnorm_bwd(_p(dy), _p(s), _p(w), _typed(fn, w), _p(rstd), _p(dsum), T, H, _p(dx), _p(dw),
+                                      beta, _p(workspace), workspace.numel() * workspace.element_size(), _s(stream)),
+           fn)
+
+
+def router_topk(logits, topk_idx, probs, score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
+    """logits [T, E] (bf16 or float32) -> topk_idx int32 [T, k], probs float32 [T, k]."""
+    fn = "mgq_router_topk"
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    _dense(fn, logits, topk_idx, probs)
+    _of(fn, torch.int32, (T, k), topk_idx)
+    _of(fn, torch.float32, (T, k), probs)
+    _check(load().mgq_router_topk(_p(logits), _typed(fn, logits), T, E, k, score, int(renorm), scale, _p(topk_idx),
+                                  _p(probs), _s(stream)), fn)
+
+
+def router_topk_bwd(logits, topk_idx, dprobs, dlogits, score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
+    """The gradient of router_topk's probs with respect to the logits, dense [T, E]."""
+    fn = "mgq_router_topk_bwd"
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    _dense(fn, logits, topk_idx, dprobs, dlogits)
+    _of(fn, torch.int32, (T, k), topk_idx)
+    _of(fn, torch.float32, (T, k), dprobs)
+    _of(fn, logits.dtype, (T, E), dlogits)
+    _check(load().mgq_router_topk_bwd(_p(logits), _typed(fn, logits), _p(topk_idx), _p(dprobs), T, E, k, score,
+                                      int(renorm), scale, _p(dlogits), _s(stream)), fn)

@@ -477,6 +477,71 @@ int mgq_moe_permute_bwd(const void* da_bf16, const int32_t* row_id_map, int T, i
 int mgq_amax_history_update(float* history, int32_t* head, float* amax, float* scale,
                             int n, int L, float fmax, void* stream);
 
+/* ---- residual addition + RMSNorm with a quantised output ---------------------
+ * The step in front of the layer: per row of H elements, in float32,
+ *   s = x + residual,  rstd = 1 / sqrt(mean(s^2) + eps),  y = s * rstd * w,
+ * and codes = the row-wise quantisation of the float32 y (one rounding; the
+ * codes of a y rounded to bf16 first can differ by one step).
+ *  x_bf16, residual_bf16  device [T, H] bf16; residual NULL = 0
+ *  w        device [H], bf16 or float32 by w_dtype (mgq_out_dtype)
+ *  sum_bf16 [T, H] receives bf16(s) (may be x or residual itself), or NULL
+ *  y_bf16   [T, H] receives bf16(y), or NULL
+ *  q        row-wise quantisation of y, or NULL: MGQ_MX32_E8M0 (128x4-tiled
+ *           scales of ceil(T/128)*128 rows; the scales of rows T.. are written
+ *           as 0), MGQ_BLK_1x128_F32 (scale_inv [H/128][T]) or MGQ_TENSOR_F32
+ *           (tensor_scale read, amax_out optional, raised); e4m3 or e5m2; no
+ *           column-wise copy (q->col.data NULL)
+ *  rstd     device [T] float32, or NULL
+ * Requires at least one output, H a multiple of 8 (with q: of 128), at most
+ * 16384, 16-byte aligned pointers. T = 0 does nothing. NaN and infinity stay
+ * in their row. MGQ_ERR_UNSUPPORTED: other scalings or formats, q->col. */
+int mgq_add_rmsnorm_quantize(const void* x_bf16, const void* residual_bf16, const void* w, int w_dtype,
+                             int64_t T, int64_t H, float eps, void* sum_bf16, void* y_bf16,
+                             const mgq_qdesc* q, float* rstd, void* stream);
+
+/* Gradient of the call above. With xh = s * rstd and g = dy * w (float32),
+ *   dx = rstd * (g - xh * mean(g * xh)) + dsum   (x's and the residual's),
+ *   dw = beta * dw + sum over the rows of dy * xh.
+ *  dy_bf16    device [T, H], the gradient of y
+ *  s_bf16     device [T, H], the forward's sum_bf16 (x without a residual)
+ *  rstd       device [T], the forward's
+ *  dsum_bf16  device [T, H], the gradient that reaches sum_bf16 from elsewhere
+ *             (the residual stream), or NULL; dx_bf16 may be dsum_bf16 itself
+ *  dw         device [H] float32; beta 0 overwrites it whatever it held
+ *  workspace  mgq_add_rmsnorm_bwd_workspace_size(T, H) bytes of the current
+ *             device (partial sums of dw, joined in a fixed order: the result
+ *             does not change from run to run)
+ * Sizes and alignment as above; T = 0 gives dw = beta * dw. */
+size_t mgq_add_rmsnorm_bwd_workspace_size(int64_t T, int64_t H);
+int mgq_add_rmsnorm_bwd(const void* dy_bf16, const void* s_bf16, const void* w, int w_dtype,
+                        const float* rstd, const void* dsum_bf16, int64_t T, int64_t H, void* dx_bf16,
+                        float* dw, float beta, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- top-k router ---------------------------------------------------------------
+ * Expert ids and probabilities (the inputs of mgq_moe_permute and
+ * mgq_moe_unpermute) from the router's logits, and the logits' gradient from
+ * dprobs (mgq_moe_unpermute_bwd). Float32 throughout.
+ *  logits   device [T, E], bf16 or float32 by dtype (mgq_out_dtype)
+ *  score    MGQ_SCORE_SOFTMAX: s = softmax over the E experts;
+ *           MGQ_SCORE_SIGMOID: s = sigmoid(logit)
+ *  topk_idx device [T, k] int32: the k largest logits of the row, largest
+ *           first, ties to the lower id (distinct ids always)
+ *  probs    device [T, k] float32: scale * s, with renorm 1 divided by the sum
+ *           of the k selected s
+ * A logit of -infinity masks its expert: it ranks last with probability 0. A
+ * NaN logit counts as -infinity. A row with nothing but masked experts gives
+ * the k lowest ids with probabilities 0 (and a zero gradient).
+ * The gradient dlogits [T, E] (dtype as the logits) is dense: with renorm 1 or
+ * sigmoid scores it is 0 outside the selected experts. An id outside [0, E) in
+ * topk_idx is skipped and reported as MGQ_ERR_DEVICE_INDEX.
+ * Requires 1 <= k <= 8, k <= E <= 1024. */
+typedef enum { MGQ_SCORE_SOFTMAX = 0, MGQ_SCORE_SIGMOID = 1 } mgq_router_score;
+int mgq_router_topk(const void* logits, int dtype, int64_t T, int E, int k, int score, int renorm,
+                    float scale, int32_t* topk_idx, float* probs, void* stream);
+int mgq_router_topk_bwd(const void* logits, int dtype, const int32_t* topk_idx, const float* dprobs,
+                        int64_t T, int E, int k, int score, int renorm, float scale, void* dlogits,
+                        void* stream);
+
 #ifdef __cplusplus
 }
 #endif

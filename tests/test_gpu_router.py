@@ -1,0 +1,146 @@
+"""GPU parity of the top-k router and its gradient with the float64 definitions.
+
+Ids are equal. With u = 2^-24: a score is an exponential (2 ulp) over a sum of
+at most 32 serial terms and a tree of the lanes, so probabilities are within
+64 u; a gradient is within 96 u of the sum of the magnitudes it is made of
+(and, for bf16 logits, half a bf16 ulp)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block as OB
+from tests.layer_check import ulp_bf16
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def _mode(score):
+    from fp8_grouped_gemm_gb300 import mgq
+    return mgq.SCORE_SOFTMAX if score == "softmax" else mgq.SCORE_SIGMOID
+
+
+def _check(logits, k, score, renorm, scale=1.0, seed=0):
+    from fp8_grouped_gemm_gb300 import mgq
+    T, E = logits.shape
+    idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    probs = torch.full((T, k), 7.0, device="cuda")
+    dp = torch.randn(T, k, generator=torch.Generator().manual_seed(seed))
+    dl = torch.full((T, E), 7.0, dtype=logits.dtype, device="cuda")
+    ld = logits.cuda()
+    mgq.router_topk(ld, idx, probs, _mode(score), renorm, scale)
+    mgq.router_topk_bwd(ld, idx, dp.cuda(), dl, _mode(score), renorm, scale)
+    assert mgq.get_error() == mgq.OK
+    l64 = logits.double().numpy()
+    sc = float(np.float32(scale))
+    ri, rp = OB.router_topk(l64, k, score, renorm, sc)
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    assert np.all(np.abs(probs.cpu().numpy() - rp) <= 64 * U * np.abs(rp) + 1e-37)
+    rg, mag = OB.router_topk_bwd(l64, ri, dp.double().numpy(), score, renorm, sc)
+    slack = 96 * U * mag + 1e-37
+    if logits.dtype == torch.bfloat16:
+        slack = slack + 0.5 * ulp_bf16(np.abs(rg) + slack) * (1 + 1e-9)
+    assert np.all(np.abs(dl.double().cpu().numpy() - rg) <= slack)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 5, 5), (17, 8, 8), (9, 31, 3), (40, 64, 6), (7, 65, 1),
+                                   (33, 128, 8), (5, 129, 4), (6, 256, 8), (4, 300, 8), (3, 1024, 7)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_router(T, E, k, score, renorm, dtype):
+    g = torch.Generator().manual_seed(T * E + k)
+    _check((torch.randn(T, E, generator=g) * 3).to(dtype), k, score, renorm, 2.5, E)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_ties_masks_and_extremes(score, renorm):
+    inf, big = float("inf"), 3.4028234e38
+    rows = [[1.0, 2.0, 2.0, 2.0, 0.0, -0.0],
+            [0.0, -0.0, 0.0, -0.0, -1.0, -inf],
+            [-inf, -inf, 3.0, -inf, -inf, -inf],
+            [-inf] * 6,
+            [float("nan"), 1.0, float("nan"), 2.0, -inf, 0.5],
+            [-big] * 6,
+            [90.0, -90.0, 100.0, -100.0, 0.0, 80.0],
+            [1e-40, -1e-40, 0.0, 2e-40, -inf, -inf]]
+    _check(torch.tensor(rows), 4, score, renorm)
+
+
+def test_many_rows_and_a_side_stream():
+    """More rows than the grid has warps, on another stream than the tensors'."""
+    from fp8_grouped_gemm_gb300 import mgq
+    T, E, k = 20000, 16, 2
+    l = torch.randn(T, E, generator=torch.Generator().manual_seed(1))
+    l = (l * 4).round() / 4                                 # ties in most rows
+    _check(l, k, "softmax", True)
+    ld = l.cuda()
+    idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    probs = torch.empty(T, k, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mgq.router_topk(ld, idx, probs, stream=s)
+    s.synchronize()
+    assert np.array_equal(idx.cpu().numpy(), OB.router_topk(l.double().numpy(), k)[0])
+
+
+def test_probabilities_feed_the_unpermute_and_its_gradient_comes_back():
+    """dprobs of mgq_moe_unpermute_bwd is what the router's backward takes: shapes and types as they are."""
+    from fp8_grouped_gemm_gb300 import mgq
+    l = torch.randn(12, 8, device="cuda")
+    idx = torch.empty(12, 2, dtype=torch.int32, device="cuda")
+    p = torch.empty(12, 2, device="cuda")
+    mgq.router_topk(l, idx, p)
+    assert torch.all((p.sum(1) - 1).abs() < 1e-6)
+
+
+def test_gradient_against_differences():
+    rng = np.random.default_rng(5)
+    from fp8_grouped_gemm_gb300 import mgq
+    l, d = rng.normal(size=(3, 9)), rng.normal(size=(3, 3))
+    l, d = l.astype(np.float32), d.astype(np.float32)
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            idx = torch.empty(3, 3, dtype=torch.int32, device="cuda")
+            p, dl = torch.empty(3, 3, device="cuda"), torch.empty(3, 9, device="cuda")
+            ld = torch.from_numpy(l).cuda()
+            mgq.router_topk(ld, idx, p, _mode(score), renorm)
+            mgq.router_topk_bwd(ld, idx, torch.from_numpy(d).cuda(), dl, _mode(score), renorm)
+            f = lambda v: (OB.router_topk(v, 3, score, renorm)[1] * d).sum()
+            h = 1e-6
+            for i in range(3):
+                for j in range(9):
+                    e = np.zeros((3, 9))
+                    e[i, j] = h
+                    diff = (f(l + e) - f(l - e)) / (2 * h)
+                    assert abs(dl[i, j].item() - diff) <= 1e-6
+
+
+def test_an_id_out_of_range_is_reported():
+    from fp8_grouped_gemm_gb300 import mgq
+    l = torch.randn(2, 4, device="cuda")
+    idx = torch.tensor([[0, 9], [1, 2]], dtype=torch.int32, device="cuda")
+    dl = torch.empty(2, 4, device="cuda")
+    mgq.router_topk_bwd(l, idx, torch.ones(2, 2, device="cuda"), dl, renorm=False)
+    assert mgq.get_error() == mgq.ERR_DEVICE_INDEX
+    assert mgq.get_error() == mgq.OK
+    assert torch.all(torch.isfinite(dl))
+
+
+def test_refusals_of_the_binding():
+    from fp8_grouped_gemm_gb300 import mgq
+    l = torch.zeros(4, 16, device="cuda")
+    idx = torch.empty(4, 2, dtype=torch.int32, device="cuda")
+    p = torch.empty(4, 2, device="cuda")
+    for bad in (dict(logits=l.t().contiguous().t()), dict(topk_idx=idx.long()), dict(probs=p[:3]),
+                dict(logits=l[:, :1].contiguous())):
+        a = dict(logits=l, topk_idx=idx, probs=p)
+        a.update(bad)
+        with pytest.raises(mgq.MGQError) as e:
+            mgq.router_topk(**a)
+        assert e.value.status == mgq.ERR_INVALID_ARG
+    with pytest.raises(mgq.MGQError) as e:
+        mgq.router_topk(l.half(), idx, p)
+    assert e.value.status == mgq.ERR_UNSUPPORTED
+    mgq.router_topk(l[:0], idx[:0], p[:0])                 # no rows
