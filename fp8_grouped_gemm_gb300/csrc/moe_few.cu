@@ -1,0 +1,908 @@
+// The whole routed-expert layer for a few tokens (decode): T of 1 to 128.
+//
+//   out[t] = sum_j probs[t, j] W2_e Q(silu(g) u),   [g | u] = W1_e Q(x_t),   e = topk_idx[t, j]
+//
+// With so few rows the layer is bound by reading the weights of the experts
+// that were picked, once. The grouped GEMMs put tokens on the 128 rows of the
+// tensor-core tile, so a group of one token costs 128 padded rows; here the
+// operands change places: 128 rows of a weight are the tile's M and the
+// expert's tokens (at most 64 a tile, in steps of 16) its N. The weights' codes
+// and block scales go from memory to shared memory by TMA and into the MMA as
+// they are, and nothing is padded in memory.
+//
+// Four launches, each started while the one before drains (programmatic
+// dependent launch):
+//   few_prep_kernel   rows of the routed tokens in expert order, quantised
+//   few_gemm_kernel   gate and up rows of W1, SwiGLU, h quantised
+//   few_gemm_kernel   W2, rows of y in float32
+//   few_combine_kernel  out[t] = sum_j probs y
+// A GEMM's work is a line of units, one per (tile, 128 bytes of contraction),
+// 32 KB of weight each; every CTA takes an equal stretch of it, whatever the
+// number of tiles. A tile that two or more CTAs share is joined by the last of
+// them to finish: the others leave float32 partial sums, which it adds in the
+// order of the CTAs, so the result does not depend on who came last. Nobody
+// waits for another CTA.
+#include "mgq_internal.h"
+#include "ptx_sm100.cuh"
+#include "rowquant.cuh"
+
+namespace mgq {
+namespace {
+
+constexpr int kMaxT = 128, kMaxK = 8, kMaxE = 1024;
+constexpr int kTok = 64;                  // tokens of one tile (tensor-memory columns of one half)
+constexpr int kThreads = 192;             // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
+constexpr uint32_t kATile = 128 * 128;    // bytes of 128 weight rows of one stage
+constexpr int kMaxStages = 6;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+enum { kMX = 0, kNV = 1, kBLK = 2, kTEN = 3 };
+
+__host__ __device__ constexpr uint32_t sf_chunks(int kind) { return kind == kMX ? 1 : kind == kNV ? 4 : 0; }
+// scale bytes of one stage: two weight halves and the tokens (BLK: 64 float32 of the tokens)
+__host__ __device__ constexpr uint32_t sf_bytes(int kind) { return kind == kBLK ? 256u : 3 * 512 * sf_chunks(kind); }
+
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// the four epilogue warps
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tmov.b32 %0, {b, b, b, b};\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r & 0xFFu;
+}
+
+// ---------------------------------------------------------------------------
+// Routed rows. Row order: by expert, then by entry i = t k + j. Tokens of an
+// expert fall into blocks of 64; block b of an expert whose rows start at s
+// keeps its scales in slot s / 64 + b + e, unique because a later block starts
+// at least one row further on and a later expert has a larger e.
+
+struct PrepArgs {
+  const uint16_t* x;
+  const int32_t* idx;
+  int R, k, E;
+  int H;
+  uint8_t* xq;
+  uint8_t* xs;
+  const float* x_scale;
+  int32_t* row_of;     // [R]
+  int32_t* cnt;        // arrival counters to clear
+  int ncnt;
+  int* err;
+};
+
+template <int KIND>
+__global__ void __launch_bounds__(128) few_prep_kernel(PrepArgs a) {
+  grid_launch();
+  const uint32_t lane = threadIdx.x & 31;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.ncnt; i += 128) a.cnt[i] = 0;
+  const int nchunk = (a.H + 1023) / 1024;
+  const int wid = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int i = wid / nchunk, ck = wid - i * nchunk;
+  if (i >= a.R) return;
+  const int e = __ldg(a.idx + i);
+  if (e < 0 || e >= a.E) {
+    if (ck == 0 && lane == 0) {
+      a.row_of[i] = -1;
+      report(a.err, MGQ_ERR_DEVICE_INDEX);
+    }
+    return;
+  }
+  int before = 0, same = 0;     // entries of lower experts; earlier entries of this one
+  for (int q = lane; q < a.R; q += 32) {
+    const int f = __ldg(a.idx + q);
+    before += f >= 0 && f < e;
+    same += f == e && q < i;
+  }
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  same = __reduce_add_sync(0xFFFFFFFFu, same);
+  const int row = before + same;
+  if (ck == 0 && lane == 0) a.row_of[i] = row;
+  const int64_t slot = before / kTok + same / kTok + e;
+  const uint32_t n = same % kTok;
+  const int c = ck * 1024 + lane * 32;
+  float v[32];
+  const bool in = c < a.H;
+  if (in) {
+    load_bf16x32(a.x + static_cast<int64_t>(i / a.k) * a.H + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+  }
+  const uint32_t in_chunk = (n & 31) * 16 + (n >> 5) * 4;    // the token's place in a 512-byte scale chunk
+  if (KIND == kNV) {
+    Block32nv b;
+    quantize32_nv(v, __ldg(a.x_scale), b);
+    if (in) {
+      *reinterpret_cast<uint4*>(a.xq + static_cast<int64_t>(row) * (a.H / 2) + c / 2) =
+          make_uint4(b.cw[0], b.cw[1], b.cw[2], b.cw[3]);
+      if ((lane & 1) == 0) *reinterpret_cast<uint32_t*>(a.xs + (slot * (a.H / 64) + c / 64) * 512 + in_chunk) = b.s4;
+    }
+  } else {
+    constexpr int SC = KIND == kMX ? MGQ_MX32_E8M0 : KIND == kBLK ? MGQ_BLK_1x128_F32 : MGQ_TENSOR_F32;
+    Block32 b;
+    quantize32<SC, MGQ_E4M3>(v, absmax_bits_f32(v, 32), KIND == kTEN ? __ldg(a.x_scale) : 1.0f, true, b);
+    if (in) {
+      uint4* dst = reinterpret_cast<uint4*>(a.xq + static_cast<int64_t>(row) * a.H + c);
+      dst[0] = make_uint4(b.cw[0], b.cw[1], b.cw[2], b.cw[3]);
+      dst[1] = make_uint4(b.cw[4], b.cw[5], b.cw[6], b.cw[7]);
+      if ((lane & 3) == 0) {
+        if (KIND == kMX) *reinterpret_cast<uint32_t*>(a.xs + (slot * (a.H / 128) + c / 128) * 512 + in_chunk) = b.s4;
+        if (KIND == kBLK) reinterpret_cast<float*>(a.xs)[(slot * (a.H / 128) + c / 128) * kTok + n] = b.sinv;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The two GEMMs. PHASE 1: 128 gate rows and the matching 128 up rows of W1 are
+// the two halves of a tile; PHASE 2: 256 consecutive rows of W2 (the second
+// half may be missing at the end).
+
+struct FewArgs {
+  const int32_t* idx;
+  int R, E;
+  int64_t rows_e;        // weight rows of an expert
+  int mt, kb;            // tiles along M, stages along the contraction
+  int half2;             // rows from the first half to the second
+  int mstep;             // rows from one tile to the next
+  int rows_end;          // phase 2: rows of an expert that exist
+  int kblk;              // BLK: 128-blocks of the contraction
+  const uint8_t* sfa;    // weight block scales (MX, NV), chunks of 512 bytes
+  int64_t sfa_kb4;       // chunks per 128 rows
+  const float* sw;       // TEN: s per expert; NV: s_g per expert; BLK: scale_inv
+  const uint8_t* sfb;    // token scales, by slot
+  const float* sx;       // TEN, NV: scale of the tokens' operand
+  float* part;           // [2 grid][nmax * 256]
+  int32_t* cnt;          // [grid]
+  int nmax;              // tokens a tile can hold (multiple of 16, at most 64)
+  int stages;
+  uint32_t idesc0;       // instruction descriptor without N
+  // phase 1
+  uint8_t* hq;
+  uint8_t* hs;
+  const float* h_scale;
+  int F;
+  // phase 2
+  float* y;
+  int H;
+  int* err;
+};
+
+struct Seg {
+  int e, m, row0, n, slot, kb0, kb1, tile;
+};
+
+struct Line {             // the CTA's view of the work
+  const int* start;       // [E + 1] first row of each expert
+  const int* nb;          // [E + 1] first token block of each expert
+  int E, mt, kb, U, G;
+};
+
+__device__ __forceinline__ void decode(const Line& w, int u, int u1, Seg& s) {
+  s.tile = u / w.kb;
+  s.kb0 = u - s.tile * w.kb;
+  s.kb1 = min(w.kb, s.kb0 + (u1 - u));
+  const int q = s.tile / w.mt;
+  int lo = 0, hi = w.E;         // the last expert whose first block is at most q
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (w.nb[mid] <= q) lo = mid;
+    else hi = mid;
+  }
+  s.e = lo;
+  const int nb = w.nb[lo + 1] - w.nb[lo];
+  const int local = s.tile - w.nb[lo] * w.mt;
+  s.m = local / nb;
+  const int b = local - s.m * nb;
+  s.row0 = w.start[lo] + kTok * b;
+  s.n = min(kTok, w.start[lo + 1] - s.row0);
+  s.slot = w.start[lo] / kTok + b + lo;
+}
+// the CTA that owns unit u
+__device__ __forceinline__ int owner(const Line& w, int u) {
+  return static_cast<int>((static_cast<int64_t>(u + 1) * w.G - 1) / w.U);
+}
+
+// h = silu(g) u of 16 tokens (nj of them real) and one ffn row per thread,
+// quantised along the rows: lane = row within a 32-row block, so an MX block
+// is one warp, an NVFP4 block half of one, a 1x128 block the four warps.
+template <int KIND>
+__device__ __forceinline__ void store_h(const FewArgs& p, const Seg& s, int c16, float (&g)[16], const float (&u)[16],
+                                        float alpha, int row, float sh, uint32_t (*smax)[4][16],
+                                        uint32_t& tick) {
+  const int nj = min(16, s.n - 16 * c16);
+  const uint32_t lane = threadIdx.x & 31, wq = row >> 5;
+  const int64_t f0 = static_cast<int64_t>(s.m) * 128;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) g[j] = swiglu_f32(g[j] * alpha, u[j] * alpha);
+  if (KIND == kBLK) {
+    uint32_t mine = 0;     // lane j keeps token j's maximum over this warp's rows
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (j >= nj) break;
+      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(g[j]) & 0x7FFFFFFFu);
+      if (lane == j) mine = m;
+    }
+    // (two buffers in turn: a warp writes one again only after the barrier
+    // that every warp reaches when it has read it)
+    ++tick;
+    if (lane < 16) smax[tick & 1][wq][lane] = mine;
+    epi_sync();
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (j >= nj) break;
+    const int col = 16 * c16 + j;
+    const int64_t r = s.row0 + col;
+    const uint32_t in_chunk = (col & 31) * 16 + (col >> 5) * 4;
+    if (KIND == kMX) {
+      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(g[j]) & 0x7FFFFFFFu);
+      const int e = mx_exponent(m, 8, true);
+      p.hq[r * p.F + f0 + row] = static_cast<uint8_t>(cvt_e4m3x2(__fmul_rn(g[j], mx_multiplier(e)), 0.0f));
+      if (lane == 0)
+        p.hs[(static_cast<int64_t>(s.slot) * (p.F / 128) + s.m) * 512 + in_chunk + wq] =
+            static_cast<uint8_t>(mx_scale_code(e));
+    } else if (KIND == kNV) {
+      uint32_t m = __float_as_uint(g[j]) & 0x7FFFFFFFu;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      const uint32_t code = cvt_ue4m3(__fmul_rn(__fdiv_rn(__uint_as_float(m), 6.0f), sh));
+      const float sc = ue4m3_value(code);
+      const float v = __fmul_rn(g[j], sc == 0.0f ? 0.0f : __fdiv_rn(sh, sc));
+      const float w = __shfl_down_sync(0xFFFFFFFFu, v, 1);
+      if ((lane & 1) == 0) p.hq[(r * p.F + f0 + row) / 2] = static_cast<uint8_t>(cvt_e2m1x2(v, w));
+      if ((lane & 15) == 0)
+        p.hs[(static_cast<int64_t>(s.slot) * (p.F / 64) + 2 * s.m + (row >> 6)) * 512 + in_chunk + ((row >> 4) & 3)] =
+            static_cast<uint8_t>(code);
+    } else if (KIND == kBLK) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) m = max(m, smax[tick & 1][q][j]);
+      const float mult = blk_scale<MGQ_E4M3>(m);
+      p.hq[r * p.F + f0 + row] = static_cast<uint8_t>(cvt_e4m3x2(__fmul_rn(g[j], mult), 0.0f));
+      if (row == 0)
+        reinterpret_cast<float*>(p.hs)[(static_cast<int64_t>(s.slot) * (p.F / 128) + s.m) * kTok + col] =
+            __fdiv_rn(1.0f, mult);
+    } else {
+      p.hq[r * p.F + f0 + row] = static_cast<uint8_t>(cvt_e4m3x2(__fmul_rn(g[j], sh), 0.0f));
+    }
+  }
+}
+
+__device__ __forceinline__ void store_y(const FewArgs& p, const Seg& s, int c16, const float (&a)[16],
+                                        const float (&b)[16], float alpha, int row) {
+  const int nj = min(16, s.n - 16 * c16);
+  const int64_t m0 = static_cast<int64_t>(s.m) * 256 + row;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (j >= nj) break;
+    float* d = p.y + static_cast<int64_t>(s.row0 + 16 * c16 + j) * p.H + m0;
+    d[0] = a[j] * alpha;
+    if (m0 + 128 < p.H) d[128] = b[j] * alpha;
+  }
+}
+
+template <int KIND, int PHASE>
+__global__ void __launch_bounds__(kThreads, 1)
+    few_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const FewArgs p) {
+  constexpr uint32_t CH = sf_chunks(KIND), SF = sf_bytes(KIND);
+  constexpr bool BS = KIND == kMX || KIND == kNV;      // block scales through tensor memory
+  constexpr uint32_t kCols = BS ? 512 : 256;           // two accumulators of 2 x 64 columns, then scale columns
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int STG = p.stages;
+  const uint32_t bt = static_cast<uint32_t>(p.nmax) * 128;
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + STG * 2 * kATile;
+  uint8_t* sSF = sB + STG * bt;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sSF + STG * SF);
+  uint64_t* full = bars;
+  uint64_t* empty = bars + kMaxStages;
+  uint64_t* t_full = bars + 2 * kMaxStages;
+  uint64_t* t_empty = t_full + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(t_empty + 2);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  volatile int* s_last = reinterpret_cast<volatile int*>(s_tmem + 2);
+  uint32_t (*smax)[4][16] = reinterpret_cast<uint32_t (*)[4][16]>(bars + 2 * kMaxStages + 8);   // [2][4][16]
+  int* s_start = reinterpret_cast<int*>(bars + 2 * kMaxStages + 8) + 128;
+  int* s_nb = s_start + p.E + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31;
+  grid_launch();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STG; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], KIND == kBLK ? 5 : 1);   // the MMAs; BLK: and the four epilogue warps
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&t_full[a], 1);
+      ptx::mbar_init(&t_empty[a], 128);
+    }
+    *s_abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmW);
+    ptx::prefetch_tmap(&tmX);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(s_tmem, kCols);
+    ptx::tmem_relinquish();
+  }
+  // rows per expert, then their prefix sums (and those of the token blocks)
+  for (int i = threadIdx.x; i < p.E; i += kThreads) s_start[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.R; i += kThreads) {
+    const int e = __ldg(p.idx + i);
+    if (e >= 0 && e < p.E) atomicAdd(&s_start[e], 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int rows = 0, blocks = 0;
+    for (int b = 0; b < p.E; b += 32) {
+      const int e = b + lane;
+      const int n = e < p.E ? s_start[e] : 0, nb = (n + kTok - 1) / kTok;
+      int r = n, q = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int r2 = __shfl_up_sync(0xFFFFFFFFu, r, o), q2 = __shfl_up_sync(0xFFFFFFFFu, q, o);
+        if (lane >= o) r += r2, q += q2;
+      }
+      if (e < p.E) s_start[e] = rows + r - n, s_nb[e] = blocks + q - nb;
+      rows += __shfl_sync(0xFFFFFFFFu, r, 31);
+      blocks += __shfl_sync(0xFFFFFFFFu, q, 31);
+    }
+    if (lane == 0) s_start[p.E] = rows, s_nb[p.E] = blocks;
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  Line w{s_start, s_nb, p.E, p.mt, p.kb, s_nb[p.E] * p.mt * p.kb, 0};
+  w.G = min(static_cast<int>(gridDim.x), w.U);
+  int u0 = 0, u1 = 0;
+  if (static_cast<int>(blockIdx.x) < w.G) {
+    u0 = static_cast<int>(static_cast<int64_t>(w.U) * blockIdx.x / w.G);
+    u1 = static_cast<int>(static_cast<int64_t>(w.U) * (blockIdx.x + 1) / w.G);
+  }
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- producer
+      // The weights do not depend on the launch before: the first stages of
+      // them are requested before the wait for it, the tokens' after.
+      auto load_w = [&](const Seg& s, int kb, uint32_t st) {
+        const bool two = PHASE == 1 || s.m * 256 + 128 < p.rows_end;
+        const int64_t row = s.e * p.rows_e + static_cast<int64_t>(s.m) * p.mstep;
+        const uint32_t n16 = (s.n + 15) / 16;
+        ptx::mbar_arrive_expect_tx(&full[st], (two ? 2 : 1) * (kATile + CH * 512) + n16 * 2048 +
+                                                  (KIND == kBLK ? 256u : CH * 512));
+        ptx::tma_load_2d(sA + st * 2 * kATile, &tmW, &full[st], kb * 128, static_cast<int32_t>(row));
+        if (two)
+          ptx::tma_load_2d(sA + st * 2 * kATile + kATile, &tmW, &full[st], kb * 128,
+                           static_cast<int32_t>(row + p.half2));
+        if (BS) {
+          const uint8_t* f = p.sfa + ((row / 128) * p.sfa_kb4 + static_cast<int64_t>(kb) * CH) * 512;
+          ptx::bulk_load(sSF + st * SF, f, CH * 512, &full[st]);
+          if (two)
+            ptx::bulk_load(sSF + st * SF + CH * 512, f + static_cast<int64_t>(p.half2 / 128) * p.sfa_kb4 * 512, CH * 512,
+                           &full[st]);
+        }
+      };
+      auto load_x = [&](const Seg& s, int kb, uint32_t st) {
+        for (int i = 0; i < (s.n + 15) / 16; ++i)
+          ptx::tma_load_2d(sB + st * bt + i * 2048, &tmX, &full[st], kb * 128, s.row0 + 16 * i);
+        if (BS)
+          ptx::bulk_load(sSF + st * SF + 2 * CH * 512, p.sfb + (static_cast<int64_t>(s.slot) * p.kb + kb) * CH * 512,
+                         CH * 512, &full[st]);
+        if (KIND == kBLK)
+          ptx::bulk_load(sSF + st * SF, p.sfb + (static_cast<int64_t>(s.slot) * p.kb + kb) * 256, 256, &full[st]);
+      };
+      Seg s;
+      uint32_t it = 0;
+      for (int u = u0; u < u1 && it < static_cast<uint32_t>(STG); u += s.kb1 - s.kb0) {
+        decode(w, u, u1, s);
+        for (int kb = s.kb0; kb < s.kb1 && it < static_cast<uint32_t>(STG); ++kb, ++it) load_w(s, kb, it);
+      }
+      const uint32_t early = it;
+      grid_wait();
+      it = 0;
+      for (int u = u0; u < u1; u += s.kb1 - s.kb0) {
+        decode(w, u, u1, s);
+        for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
+          const uint32_t st = it % STG;
+          if (it >= early) {
+            if (*s_abort) break;
+            if (!ptx::mbar_wait(&empty[st], ((it / STG) & 1) ^ 1, kWaitNs)) {
+              report(p.err, MGQ_ERR_TIMEOUT);
+              *s_abort = 1;
+              break;
+            }
+            load_w(s, kb, st);
+          }
+          load_x(s, kb, st);
+        }
+        if (*s_abort) break;
+      }
+      // given up: no copy of this CTA may land after it has left
+      if (*s_abort)
+        for (uint32_t i = it > static_cast<uint32_t>(STG) ? it - STG : 0; i < it; ++i)
+          ptx::mbar_wait(&full[i % STG], (i / STG) & 1, kWaitNs / 100);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint32_t sA0 = ptx::smem_u32(sA), sB0 = ptx::smem_u32(sB), sF0 = ptx::smem_u32(sSF);
+      Seg s;
+      uint32_t it = 0, tc = 0;
+      bool ok = true;
+      for (int u = u0; u < u1 && ok; u += s.kb1 - s.kb0) {
+        decode(w, u, u1, s);
+        const bool two = PHASE == 1 || s.m * 256 + 128 < p.rows_end;
+        const uint32_t idesc = p.idesc0 | (static_cast<uint32_t>((s.n + 15) / 16 * 2) << 17);
+        uint32_t a = tc & 1;
+        for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
+          const uint32_t st = it % STG;
+          if (KIND == kBLK || kb == s.kb0) {
+            a = tc & 1;
+            ok = !*s_abort && ptx::mbar_wait(&t_empty[a], ((tc >> 1) & 1) ^ 1, kWaitNs);
+          }
+          ok = ok && !*s_abort && ptx::mbar_wait(&full[st], (it / STG) & 1, kWaitNs);
+          if (!ok) {
+            report(p.err, MGQ_ERR_TIMEOUT);
+            *s_abort = 1;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sf_t = tmem + 256 + st * 12 * CH;
+          if constexpr (BS) {
+#pragma unroll
+            for (uint32_t c = 0; c < CH; ++c) {
+              ptx::tmem_cp_32x128b_x4(sf_t + c * 4, ptx::sdesc_sf(sF0 + st * SF + c * 512));
+              if (two) ptx::tmem_cp_32x128b_x4(sf_t + (CH + c) * 4, ptx::sdesc_sf(sF0 + st * SF + (CH + c) * 512));
+              ptx::tmem_cp_32x128b_x4(sf_t + (2 * CH + c) * 4, ptx::sdesc_sf(sF0 + st * SF + (2 * CH + c) * 512));
+            }
+          }
+          const uint64_t bd = ptx::sdesc_kmajor_sw128(sB0 + st * bt);
+          for (int h = 0; h < (two ? 2 : 1); ++h) {
+            const uint64_t ad = ptx::sdesc_kmajor_sw128(sA0 + (st * 2 + h) * kATile);
+            const uint32_t d = tmem + a * 2 * kTok + h * kTok;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t acc = ((KIND != kBLK && kb > s.kb0) || kk > 0) ? 1u : 0u;
+              if (KIND == kNV)
+                ptx::mma_mxf4nvf4(d, ad + kk * 2, bd + kk * 2, idesc, sf_t + (h * CH + kk) * 4, sf_t + (2 * CH + kk) * 4,
+                                  acc);
+              else if (KIND == kMX)
+                ptx::mma_mxf8f6f4(d, ad + kk * 2, bd + kk * 2, idesc | ptx::idesc_sf_ids(kk, kk), sf_t + h * 4,
+                                  sf_t + 8, acc);
+              else
+                ptx::mma_f8f6f4(d, ad + kk * 2, bd + kk * 2, idesc, acc);
+            }
+          }
+          ptx::mma_commit(&empty[st]);
+          if (KIND == kBLK || kb == s.kb1 - 1) {
+            ptx::mma_commit(&t_full[a]);
+            ++tc;
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    // thread = one weight row of each half (tensor-memory lane), all tokens
+    grid_wait();
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t tlane = static_cast<uint32_t>(warp & 3) << 21;
+    const float sx = KIND == kNV || KIND == kTEN ? __ldg(p.sx) : 1.0f;
+    const float sh = PHASE == 1 && (KIND == kNV || KIND == kTEN) ? __ldg(p.h_scale) : 1.0f;
+    Seg s;
+    uint32_t it = 0, tc = 0, tick = 0;
+    for (int u = u0; u < u1; u += s.kb1 - s.kb0) {
+      decode(w, u, u1, s);
+      const int n16 = (s.n + 15) / 16;
+      const bool whole = s.kb1 - s.kb0 == p.kb;
+      float alpha = 1.0f;
+      if (KIND == kNV || KIND == kTEN) alpha = 1.0f / (sx * __ldg(p.sw + s.e));
+      // the tile's first and last CTA, and this CTA's place for partial sums
+      int ca = 0, cb = 0;
+      float* mine = nullptr;
+      if (!whole) {
+        const int first = s.tile * p.kb;
+        ca = owner(w, first);
+        cb = owner(w, first + p.kb - 1);
+        mine = p.part + static_cast<int64_t>(2 * blockIdx.x + (ca == static_cast<int>(blockIdx.x) ? 1 : 0)) * p.nmax * 256;
+      }
+      bool alive = true;
+      if (KIND == kBLK) {
+        // every stage's product is scaled and added in float32 registers
+        float acc[2][kTok / 16][16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < kTok / 16; ++c)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[h][c][j] = 0.0f;
+        const int64_t wr = (s.e * p.rows_e + static_cast<int64_t>(s.m) * p.mstep) / 128;
+        const bool two = PHASE == 1 || s.m * 256 + 128 < p.rows_end;
+        for (int kb = s.kb0; kb < s.kb1; ++kb, ++it, ++tc) {
+          const uint32_t st = it % STG, a = tc & 1;
+          const float w0 = __ldg(p.sw + wr * p.kblk + kb);
+          const float w1 = two ? __ldg(p.sw + (wr + p.half2 / 128) * p.kblk + kb) : 0.0f;
+          alive = __all_sync(0xFFFFFFFFu, !*s_abort && ptx::mbar_wait(&full[st], (it / STG) & 1, kWaitNs) &&
+                                              ptx::mbar_wait(&t_full[a], (tc >> 1) & 1, kWaitNs));
+          if (!alive) break;
+          ptx::tc_fence_after();
+          const float4* fx = reinterpret_cast<const float4*>(sSF + st * SF);
+#pragma unroll
+          for (int c = 0; c < kTok / 16; ++c) {
+            if (c >= n16) break;
+            uint32_t v0[16], v1[16];
+            ptx::tmem_ld_32x32b_x16(tmem + tlane + a * 2 * kTok + 16 * c, v0);
+            ptx::tmem_ld_32x32b_x16(tmem + tlane + a * 2 * kTok + kTok + 16 * c, v1);
+            ptx::tmem_ld_wait_regs(v0);
+            ptx::tmem_ld_wait_regs(v1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 f = fx[4 * c + j];
+              const float f4[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                acc[0][c][4 * j + i] = fmaf(__uint_as_float(v0[4 * j + i]), f4[i] * w0, acc[0][c][4 * j + i]);
+                if (two) acc[1][c][4 * j + i] = fmaf(__uint_as_float(v1[4 * j + i]), f4[i] * w1, acc[1][c][4 * j + i]);
+              }
+            }
+          }
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&t_empty[a]);
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&empty[st]);
+        }
+        if (alive) {
+#pragma unroll
+          for (int c = 0; c < kTok / 16; ++c) {
+            if (c >= n16) break;
+            if (!whole) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (16 * c + j >= s.n) break;
+                mine[(16 * c + j) * 256 + row] = acc[0][c][j];
+                mine[(16 * c + j) * 256 + 128 + row] = acc[1][c][j];
+              }
+            } else if (PHASE == 1) {
+              store_h<KIND>(p, s, c, acc[0][c], acc[1][c], alpha, row, sh, smax, tick);
+            } else {
+              store_y(p, s, c, acc[0][c], acc[1][c], alpha, row);
+            }
+          }
+        }
+      } else {
+        const uint32_t a = tc & 1;
+        alive = __all_sync(0xFFFFFFFFu, !*s_abort && ptx::mbar_wait(&t_full[a], (tc >> 1) & 1, kWaitNs));
+        ++tc;
+        if (alive) {
+          ptx::tc_fence_after();
+          for (int c = 0; c < n16; ++c) {
+            uint32_t v0[16], v1[16];
+            ptx::tmem_ld_32x32b_x16(tmem + tlane + a * 2 * kTok + 16 * c, v0);
+            ptx::tmem_ld_32x32b_x16(tmem + tlane + a * 2 * kTok + kTok + 16 * c, v1);
+            ptx::tmem_ld_wait_regs(v0);
+            ptx::tmem_ld_wait_regs(v1);
+            float g[16], h[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) g[j] = __uint_as_float(v0[j]), h[j] = __uint_as_float(v1[j]);
+            if (!whole) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (16 * c + j >= s.n) break;
+                mine[(16 * c + j) * 256 + row] = g[j];
+                mine[(16 * c + j) * 256 + 128 + row] = h[j];
+              }
+            } else if (PHASE == 1) {
+              store_h<KIND>(p, s, c, g, h, alpha, row, sh, smax, tick);
+            } else {
+              store_y(p, s, c, g, h, alpha, row);
+            }
+          }
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&t_empty[a]);
+        }
+      }
+      if (!alive) {
+        report(p.err, MGQ_ERR_TIMEOUT);
+        *s_abort = 1;
+        break;
+      }
+      if (!whole) {
+        __threadfence();
+        epi_sync();
+        if (threadIdx.x == 64) *s_last = atomicAdd(p.cnt + ca, 1) == cb - ca;
+        epi_sync();
+        if (*s_last) {
+          __threadfence();
+          for (int c = 0; c < n16; ++c) {
+            float g[16], h[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) g[j] = 0.0f, h[j] = 0.0f;
+            for (int q = ca; q <= cb; ++q) {
+              const float* o = p.part + static_cast<int64_t>(2 * q + (q == ca ? 1 : 0)) * p.nmax * 256 + c * 16 * 256 + row;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (16 * c + j >= s.n) break;
+                g[j] += __ldcg(o + j * 256);
+                h[j] += __ldcg(o + j * 256 + 128);
+              }
+            }
+            if (PHASE == 1) store_h<KIND>(p, s, c, g, h, alpha, row, sh, smax, tick);
+            else store_y(p, s, c, g, h, alpha, row);
+          }
+        }
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kCols);
+  }
+}
+
+// out[t] = sum_j probs[t, j] y[row(t, j)] in float32, j ascending, rounded once
+__global__ void __launch_bounds__(128) few_combine_kernel(const float* y, const int32_t* row_of, const float* probs, int T,
+                                                          int k, int H, uint16_t* out) {
+  grid_wait();
+  const int t = blockIdx.y, c = (blockIdx.x * 128 + threadIdx.x) * 4;
+  if (c >= H) return;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int j = 0; j < k; ++j) {
+    const int r = row_of[t * k + j];
+    if (r < 0) continue;
+    const float pr = __ldg(probs + t * k + j);
+    const float4 v = *reinterpret_cast<const float4*>(y + static_cast<int64_t>(r) * H + c);
+    o.x = fmaf(pr, v.x, o.x);
+    o.y = fmaf(pr, v.y, o.y);
+    o.z = fmaf(pr, v.z, o.z);
+    o.w = fmaf(pr, v.w, o.w);
+  }
+  *reinterpret_cast<uint2*>(out + static_cast<int64_t>(t) * H + c) =
+      make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+}
+
+// ---------------------------------------------------------------------------
+// host side
+
+int kind_of(int scaling) {
+  switch (scaling) {
+    case MGQ_MX32_E8M0: return kMX;
+    case MGQ_NV16_UE4M3: return kNV;
+    case MGQ_BLK_1x128_F32: return kBLK;
+    case MGQ_TENSOR_F32: return kTEN;
+    default: return -1;
+  }
+}
+
+bool few_sizes_ok(int T, int k, int E, int64_t H, int64_t F, int kind) {
+  const int64_t unit = kind == kNV ? 256 : 128;
+  return T >= 0 && T <= kMaxT && k >= 1 && k <= kMaxK && E >= 1 && E <= kMaxE && k <= E && H >= unit && F >= unit &&
+         H % unit == 0 && F % unit == 0 && H <= 65536 && F <= 65536;
+}
+
+struct Layout {
+  int64_t row_of, cnt, xq, xs, hq, hs, y, part, total;
+  int nmax, grid;
+};
+
+Layout layout_of(int T, int k, int E, int64_t H, int64_t F, int kind) {
+  Layout l{};
+  const int64_t R = static_cast<int64_t>(T) * k, slots = R / kTok + E;
+  l.nmax = (T < kTok ? T + 15 : kTok) / 16 * 16;
+  l.grid = num_sms();
+  const int64_t per = kind == kNV ? 2 : 1;                      // codes per byte
+  auto scales = [&](int64_t K) {
+    return kind == kMX ? slots * (K / 128) * 512 : kind == kNV ? slots * (K / 64) * 512 :
+           kind == kBLK ? slots * (K / 128) * 256 : int64_t(0);
+  };
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  l.row_of = take(R * 4);
+  l.cnt = take(2 * l.grid * 4);
+  l.xq = take(R * H / per);
+  l.xs = take(scales(H));
+  l.hq = take(R * F / per);
+  l.hs = take(scales(F));
+  l.y = take(R * H * 4);
+  l.part = take(2 * static_cast<int64_t>(l.grid) * l.nmax * 256 * 4);
+  l.total = at;
+  return l;
+}
+
+// a launch that may start while the one before it in the stream still runs
+template <typename... P, typename... A>
+bool launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
+}
+
+constexpr size_t kSmemMax = 227 * 1024;
+
+template <int KIND, int PHASE>
+int launch_gemm(const CUtensorMap& tw, const CUtensorMap& tx, FewArgs p, int grid, cudaStream_t s) {
+  auto kern = few_gemm_kernel<KIND, PHASE>;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MGQ_ERR_CUDA;
+  if (dev >= 64 || !attr_set[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemMax)) != cudaSuccess)
+      return MGQ_ERR_CUDA;
+    if (dev < 64) attr_set[dev] = true;
+  }
+  // what is not a stage: alignment, barriers and flags, block maxima, the experts' prefix sums
+  const size_t fixed = 1024 + (2 * kMaxStages + 8) * 8 + 128 * 4 + 2 * (static_cast<size_t>(p.E) + 1) * 4;
+  const size_t stage = 2 * kATile + static_cast<size_t>(p.nmax) * 128 + sf_bytes(KIND);
+  int stages = static_cast<int>((kSmemMax - fixed) / stage);
+  const int most = KIND == kNV ? 5 : kMaxStages;       // NVFP4: 48 scale columns a stage in tensor memory
+  p.stages = stages < most ? stages : most;
+  if (!launch_after(kern, dim3(grid), kThreads, fixed + p.stages * stage, s, tw, tx, p)) {
+    (void)cudaGetLastError();
+    return MGQ_ERR_CUDA;
+  }
+  return MGQ_OK;
+}
+
+template <int KIND>
+int few_forward(const void* x, int T, int64_t H, int64_t F, const int32_t* idx, const float* probs, int k, int E,
+                const mgq_operand* W1, const mgq_operand* W2, const float* x_scale, const float* h_scale, void* out,
+                uint8_t* ws, cudaStream_t s) {
+  const Layout l = layout_of(T, k, E, H, F, KIND);
+  const int R = T * k;
+  const int64_t per = KIND == kNV ? 2 : 1;
+  CUtensorMap tw1, tw2, tx, th;
+  if (!encode_tmap_u8_2d(&tw1, W1->data, H / per, static_cast<uint64_t>(E) * 2 * F, W1->ld / per, 128, 128) ||
+      !encode_tmap_u8_2d(&tw2, W2->data, F / per, static_cast<uint64_t>(E) * H, W2->ld / per, 128, 128) ||
+      !encode_tmap_u8_2d(&tx, ws + l.xq, H / per, R, H / per, 128, 16) ||
+      !encode_tmap_u8_2d(&th, ws + l.hq, F / per, R, F / per, 128, 16))
+    return MGQ_ERR_CUDA;
+  int* err = error_word();
+
+  PrepArgs pa{};
+  pa.x = static_cast<const uint16_t*>(x);
+  pa.idx = idx;
+  pa.R = R;
+  pa.k = k;
+  pa.E = E;
+  pa.H = static_cast<int>(H);
+  pa.xq = ws + l.xq;
+  pa.xs = ws + l.xs;
+  pa.x_scale = x_scale;
+  pa.row_of = reinterpret_cast<int32_t*>(ws + l.row_of);
+  pa.cnt = reinterpret_cast<int32_t*>(ws + l.cnt);
+  pa.ncnt = 2 * l.grid;
+  pa.err = err;
+  const int warps = R * static_cast<int>((H + 1023) / 1024);
+  few_prep_kernel<KIND><<<(warps + 3) / 4, 128, 0, s>>>(pa);
+  MGQ_LAUNCH_CHECK();
+
+  FewArgs a{};
+  a.idx = idx;
+  a.R = R;
+  a.E = E;
+  a.part = reinterpret_cast<float*>(ws + l.part);
+  a.nmax = l.nmax;
+  a.err = err;
+  a.hq = ws + l.hq;
+  a.hs = ws + l.hs;
+  a.h_scale = h_scale;
+  a.F = static_cast<int>(F);
+  a.y = reinterpret_cast<float*>(ws + l.y);
+  a.H = static_cast<int>(H);
+  a.idesc0 = KIND == kNV ? ptx::idesc_mxf4nvf4_ue4m3(128, 0) : KIND == kMX ? ptx::idesc_mxf8f6f4(0, 0, 128, 0)
+                                                              : ptx::idesc_f8f6f4(0, 0, 128, 0);
+  auto weight = [&](const mgq_operand* W) {
+    a.sfa = static_cast<const uint8_t*>(W->scale);
+    a.sfa_kb4 = W->ld / (KIND == kNV ? 64 : 128);
+    a.sw = KIND == kNV ? W->global_scale : static_cast<const float*>(W->scale);
+  };
+  // gate and up
+  a.rows_e = 2 * F;
+  a.mt = static_cast<int>(F / 128);
+  a.kb = static_cast<int>(H / per / 128);
+  a.kblk = static_cast<int>(H / 128);
+  a.half2 = static_cast<int>(F);
+  a.mstep = 128;
+  a.sfb = ws + l.xs;
+  a.sx = x_scale;
+  a.cnt = reinterpret_cast<int32_t*>(ws + l.cnt);
+  weight(W1);
+  int rc = launch_gemm<KIND, 1>(tw1, tx, a, l.grid, s);
+  if (rc != MGQ_OK) return rc;
+  // down
+  a.rows_e = H;
+  a.rows_end = static_cast<int>(H);
+  a.mt = static_cast<int>((H + 255) / 256);
+  a.kb = static_cast<int>(F / per / 128);
+  a.kblk = static_cast<int>(F / 128);
+  a.half2 = 128;
+  a.mstep = 256;
+  a.sfb = ws + l.hs;
+  a.sx = h_scale;
+  a.cnt += l.grid;
+  weight(W2);
+  rc = launch_gemm<KIND, 2>(tw2, th, a, l.grid, s);
+  if (rc != MGQ_OK) return rc;
+  if (!launch_after(few_combine_kernel, dim3((H + 511) / 512, T), 128, 0, s, static_cast<const float*>(a.y),
+                    static_cast<const int32_t*>(pa.row_of), probs, T, k, static_cast<int>(H),
+                    static_cast<uint16_t*>(out))) {
+    (void)cudaGetLastError();
+    return MGQ_ERR_CUDA;
+  }
+  return MGQ_OK;
+}
+
+}  // namespace
+}  // namespace mgq
+
+using namespace mgq;
+
+extern "C" size_t mgq_moe_few_workspace_size(int T, int k, int E, int64_t H, int64_t F, int scaling) {
+  const int kind = kind_of(scaling);
+  if (kind < 0 || !few_sizes_ok(T, k, E, H, F, kind)) return 0;
+  return static_cast<size_t>(layout_of(T, k, E, H, F, kind).total);
+}
+
+extern "C" int mgq_moe_few_forward(const void* x_bf16, int T, int64_t H, int64_t F, const int32_t* topk_idx,
+                                   const float* probs, int k, int E, const mgq_operand* W1, const mgq_operand* W2,
+                                   int scaling, const float* x_scale, const float* h_scale, void* out_bf16,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  MGQ_CHECK_ARG(W1 && W2);
+  const int kind = kind_of(scaling);
+  if (kind < 0) return MGQ_ERR_UNSUPPORTED;
+  const int dt = kind == kNV ? MGQ_E2M1 : MGQ_E4M3;
+  if (W1->dtype != dt || W2->dtype != dt) return MGQ_ERR_UNSUPPORTED;
+  if (W1->layout != MGQ_LAYOUT_K || W2->layout != MGQ_LAYOUT_K) return MGQ_ERR_UNSUPPORTED;
+  MGQ_CHECK_ARG(few_sizes_ok(T, k, E, H, F, kind));
+  if (T == 0) return MGQ_OK;
+  MGQ_CHECK_ARG(x_bf16 && topk_idx && probs && out_bf16 && workspace);
+  MGQ_CHECK_ARG(aligned16(x_bf16) && aligned16(out_bf16) && (reinterpret_cast<uintptr_t>(workspace) & 255) == 0);
+  for (const mgq_operand* W : {W1, W2}) {
+    const int64_t K = W == W1 ? H : F;
+    MGQ_CHECK_ARG(W->data && W->scale && aligned16(W->data) && aligned16(W->scale));
+    MGQ_CHECK_ARG(W->ld >= K && W->ld % (kind == kNV ? 256 : 128) == 0);
+    if (kind == kNV) MGQ_CHECK_ARG(W->global_scale);
+    if (kind == kBLK) MGQ_CHECK_ARG(W->ld == K);          // 128x128 scales are laid out by K
+  }
+  if (kind == kNV || kind == kTEN) MGQ_CHECK_ARG(x_scale && h_scale);
+  MGQ_CHECK_ARG(ws_bytes >= mgq_moe_few_workspace_size(T, k, E, H, F, scaling));
+  cudaStream_t s = as_stream(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  switch (kind) {
+    case kMX:
+      return few_forward<kMX>(x_bf16, T, H, F, topk_idx, probs, k, E, W1, W2, x_scale, h_scale, out_bf16, ws, s);
+    case kNV:
+      return few_forward<kNV>(x_bf16, T, H, F, topk_idx, probs, k, E, W1, W2, x_scale, h_scale, out_bf16, ws, s);
+    case kBLK:
+      return few_forward<kBLK>(x_bf16, T, H, F, topk_idx, probs, k, E, W1, W2, x_scale, h_scale, out_bf16, ws, s);
+    default:
+      return few_forward<kTEN>(x_bf16, T, H, F, topk_idx, probs, k, E, W1, W2, x_scale, h_scale, out_bf16, ws, s);
+  }
+}

@@ -42,6 +42,7 @@ EXPORTS = (
     "mgq_moe_unpermute_bwd", "mgq_moe_permute_bwd", "mgq_amax_history_update", "mgq_set_gemm_option",
     "mgq_get_gemm_option", "mgq_nv_scale_image", "mgq_add_rmsnorm_quantize", "mgq_add_rmsnorm_bwd_workspace_size",
     "mgq_add_rmsnorm_bwd", "mgq_router_topk", "mgq_router_topk_bwd",
+    "mgq_moe_few_workspace_size", "mgq_moe_few_forward",
 )
 
 
@@ -115,6 +116,10 @@ def load() -> ctypes.CDLL:
         lib.mgq_add_rmsnorm_bwd.argtypes = [vp, vp, vp, i32, vp, vp, i64, i64, vp, vp, f32, vp, sz, vp]
         lib.mgq_router_topk.argtypes = [vp, i32, i64, i32, i32, i32, i32, f32, vp, vp, vp]
         lib.mgq_router_topk_bwd.argtypes = [vp, i32, vp, vp, i64, i32, i32, i32, i32, f32, vp, vp]
+        lib.mgq_moe_few_workspace_size.restype = sz
+        lib.mgq_moe_few_workspace_size.argtypes = [i32, i32, i32, i64, i64, i32]
+        lib.mgq_moe_few_forward.argtypes = [vp, i32, i64, i64, vp, vp, i32, i32, P(Operand), P(Operand), i32, vp, vp,
+                                            vp, vp, sz, vp]
         for name in EXPORTS:
             if name != "mgq_status_string" and not name.endswith("_workspace_size"):
                 getattr(lib, name).restype = i32
@@ -418,3 +423,23 @@ def router_topk_bwd(logits, topk_idx, dprobs, dlogits, score=SCORE_SOFTMAX, reno
     _of(fn, logits.dtype, (T, E), dlogits)
     _check(load().mgq_router_topk_bwd(_p(logits), _typed(fn, logits), _p(topk_idx), _p(dprobs), T, E, k, score,
                                       int(renorm), scale, _p(dlogits), _s(stream)), fn)
+
+
+def moe_few_workspace_size(T: int, k: int, E: int, H: int, F: int, scaling: int) -> int:
+    return int(load().mgq_moe_few_workspace_size(T, k, E, H, F, scaling))
+
+
+def moe_few_forward(x, topk_idx, probs, W1: Operand, W2: Operand, scaling, E, F, out, workspace, x_scale=None,
+                    h_scale=None, stream=None):
+    """The expert layer for a few tokens: x, out bf16 [T, H]; topk_idx int32 and probs float32 [T, k]."""
+    fn = "mgq_moe_few_forward"
+    T, H = x.shape
+    k = topk_idx.shape[1]
+    _dense(fn, x, topk_idx, probs, out, workspace, x_scale, h_scale)
+    _of(fn, torch.bfloat16, x.shape, x, out)
+    _of(fn, torch.int32, (T, k), topk_idx)
+    _of(fn, torch.float32, (T, k), probs)
+    _of(fn, torch.float32, (1,), x_scale, h_scale)
+    _check(load().mgq_moe_few_forward(_p(x), T, H, F, _p(topk_idx), _p(probs), k, E, ctypes.byref(W1),
+                                      ctypes.byref(W2), scaling, _p(x_scale), _p(h_scale), _p(out), _p(workspace),
+                                      workspace.numel() * workspace.element_size(), _s(stream)), fn)

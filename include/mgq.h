@@ -542,6 +542,35 @@ int mgq_router_topk_bwd(const void* logits, int dtype, const int32_t* topk_idx, 
                         int64_t T, int E, int k, int score, int renorm, float scale, void* dlogits,
                         void* stream);
 
+/* ---- the whole layer for a few tokens ------------------------------------------
+ * The expert layer for decode batches (1 to 128 tokens) in one call, without
+ * padding and bound by one read of the picked experts' weights:
+ *   out[t] = sum_j probs[t, j] W2_e Q(silu(g) u),  [g | u] = W1_e Q(x_t),  e = topk_idx[t, j]
+ * Q is the recipe's row-wise quantisation (e4m3; NVFP4 e2m1) of the float32
+ * values; g, u, h and y stay in float32, out is rounded to bf16 once.
+ *  x_bf16   device [T, H] bf16
+ *  topk_idx device [T, k] int32 (an id outside [0, E) contributes nothing and
+ *           is reported as MGQ_ERR_DEVICE_INDEX); probs device [T, k] float32
+ *  W1       [E, 2F, H] gate rows then up rows, W2 [E, H, F]: operands as the
+ *           grouped GEMMs take them (K-major); scale_image is not used
+ *  scaling  MGQ_MX32_E8M0, MGQ_BLK_1x128_F32 (128x128 weight scales, ld the
+ *           contraction), MGQ_TENSOR_F32 (weight scale s per expert) or
+ *           MGQ_NV16_UE4M3 (global_scale per expert)
+ *  x_scale, h_scale  device float32, MGQ_TENSOR_F32: the scale s of x and of
+ *           h; MGQ_NV16_UE4M3: their global scale s_g (calibrated beforehand:
+ *           a token's result does not depend on its batch); else unused
+ *  workspace  mgq_moe_few_workspace_size() bytes, 256-byte aligned; calls that
+ *           can overlap need workspaces of their own
+ * The result does not depend on the order in which CTAs run. Requires
+ * 0 <= T <= 128, 1 <= k <= 8, k <= E <= 1024, H and F multiples of 128 (NVFP4:
+ * of 256) up to 65536, 16-byte aligned pointers. The workspace size is that of
+ * the current device, 0 for sizes that are refused. */
+size_t mgq_moe_few_workspace_size(int T, int k, int E, int64_t H, int64_t F, int scaling);
+int mgq_moe_few_forward(const void* x_bf16, int T, int64_t H, int64_t F, const int32_t* topk_idx,
+                        const float* probs, int k, int E, const mgq_operand* W1, const mgq_operand* W2,
+                        int scaling, const float* x_scale, const float* h_scale, void* out_bf16,
+                        void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -98,9 +98,10 @@ def quantize_rows(v, recipe, scale=None):
     return OQ.dequantize_tensor(OQ.quantize_tensor(v, np.float32(scale))[0], np.float32(scale))
 
 
-def moe_few(x, idx, probs, w1, w2, recipe, x_scale=None, h_scale=None):
+def moe_few(x, idx, probs, w1, w2, recipe, x_scale=None, h_scale=None, nudge=0.0):
     """out[t] = sum_j probs[t, j] W2_e Q(silu(g) u), [g | u] = W1_e Q(x_t), e = idx[t, j];
-    w1 [E, 2F, H], w2 [E, H, F]: the values of the quantised weights."""
+    w1 [E, 2F, H], w2 [E, H, F]: the values of the quantised weights. nudge:
+    relative change of h before its quantisation."""
     T, k = idx.shape
     E, F = w1.shape[0], w2.shape[2]
     xq = quantize_rows(x, recipe, x_scale)
@@ -111,6 +112,6 @@ def moe_few(x, idx, probs, w1, w2, recipe, x_scale=None, h_scale=None):
             continue
         gu = xq[t] @ w1[e].T
         g, u = gu[:, :F], gu[:, F:]
-        h = quantize_rows(g / (1.0 + np.exp(-g)) * u, recipe, h_scale)
+        h = quantize_rows(g / (1.0 + np.exp(-g)) * u * (1.0 + nudge), recipe, h_scale)
         np.add.at(out, t, (h @ w2[e].T) * np.asarray(probs, np.float64)[t, j][:, None])
     return out

@@ -88,3 +88,44 @@ def test_router_refusals(lib):
             assert f(**bad) == INV, (f.__name__, bad)
         assert f(T=0) == mgq.OK
     assert fwd(p=None) == INV and bwd(d=None) == INV and bwd(dl=None) == INV
+
+
+def test_few_token_layer_refusals(lib):
+    from fp8_grouped_gemm_gb300 import mgq
+    INV, UNS = mgq.ERR_INVALID_ARG, mgq.ERR_UNSUPPORTED
+    size = lib.mgq_moe_few_workspace_size
+    ws = size(4, 2, 8, 512, 256, mgq.MX32_E8M0)
+    assert ws > 0
+    for bad in ((129, 2, 8, 512, 256), (4, 9, 16, 512, 256), (4, 3, 2, 512, 256), (4, 2, 1025, 512, 256),
+                (4, 2, 8, 500, 256), (4, 2, 8, 512, 64), (-1, 2, 8, 512, 256), (4, 0, 8, 512, 256)):
+        assert size(*bad, mgq.MX32_E8M0) == 0
+    assert size(4, 2, 8, 384, 256, mgq.NV16_UE4M3) == 0       # NVFP4: multiples of 256
+    assert size(4, 2, 8, 512, 256, mgq.BLK_128x128_F32) == 0
+    op = lambda ld, dt=mgq.E4M3, **k: mgq.operand(k.pop("data", P), k.pop("scale", P), ld, dt, **k)
+
+    def run(**kw):
+        a = dict(x=P, T=4, H=512, F=256, idx=P, p=P, k=2, E=8, W1=op(512), W2=op(256), sc=mgq.MX32_E8M0, xs=None,
+                 hs=None, out=P, ws=P, n=1 << 40)
+        a.update(kw)
+        r = lambda o: ctypes.byref(o) if o is not None else None
+        return lib.mgq_moe_few_forward(a["x"], a["T"], a["H"], a["F"], a["idx"], a["p"], a["k"], a["E"], r(a["W1"]),
+                                       r(a["W2"]), a["sc"], a["xs"], a["hs"], a["out"], a["ws"], a["n"], None)
+
+    for name in ("x", "idx", "p", "out", "ws", "W1", "W2"):
+        assert run(**{name: None}) == INV, name
+    for name in ("x", "out"):
+        assert run(**{name: P + 8}) == INV, name
+    assert run(ws=P + 16) == INV and run(n=ws - 1) == INV
+    assert run(T=129) == INV and run(H=520) == INV and run(F=100) == INV and run(k=9) == INV and run(E=1) == INV
+    assert run(sc=mgq.BLK_128x128_F32) == UNS and run(W1=op(512, mgq.E5M2)) == UNS
+    assert run(sc=mgq.NV16_UE4M3) == UNS                      # e4m3 codes
+    assert run(W2=op(256, layout=mgq.LAYOUT_MN)) == UNS
+    assert run(W1=op(256)) == INV and run(W1=op(520)) == INV  # row pitch
+    assert run(W1=op(512, data=None)) == INV and run(W2=op(256, scale=None)) == INV and run(W1=op(512, data=P + 8)) == INV
+    nv = dict(sc=mgq.NV16_UE4M3, W1=op(512, mgq.E2M1, global_scale=P), W2=op(256, mgq.E2M1, global_scale=P), xs=P, hs=P)
+    assert run(**{**nv, "xs": None}) == INV and run(**{**nv, "hs": None}) == INV
+    assert run(**{**nv, "W1": op(512, mgq.E2M1)}) == INV
+    assert run(**{**nv, "H": 384}) == INV
+    assert run(sc=mgq.TENSOR_F32) == INV                      # no scales of x and h
+    assert run(sc=mgq.BLK_1x128_F32, W1=op(640)) == INV       # 128x128 scales: no padding of the rows
+    assert run(T=0) == mgq.OK
