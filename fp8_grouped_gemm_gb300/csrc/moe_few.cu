@@ -44,6 +44,14 @@ __host__ __device__ constexpr uint32_t sf_bytes(int kind) { return kind == kBLK 
 
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// true in one lane of the (converged) warp. Unlike a test of the lane index it
+// tells the compiler that one thread is left, so that the operands of TMA and
+// MMA instructions are kept in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 // the four epilogue warps
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -160,8 +168,9 @@ struct FewArgs {
   const float* sx;       // TEN, NV: scale of the tokens' operand
   float* part;           // [2 grid][nmax * 256]
   int32_t* cnt;          // [grid]
-  int nmax;              // tokens a tile can hold (multiple of 16, at most 64)
-  int stages;
+  int nmax;              // tokens a place of `part` can hold (multiple of 16, at most 64)
+  int list;              // experts that can be active at once
+  uint32_t stage_mem;    // shared memory for the stages
   uint32_t idesc0;       // instruction descriptor without N
   // phase 1
   uint8_t* hq;
@@ -174,46 +183,102 @@ struct FewArgs {
   int* err;
 };
 
-struct Seg {
-  int e, m, row0, n, slot, kb0, kb1, tile;
-};
+// The line of units, in order: active expert, tile along M, token block of the
+// expert (so that an expert of more than 64 tokens finds its weights in L2),
+// stage of the contraction. A CTA walks from its first unit without divisions.
+struct Walk {
+  const int4* list;       // active experts: e, first row, rows, first block
+  int mt, kb;             // tiles and stages
+  int left;               // units still to do
+  int a, m, b;            // where the walk stands
+  int e, start, n_e, nb;  // of the active expert
+  int tile, kb0, kb1;     // the current tile (its index on the line) and its stretch of stages
+  int row0, n, slot;      // its token rows
 
-struct Line {             // the CTA's view of the work
-  const int* start;       // [E + 1] first row of each expert
-  const int* nb;          // [E + 1] first token block of each expert
-  int E, mt, kb, U, G;
-};
-
-__device__ __forceinline__ void decode(const Line& w, int u, int u1, Seg& s) {
-  s.tile = u / w.kb;
-  s.kb0 = u - s.tile * w.kb;
-  s.kb1 = min(w.kb, s.kb0 + (u1 - u));
-  const int q = s.tile / w.mt;
-  int lo = 0, hi = w.E;         // the last expert whose first block is at most q
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (w.nb[mid] <= q) lo = mid;
-    else hi = mid;
+  __device__ __forceinline__ void expert() {
+    const int4 x = list[a];
+    e = x.x;
+    start = x.y;
+    n_e = x.z;
+    nb = (x.z + kTok - 1) / kTok;
   }
-  s.e = lo;
-  const int nb = w.nb[lo + 1] - w.nb[lo];
-  const int local = s.tile - w.nb[lo] * w.mt;
-  s.m = local / nb;
-  const int b = local - s.m * nb;
-  s.row0 = w.start[lo] + kTok * b;
-  s.n = min(kTok, w.start[lo + 1] - s.row0);
-  s.slot = w.start[lo] / kTok + b + lo;
-}
-// the CTA that owns unit u
-__device__ __forceinline__ int owner(const Line& w, int u) {
-  return static_cast<int>((static_cast<int64_t>(u + 1) * w.G - 1) / w.U);
+  __device__ __forceinline__ void block() {
+    kb1 = min(kb, kb0 + left);
+    row0 = start + kTok * b;
+    n = min(kTok, n_e - kTok * b);
+    slot = start / kTok + b + e;
+  }
+  __device__ __forceinline__ bool any() const { return left > 0; }
+  __device__ __forceinline__ void begin(const int4* l, const int* at, int mt_, int kb_, int units) {
+    list = l;
+    mt = mt_;
+    kb = kb_;
+    left = units;
+    a = at[0];
+    m = at[1];
+    b = at[2];
+    kb0 = at[3];
+    tile = at[4];
+    if (left > 0) {
+      expert();
+      block();
+    }
+  }
+  __device__ __forceinline__ void next() {
+    left -= kb1 - kb0;
+    kb0 = 0;
+    ++tile;
+    if (left <= 0) return;
+    if (++b == nb) {
+      b = 0;
+      if (++m == mt) {
+        m = 0;
+        ++a;
+        expert();
+      }
+    }
+    block();
+  }
+};
+// The line's U units over G CTAs: the first U % G of them take one more.
+struct Split {
+  int U, G, base, more;
+  __device__ __forceinline__ int owner(int u) const {     // the CTA that has unit u
+    const int edge = more * (base + 1);
+    return u < edge ? u / (base + 1) : more + (u - edge) / base;
+  }
+};
+
+// Sum of the 4 columns at `o` of the partial results of CTAs ca..cb, added in
+// that order; four CTAs' values are requested together.
+__device__ __forceinline__ void join4(const float* part, int64_t place, int ca, int cb, int nc, float* g, float* h) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) g[j] = h[j] = 0.0f;
+  for (int q0 = ca; q0 <= cb; q0 += 4) {
+    float t[4][4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = q0 + i;
+      const float* o = part + (2 * q + (q == ca ? 1 : 0)) * place;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool on = q <= cb && j < nc;
+        t[i][j][0] = on ? __ldcg(o + j * 256) : 0.0f;
+        t[i][j][1] = on ? __ldcg(o + j * 256 + 128) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] += t[i][j][0], h[j] += t[i][j][1];
+  }
 }
 
 // h = silu(g) u of 16 tokens (nj of them real) and one ffn row per thread,
 // quantised along the rows: lane = row within a 32-row block, so an MX block
 // is one warp, an NVFP4 block half of one, a 1x128 block the four warps.
 template <int KIND>
-__device__ __forceinline__ void store_h(const FewArgs& p, const Seg& s, int c16, float (&g)[16], const float (&u)[16],
+__device__ __forceinline__ void store_h(const FewArgs& p, const Walk& s, int c16, float (&g)[16], const float (&u)[16],
                                         float alpha, int row, float sh, uint32_t (*smax)[4][16],
                                         uint32_t& tick) {
   const int nj = min(16, s.n - 16 * c16);
@@ -275,7 +340,7 @@ __device__ __forceinline__ void store_h(const FewArgs& p, const Seg& s, int c16,
   }
 }
 
-__device__ __forceinline__ void store_y(const FewArgs& p, const Seg& s, int c16, const float (&a)[16],
+__device__ __forceinline__ void store_y(const FewArgs& p, const Walk& s, int c16, const float (&a)[16],
                                         const float (&b)[16], float alpha, int row) {
   const int nj = min(16, s.n - 16 * c16);
   const int64_t m0 = static_cast<int64_t>(s.m) * 256 + row;
@@ -294,15 +359,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t CH = sf_chunks(KIND), SF = sf_bytes(KIND);
   constexpr bool BS = KIND == kMX || KIND == kNV;      // block scales through tensor memory
   constexpr uint32_t kCols = BS ? 512 : 256;           // two accumulators of 2 x 64 columns, then scale columns
+  constexpr int kMost = KIND == kNV ? 5 : kMaxStages;  // NVFP4: 48 scale columns a stage
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  const int STG = p.stages;
-  const uint32_t bt = static_cast<uint32_t>(p.nmax) * 128;
-  uint8_t* sA = smem;
-  uint8_t* sB = sA + STG * 2 * kATile;
-  uint8_t* sSF = sB + STG * bt;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sSF + STG * SF);
+  // stages first (1024-byte aligned operand tiles), then the small things
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.stage_mem);
   uint64_t* full = bars;
   uint64_t* empty = bars + kMaxStages;
   uint64_t* t_full = bars + 2 * kMaxStages;
@@ -310,15 +372,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(t_empty + 2);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_last = reinterpret_cast<volatile int*>(s_tmem + 2);
-  uint32_t (*smax)[4][16] = reinterpret_cast<uint32_t (*)[4][16]>(bars + 2 * kMaxStages + 8);   // [2][4][16]
-  int* s_start = reinterpret_cast<int*>(bars + 2 * kMaxStages + 8) + 128;
-  int* s_nb = s_start + p.E + 1;
+  int* s_at = reinterpret_cast<int*>(s_tmem + 4);      // [8] start of the walk, blocks, rows of the largest group
+  uint32_t (*smax)[4][16] = reinterpret_cast<uint32_t (*)[4][16]>(bars + 24);   // [2][4][16]
+  int4* s_list = reinterpret_cast<int4*>(bars + 24 + 64);
+  int* s_cnt = reinterpret_cast<int*>(s_list + p.list);
 
   const int warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
   grid_launch();
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < STG; ++s) {
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < kMost; ++s) {
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], KIND == kBLK ? 5 : 1);   // the MMAs; BLK: and the four epilogue warps
     }
@@ -331,53 +394,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::prefetch_tmap(&tmW);
     ptx::prefetch_tmap(&tmX);
   }
+  // rows per expert
+  for (int i = threadIdx.x; i < p.E; i += kThreads) s_cnt[i] = 0;
+  int e0 = threadIdx.x < p.R ? __ldg(p.idx + threadIdx.x) : -1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.R; i += kThreads) {
+    const int e = i < kThreads ? e0 : __ldg(p.idx + i);
+    if (e >= 0 && e < p.E) atomicAdd(&s_cnt[e], 1);
+  }
   if (warp == 1) {
+    __syncwarp();
     ptx::tmem_alloc(s_tmem, kCols);
     ptx::tmem_relinquish();
   }
-  // rows per expert, then their prefix sums (and those of the token blocks)
-  for (int i = threadIdx.x; i < p.E; i += kThreads) s_start[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.R; i += kThreads) {
-    const int e = __ldg(p.idx + i);
-    if (e >= 0 && e < p.E) atomicAdd(&s_start[e], 1);
-  }
   __syncthreads();
   if (warp == 0) {
-    int rows = 0, blocks = 0;
-    for (int b = 0; b < p.E; b += 32) {
-      const int e = b + lane;
-      const int n = e < p.E ? s_start[e] : 0, nb = (n + kTok - 1) / kTok;
-      int r = n, q = nb;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int r2 = __shfl_up_sync(0xFFFFFFFFu, r, o), q2 = __shfl_up_sync(0xFFFFFFFFu, q, o);
-        if (lane >= o) r += r2, q += q2;
-      }
-      if (e < p.E) s_start[e] = rows + r - n, s_nb[e] = blocks + q - nb;
-      rows += __shfl_sync(0xFFFFFFFFu, r, 31);
-      blocks += __shfl_sync(0xFFFFFFFFu, q, 31);
+    // The active experts in order. A lane takes a run of experts; one scan
+    // gives its first row, block and place (rows and blocks below 2^11 each,
+    // places below 2^10).
+    const int per = (p.E + 31) / 32, lo = lane * per, hi = min(p.E, lo + per);
+    uint32_t mine = 0, most = 0;
+    for (int e = lo; e < hi; ++e) {
+      const uint32_t n = s_cnt[e];
+      most = max(most, n);
+      if (n) mine += n | ((n + kTok - 1) / kTok) << 11 | 1u << 22;
     }
-    if (lane == 0) s_start[p.E] = rows, s_nb[p.E] = blocks;
+    uint32_t sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const uint32_t all = __shfl_sync(0xFFFFFFFFu, sum, 31);
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    sum -= mine;
+    int row = sum & 2047, blk = (sum >> 11) & 2047, at = sum >> 22;
+    // this CTA's first unit and the expert it falls in
+    const int U = static_cast<int>((all >> 11) & 2047) * p.mt * p.kb;
+    const int G = max(1, min(static_cast<int>(gridDim.x), U));
+    const int u0 = min(static_cast<int>(blockIdx.x), G) * (U / G) + min(static_cast<int>(blockIdx.x), U % G);
+    const int tile = u0 / p.kb;
+    for (int e = lo; e < hi; ++e) {
+      const int n = s_cnt[e];
+      if (n == 0) continue;
+      const int nb = (n + kTok - 1) / kTok;
+      s_list[at] = make_int4(e, row, n, blk);
+      const int local = tile - blk * p.mt;
+      if (local >= 0 && local < nb * p.mt) {
+        s_at[0] = at;
+        s_at[1] = local / nb;
+        s_at[2] = local % nb;
+        s_at[3] = u0 - tile * p.kb;
+        s_at[4] = tile;
+      }
+      row += n;
+      blk += nb;
+      ++at;
+    }
+    if (lane == 0) s_at[5] = U, s_at[6] = static_cast<int>(most);
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  Line w{s_start, s_nb, p.E, p.mt, p.kb, s_nb[p.E] * p.mt * p.kb, 0};
-  w.G = min(static_cast<int>(gridDim.x), w.U);
-  int u0 = 0, u1 = 0;
-  if (static_cast<int>(blockIdx.x) < w.G) {
-    u0 = static_cast<int>(static_cast<int64_t>(w.U) * blockIdx.x / w.G);
-    u1 = static_cast<int>(static_cast<int64_t>(w.U) * (blockIdx.x + 1) / w.G);
-  }
+  Split sp;
+  sp.U = s_at[5];
+  sp.G = max(1, min(static_cast<int>(gridDim.x), sp.U));
+  sp.base = sp.U / sp.G;
+  sp.more = sp.U - sp.base * sp.G;
+  const int units = static_cast<int>(blockIdx.x) < sp.G ? sp.base + (static_cast<int>(blockIdx.x) < sp.more ? 1 : 0) : 0;
+  // as many stages as the largest token block of the call leaves room for
+  const uint32_t bt = static_cast<uint32_t>((min(s_at[6], kTok) + 15) / 16) * 2048;
+  const int STG = min(kMost, static_cast<int>(p.stage_mem / (2 * kATile + bt + SF)));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + STG * 2 * kATile;
+  uint8_t* sSF = sB + STG * bt;
+  Walk s;
+  s.begin(s_list, s_at, p.mt, p.kb, units);
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---------------------------------------------------------- producer
       // The weights do not depend on the launch before: the first stages of
       // them are requested before the wait for it, the tokens' after.
-      auto load_w = [&](const Seg& s, int kb, uint32_t st) {
+      auto load_w = [&](const Walk& s, int kb, int st) {
         const bool two = PHASE == 1 || s.m * 256 + 128 < p.rows_end;
         const int64_t row = s.e * p.rows_e + static_cast<int64_t>(s.m) * p.mstep;
         const uint32_t n16 = (s.n + 15) / 16;
@@ -395,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            &full[st]);
         }
       };
-      auto load_x = [&](const Seg& s, int kb, uint32_t st) {
+      auto load_x = [&](const Walk& s, int kb, int st) {
         for (int i = 0; i < (s.n + 15) / 16; ++i)
           ptx::tma_load_2d(sB + st * bt + i * 2048, &tmX, &full[st], kb * 128, s.row0 + 16 * i);
         if (BS)
@@ -404,22 +504,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (KIND == kBLK)
           ptx::bulk_load(sSF + st * SF, p.sfb + (static_cast<int64_t>(s.slot) * p.kb + kb) * 256, 256, &full[st]);
       };
-      Seg s;
-      uint32_t it = 0;
-      for (int u = u0; u < u1 && it < static_cast<uint32_t>(STG); u += s.kb1 - s.kb0) {
-        decode(w, u, u1, s);
-        for (int kb = s.kb0; kb < s.kb1 && it < static_cast<uint32_t>(STG); ++kb, ++it) load_w(s, kb, it);
-      }
-      const uint32_t early = it;
+      int early = 0;
+      for (Walk v = s; v.any() && early < STG; v.next())
+        for (int kb = v.kb0; kb < v.kb1 && early < STG; ++kb, ++early) load_w(v, kb, early);
       grid_wait();
-      it = 0;
-      for (int u = u0; u < u1; u += s.kb1 - s.kb0) {
-        decode(w, u, u1, s);
+      int it = 0, st = 0;
+      uint32_t ph = 1;                    // (a first pass over the ring waits for nothing)
+      for (; s.any(); s.next()) {
         for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
-          const uint32_t st = it % STG;
           if (it >= early) {
             if (*s_abort) break;
-            if (!ptx::mbar_wait(&empty[st], ((it / STG) & 1) ^ 1, kWaitNs)) {
+            if (!ptx::mbar_wait(&empty[st], ph, kWaitNs)) {
               report(p.err, MGQ_ERR_TIMEOUT);
               *s_abort = 1;
               break;
@@ -427,33 +522,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             load_w(s, kb, st);
           }
           load_x(s, kb, st);
+          if (++st == STG) st = 0, ph ^= 1;
         }
         if (*s_abort) break;
       }
       // given up: no copy of this CTA may land after it has left
       if (*s_abort)
-        for (uint32_t i = it > static_cast<uint32_t>(STG) ? it - STG : 0; i < it; ++i)
+        for (int i = it > STG ? it - STG : 0; i < it; ++i)
           ptx::mbar_wait(&full[i % STG], (i / STG) & 1, kWaitNs / 100);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---------------------------------------------------------- MMA issuer
       const uint32_t sA0 = ptx::smem_u32(sA), sB0 = ptx::smem_u32(sB), sF0 = ptx::smem_u32(sSF);
-      Seg s;
-      uint32_t it = 0, tc = 0;
+      int st = 0;
+      uint32_t ph = 0, tc = 0;
       bool ok = true;
-      for (int u = u0; u < u1 && ok; u += s.kb1 - s.kb0) {
-        decode(w, u, u1, s);
+      for (; s.any() && ok; s.next()) {
         const bool two = PHASE == 1 || s.m * 256 + 128 < p.rows_end;
         const uint32_t idesc = p.idesc0 | (static_cast<uint32_t>((s.n + 15) / 16 * 2) << 17);
         uint32_t a = tc & 1;
-        for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
-          const uint32_t st = it % STG;
+        for (int kb = s.kb0; kb < s.kb1; ++kb) {
           if (KIND == kBLK || kb == s.kb0) {
             a = tc & 1;
             ok = !*s_abort && ptx::mbar_wait(&t_empty[a], ((tc >> 1) & 1) ^ 1, kWaitNs);
           }
-          ok = ok && !*s_abort && ptx::mbar_wait(&full[st], (it / STG) & 1, kWaitNs);
+          ok = ok && !*s_abort && ptx::mbar_wait(&full[st], ph, kWaitNs);
           if (!ok) {
             report(p.err, MGQ_ERR_TIMEOUT);
             *s_abort = 1;
@@ -470,20 +564,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const uint64_t bd = ptx::sdesc_kmajor_sw128(sB0 + st * bt);
-          for (int h = 0; h < (two ? 2 : 1); ++h) {
-            const uint64_t ad = ptx::sdesc_kmajor_sw128(sA0 + (st * 2 + h) * kATile);
-            const uint32_t d = tmem + a * 2 * kTok + h * kTok;
+          const uint64_t ad = ptx::sdesc_kmajor_sw128(sA0 + st * 2 * kATile);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t acc = ((KIND != kBLK && kb > s.kb0) || kk > 0) ? 1u : 0u;
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t acc = ((KIND != kBLK && kb > s.kb0) || kk > 0) ? 1u : 0u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1 && !two) break;
+              const uint64_t adk = ad + h * (kATile >> 4) + kk * 2;
+              const uint32_t d = tmem + a * 2 * kTok + h * kTok;
               if (KIND == kNV)
-                ptx::mma_mxf4nvf4(d, ad + kk * 2, bd + kk * 2, idesc, sf_t + (h * CH + kk) * 4, sf_t + (2 * CH + kk) * 4,
-                                  acc);
+                ptx::mma_mxf4nvf4(d, adk, bd + kk * 2, idesc, sf_t + (h * CH + kk) * 4, sf_t + (2 * CH + kk) * 4, acc);
               else if (KIND == kMX)
-                ptx::mma_mxf8f6f4(d, ad + kk * 2, bd + kk * 2, idesc | ptx::idesc_sf_ids(kk, kk), sf_t + h * 4,
-                                  sf_t + 8, acc);
+                ptx::mma_mxf8f6f4(d, adk, bd + kk * 2, idesc | ptx::idesc_sf_ids(kk, kk), sf_t + h * 4, sf_t + 8, acc);
               else
-                ptx::mma_f8f6f4(d, ad + kk * 2, bd + kk * 2, idesc, acc);
+                ptx::mma_f8f6f4(d, adk, bd + kk * 2, idesc, acc);
             }
           }
           ptx::mma_commit(&empty[st]);
@@ -491,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mma_commit(&t_full[a]);
             ++tc;
           }
+          if (++st == STG) st = 0, ph ^= 1;
         }
       }
     }
@@ -500,12 +596,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_wait();
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tlane = static_cast<uint32_t>(warp & 3) << 21;
+    const int64_t place = static_cast<int64_t>(p.nmax) * 256;
     const float sx = KIND == kNV || KIND == kTEN ? __ldg(p.sx) : 1.0f;
     const float sh = PHASE == 1 && (KIND == kNV || KIND == kTEN) ? __ldg(p.h_scale) : 1.0f;
-    Seg s;
-    uint32_t it = 0, tc = 0, tick = 0;
-    for (int u = u0; u < u1; u += s.kb1 - s.kb0) {
-      decode(w, u, u1, s);
+    int st = 0;
+    uint32_t ph = 0, tc = 0, tick = 0;
+    for (; s.any(); s.next()) {
       const int n16 = (s.n + 15) / 16;
       const bool whole = s.kb1 - s.kb0 == p.kb;
       float alpha = 1.0f;
@@ -515,9 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* mine = nullptr;
       if (!whole) {
         const int first = s.tile * p.kb;
-        ca = owner(w, first);
-        cb = owner(w, first + p.kb - 1);
-        mine = p.part + static_cast<int64_t>(2 * blockIdx.x + (ca == static_cast<int>(blockIdx.x) ? 1 : 0)) * p.nmax * 256;
+        ca = sp.owner(first);
+        cb = sp.owner(first + p.kb - 1);
+        mine = p.part + (2 * blockIdx.x + (ca == static_cast<int>(blockIdx.x) ? 1 : 0)) * place;
       }
       bool alive = true;
       if (KIND == kBLK) {
@@ -531,11 +627,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 16; ++j) acc[h][c][j] = 0.0f;
         const int64_t wr = (s.e * p.rows_e + static_cast<int64_t>(s.m) * p.mstep) / 128;
         const bool two = PHASE == 1 || s.m * 256 + 128 < p.rows_end;
-        for (int kb = s.kb0; kb < s.kb1; ++kb, ++it, ++tc) {
-          const uint32_t st = it % STG, a = tc & 1;
+        for (int kb = s.kb0; kb < s.kb1; ++kb, ++tc) {
+          const uint32_t a = tc & 1;
           const float w0 = __ldg(p.sw + wr * p.kblk + kb);
           const float w1 = two ? __ldg(p.sw + (wr + p.half2 / 128) * p.kblk + kb) : 0.0f;
-          alive = __all_sync(0xFFFFFFFFu, !*s_abort && ptx::mbar_wait(&full[st], (it / STG) & 1, kWaitNs) &&
+          alive = __all_sync(0xFFFFFFFFu, !*s_abort && ptx::mbar_wait(&full[st], ph, kWaitNs) &&
                                               ptx::mbar_wait(&t_full[a], (tc >> 1) & 1, kWaitNs));
           if (!alive) break;
           ptx::tc_fence_after();
@@ -563,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(&t_empty[a]);
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&empty[st]);
+          if (++st == STG) st = 0, ph ^= 1;
         }
         if (alive) {
 #pragma unroll
@@ -620,24 +717,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       if (!whole) {
-        __threadfence();
+        // the barrier orders the four warps' stores before the fence of the
+        // thread that counts this CTA in
         epi_sync();
-        if (threadIdx.x == 64) *s_last = atomicAdd(p.cnt + ca, 1) == cb - ca;
+        if (threadIdx.x == 64) {
+          __threadfence();
+          *s_last = atomicAdd(p.cnt + ca, 1) == cb - ca;
+          __threadfence();
+        }
         epi_sync();
         if (*s_last) {
-          __threadfence();
           for (int c = 0; c < n16; ++c) {
             float g[16], h[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) g[j] = 0.0f, h[j] = 0.0f;
-            for (int q = ca; q <= cb; ++q) {
-              const float* o = p.part + static_cast<int64_t>(2 * q + (q == ca ? 1 : 0)) * p.nmax * 256 + c * 16 * 256 + row;
+            for (int j = 0; j < 16; ++j) g[j] = h[j] = 0.0f;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if (16 * c + j >= s.n) break;
-                g[j] += __ldcg(o + j * 256);
-                h[j] += __ldcg(o + j * 256 + 128);
-              }
+            for (int j = 0; j < 4; ++j) {
+              if (16 * c + 4 * j < s.n)
+                join4(p.part + (16 * c + 4 * j) * 256 + row, place, ca, cb, s.n - 16 * c - 4 * j, g + 4 * j, h + 4 * j);
             }
             if (PHASE == 1) store_h<KIND>(p, s, c, g, h, alpha, row, sh, smax, tick);
             else store_y(p, s, c, g, h, alpha, row);
@@ -757,13 +854,11 @@ int launch_gemm(const CUtensorMap& tw, const CUtensorMap& tx, FewArgs p, int gri
       return MGQ_ERR_CUDA;
     if (dev < 64) attr_set[dev] = true;
   }
-  // what is not a stage: alignment, barriers and flags, block maxima, the experts' prefix sums
-  const size_t fixed = 1024 + (2 * kMaxStages + 8) * 8 + 128 * 4 + 2 * (static_cast<size_t>(p.E) + 1) * 4;
-  const size_t stage = 2 * kATile + static_cast<size_t>(p.nmax) * 128 + sf_bytes(KIND);
-  int stages = static_cast<int>((kSmemMax - fixed) / stage);
-  const int most = KIND == kNV ? 5 : kMaxStages;       // NVFP4: 48 scale columns a stage in tensor memory
-  p.stages = stages < most ? stages : most;
-  if (!launch_after(kern, dim3(grid), kThreads, fixed + p.stages * stage, s, tw, tx, p)) {
+  // what is not a stage: alignment, barriers and flags, block maxima, the
+  // list of active experts, the counts
+  const size_t small = 24 * 8 + 128 * 4 + static_cast<size_t>(p.list) * 16 + static_cast<size_t>(p.E) * 4;
+  p.stage_mem = static_cast<uint32_t>((kSmemMax - 1024 - small) / 1024 * 1024);
+  if (!launch_after(kern, dim3(grid), kThreads, 1024 + p.stage_mem + small, s, tw, tx, p)) {
     (void)cudaGetLastError();
     return MGQ_ERR_CUDA;
   }
@@ -809,6 +904,7 @@ int few_forward(const void* x, int T, int64_t H, int64_t F, const int32_t* idx, 
   a.E = E;
   a.part = reinterpret_cast<float*>(ws + l.part);
   a.nmax = l.nmax;
+  a.list = E < R ? E : R;
   a.err = err;
   a.hq = ws + l.hq;
   a.hs = ws + l.hs;
