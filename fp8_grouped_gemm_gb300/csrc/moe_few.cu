@@ -63,6 +63,16 @@ __device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
   return r & 0xFFu;
 }
 
+// 1x128 scale of a block of x or h: s = 448 (1 / amax) in two float32 roundings,
+// as perf/operators.py defines it (1 for an all-zero block, the largest float32
+// on overflow). The quantisers' IEEE quotient 448 / amax can differ in the last
+// bit, and bf16 inputs do lie on rounding boundaries of their codes: a value in
+// some 500 takes the other neighbour, which requantising h then amplifies.
+__device__ __forceinline__ float blk_scale_few(uint32_t amax_bits) {
+  const float s = amax_bits == 0 ? 1.0f : __fmul_rn(448.0f, __fdiv_rn(1.0f, __uint_as_float(amax_bits)));
+  return isinf(s) ? 3.40282347e38f : s;
+}
+
 // ---------------------------------------------------------------------------
 // Routed rows. Row order: by expert, then by entry i = t k + j. Tokens of an
 // expert fall into blocks of 64; block b of an expert whose rows start at s
@@ -132,9 +142,20 @@ __global__ void __launch_bounds__(128) few_prep_kernel(PrepArgs a) {
       if ((lane & 1) == 0) *reinterpret_cast<uint32_t*>(a.xs + (slot * (a.H / 64) + c / 64) * 512 + in_chunk) = b.s4;
     }
   } else {
-    constexpr int SC = KIND == kMX ? MGQ_MX32_E8M0 : KIND == kBLK ? MGQ_BLK_1x128_F32 : MGQ_TENSOR_F32;
+    constexpr int SC = KIND == kMX ? MGQ_MX32_E8M0 : MGQ_TENSOR_F32;
     Block32 b;
-    quantize32<SC, MGQ_E4M3>(v, absmax_bits_f32(v, 32), KIND == kTEN ? __ldg(a.x_scale) : 1.0f, true, b);
+    if (KIND == kBLK) {
+      uint32_t m = absmax_bits_f32(v, 32);
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      const float mult = blk_scale_few(m);
+      b.sinv = __fdiv_rn(1.0f, mult);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        b.cw[j] = cvt_fp8x4_mul<MGQ_E4M3>(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], mult);
+    } else {
+      quantize32<SC, MGQ_E4M3>(v, absmax_bits_f32(v, 32), KIND == kTEN ? __ldg(a.x_scale) : 1.0f, true, b);
+    }
     if (in) {
       uint4* dst = reinterpret_cast<uint4*>(a.xq + static_cast<int64_t>(row) * a.H + c);
       dst[0] = make_uint4(b.cw[0], b.cw[1], b.cw[2], b.cw[3]);
@@ -329,7 +350,7 @@ __device__ __forceinline__ void store_h(const FewArgs& p, const Walk& s, int c16
       uint32_t m = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) m = max(m, smax[tick & 1][q][j]);
-      const float mult = blk_scale<MGQ_E4M3>(m);
+      const float mult = blk_scale_few(m);
       p.hq[r * p.F + f0 + row] = static_cast<uint8_t>(cvt_e4m3x2(__fmul_rn(g[j], mult), 0.0f));
       if (row == 0)
         reinterpret_cast<float*>(p.hs)[(static_cast<int64_t>(s.slot) * (p.F / 128) + s.m) * kTok + col] =

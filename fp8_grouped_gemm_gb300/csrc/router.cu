@@ -10,11 +10,11 @@
 //   sigmoid:               dl_j = scale d_j s_j (1 - s_j)
 //   sigmoid, renormalised: dl_j = scale / S (d_j - sum_i d_i s_i / S) s_j (1 - s_j)
 //
-// One warp takes one row and holds it in registers (V values a lane). Each of
-// the k rounds finds the largest ordered key with one integer warp reduction
-// and the lowest id that has it with a second one; no memory is touched
-// between the load of the logits and the store of the k results, so the
-// kernels are bound by the logits' traffic (or, for few rows, by latency).
+// One warp takes one row and holds it in registers, lane l the V consecutive
+// experts V l .. V l + V - 1, sorted. Each of the k rounds finds the largest
+// ordered key among the lanes' heads with one integer warp reduction; the
+// lowest lane that has it holds the lowest such id. No memory is touched
+// between the load of the logits and the store of the k results.
 #include "mgq_internal.h"
 #include "device_common.cuh"
 
@@ -24,11 +24,12 @@ namespace {
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kMaxTopK = 8;
 
+// NaN ranks with the masked experts; -0 becomes +0
+__device__ __forceinline__ float clean(float v) { return v != v ? -INFINITY : v + 0.0f; }
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
-  const float v = BF16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << 16)
-                       : __ldg(static_cast<const float*>(p) + i);
-  return v != v ? -INFINITY : v + 0.0f;   // NaN ranks with the masked experts; -0 becomes +0
+  return clean(BF16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << 16)
+                    : __ldg(static_cast<const float*>(p) + i));
 }
 // unsigned key with the order of the floats; 0 is below every float's key
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -55,7 +56,7 @@ __device__ __forceinline__ float softmax_term(float x, float m) { return m == -I
 struct RouterArgs {
   const void* logits;
   int64_t T;
-  int E, k;
+  int E, k, vec;
   float scale;
   int32_t* idx;
   float* probs;
@@ -66,54 +67,114 @@ struct RouterArgs {
   int* err;
 };
 
+// the V logits of a row from expert e0 on; -infinity past the end (vec: whole
+// aligned vectors)
+template <int V, bool BF16>
+__device__ __forceinline__ void load_row(const RouterArgs& a, int64_t r, int e0, float* v) {
+  const int64_t at = r * a.E + e0;
+  if (V >= 4 && a.vec) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      if (e0 + i < a.E) {
+        if (BF16) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + at + i));
+          v[i] = bf16_lo(w.x), v[i + 1] = bf16_hi(w.x), v[i + 2] = bf16_lo(w.y), v[i + 3] = bf16_hi(w.y);
+        } else {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at + i));
+          v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i + j] = clean(v[i + j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i + j] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = e0 + i < a.E ? load_logit<BF16>(a.logits, at + i) : -INFINITY;
+  }
+}
+
+// sorts a lane's keys (largest first, equal keys in their order) with their
+// place 0..V-1: exchanges of neighbours only
+template <int V>
+__device__ __forceinline__ void sort_lane(uint32_t* key, int* at) {
+#pragma unroll
+  for (int i = 1; i < V; ++i)
+#pragma unroll
+    for (int j = V - 1; j >= i; --j) {
+      const bool swap = key[j] > key[j - 1];
+      const uint32_t k0 = swap ? key[j] : key[j - 1], k1 = swap ? key[j - 1] : key[j];
+      const int a0 = swap ? at[j] : at[j - 1], a1 = swap ? at[j - 1] : at[j];
+      key[j - 1] = k0, key[j] = k1, at[j - 1] = a0, at[j] = a1;
+    }
+}
+
 template <int V, bool BF16, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
-  const int lane = threadIdx.x & 31;
+  constexpr bool SORTED = V <= 4;     // longer runs: find the next best when the head is taken
+  const int lane = threadIdx.x & 31, e0 = lane * V;
   const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   for (int64_t r = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); r < a.T; r += nw) {
+    float v[V];
     uint32_t key[V];
+    int at[V];
+    load_row<V, BF16>(a, r, e0, v);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = lane + 32 * i;
-      key[i] = e < a.E ? order_key(load_logit<BF16>(a.logits, r * a.E + e)) : 0u;
+      key[i] = e0 + i < a.E ? order_key(v[i]) : 0u;
+      at[i] = i;
     }
-    float l_sel = 0.0f;   // lane j: the j-th selected logit and its expert
+    uint32_t head = 0;
+    int hi = 0;
+    if (SORTED) {
+      sort_lane<V>(key, at);
+      head = key[0], hi = at[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[i] > head) head = key[i], hi = i;
+    }
+    uint32_t k_sel = 0;   // lane j: the j-th selected key and its expert
     int e_sel = 0;
-    float top = 0.0f;
-    float all = 0.0f;
-    uint32_t best = 0;
-    int bi = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (key[i] > best) best = key[i], bi = i;
+    uint32_t top = 0;
     for (int j = 0; j < a.k; ++j) {
-      const uint32_t m = __reduce_max_sync(kFull, best);
-      const uint32_t mine = best == m ? static_cast<uint32_t>(lane + 32 * bi) : kFull;
-      const uint32_t e = __reduce_min_sync(kFull, mine);
-      if (lane == j) l_sel = from_key(m), e_sel = static_cast<int>(e);
-      if (j == 0) {
-        top = from_key(m);
-        if (!SIGMOID && !RENORM) {   // the whole row's softmax denominator, before keys are taken out
+      const uint32_t m = __reduce_max_sync(kFull, head);
+      const int w = __ffs(__ballot_sync(kFull, head == m)) - 1;
+      const int e = __shfl_sync(kFull, e0 + hi, w);
+      if (lane == j) k_sel = m, e_sel = e;
+      if (j == 0) top = m;
+      if (lane == w) {    // the owner takes it out
+        if (SORTED) {
 #pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (key[i]) all += softmax_term(from_key(key[i]), top);
-          all = warp_sum(all);
-        }
-      }
-      if (mine == e) {   // the owner takes it out and finds its next best
-        best = 0;
-        const int taken = bi;
-        bi = 0;
+          for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1], at[i] = at[i + 1];
+          key[V - 1] = 0;
+          head = key[0], hi = at[0];
+        } else {
+          head = 0;
+          const int taken = hi;
+          hi = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (i == taken) key[i] = 0;
-          if (key[i] > best) best = key[i], bi = i;
+          for (int i = 0; i < V; ++i) {
+            if (i == taken) key[i] = 0;
+            if (key[i] > head) head = key[i], hi = i;
+          }
         }
       }
     }
     const bool on = lane < a.k;
-    const float s = !on ? 0.0f : SIGMOID ? sigmoid_f32(l_sel) : softmax_term(l_sel, top);
-    const float S = RENORM ? warp_sum(s) : SIGMOID ? 1.0f : all;
+    const float mx = from_key(top), l = from_key(k_sel);
+    const float s = !on ? 0.0f : SIGMOID ? sigmoid_f32(l) : softmax_term(l, mx);
+    float S = 1.0f;
+    if (RENORM) {
+      S = warp_sum(s);
+    } else if (!SIGMOID) {
+      S = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) S += softmax_term(v[i], mx);
+      S = warp_sum(S);
+    }
     if (on) {
       a.idx[r * a.k + lane] = e_sel;
       a.probs[r * a.k + lane] = S == 0.0f ? 0.0f : a.scale * (s / S);
@@ -123,7 +184,13 @@ __global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
 
 template <int V, bool BF16, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(256) router_bwd_kernel(RouterArgs a) {
-  const int lane = threadIdx.x & 31;
+  // the dense row is put together in shared memory: zeros, the selected
+  // experts' gradients by id, then V consecutive values a lane
+  __shared__ __align__(16) float rows[8][32 * V];
+  const int lane = threadIdx.x & 31, e0 = lane * V;
+  float* row = rows[threadIdx.x >> 5];
+#pragma unroll
+  for (int i = 0; i < V; ++i) row[e0 + i] = 0.0f;
   const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   for (int64_t r = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); r < a.T; r += nw) {
     int e = -1;
@@ -140,7 +207,7 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(RouterArgs a) {
     const float l = on ? load_logit<BF16>(a.logits, r * a.E + e) : -INFINITY;
     float g = 0.0f;         // lane j: the selected logit's own gradient
     float back = 0.0f;      // softmax over the row: what every expert's score loses
-    float top = 0.0f, inv = 0.0f, v[V];
+    float top = 0.0f, v[V];
     if (SIGMOID) {
       const float s = on ? sigmoid_f32(l) : 0.0f;
       if (RENORM) {
@@ -160,38 +227,47 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(RouterArgs a) {
       g = q > 0.0f ? a.scale * q * (d - c) : 0.0f;
     } else {
       uint32_t km = 0;
+      load_row<V, BF16>(a, r, e0, v);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int x = lane + 32 * i;
-        v[i] = x < a.E ? load_logit<BF16>(a.logits, r * a.E + x) : -INFINITY;
-        km = max(km, order_key(v[i]));
-      }
+      for (int i = 0; i < V; ++i) km = max(km, order_key(v[i]));
       top = from_key(__reduce_max_sync(kFull, km));
       float all = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) all += softmax_term(v[i], top);
       all = warp_sum(all);
-      inv = all == 0.0f ? 0.0f : 1.0f / all;
+      const float inv = all == 0.0f ? 0.0f : 1.0f / all;
       const float s = on ? softmax_term(l, top) * inv : 0.0f;
-      back = a.scale * warp_sum(s > 0.0f ? s * d : 0.0f);
+      back = a.scale * warp_sum(s > 0.0f ? s * d : 0.0f) * inv;
       g = s > 0.0f ? a.scale * s * d : 0.0f;
     }
-    // dense row: the selected experts' gradients by id
+    if (on) atomicAdd(row + e, g);      // (ids of a row are distinct: one addition each)
+    __syncwarp();
+    float o[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int x = lane + 32 * i;
-      float o = 0.0f;
-      if (!SIGMOID && !RENORM) o = -softmax_term(v[i], top) * inv * back;
-      for (int j = 0; j < a.k; ++j) {
-        const int ej = __shfl_sync(kFull, e, j);
-        const float gj = __shfl_sync(kFull, g, j);
-        if (ej == x) o += gj;
-      }
-      if (x < a.E) {
+      o[i] = row[e0 + i];
+      row[e0 + i] = 0.0f;
+      if (!SIGMOID && !RENORM) o[i] -= softmax_term(v[i], top) * back;
+    }
+    __syncwarp();
+    const int64_t at = r * a.E + e0;
+    if (V >= 4 && a.vec) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        if (e0 + i >= a.E) continue;
         if (BF16)
-          static_cast<__nv_bfloat16*>(a.dlogits)[r * a.E + x] = __float2bfloat16_rn(o);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dlogits) + at + i) =
+              make_uint2(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]));
         else
-          static_cast<float*>(a.dlogits)[r * a.E + x] = o;
+          *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + at + i) =
+              make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (e0 + i >= a.E) continue;
+        if (BF16) static_cast<__nv_bfloat16*>(a.dlogits)[at + i] = __float2bfloat16_rn(o[i]);
+        else static_cast<float*>(a.dlogits)[at + i] = o[i];
       }
     }
   }
@@ -213,13 +289,17 @@ void launch_mode(const RouterArgs& a, bool bwd, bool sigmoid, bool renorm, int g
 }
 
 template <bool BF16>
-void launch_router(const RouterArgs& a, bool bwd, bool sigmoid, bool renorm, cudaStream_t s) {
+void launch_router(RouterArgs a, bool bwd, bool sigmoid, bool renorm, cudaStream_t s) {
+  // vectors of four logits: rows of a multiple of four, aligned bases
+  const uintptr_t size = BF16 ? 8 : 16;
+  a.vec = a.E % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits)) & (size - 1)) == 0;
   const int64_t ctas = (a.T + 7) / 8, most = static_cast<int64_t>(num_sms()) * 8;
   const int grid = static_cast<int>(ctas < most ? ctas : most);
   if (a.E <= 32) launch_mode<1, BF16>(a, bwd, sigmoid, renorm, grid, s);
   else if (a.E <= 64) launch_mode<2, BF16>(a, bwd, sigmoid, renorm, grid, s);
   else if (a.E <= 128) launch_mode<4, BF16>(a, bwd, sigmoid, renorm, grid, s);
   else if (a.E <= 256) launch_mode<8, BF16>(a, bwd, sigmoid, renorm, grid, s);
+  else if (a.E <= 512) launch_mode<16, BF16>(a, bwd, sigmoid, renorm, grid, s);
   else launch_mode<32, BF16>(a, bwd, sigmoid, renorm, grid, s);
 }
 
@@ -268,6 +348,7 @@ extern "C" int mgq_router_topk_bwd(const void* logits, int dtype, const int32_t*
   if (rc != MGQ_OK) return rc;
   if (T == 0) return MGQ_OK;
   MGQ_CHECK_ARG(topk_idx && dprobs && dlogits);
+  MGQ_CHECK_ARG((reinterpret_cast<uintptr_t>(dlogits) & (dtype == MGQ_OUT_BF16 ? 1 : 3)) == 0);
   RouterArgs a{};
   a.logits = logits;
   a.T = T;

@@ -142,8 +142,8 @@ def _p(t):
 
 
 def _s(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:      # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -344,14 +344,24 @@ def amax_history_update(history, head, amax, scale, fmax, stream=None):
                                           ctypes.c_float(fmax), _s(stream)), "mgq_amax_history_update")
 
 
-def _dense(where, *tensors):
-    """The row-major tensors these calls read and write: contiguous, on the GPU."""
-    for t in tensors:
-        if t is not None and not (t.is_cuda and t.is_contiguous()):
-            raise MGQError(ERR_INVALID_ARG, where)
-
-
+# The calls below check what the C entry points cannot see: place, type, shape
+# and strides of the tensors. One expression a call, since a decode step waits
+# for this code.
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _OUT_DTYPE = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
+
+
+def _ok(t, dtype, shape):
+    return t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _opt(t, dtype, shape):
+    return t is None or _ok(t, dtype, shape)
+
+
+def _require(good, where):
+    if not good:
+        raise MGQError(ERR_INVALID_ARG, where)
 
 
 def _typed(where, t):
@@ -361,11 +371,8 @@ def _typed(where, t):
     return dt
 
 
-def _of(where, dtype, shape, *tensors):
-    """Tensors (or None) of one dtype and shape."""
-    for t in tensors:
-        if t is not None and (t.dtype != dtype or t.shape != shape):
-            raise MGQError(ERR_INVALID_ARG, where)
+def _bytes(t):
+    return t.numel() * t.element_size() if t.is_cuda and t.is_contiguous() else 0
 
 
 def add_rmsnorm_quantize(x, w, eps, q: QDesc | None = None, residual=None, sum_out=None, y=None, rstd=None,
@@ -373,12 +380,12 @@ def add_rmsnorm_quantize(x, w, eps, q: QDesc | None = None, residual=None, sum_o
     """s = x + residual; y = s / rms(s) * w, quantised row-wise into q (x, residual,
     sum_out, y: bf16 [T, H]; w [H] bf16 or float32; rstd float32 [T])."""
     fn = "mgq_add_rmsnorm_quantize"
-    T, H = x.shape
-    _dense(fn, x, w, residual, sum_out, y, rstd)
-    _of(fn, torch.bfloat16, x.shape, x, residual, sum_out, y)
-    _of(fn, torch.float32, (T,), rstd)
-    _of(fn, w.dtype, (H,), w)
-    _check(load().mgq_add_rmsnorm_quantize(_p(x), _p(residual), _p(w), _typed(fn, w), T, H, eps, _p(sum_out), _p(y),
+    shape = x.shape
+    T, H = shape
+    dt = _typed(fn, w)
+    _require(_ok(x, _BF16, shape) and _ok(w, w.dtype, (H,)) and _opt(residual, _BF16, shape) and
+             _opt(sum_out, _BF16, shape) and _opt(y, _BF16, shape) and _opt(rstd, _F32, (T,)), fn)
+    _check(load().mgq_add_rmsnorm_quantize(x.data_ptr(), _p(residual), w.data_ptr(), dt, T, H, eps, _p(sum_out), _p(y),
                                            ctypes.byref(q) if q is not None else None, _p(rstd), _s(stream)), fn)
 
 
@@ -389,15 +396,14 @@ def add_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
 def add_rmsnorm_bwd(dy, s, w, rstd, dx, dw, workspace, dsum=None, beta=0.0, stream=None):
     """Gradients of add_rmsnorm_quantize: dx bf16 [T, H] (+ dsum), dw float32 [H] (beta dw + ...)."""
     fn = "mgq_add_rmsnorm_bwd"
-    T, H = dy.shape
-    _dense(fn, dy, s, w, rstd, dx, dw, workspace, dsum)
-    _of(fn, torch.bfloat16, dy.shape, dy, s, dx, dsum)
-    _of(fn, torch.float32, (T,), rstd)
-    _of(fn, torch.float32, (H,), dw)
-    _of(fn, w.dtype, (H,), w)
-    _check(load().mgq_add_rmsnorm_bwd(_p(dy), _p(s), _p(w), _typed(fn, w), _p(rstd), _p(dsum), T, H, _p(dx), _p(dw),
-                                      beta, _p(workspace), workspace.numel() * workspace.element_size(), _s(stream)),
-           fn)
+    shape = dy.shape
+    T, H = shape
+    dt = _typed(fn, w)
+    _require(_ok(dy, _BF16, shape) and _ok(s, _BF16, shape) and _ok(w, w.dtype, (H,)) and _ok(rstd, _F32, (T,)) and
+             _ok(dx, _BF16, shape) and _ok(dw, _F32, (H,)) and _opt(dsum, _BF16, shape), fn)
+    _check(load().mgq_add_rmsnorm_bwd(dy.data_ptr(), s.data_ptr(), w.data_ptr(), dt, rstd.data_ptr(), _p(dsum), T, H,
+                                      dx.data_ptr(), dw.data_ptr(), beta, workspace.data_ptr(), _bytes(workspace),
+                                      _s(stream)), fn)
 
 
 def router_topk(logits, topk_idx, probs, score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
@@ -405,11 +411,10 @@ def router_topk(logits, topk_idx, probs, score=SCORE_SOFTMAX, renorm=True, scale
     fn = "mgq_router_topk"
     T, E = logits.shape
     k = topk_idx.shape[1]
-    _dense(fn, logits, topk_idx, probs)
-    _of(fn, torch.int32, (T, k), topk_idx)
-    _of(fn, torch.float32, (T, k), probs)
-    _check(load().mgq_router_topk(_p(logits), _typed(fn, logits), T, E, k, score, int(renorm), scale, _p(topk_idx),
-                                  _p(probs), _s(stream)), fn)
+    dt = _typed(fn, logits)
+    _require(_ok(logits, logits.dtype, (T, E)) and _ok(topk_idx, _I32, (T, k)) and _ok(probs, _F32, (T, k)), fn)
+    _check(load().mgq_router_topk(logits.data_ptr(), dt, T, E, k, score, renorm, scale, topk_idx.data_ptr(),
+                                  probs.data_ptr(), _s(stream)), fn)
 
 
 def router_topk_bwd(logits, topk_idx, dprobs, dlogits, score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
@@ -417,12 +422,11 @@ def router_topk_bwd(logits, topk_idx, dprobs, dlogits, score=SCORE_SOFTMAX, reno
     fn = "mgq_router_topk_bwd"
     T, E = logits.shape
     k = topk_idx.shape[1]
-    _dense(fn, logits, topk_idx, dprobs, dlogits)
-    _of(fn, torch.int32, (T, k), topk_idx)
-    _of(fn, torch.float32, (T, k), dprobs)
-    _of(fn, logits.dtype, (T, E), dlogits)
-    _check(load().mgq_router_topk_bwd(_p(logits), _typed(fn, logits), _p(topk_idx), _p(dprobs), T, E, k, score,
-                                      int(renorm), scale, _p(dlogits), _s(stream)), fn)
+    dt = _typed(fn, logits)
+    _require(_ok(logits, logits.dtype, (T, E)) and _ok(topk_idx, _I32, (T, k)) and _ok(dprobs, _F32, (T, k)) and
+             _ok(dlogits, logits.dtype, (T, E)), fn)
+    _check(load().mgq_router_topk_bwd(logits.data_ptr(), dt, topk_idx.data_ptr(), dprobs.data_ptr(), T, E, k, score,
+                                      renorm, scale, dlogits.data_ptr(), _s(stream)), fn)
 
 
 def moe_few_workspace_size(T: int, k: int, E: int, H: int, F: int, scaling: int) -> int:
@@ -433,13 +437,11 @@ def moe_few_forward(x, topk_idx, probs, W1: Operand, W2: Operand, scaling, E, F,
                     h_scale=None, stream=None):
     """The expert layer for a few tokens: x, out bf16 [T, H]; topk_idx int32 and probs float32 [T, k]."""
     fn = "mgq_moe_few_forward"
-    T, H = x.shape
+    shape = x.shape
+    T, H = shape
     k = topk_idx.shape[1]
-    _dense(fn, x, topk_idx, probs, out, workspace, x_scale, h_scale)
-    _of(fn, torch.bfloat16, x.shape, x, out)
-    _of(fn, torch.int32, (T, k), topk_idx)
-    _of(fn, torch.float32, (T, k), probs)
-    _of(fn, torch.float32, (1,), x_scale, h_scale)
-    _check(load().mgq_moe_few_forward(_p(x), T, H, F, _p(topk_idx), _p(probs), k, E, ctypes.byref(W1),
-                                      ctypes.byref(W2), scaling, _p(x_scale), _p(h_scale), _p(out), _p(workspace),
-                                      workspace.numel() * workspace.element_size(), _s(stream)), fn)
+    _require(_ok(x, _BF16, shape) and _ok(out, _BF16, shape) and _ok(topk_idx, _I32, (T, k)) and
+             _ok(probs, _F32, (T, k)) and _opt(x_scale, _F32, (1,)) and _opt(h_scale, _F32, (1,)), fn)
+    _check(load().mgq_moe_few_forward(x.data_ptr(), T, H, F, topk_idx.data_ptr(), probs.data_ptr(), k, E,
+                                      ctypes.byref(W1), ctypes.byref(W2), scaling, _p(x_scale), _p(h_scale),
+                                      out.data_ptr(), workspace.data_ptr(), _bytes(workspace), _s(stream)), fn)

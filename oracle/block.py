@@ -9,6 +9,7 @@ from __future__ import annotations
 import numpy as np
 
 from . import quant as OQ
+from .formats import E4M3, decode, encode, f32
 
 
 # ---- residual addition + RMSNorm ----------------------------------------------
@@ -84,15 +85,26 @@ def router_topk_bwd(logits, idx, dprobs, score="softmax", renorm=True, scale=1.0
 
 # ---- the expert layer for a few tokens -------------------------------------------
 
+def _blockwise_rows(v):
+    """1x128 blocks with s = 448 * (1 / amax), each step rounded to float32."""
+    b = f32(v).astype(np.float64).reshape(v.shape[0], -1, 128)
+    amax = np.abs(b).max(-1, keepdims=True)
+    with np.errstate(divide="ignore", over="ignore", invalid="ignore"):
+        s = f32(448.0 * f32(1.0 / amax).astype(np.float64)).astype(np.float64)
+    s = np.where(amax == 0, 1.0, np.where(np.isinf(s), OQ.FLT_MAX, s))
+    codes = encode(f32(b * s).astype(np.float64), E4M3)
+    return (decode(codes, E4M3) * f32(1.0 / s).astype(np.float64)).reshape(v.shape)
+
+
 def quantize_rows(v, recipe, scale=None):
-    """The values that the recipe's row-wise quantisation of v [R, K] stands for."""
+    """The values that the few-token layer's row-wise quantisation of v [R, K] stands for."""
     v = np.asarray(v, np.float64)
     if v.shape[0] == 0:
         return v
     if recipe == "mxfp8":
         return OQ.dequantize_mx(*OQ.quantize_mx(v, "e4m3"))
     if recipe == "blockwise":
-        return OQ.dequantize_block_1x128(*OQ.quantize_block_1x128(v, "e4m3"))
+        return _blockwise_rows(v)
     if recipe == "nvfp4":
         return OQ.dequantize_nvfp4(*OQ.quantize_nvfp4(v, np.float32(scale)), np.float32(scale), v.shape[1])
     return OQ.dequantize_tensor(OQ.quantize_tensor(v, np.float32(scale))[0], np.float32(scale))

@@ -66,6 +66,26 @@ def test_forward_without_codes(T, H, residual, wdt):
         _near_bf16(bf16_np(o["sum_out"]), s, U * np.abs(s))
 
 
+@pytest.mark.parametrize("T,H,wdt", [(40000, 128, torch.float32), (6001, 1000, torch.bfloat16),
+                                     (2003, 4096, torch.bfloat16), (1300, 5120, torch.float32),
+                                     (700, 16384, torch.bfloat16)])
+@pytest.mark.parametrize("residual", [True, False])
+def test_forward_of_many_rows(T, H, wdt, residual):
+    """Enough rows for the streamed form (two rows a CTA and more)."""
+    test_forward_without_codes(T, H, residual, wdt)
+
+
+@pytest.mark.parametrize("T,H", [(20001, 128), (2003, 4096), (1300, 5120)])
+def test_mx_codes_of_many_rows(T, H):
+    test_mx_codes(T, H, 0, "rceil")
+
+
+@pytest.mark.parametrize("T,H", [(20001, 128), (3001, 1000), (2003, 4096), (1300, 5120), (700, 8200)])
+@pytest.mark.parametrize("dsum", [True, False])
+def test_backward_of_many_rows(T, H, dsum):
+    test_backward(T, H, dsum)
+
+
 @pytest.mark.parametrize("T,H", [(1, 128), (5, 384), (130, 2048), (33, 5120), (256, 4096), (3, 16384)])
 @pytest.mark.parametrize("dt", [0, 1])
 @pytest.mark.parametrize("mode", ["rceil", "floor"])

@@ -82,3 +82,17 @@ def test_few_token_layer_is_the_sum_over_its_experts(recipe):
         # the same float64 sums in another order; a product at a rounding
         # boundary of h may flip one code (1/8 of a value among F)
         assert np.linalg.norm(out[t] - ref) <= 1e-2 * np.linalg.norm(ref)
+
+
+def test_few_token_blockwise_rows():
+    """Exact round trip of blocks whose scale is a power of two; the all-zero
+    block; a value within half an e4m3 step of its block's scale otherwise."""
+    rng = np.random.default_rng(7)
+    v = rng.integers(-15, 16, size=(3, 256)).astype(np.float64)
+    v[:, 0], v[:, 128] = 7 * 64.0, 3.5
+    v[:, 129:] = np.clip(v[:, 129:], -3, 3)
+    assert np.array_equal(OB.quantize_rows(v, "blockwise"), v)
+    assert np.all(OB.quantize_rows(np.zeros((2, 128)), "blockwise") == 0)
+    w = rng.normal(size=(4, 384))
+    amax = np.abs(w).reshape(4, 3, 128).max(-1).repeat(128, 1)
+    assert np.all(np.abs(OB.quantize_rows(w, "blockwise") - w) <= np.maximum(np.abs(w) / 16, amax / 448 * 2.0 ** -10) * 1.001)
