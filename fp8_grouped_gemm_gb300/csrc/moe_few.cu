@@ -22,7 +22,7 @@
 // them to finish: the others leave float32 partial sums, which it adds in the
 // order of the CTAs, so the result does not depend on who came last. Nobody
 // waits for another CTA.
-#include "mgq_internal.h"
+#include "moe_few.h"
 #include "ptx_sm100.cuh"
 #include "rowquant.cuh"
 
@@ -35,8 +35,6 @@ constexpr int kThreads = 192;             // warp 0 TMA, warp 1 MMA, warps 2-5 e
 constexpr uint32_t kATile = 128 * 128;    // bytes of 128 weight rows of one stage
 constexpr int kMaxStages = 6;
 constexpr uint64_t kWaitNs = 2000000000ull;
-
-enum { kMX = 0, kNV = 1, kBLK = 2, kTEN = 3 };
 
 __host__ __device__ constexpr uint32_t sf_chunks(int kind) { return kind == kMX ? 1 : kind == kNV ? 4 : 0; }
 // scale bytes of one stage: two weight halves and the tokens (BLK: 64 float32 of the tokens)
@@ -984,6 +982,7 @@ using namespace mgq;
 extern "C" size_t mgq_moe_few_workspace_size(int T, int k, int E, int64_t H, int64_t F, int scaling) {
   const int kind = kind_of(scaling);
   if (kind < 0 || !few_sizes_ok(T, k, E, H, F, kind)) return 0;
+  if (few_is_small(kind, T, k, E, H, F)) return few_small_workspace(T, k, F, kind);
   return static_cast<size_t>(layout_of(T, k, E, H, F, kind).total);
 }
 
@@ -1012,6 +1011,8 @@ extern "C" int mgq_moe_few_forward(const void* x_bf16, int T, int64_t H, int64_t
   MGQ_CHECK_ARG(ws_bytes >= mgq_moe_few_workspace_size(T, k, E, H, F, scaling));
   cudaStream_t s = as_stream(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (few_is_small(kind, T, k, E, H, F))
+    return few_small_forward(kind, x_bf16, T, H, F, topk_idx, probs, k, E, W1, W2, x_scale, h_scale, out_bf16, ws, s);
   switch (kind) {
     case kMX:
       return few_forward<kMX>(x_bf16, T, H, F, topk_idx, probs, k, E, W1, W2, x_scale, h_scale, out_bf16, ws, s);

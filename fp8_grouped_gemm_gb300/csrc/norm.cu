@@ -49,6 +49,14 @@ __device__ __forceinline__ void load_w8(const void* w, bool wf32, int c, float* 
   }
 }
 
+// max |v| with NaN winning, as float bits
+__device__ __forceinline__ uint32_t absmax8(const float* v) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[j])));
+  return __float_as_uint(m);
+}
+
 // Sum over the CTA; `slot` alternates between two shared arrays from one call
 // to the next, so that one barrier a call is enough.
 __device__ __forceinline__ float block_sum(float v, float (*red)[32], int slot) {
@@ -190,11 +198,19 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
           float u[8];
           unpack8(rr[c], u);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] += u[j];
+          for (int j = 0; j < 8; j += 2) {
+            const f32x2 t = add2(f32x2{v[i][j], v[i][j + 1]}, f32x2{u[j], u[j + 1]});
+            v[i][j] = t.x, v[i][j + 1] = t.y;
+          }
         }
         if (a.sum) *(reinterpret_cast<uint4*>(a.sum + r * a.H) + c) = pack8(v[i]);
+        f32x2 sq{0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+        for (int j = 0; j < 8; j += 2) {
+          const f32x2 t{v[i][j], v[i][j + 1]};
+          sq = fma2(t, t, sq);
+        }
+        ss += sq.x + sq.y;
       }
     }
     ss = block_sum(ss, red, slot);
@@ -217,11 +233,12 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
       float* y = v[i];
       if (in) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float t = __fmul_rn(y[j], rstd);
-          const float e = fmaf(y[j], lo, fmaf(y[j], rstd, -t));
-          const float z = fmaf(t, w[i][j], __fmul_rn(e, w[i][j]));
-          y[j] = isfinite(t) ? z : t * w[i][j];          // (infinity has no remainder)
+        for (int j = 0; j < 8; j += 2) {
+          const f32x2 s2{y[j], y[j + 1]}, w2{w[i][j], w[i][j + 1]}, r2{rstd, rstd}, lo2{lo, lo};
+          const f32x2 t = mul2(s2, r2);
+          const f32x2 e = fma2(s2, lo2, fma2(s2, r2, f32x2{-t.x, -t.y}));
+          const f32x2 z = fma2(t, w2, mul2(e, w2));
+          y[j] = z.x, y[j + 1] = z.y;
         }
         if (a.y) *(reinterpret_cast<uint4*>(a.y + r * a.H) + c) = pack8(y);
       } else {
@@ -229,7 +246,7 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
         for (int j = 0; j < 8; ++j) y[j] = 0.0f;
       }
       if (SC == kNoQuant) continue;
-      uint32_t m = absmax_bits_f32(y, 8);
+      uint32_t m = absmax8(y);
       float mult = ts;
       uint32_t word = 0;
       float sinv = 0.0f;
@@ -307,7 +324,7 @@ int launch_norm_ch(NormArgs a, int threads, cudaStream_t s) {
   int ctas;
   ring_shape(threads, kNormThreads, slot, &ctas, &a.slots);
   const int64_t grid = static_cast<int64_t>(num_sms()) * ctas;
-  if (a.T >= 2 * grid) {
+  if (a.T >= 4 * grid) {
     auto kern = norm_kernel<SC, DT, CH, true>;
     const size_t smem = slot * a.slots;
     if (!allow_smem(kern, smem)) return MGQ_ERR_CUDA;

@@ -182,22 +182,33 @@ __global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
   }
 }
 
+// sum over the eight lanes of a row
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// A warp takes four rows at a time: eight lanes each work out the gradients of
+// their row's selected logits, then all lanes write the four dense rows.
 template <int V, bool BF16, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(256) router_bwd_kernel(RouterArgs a) {
-  // the dense row is put together in shared memory: zeros, the selected
+  // a dense row is put together in shared memory: zeros, the selected
   // experts' gradients by id, then V consecutive values a lane
   __shared__ __align__(16) float rows[8][32 * V];
-  const int lane = threadIdx.x & 31, e0 = lane * V;
+  constexpr bool DENSE = !SIGMOID && !RENORM;      // every expert's score takes part
+  const int lane = threadIdx.x & 31, e0 = lane * V, sub = lane & 7;
   float* row = rows[threadIdx.x >> 5];
 #pragma unroll
   for (int i = 0; i < V; ++i) row[e0 + i] = 0.0f;
   const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t r = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); r < a.T; r += nw) {
+  for (int64_t r4 = 4 * (blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5)); r4 < a.T; r4 += 4 * nw) {
+    const int64_t r = r4 + (lane >> 3);
     int e = -1;
     float d = 0.0f;
-    if (lane < a.k) {
-      e = __ldg(a.sel + r * a.k + lane);
-      d = __ldg(a.dprobs + r * a.k + lane);
+    if (sub < a.k && r < a.T) {
+      e = __ldg(a.sel + r * a.k + sub);
+      d = __ldg(a.dprobs + r * a.k + sub);
       if (e < 0 || e >= a.E) {
         report(a.err, MGQ_ERR_DEVICE_INDEX);
         e = -1;
@@ -205,69 +216,78 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(RouterArgs a) {
     }
     const bool on = e >= 0;
     const float l = on ? load_logit<BF16>(a.logits, r * a.E + e) : -INFINITY;
-    float g = 0.0f;         // lane j: the selected logit's own gradient
-    float back = 0.0f;      // softmax over the row: what every expert's score loses
-    float top = 0.0f, v[V];
+    float g = 0.0f;         // the selected logit's own gradient (DENSE: dprobs times scale, for now)
     if (SIGMOID) {
       const float s = on ? sigmoid_f32(l) : 0.0f;
       if (RENORM) {
-        const float S = warp_sum(s);
+        const float S = sum8(s);
         const float q = S == 0.0f ? 0.0f : s / S;
-        const float c = warp_sum(q > 0.0f ? d * q : 0.0f);
+        const float c = sum8(q > 0.0f ? d * q : 0.0f);
         g = q > 0.0f ? a.scale * (d - c) * q * sigmoid_f32(-l) : 0.0f;
       } else {
         g = s > 0.0f ? a.scale * d * s * sigmoid_f32(-l) : 0.0f;
       }
     } else if (RENORM) {
-      const float m = from_key(__reduce_max_sync(kFull, order_key(l)));
+      float m = l;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
       const float s = on ? softmax_term(l, m) : 0.0f;
-      const float S = warp_sum(s);
+      const float S = sum8(s);
       const float q = S == 0.0f ? 0.0f : s / S;
-      const float c = warp_sum(q > 0.0f ? d * q : 0.0f);
+      const float c = sum8(q > 0.0f ? d * q : 0.0f);
       g = q > 0.0f ? a.scale * q * (d - c) : 0.0f;
     } else {
-      uint32_t km = 0;
-      load_row<V, BF16>(a, r, e0, v);
-#pragma unroll
-      for (int i = 0; i < V; ++i) km = max(km, order_key(v[i]));
-      top = from_key(__reduce_max_sync(kFull, km));
-      float all = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) all += softmax_term(v[i], top);
-      all = warp_sum(all);
-      const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-      const float s = on ? softmax_term(l, top) * inv : 0.0f;
-      back = a.scale * warp_sum(s > 0.0f ? s * d : 0.0f) * inv;
-      g = s > 0.0f ? a.scale * s * d : 0.0f;
+      g = a.scale * d;
     }
-    if (on) atomicAdd(row + e, g);      // (ids of a row are distinct: one addition each)
-    __syncwarp();
-    float o[V];
+    const int nr = static_cast<int>(a.T - r4 < 4 ? a.T - r4 : 4);
+    for (int t = 0; t < nr; ++t) {
+      const int64_t rt = r4 + t;
+      const bool own = on && (lane >> 3) == t;
+      float v[V], top = 0.0f, back = 0.0f, gt = g;
+      if (DENSE) {
+        uint32_t km = 0;
+        load_row<V, BF16>(a, rt, e0, v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      o[i] = row[e0 + i];
-      row[e0 + i] = 0.0f;
-      if (!SIGMOID && !RENORM) o[i] -= softmax_term(v[i], top) * back;
-    }
-    __syncwarp();
-    const int64_t at = r * a.E + e0;
-    if (V >= 4 && a.vec) {
+        for (int i = 0; i < V; ++i) km = max(km, order_key(v[i]));
+        top = from_key(__reduce_max_sync(kFull, km));
+        float all = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        if (e0 + i >= a.E) continue;
-        if (BF16)
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dlogits) + at + i) =
-              make_uint2(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]));
-        else
-          *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + at + i) =
-              make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        for (int i = 0; i < V; ++i) all += softmax_term(v[i], top);
+        all = warp_sum(all);
+        const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+        const float s = own ? softmax_term(l, top) * inv : 0.0f;
+        gt = s > 0.0f ? g * s : 0.0f;
+        back = warp_sum(gt) * inv;
       }
-    } else {
+      if (own) atomicAdd(row + e, gt);    // (ids of a row are distinct: one addition each)
+      __syncwarp();
+      float o[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (e0 + i >= a.E) continue;
-        if (BF16) static_cast<__nv_bfloat16*>(a.dlogits)[at + i] = __float2bfloat16_rn(o[i]);
-        else static_cast<float*>(a.dlogits)[at + i] = o[i];
+        o[i] = row[e0 + i];
+        row[e0 + i] = 0.0f;
+        if (DENSE) o[i] -= softmax_term(v[i], top) * back;
+      }
+      __syncwarp();
+      const int64_t at = rt * a.E + e0;
+      if (V >= 4 && a.vec) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          if (e0 + i >= a.E) continue;
+          if (BF16)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dlogits) + at + i) =
+                make_uint2(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]));
+          else
+            *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + at + i) =
+                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (e0 + i >= a.E) continue;
+          if (BF16) static_cast<__nv_bfloat16*>(a.dlogits)[at + i] = __float2bfloat16_rn(o[i]);
+          else static_cast<float*>(a.dlogits)[at + i] = o[i];
+        }
       }
     }
   }
@@ -293,7 +313,8 @@ void launch_router(RouterArgs a, bool bwd, bool sigmoid, bool renorm, cudaStream
   // vectors of four logits: rows of a multiple of four, aligned bases
   const uintptr_t size = BF16 ? 8 : 16;
   a.vec = a.E % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits)) & (size - 1)) == 0;
-  const int64_t ctas = (a.T + 7) / 8, most = static_cast<int64_t>(num_sms()) * 8;
+  const int64_t per = bwd ? 32 : 8;      // rows of a CTA at a time
+  const int64_t ctas = (a.T + per - 1) / per, most = static_cast<int64_t>(num_sms()) * 8;
   const int grid = static_cast<int>(ctas < most ? ctas : most);
   if (a.E <= 32) launch_mode<1, BF16>(a, bwd, sigmoid, renorm, grid, s);
   else if (a.E <= 64) launch_mode<2, BF16>(a, bwd, sigmoid, renorm, grid, s);

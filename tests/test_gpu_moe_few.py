@@ -102,7 +102,8 @@ def _rows_close(out, x, idx, p, v1, v2, recipe, rows=slice(None)):
     assert np.all(least <= TOL[recipe]), (np.argmax(least), least.max())
 
 
-SHAPES = [(1, 4, 2, 256, 256), (1, 8, 1, 512, 768), (2, 3, 3, 768, 256), (5, 16, 4, 512, 512), (16, 4, 2, 1024, 256),
+SHAPES = [(8, 16, 8, 512, 1024), (8, 1, 1, 256, 512), (9, 16, 8, 512, 1024), (4, 64, 8, 2048, 768), (7, 8, 2, 1280, 256),
+          (1, 4, 2, 256, 256), (1, 8, 1, 512, 768), (2, 3, 3, 768, 256), (5, 16, 4, 512, 512), (16, 4, 2, 1024, 256),
           (17, 8, 2, 256, 1536), (33, 5, 1, 512, 512), (64, 32, 8, 256, 256), (100, 2, 2, 256, 512),
           (128, 7, 3, 512, 256), (128, 64, 8, 256, 256)]
 
@@ -120,7 +121,7 @@ def test_layer(recipe, T, E, k, H, F):
 
 
 @pytest.mark.parametrize("recipe", RECIPES[:3])
-@pytest.mark.parametrize("T,E,k,H,F", [(3, 4, 2, 128, 128), (9, 4, 2, 384, 640), (70, 3, 1, 640, 128)])
+@pytest.mark.parametrize("T,E,k,H,F", [(3, 4, 2, 128, 128), (1, 2, 1, 384, 640), (9, 4, 2, 384, 640), (70, 3, 1, 640, 128)])
 def test_odd_multiples_of_128(recipe, T, E, k, H, F):
     """The last tile of W2 has one half only."""
     test_layer(recipe, T, E, k, H, F)
