@@ -50,11 +50,23 @@ __device__ __forceinline__ void load_w8(const void* w, bool wf32, int c, float* 
 }
 
 // max |v| with NaN winning, as float bits
-__device__ __forceinline__ uint32_t absmax8(const float* v) {
+template <int N>
+__device__ __forceinline__ uint32_t absmax(const float* v) {
   float m = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[j])));
+  for (int j = 0; j < N; ++j) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v[j])));
   return __float_as_uint(m);
+}
+
+// mx_exponent, mx_scale_code and mx_multiplier of an amax in one: a subnormal
+// amax lies below the smallest exponent whatever its bits, and a finite one
+// never reaches the largest.
+__device__ __forceinline__ void mx_scale(uint32_t amax_bits, int emax, int rceil, uint32_t& code, float& mult) {
+  const int up = (rceil && (amax_bits & 0x7FFFFFu) > 0x600000u) ? 1 : 0;
+  const int c = max(0, static_cast<int>(amax_bits >> 23) - emax + up);      // exponent + 127
+  const bool fine = amax_bits < 0x7F800000u;
+  code = fine ? static_cast<uint32_t>(c) : 255u;
+  mult = __uint_as_float(fine ? static_cast<uint32_t>(254 - c) << 23 : 0x7FC00000u);
 }
 
 // Sum over the CTA; `slot` alternates between two shared arrays from one call
@@ -149,82 +161,96 @@ struct NormArgs {
   int rceil;
   float* rstd;           // or null
   int slots;             // streamed: ring slots
+  int wide;              // streamed: 32-byte aligned bf16 outputs
   int* err;
 };
 
-// SC: the mgq_scaling of the codes or kNoQuant; CH: chunks per thread; STREAM:
-// rows through the ring
-template <int SC, int DT, int CH, bool STREAM>
-__global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
+// rstd = 1 / sqrt(ss / H + eps) as a pair rstd + lo, so that y = s (rstd + lo) w
+// is off by little more than its last rounding (y decides the codes): the
+// hardware's reciprocal root r0, good to about 22 bits, and one Newton step
+// r0 (1 - ms r0^2) / 2 whose residual is exact to second order; ms = ss / H with
+// its remainder.
+__device__ __forceinline__ float root_pair(float ss, float h, float inv_h, float eps, float& lo) {
+  const float q0 = ss * inv_h;
+  const float ms = (isfinite(q0) ? fmaf(fmaf(-q0, h, ss), inv_h, q0) : q0) + eps;
+  const float r0 = rsqrtf(ms);
+  const float p = ms * r0;
+  const float step = 0.5f * r0 * (fmaf(-p, r0, 1.0f) - fmaf(ms, r0, -p) * r0);
+  const bool fine = isfinite(step);       // (not for ms = 0 or infinity)
+  const float rstd = fine ? r0 + step : r0;
+  lo = fine ? step - (rstd - r0) : 0.0f;
+  return rstd;
+}
+// y of N elements in place of s
+template <int N>
+__device__ __forceinline__ void scale_row(float* y, const float* w, float rstd, float lo) {
+  const f32x2 r2{rstd, rstd}, lo2{lo, lo};
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    const f32x2 s2{y[j], y[j + 1]}, w2{w[j], w[j + 1]};
+    const f32x2 t = mul2(s2, r2);
+    const f32x2 e = fma2(s2, lo2, fma2(s2, r2, f32x2{-t.x, -t.y}));
+    const f32x2 z = fma2(t, w2, mul2(e, w2));
+    y[j] = z.x, y[j + 1] = z.y;
+  }
+}
+// s = x + residual of N elements, and the sum of its squares
+template <int N>
+__device__ __forceinline__ void add_row(float* v, const float* u) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    const f32x2 t = add2(f32x2{v[j], v[j + 1]}, f32x2{u[j], u[j + 1]});
+    v[j] = t.x, v[j + 1] = t.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ float square_sum(const float* v) {
+  f32x2 sq{0.0f, 0.0f};
+#pragma unroll
+  for (int j = 0; j < N; j += 2) sq = fma2(f32x2{v[j], v[j + 1]}, f32x2{v[j], v[j + 1]}, sq);
+  return sq.x + sq.y;
+}
+
+// the scale bytes of the rows that fill the last 128-row tile are zero
+__device__ __forceinline__ void zero_scale_rows(const NormArgs& a) {
+  const int kb4 = a.H >> 7, rest = static_cast<int>((128 - (a.T & 127)) & 127) * kb4;
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < rest; i += gridDim.x * blockDim.x)
+    *reinterpret_cast<uint32_t*>(a.scales + tiled_scale_offset(a.T + i / kb4, 4 * (i % kb4), kb4)) = 0;
+}
+
+// A CTA per row (few rows). SC: the mgq_scaling of the codes or kNoQuant; CH:
+// 8-element chunks per thread.
+template <int SC, int DT, int CH>
+__global__ void __launch_bounds__(512, CH < 4 ? 2 : 1) norm_kernel(NormArgs a) {
   __shared__ float red[2][32];
-  __shared__ uint64_t bars[kMaxSlots];
-  extern __shared__ __align__(16) uint8_t ring_mem[];
   const int nchunk = a.H >> 3, stride = blockDim.x;
   const uint32_t lane = threadIdx.x & 31;
+  const float h = static_cast<float>(a.H), inv_h = 1.0f / h;
   float ts = 1.0f;
   if (SC == MGQ_TENSOR_F32) ts = __ldg(a.ts);
-  RowRing<2> ring;
-  const uint16_t* const src[2] = {a.x, a.res};
-  if (STREAM) {
-    ring.init(ring_mem, bars, a.slots, a.H * 2u);
-    if (threadIdx.x == 0)
-      for (int i = 0; i < a.slots; ++i) ring.request(src, a.T);
-  }
-  float w[CH][8];
-  if (STREAM) {
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-      if (static_cast<int>(threadIdx.x) + i * stride < nchunk) load_w8(a.w, a.wf32, threadIdx.x + i * stride, w[i]);
-  }
   uint32_t amax = 0;
   int slot = 0;
   for (int64_t r = blockIdx.x; r < a.T; r += gridDim.x, slot ^= 1) {
-    if (STREAM && !ring.wait()) {
-      report(a.err, MGQ_ERR_TIMEOUT);
-      ring.drain();
-      break;
-    }
-    const uint4* xr = STREAM ? ring.row(0) : reinterpret_cast<const uint4*>(a.x + r * a.H);
-    const uint4* rr = STREAM ? ring.row(1) : reinterpret_cast<const uint4*>(a.res + r * a.H);
-    float v[CH][8];
+    float v[CH][8], w[CH][8];
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = threadIdx.x + i * stride;
       if (c < nchunk) {
-        if (!STREAM) load_w8(a.w, a.wf32, c, w[i]);
-        unpack8(xr[c], v[i]);
+        load_w8(a.w, a.wf32, c, w[i]);
+        unpack8(*(reinterpret_cast<const uint4*>(a.x + r * a.H) + c), v[i]);
         if (a.res) {
           float u[8];
-          unpack8(rr[c], u);
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const f32x2 t = add2(f32x2{v[i][j], v[i][j + 1]}, f32x2{u[j], u[j + 1]});
-            v[i][j] = t.x, v[i][j + 1] = t.y;
-          }
+          unpack8(*(reinterpret_cast<const uint4*>(a.res + r * a.H) + c), u);
+          add_row<8>(v[i], u);
         }
         if (a.sum) *(reinterpret_cast<uint4*>(a.sum + r * a.H) + c) = pack8(v[i]);
-        f32x2 sq{0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const f32x2 t{v[i][j], v[i][j + 1]};
-          sq = fma2(t, t, sq);
-        }
-        ss += sq.x + sq.y;
+        ss += square_sum<8>(v[i]);
       }
     }
     ss = block_sum(ss, red, slot);
-    if (STREAM) {
-      ring.advance();                      // every thread has read the slot
-      if (threadIdx.x == 0) ring.request(src, a.T);
-    }
-    // rstd as a pair rstd + lo (lo: one Newton step's correction), so that y
-    // below is off by little more than its last rounding: y decides the codes
-    const float ms = __fadd_rn(__fdiv_rn(ss, static_cast<float>(a.H)), a.eps);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(ms));
-    const float p = __fmul_rn(ms, rstd);
-    float lo = 0.5f * rstd * (fmaf(-p, rstd, 1.0f) - __fmul_rn(fmaf(ms, rstd, -p), rstd));
-    if (!isfinite(lo)) lo = 0.0f;
+    float lo;
+    const float rstd = root_pair(ss, h, inv_h, a.eps, lo);
     if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -232,23 +258,16 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
       const bool in = c < nchunk;
       float* y = v[i];
       if (in) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const f32x2 s2{y[j], y[j + 1]}, w2{w[i][j], w[i][j + 1]}, r2{rstd, rstd}, lo2{lo, lo};
-          const f32x2 t = mul2(s2, r2);
-          const f32x2 e = fma2(s2, lo2, fma2(s2, r2, f32x2{-t.x, -t.y}));
-          const f32x2 z = fma2(t, w2, mul2(e, w2));
-          y[j] = z.x, y[j + 1] = z.y;
-        }
+        scale_row<8>(y, w[i], rstd, lo);
         if (a.y) *(reinterpret_cast<uint4*>(a.y + r * a.H) + c) = pack8(y);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = 0.0f;
       }
       if (SC == kNoQuant) continue;
-      uint32_t m = absmax8(y);
+      uint32_t m = absmax<8>(y);
       float mult = ts;
-      uint32_t word = 0;
+      uint32_t sc = 0;
       float sinv = 0.0f;
       if (SC == MGQ_TENSOR_F32) {
         amax = max(amax, m);
@@ -256,12 +275,7 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
         if (SC == MGQ_MX32_E8M0) {
-          const int e = mx_exponent(m, FmtInfo<DT>::emax, a.rceil != 0);
-          mult = mx_multiplier(e);
-          // the four blocks' scale bytes of these 128 elements, in lane 16 j
-          const uint32_t sc = mx_scale_code(e);
-          word = sc | (__shfl_down_sync(0xFFFFFFFFu, sc, 4) << 8) | (__shfl_down_sync(0xFFFFFFFFu, sc, 8) << 16) |
-                 (__shfl_down_sync(0xFFFFFFFFu, sc, 12) << 24);
+          mx_scale(m, FmtInfo<DT>::emax, a.rceil, sc, mult);
         } else {
           m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
           m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
@@ -274,8 +288,7 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
       cw.x = cvt_fp8x4_mul<DT>(y[0], y[1], y[2], y[3], mult);
       cw.y = cvt_fp8x4_mul<DT>(y[4], y[5], y[6], y[7], mult);
       *(reinterpret_cast<uint2*>(a.codes + r * a.H) + c) = cw;
-      if (SC == MGQ_MX32_E8M0 && (lane & 15) == 0)
-        *reinterpret_cast<uint32_t*>(a.scales + tiled_scale_offset(r, c >> 2, a.H >> 7)) = word;
+      if (SC == MGQ_MX32_E8M0 && (lane & 3) == 0) a.scales[tiled_scale_offset(r, c >> 2, a.H >> 7)] = static_cast<uint8_t>(sc);
       if (SC == MGQ_BLK_1x128_F32 && (lane & 15) == 0)
         reinterpret_cast<float*>(a.scales)[static_cast<int64_t>(c >> 4) * a.T + r] = sinv;
     }
@@ -284,12 +297,141 @@ __global__ void __launch_bounds__(512) norm_kernel(NormArgs a) {
     amax = warp_max_u32(amax);
     if (lane == 0 && amax) atomicMax(reinterpret_cast<unsigned int*>(a.amax), amax);
   }
-  // the scale bytes of the rows that fill the last 128-row tile are zero
-  if (SC == MGQ_MX32_E8M0) {
-    const int kb4 = a.H >> 7, rest = static_cast<int>((128 - (a.T & 127)) & 127) * kb4;
-    for (int i = blockIdx.x * stride + threadIdx.x; i < rest; i += gridDim.x * stride)
-      *reinterpret_cast<uint32_t*>(a.scales + tiled_scale_offset(a.T + i / kb4, 4 * (i % kb4), kb4)) = 0;
+  if (SC == MGQ_MX32_E8M0) zero_scale_rows(a);
+}
+
+// 16 bf16 values of a lane, 32 bytes: one store where the row is 32-byte aligned
+__device__ __forceinline__ void store16(uint16_t* p, const float* v, bool wide) {
+  const uint4 a = pack8(v), b = pack8(v + 8);
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = a;
+    reinterpret_cast<uint4*>(p)[1] = b;
   }
+}
+
+// Many rows (H a multiple of 128). The instructions of a row that do not
+// depend on its length (wait, reduction, root) are paid by every thread, so a
+// thread takes U runs of 16 elements: two lanes hold an MX block, eight a 1x128
+// block.
+template <int SC, int DT, int U>
+__global__ void __launch_bounds__(512) norm_stream_kernel(NormArgs a) {
+  __shared__ __align__(16) float red[2][16];
+  __shared__ uint64_t bars[kMaxSlots];
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  const int nrun = a.H >> 4, stride = blockDim.x, nw = blockDim.x >> 5;
+  const uint32_t lane = threadIdx.x & 31;
+  const float h = static_cast<float>(a.H), inv_h = 1.0f / h;
+  float ts = 1.0f;
+  if (SC == MGQ_TENSOR_F32) ts = __ldg(a.ts);
+  RowRing<2> ring;
+  const uint16_t* const src[2] = {a.x, a.res};
+  ring.init(ring_mem, bars, a.slots, a.H * 2u);
+  if (threadIdx.x == 0)
+    for (int i = 0; i < a.slots; ++i) ring.request(src, a.T);
+  float w[U][16];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int c = threadIdx.x + i * stride;
+    if (c < nrun) {
+      load_w8(a.w, a.wf32, 2 * c, w[i]);
+      load_w8(a.w, a.wf32, 2 * c + 1, w[i] + 8);
+    }
+  }
+  if (threadIdx.x < 32) (&red[0][0])[threadIdx.x] = 0.0f;
+  __syncthreads();
+  uint32_t amax = 0;
+  int slot = 0;
+  for (int64_t r = blockIdx.x; r < a.T; r += gridDim.x, slot ^= 1) {
+    if (!ring.wait()) {
+      report(a.err, MGQ_ERR_TIMEOUT);
+      ring.drain();
+      break;
+    }
+    const uint4 *xr = ring.row(0), *rr = ring.row(1);
+    const int64_t base = r * a.H;
+    float v[U][16];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = threadIdx.x + i * stride;
+      if (c < nrun) {
+        unpack8(xr[2 * c], v[i]);
+        unpack8(xr[2 * c + 1], v[i] + 8);
+        if (a.res) {
+          float u[16];
+          unpack8(rr[2 * c], u);
+          unpack8(rr[2 * c + 1], u + 8);
+          add_row<16>(v[i], u);
+        }
+        ss += square_sum<16>(v[i]);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    if (lane == 0) red[slot][threadIdx.x >> 5] = ss;
+    __syncthreads();
+    ring.advance();                      // every thread has read the slot
+    if (threadIdx.x == 0) ring.request(src, a.T);
+    const float4* part = reinterpret_cast<const float4*>(red[slot]);
+    float4 s4 = part[0];
+    ss = (s4.x + s4.y) + (s4.z + s4.w);
+    for (int i = 1; 4 * i < nw; ++i) {
+      s4 = part[i];
+      ss += (s4.x + s4.y) + (s4.z + s4.w);
+    }
+    float lo;
+    const float rstd = root_pair(ss, h, inv_h, a.eps, lo);
+    if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
+    uint8_t* srow = SC == MGQ_MX32_E8M0 ? a.scales + tiled_scale_offset(r, 0, a.H >> 7) : nullptr;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int c = threadIdx.x + i * stride;
+      const bool in = c < nrun;          // (whole groups of eight lanes: H is a multiple of 128)
+      float* y = v[i];
+      if (in) {
+        if (a.sum) store16(a.sum + base + 16 * c, y, a.wide);
+        scale_row<16>(y, w[i], rstd, lo);
+        if (a.y) store16(a.y + base + 16 * c, y, a.wide);
+      }
+      if (SC == kNoQuant) continue;
+      uint32_t m = in ? absmax<16>(y) : 0u;
+      float mult = ts;
+      uint32_t sc = 0;
+      float sinv = 0.0f;
+      if (SC == MGQ_TENSOR_F32) {
+        amax = max(amax, m);
+      } else {
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        if (SC == MGQ_MX32_E8M0) {
+          mx_scale(m, FmtInfo<DT>::emax, a.rceil, sc, mult);
+        } else {
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+          mult = blk_scale<DT>(m);
+          sinv = __fdiv_rn(1.0f, mult);
+        }
+      }
+      if (!in) continue;
+      uint4 cw;
+      cw.x = cvt_fp8x4_mul<DT>(y[0], y[1], y[2], y[3], mult);
+      cw.y = cvt_fp8x4_mul<DT>(y[4], y[5], y[6], y[7], mult);
+      cw.z = cvt_fp8x4_mul<DT>(y[8], y[9], y[10], y[11], mult);
+      cw.w = cvt_fp8x4_mul<DT>(y[12], y[13], y[14], y[15], mult);
+      *reinterpret_cast<uint4*>(a.codes + base + 16 * c) = cw;
+      if (SC == MGQ_MX32_E8M0 && (lane & 1) == 0) srow[(c >> 3) * 512 + ((c >> 1) & 3)] = static_cast<uint8_t>(sc);
+      if (SC == MGQ_BLK_1x128_F32 && (lane & 7) == 0)
+        reinterpret_cast<float*>(a.scales)[static_cast<int64_t>(c >> 3) * a.T + r] = sinv;
+    }
+  }
+  if (SC == MGQ_TENSOR_F32 && a.amax) {
+    amax = warp_max_u32(amax);
+    if (lane == 0 && amax) atomicMax(reinterpret_cast<unsigned int*>(a.amax), amax);
+  }
+  if (SC == MGQ_MX32_E8M0) zero_scale_rows(a);
 }
 
 // CTA size and chunks per thread for a row of `nchunk` 16-byte chunks.
@@ -298,7 +440,7 @@ void row_shape(int nchunk, int* threads, int* ch) {
   *threads = ((nchunk + *ch - 1) / *ch + 31) / 32 * 32;
 }
 
-constexpr int kNormThreads = 1024, kNormBwdThreads = 512;   // streamed: threads of an SM
+constexpr int kNormThreads = 512, kNormBwdThreads = 512;   // streamed: threads of an SM
 constexpr size_t kRingPerSm = 192 * 1024;    // shared memory for the rings of an SM's CTAs
 
 // CTAs per SM and ring slots of a streamed kernel whose slot takes `slot`
@@ -318,31 +460,38 @@ bool allow_smem(K kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
 }
 
-template <int SC, int DT, int CH>
-int launch_norm_ch(NormArgs a, int threads, cudaStream_t s) {
-  const size_t slot = static_cast<size_t>(a.H) * 4;
-  int ctas;
-  ring_shape(threads, kNormThreads, slot, &ctas, &a.slots);
-  const int64_t grid = static_cast<int64_t>(num_sms()) * ctas;
-  if (a.T >= 4 * grid) {
-    auto kern = norm_kernel<SC, DT, CH, true>;
-    const size_t smem = slot * a.slots;
-    if (!allow_smem(kern, smem)) return MGQ_ERR_CUDA;
-    kern<<<static_cast<int>(grid), threads, smem, s>>>(a);
-  } else {
-    const int64_t most = static_cast<int64_t>(num_sms()) * (2048 / threads);
-    norm_kernel<SC, DT, CH, false><<<static_cast<int>(a.T < most ? a.T : most), threads, 0, s>>>(a);
-  }
+template <int SC, int DT, int U>
+int launch_norm_stream(const NormArgs& a, int threads, int grid, size_t smem, cudaStream_t s) {
+  auto kern = norm_stream_kernel<SC, DT, U>;
+  if (!allow_smem(kern, smem)) return MGQ_ERR_CUDA;
+  kern<<<grid, threads, smem, s>>>(a);
   MGQ_LAUNCH_CHECK();
   return MGQ_OK;
 }
 
 template <int SC, int DT>
-int launch_norm(const NormArgs& a, cudaStream_t s) {
+int launch_norm(NormArgs a, cudaStream_t s) {
+  if (a.H % 128 == 0) {
+    const int u = a.H > 1024 ? 2 : 1, st = ((a.H / 16 + u - 1) / u + 31) / 32 * 32;
+    const size_t slot = static_cast<size_t>(a.H) * 4;
+    int ctas;
+    ring_shape(st, kNormThreads, slot, &ctas, &a.slots);
+    const int64_t grid = static_cast<int64_t>(num_sms()) * ctas;
+    if (a.T >= 4 * grid) {
+      a.wide = ((reinterpret_cast<uintptr_t>(a.sum) | reinterpret_cast<uintptr_t>(a.y)) & 31) == 0;
+      return u == 2 ? launch_norm_stream<SC, DT, 2>(a, st, static_cast<int>(grid), slot * a.slots, s)
+                    : launch_norm_stream<SC, DT, 1>(a, st, static_cast<int>(grid), slot * a.slots, s);
+    }
+  }
   int threads, ch;
   row_shape(a.H >> 3, &threads, &ch);
-  return ch == 1 ? launch_norm_ch<SC, DT, 1>(a, threads, s) : ch == 2 ? launch_norm_ch<SC, DT, 2>(a, threads, s)
-                                                                      : launch_norm_ch<SC, DT, 4>(a, threads, s);
+  const int64_t most = static_cast<int64_t>(num_sms()) * (2048 / threads);
+  const int grid = static_cast<int>(a.T < most ? a.T : most);
+  if (ch == 1) norm_kernel<SC, DT, 1><<<grid, threads, 0, s>>>(a);
+  else if (ch == 2) norm_kernel<SC, DT, 2><<<grid, threads, 0, s>>>(a);
+  else norm_kernel<SC, DT, 4><<<grid, threads, 0, s>>>(a);
+  MGQ_LAUNCH_CHECK();
+  return MGQ_OK;
 }
 
 struct NormBwdArgs {

@@ -97,18 +97,24 @@ __device__ __forceinline__ void load_row(const RouterArgs& a, int64_t r, int e0,
 }
 
 // sorts a lane's keys (largest first, equal keys in their order) with their
-// place 0..V-1: exchanges of neighbours only
+// places, a byte each: exchanges of neighbours only
 template <int V>
-__device__ __forceinline__ void sort_lane(uint32_t* key, int* at) {
+__device__ __forceinline__ void sort_lane(uint32_t* key, uint32_t& at4) {
+  uint32_t at[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) at[i] = i;
 #pragma unroll
   for (int i = 1; i < V; ++i)
 #pragma unroll
     for (int j = V - 1; j >= i; --j) {
       const bool swap = key[j] > key[j - 1];
-      const uint32_t k0 = swap ? key[j] : key[j - 1], k1 = swap ? key[j - 1] : key[j];
-      const int a0 = swap ? at[j] : at[j - 1], a1 = swap ? at[j - 1] : at[j];
-      key[j - 1] = k0, key[j] = k1, at[j - 1] = a0, at[j] = a1;
+      const uint32_t hi = max(key[j], key[j - 1]), lo = min(key[j], key[j - 1]);
+      const uint32_t a0 = swap ? at[j] : at[j - 1], a1 = swap ? at[j - 1] : at[j];
+      key[j - 1] = hi, key[j] = lo, at[j - 1] = a0, at[j] = a1;
     }
+  at4 = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) at4 |= at[i] << (8 * i);
 }
 
 template <int V, bool BF16, bool SIGMOID, bool RENORM>
@@ -119,47 +125,45 @@ __global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
   for (int64_t r = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); r < a.T; r += nw) {
     float v[V];
     uint32_t key[V];
-    int at[V];
     load_row<V, BF16>(a, r, e0, v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      key[i] = e0 + i < a.E ? order_key(v[i]) : 0u;
-      at[i] = i;
-    }
-    uint32_t head = 0;
-    int hi = 0;
+    for (int i = 0; i < V; ++i) key[i] = e0 + i < a.E ? order_key(v[i]) : 0u;
+    uint32_t head = 0, at4 = 0;       // best key left; its place in the low byte
     if (SORTED) {
-      sort_lane<V>(key, at);
-      head = key[0], hi = at[0];
+      sort_lane<V>(key, at4);
+      head = key[0];
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (key[i] > head) head = key[i], hi = i;
+        if (key[i] > head) head = key[i], at4 = i;
     }
     uint32_t k_sel = 0;   // lane j: the j-th selected key and its expert
     int e_sel = 0;
     uint32_t top = 0;
-    for (int j = 0; j < a.k; ++j) {
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j) {
+      if (j >= a.k) break;
       const uint32_t m = __reduce_max_sync(kFull, head);
-      const int w = __ffs(__ballot_sync(kFull, head == m)) - 1;
-      const int e = __shfl_sync(kFull, e0 + hi, w);
+      const uint32_t have = __ballot_sync(kFull, head == m);
+      const int w = __ffs(have) - 1;
+      const int e = __shfl_sync(kFull, e0 + static_cast<int>(at4 & 255u), w);
       if (lane == j) k_sel = m, e_sel = e;
       if (j == 0) top = m;
-      if (lane == w) {    // the owner takes it out
-        if (SORTED) {
+      const bool mine = lane == w;    // the owner takes it out
+      if (SORTED) {
 #pragma unroll
-          for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1], at[i] = at[i + 1];
-          key[V - 1] = 0;
-          head = key[0], hi = at[0];
-        } else {
-          head = 0;
-          const int taken = hi;
-          hi = 0;
+        for (int i = 0; i + 1 < V; ++i) key[i] = mine ? key[i + 1] : key[i];
+        key[V - 1] = mine ? 0u : key[V - 1];
+        at4 = mine ? at4 >> 8 : at4;
+        head = key[0];
+      } else if (mine) {
+        head = 0;
+        const int taken = at4;
+        at4 = 0;
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            if (i == taken) key[i] = 0;
-            if (key[i] > head) head = key[i], hi = i;
-          }
+        for (int i = 0; i < V; ++i) {
+          if (i == taken) key[i] = 0;
+          if (key[i] > head) head = key[i], at4 = i;
         }
       }
     }
