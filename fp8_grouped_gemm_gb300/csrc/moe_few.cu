@@ -1002,7 +1002,9 @@ extern "C" int mgq_moe_few_forward(const void* x_bf16, int T, int64_t H, int64_t
   MGQ_CHECK_ARG(aligned16(x_bf16) && aligned16(out_bf16) && (reinterpret_cast<uintptr_t>(workspace) & 255) == 0);
   for (const mgq_operand* W : {W1, W2}) {
     const int64_t K = W == W1 ? H : F;
-    MGQ_CHECK_ARG(W->data && W->scale && aligned16(W->data) && aligned16(W->scale));
+    MGQ_CHECK_ARG(W->data && W->scale && aligned16(W->data));
+    // (block scale bytes are copied in vectors, float32 scales read one by one)
+    MGQ_CHECK_ARG((reinterpret_cast<uintptr_t>(W->scale) & (kind == kMX || kind == kNV ? 15 : 3)) == 0);
     MGQ_CHECK_ARG(W->ld >= K && W->ld % (kind == kNV ? 256 : 128) == 0);
     if (kind == kNV) MGQ_CHECK_ARG(W->global_scale);
     if (kind == kBLK) MGQ_CHECK_ARG(W->ld == K);          // 128x128 scales are laid out by K

@@ -461,6 +461,39 @@ class ExpertLayer:
             op()
         return self.dx
 
+    def forward_few(self, x, topk_idx, probs, out=None, stream=None):
+        """The layer for a decode batch (x bf16 [T, H], T of 1 to 128, whatever the
+        workload's T) on the weights that quantize_weights() wrote: one call that
+        reads the picked experts' weights once (mgq_moe_few_forward). The
+        per-tensor scales of x and h (delayed) and their NVFP4 global scales are
+        those that the layer holds from its last step. Calls share the layer's
+        buffers: one at a time."""
+        w, (T, H) = self.w, x.shape
+        k = topk_idx.shape[1]
+        if not hasattr(self, "_few"):
+            self._few = self._few_operands(), {}
+        (W1, W2, xs, hs), spaces = self._few
+        ws = spaces.get((T, k))
+        if ws is None:
+            n = mgq.moe_few_workspace_size(T, k, w.E, H, w.F, self.scaling)
+            ws = spaces[T, k] = torch.empty(max(256, n), dtype=torch.uint8, device=self.dev)
+        if out is None:
+            out = torch.empty_like(x)
+        mgq.moe_few_forward(x, topk_idx, probs, W1, W2, self.scaling, w.E, w.F, out, ws, xs, hs, stream)
+        return out
+
+    def _few_operands(self):
+        """(W1, W2, x scale, h scale) of forward_few: the forward's own weight operands."""
+        E, H, F = self.w.E, self.w.H, self.w.F
+        if self.nv:
+            g = self.nv_sg
+            return (mgq.operand(self.w1q, self.w1s, H, mgq.E2M1, g[2:2 + E]),
+                    mgq.operand(self.w2q, self.w2s, F, mgq.E2M1, g[2 + E:2 + 2 * E]), g[0:1], g[1:2])
+        if self.delayed:
+            return (mgq.operand(self.w1q, self._fs(2, E), H, mgq.E4M3),
+                    mgq.operand(self.w2q, self._fs(2 + E, E), F, mgq.E4M3), self._fs(0), self._fs(1))
+        return (mgq.operand(self.w1q, self.w1s, H, mgq.E4M3), mgq.operand(self.w2q, self.w2s, F, mgq.E4M3), None, None)
+
     def update_scaling(self, stream=None):
         """Delayed scaling: push this step's amaxes into the histories and
         derive the scales of the next step (nothing to do for MX scaling)."""

@@ -1,0 +1,100 @@
+"""The MoE half of a decoder layer (block.py) on the GPU: its norm and router
+and their gradients against the float64 definitions on the values that the step
+itself produced, and decode batches on the same weights against the definition."""
+import numpy as np
+import pytest
+import torch
+
+from fp8_grouped_gemm_gb300 import mgq
+from fp8_grouped_gemm_gb300 import workloads as W
+from oracle import block as OB
+from oracle import quant as OQ
+from tests.layer_check import bf16_np, u8_np, ulp_bf16, untile_mx_scales
+from tests.test_gpu_moe_few import _rows_close
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def _block(recipe="mxfp8", T=64, train=True, **kw):
+    from fp8_grouped_gemm_gb300 import block as B
+    w = W.WORKLOADS["tiny"].scaled(T=T, E=8)
+    b = B.MoEBlock(w, "cuda:0", recipe, train=train, **kw)
+    g = torch.Generator().manual_seed(5)
+    w1, w2 = W.make_weights(w)
+    b.load(w1.cuda(), w2.cuda(), (1 + 0.1 * torch.randn(w.H, generator=g)).bfloat16().cuda(),
+           (torch.randn(w.E, w.H, generator=g) * w.H ** -0.5).cuda())
+    x = torch.randn(T, w.H, generator=g).bfloat16().cuda()
+    r = torch.randn(T, w.H, generator=g).bfloat16().cuda()
+    return b, x, r
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+def test_steps_of_forward_and_backward(score, renorm):
+    b, x, r = _block(score=mgq.SCORE_SOFTMAX if score == "softmax" else mgq.SCORE_SIGMOID, renorm=renorm, route_scale=1.5)
+    out, s = b.forward(x, r)
+    rs, rstd, ry = OB.rmsnorm(bf16_np(x), bf16_np(r), bf16_np(b.norm_w), b.eps)
+    assert np.all(np.abs(bf16_np(s) - rs) <= 0.5 * ulp_bf16(rs) * (1 + 1e-9) + U * np.abs(rs))
+    assert np.all(np.abs(bf16_np(b.y) - ry) <= 0.5 * ulp_bf16(ry) * (1 + 1e-9) + 72 * U * np.abs(ry))
+    l = b.logits.double().cpu().numpy()
+    idx, p = OB.router_topk(l, b.w.k, score, renorm, 1.5)
+    assert np.array_equal(b.topk_idx.cpu().numpy(), idx)
+    assert np.all(np.abs(b.probs.cpu().numpy() - p) <= 64 * U * p)
+    g = torch.Generator().manual_seed(6)
+    dout = torch.randn(x.shape, generator=g).bfloat16().cuda()
+    dsum = torch.randn(x.shape, generator=g).bfloat16().cuda()
+    dx = b.backward(dout, dsum)
+    rl, mag = OB.router_topk_bwd(l, idx, b.experts.dprobs.double().cpu().numpy(), score, renorm, 1.5)
+    assert np.all(np.abs(b.dlogits.double().cpu().numpy() - rl) <= 96 * U * mag + 1e-37)
+    # the norm's gradient from the dy that reached it
+    dy = (b.experts.dx.float() + b.dlogits @ b.router_w).bfloat16()
+    rdx, rdw = OB.rmsnorm_bwd(bf16_np(dy), bf16_np(s), bf16_np(b.norm_w), b.rstd.double().cpu().numpy(), bf16_np(dsum))
+    got = bf16_np(dx)
+    # dy's bf16 rounding may fall the other way in an element (addmm against @): 2^-8 of it
+    assert np.linalg.norm(got - rdx) <= 4e-3 * np.linalg.norm(rdx)
+    assert np.linalg.norm(b.dnorm_w.cpu().numpy() - rdw) <= 1e-3 * np.linalg.norm(rdw)
+    assert mgq.get_error() == mgq.OK
+
+
+def _values(codes, scale, recipe, E, N, K, sg=None):
+    """float64 values of the layer's quantised weight [E, N, K]."""
+    c = u8_np(codes)
+    if recipe == "mxfp8":
+        return OQ.dequantize_mx(c.reshape(E * N, K), untile_mx_scales(u8_np(scale), E * N, K)).reshape(E, N, K)
+    if recipe == "nvfp4":
+        s = untile_mx_scales(u8_np(scale), E * N, K, block=16).reshape(E, N, K // 16)
+        return np.stack([OQ.dequantize_nvfp4(c[e], s[e], np.float32(sg[e]), K) for e in range(E)])
+    s = scale.cpu().numpy()
+    if recipe == "blockwise":
+        return np.stack([OQ.dequantize_block_128x128(c[e], s[e]) for e in range(E)])
+    return np.stack([OQ.dequantize_tensor(c[e], s[e]) for e in range(E)])
+
+
+@pytest.mark.parametrize("recipe", ["mxfp8", "blockwise", "nvfp4", "delayed"])
+def test_decode(recipe):
+    """Decode batches on the weights and scales that a many-token step left: the
+    same sums and selections as that step, outputs as the definition has them."""
+    b, x, r = _block(recipe, T=64, train=None)
+    w, ex = b.w, b.experts
+    if recipe == "delayed":                 # a first step sets the scales
+        b.forward(x, r)
+        ex.update_scaling()
+        ex.quantize_weights(*(t.cuda() for t in W.make_weights(w)))
+    _, s = b.forward(x, r)
+    E, H, F = w.E, w.H, w.F
+    sg = ex.nv_sg.cpu().numpy() if recipe == "nvfp4" else None
+    fs = ex.fwd_scale if recipe == "delayed" else None
+    v1 = _values(ex.w1q, fs[2:2 + E] if recipe == "delayed" else ex.w1s, recipe, E, 2 * F, H,
+                 None if sg is None else sg[2:2 + E])
+    v2 = _values(ex.w2q, fs[2 + E:2 + 2 * E] if recipe == "delayed" else ex.w2s, recipe, E, H, F,
+                 None if sg is None else sg[2 + E:2 + 2 * E])
+    xs, hs = (sg[0], sg[1]) if sg is not None else (fs[0].item(), fs[1].item()) if fs is not None else (None, None)
+    at = 0
+    for n in (1, 3, 8, 17, 35):
+        out, s1 = b.decode(x[at:at + n].contiguous(), r[at:at + n].contiguous())
+        assert torch.equal(s1, s[at:at + n])
+        y, idx, probs = b.few
+        assert torch.equal(y, b.y[at:at + n])
+        _rows_close(out, y, idx.cpu().numpy(), probs.cpu().numpy(), v1, v2, recipe, scales=(xs, hs))
+        at += n
+    assert mgq.get_error() == mgq.OK
