@@ -345,30 +345,14 @@ def amax_history_update(history, head, amax, scale, fmax, stream=None):
 
 
 # The calls below check what the C entry points cannot see: place, type, shape
-# and strides of the tensors. One expression a call, since a decode step waits
-# for this code.
+# and strides of the tensors. A decode step waits for this code, so the checks
+# are written out where they are made: a helper's call costs as much as they do.
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _OUT_DTYPE = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
 
 
-def _ok(t, dtype, shape):
-    return t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-
-
-def _opt(t, dtype, shape):
-    return t is None or _ok(t, dtype, shape)
-
-
-def _require(good, where):
-    if not good:
-        raise MGQError(ERR_INVALID_ARG, where)
-
-
-def _typed(where, t):
-    dt = _OUT_DTYPE.get(t.dtype)
-    if dt is None:
-        raise MGQError(ERR_UNSUPPORTED, where)
-    return dt
+def _refuse(where, status=ERR_INVALID_ARG):
+    raise MGQError(status, where)
 
 
 def _bytes(t):
@@ -382,11 +366,21 @@ def add_rmsnorm_quantize(x, w, eps, q: QDesc | None = None, residual=None, sum_o
     fn = "mgq_add_rmsnorm_quantize"
     shape = x.shape
     T, H = shape
-    dt = _typed(fn, w)
-    _require(_ok(x, _BF16, shape) and _ok(w, w.dtype, (H,)) and _opt(residual, _BF16, shape) and
-             _opt(sum_out, _BF16, shape) and _opt(y, _BF16, shape) and _opt(rstd, _F32, (T,)), fn)
-    _check(load().mgq_add_rmsnorm_quantize(x.data_ptr(), _p(residual), w.data_ptr(), dt, T, H, eps, _p(sum_out), _p(y),
-                                           ctypes.byref(q) if q is not None else None, _p(rstd), _s(stream)), fn)
+    dt = _OUT_DTYPE.get(w.dtype)
+    if dt is None:
+        _refuse(fn, ERR_UNSUPPORTED)
+    for t in (x, residual, sum_out, y):
+        if t is not None and not (t.dtype is _BF16 and t.shape == shape and t.is_contiguous() and t.is_cuda):
+            _refuse(fn)
+    if not (w.numel() == H and w.dim() == 1 and w.is_contiguous() and w.is_cuda) or \
+            (rstd is not None and not (rstd.dtype is _F32 and rstd.shape == (T,) and rstd.is_contiguous() and rstd.is_cuda)):
+        _refuse(fn)
+    rc = (_lib or load()).mgq_add_rmsnorm_quantize(
+        x.data_ptr(), None if residual is None else residual.data_ptr(), w.data_ptr(), dt, T, H, eps,
+        None if sum_out is None else sum_out.data_ptr(), None if y is None else y.data_ptr(),
+        None if q is None else ctypes.byref(q), None if rstd is None else rstd.data_ptr(), _s(stream))
+    if rc:
+        raise MGQError(rc, fn)
 
 
 def add_rmsnorm_bwd_workspace_size(T: int, H: int) -> int:
@@ -398,35 +392,59 @@ def add_rmsnorm_bwd(dy, s, w, rstd, dx, dw, workspace, dsum=None, beta=0.0, stre
     fn = "mgq_add_rmsnorm_bwd"
     shape = dy.shape
     T, H = shape
-    dt = _typed(fn, w)
-    _require(_ok(dy, _BF16, shape) and _ok(s, _BF16, shape) and _ok(w, w.dtype, (H,)) and _ok(rstd, _F32, (T,)) and
-             _ok(dx, _BF16, shape) and _ok(dw, _F32, (H,)) and _opt(dsum, _BF16, shape), fn)
-    _check(load().mgq_add_rmsnorm_bwd(dy.data_ptr(), s.data_ptr(), w.data_ptr(), dt, rstd.data_ptr(), _p(dsum), T, H,
-                                      dx.data_ptr(), dw.data_ptr(), beta, workspace.data_ptr(), _bytes(workspace),
-                                      _s(stream)), fn)
+    dt = _OUT_DTYPE.get(w.dtype)
+    if dt is None:
+        _refuse(fn, ERR_UNSUPPORTED)
+    for t in (dy, s, dx, dsum):
+        if t is not None and not (t.dtype is _BF16 and t.shape == shape and t.is_contiguous() and t.is_cuda):
+            _refuse(fn)
+    if not (w.numel() == H and w.dim() == 1 and w.is_contiguous() and w.is_cuda and
+            rstd.dtype is _F32 and rstd.shape == (T,) and rstd.is_contiguous() and rstd.is_cuda and
+            dw.dtype is _F32 and dw.shape == (H,) and dw.is_contiguous() and dw.is_cuda):
+        _refuse(fn)
+    rc = (_lib or load()).mgq_add_rmsnorm_bwd(
+        dy.data_ptr(), s.data_ptr(), w.data_ptr(), dt, rstd.data_ptr(), None if dsum is None else dsum.data_ptr(), T, H,
+        dx.data_ptr(), dw.data_ptr(), beta, workspace.data_ptr(), _bytes(workspace), _s(stream))
+    if rc:
+        raise MGQError(rc, fn)
 
 
 def router_topk(logits, topk_idx, probs, score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
     """logits [T, E] (bf16 or float32) -> topk_idx int32 [T, k], probs float32 [T, k]."""
     fn = "mgq_router_topk"
     T, E = logits.shape
-    k = topk_idx.shape[1]
-    dt = _typed(fn, logits)
-    _require(_ok(logits, logits.dtype, (T, E)) and _ok(topk_idx, _I32, (T, k)) and _ok(probs, _F32, (T, k)), fn)
-    _check(load().mgq_router_topk(logits.data_ptr(), dt, T, E, k, score, renorm, scale, topk_idx.data_ptr(),
-                                  probs.data_ptr(), _s(stream)), fn)
+    sel = topk_idx.shape
+    dt = _OUT_DTYPE.get(logits.dtype)
+    if dt is None:
+        _refuse(fn, ERR_UNSUPPORTED)
+    if not (logits.is_contiguous() and logits.is_cuda and
+            topk_idx.dtype is _I32 and sel[0] == T and topk_idx.is_contiguous() and topk_idx.is_cuda and
+            probs.dtype is _F32 and probs.shape == sel and probs.is_contiguous() and probs.is_cuda):
+        _refuse(fn)
+    rc = (_lib or load()).mgq_router_topk(logits.data_ptr(), dt, T, E, sel[1], score, renorm, scale, topk_idx.data_ptr(),
+                                          probs.data_ptr(), _s(stream))
+    if rc:
+        raise MGQError(rc, fn)
 
 
 def router_topk_bwd(logits, topk_idx, dprobs, dlogits, score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
     """The gradient of router_topk's probs with respect to the logits, dense [T, E]."""
     fn = "mgq_router_topk_bwd"
     T, E = logits.shape
-    k = topk_idx.shape[1]
-    dt = _typed(fn, logits)
-    _require(_ok(logits, logits.dtype, (T, E)) and _ok(topk_idx, _I32, (T, k)) and _ok(dprobs, _F32, (T, k)) and
-             _ok(dlogits, logits.dtype, (T, E)), fn)
-    _check(load().mgq_router_topk_bwd(logits.data_ptr(), dt, topk_idx.data_ptr(), dprobs.data_ptr(), T, E, k, score,
-                                      renorm, scale, dlogits.data_ptr(), _s(stream)), fn)
+    sel = topk_idx.shape
+    dt = _OUT_DTYPE.get(logits.dtype)
+    if dt is None:
+        _refuse(fn, ERR_UNSUPPORTED)
+    if not (logits.is_contiguous() and logits.is_cuda and
+            topk_idx.dtype is _I32 and sel[0] == T and topk_idx.is_contiguous() and topk_idx.is_cuda and
+            dprobs.dtype is _F32 and dprobs.shape == sel and dprobs.is_contiguous() and dprobs.is_cuda and
+            dlogits.dtype is logits.dtype and dlogits.shape == logits.shape and dlogits.is_contiguous() and
+            dlogits.is_cuda):
+        _refuse(fn)
+    rc = (_lib or load()).mgq_router_topk_bwd(logits.data_ptr(), dt, topk_idx.data_ptr(), dprobs.data_ptr(), T, E, sel[1],
+                                              score, renorm, scale, dlogits.data_ptr(), _s(stream))
+    if rc:
+        raise MGQError(rc, fn)
 
 
 def moe_few_workspace_size(T: int, k: int, E: int, H: int, F: int, scaling: int) -> int:
@@ -437,11 +455,19 @@ def moe_few_forward(x, topk_idx, probs, W1: Operand, W2: Operand, scaling, E, F,
                     h_scale=None, stream=None):
     """The expert layer for a few tokens: x, out bf16 [T, H]; topk_idx int32 and probs float32 [T, k]."""
     fn = "mgq_moe_few_forward"
-    shape = x.shape
+    shape, sel = x.shape, topk_idx.shape
     T, H = shape
-    k = topk_idx.shape[1]
-    _require(_ok(x, _BF16, shape) and _ok(out, _BF16, shape) and _ok(topk_idx, _I32, (T, k)) and
-             _ok(probs, _F32, (T, k)) and _opt(x_scale, _F32, (1,)) and _opt(h_scale, _F32, (1,)), fn)
-    _check(load().mgq_moe_few_forward(x.data_ptr(), T, H, F, topk_idx.data_ptr(), probs.data_ptr(), k, E,
-                                      ctypes.byref(W1), ctypes.byref(W2), scaling, _p(x_scale), _p(h_scale),
-                                      out.data_ptr(), workspace.data_ptr(), _bytes(workspace), _s(stream)), fn)
+    if not (x.dtype is _BF16 and x.is_contiguous() and x.is_cuda and
+            out.dtype is _BF16 and out.shape == shape and out.is_contiguous() and out.is_cuda and
+            topk_idx.dtype is _I32 and sel[0] == T and topk_idx.is_contiguous() and topk_idx.is_cuda and
+            probs.dtype is _F32 and probs.shape == sel and probs.is_contiguous() and probs.is_cuda):
+        _refuse(fn)
+    for t in (x_scale, h_scale):
+        if t is not None and not (t.dtype is _F32 and t.numel() == 1 and t.is_cuda):
+            _refuse(fn)
+    rc = (_lib or load()).mgq_moe_few_forward(
+        x.data_ptr(), T, H, F, topk_idx.data_ptr(), probs.data_ptr(), sel[1], E, ctypes.byref(W1), ctypes.byref(W2), scaling,
+        None if x_scale is None else x_scale.data_ptr(), None if h_scale is None else h_scale.data_ptr(), out.data_ptr(),
+        workspace.data_ptr(), _bytes(workspace), _s(stream))
+    if rc:
+        raise MGQError(rc, fn)
