@@ -52,6 +52,17 @@ __device__ __forceinline__ bool elect_one() {
 }
 // the four epilogue warps
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// the same barrier, true if `ok` is true in all four warps (a wait that ran out
+// in one of them must not leave the others at a barrier that it never reaches)
+__device__ __forceinline__ bool epi_all(bool ok) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\t"
+               "selp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"(static_cast<uint32_t>(ok))
+               : "memory");
+  return r != 0;
+}
 
 __device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
   uint32_t r;
@@ -259,6 +270,12 @@ struct Walk {
     block();
   }
 };
+// What the stores of a tile need to know of it, and who shares it.
+struct Tile {
+  int m, row0, n, slot;
+  int ca, cb;             // its first and last CTA
+};
+
 // The line's U units over G CTAs: the first U % G of them take one more.
 struct Split {
   int U, G, base, more;
@@ -293,80 +310,90 @@ __device__ __forceinline__ void join4(const float* part, int64_t place, int ca, 
   }
 }
 
-// h = silu(g) u of 16 tokens (nj of them real) and one ffn row per thread,
-// quantised along the rows: lane = row within a 32-row block, so an MX block
-// is one warp, an NVFP4 block half of one, a 1x128 block the four warps.
+// h = silu(g) u of four tokens (nj of them real, from column c0 on) and one ffn
+// row per thread, quantised along the rows: lane = row within a 32-row block, so
+// an MX block is one warp, an NVFP4 block half of one, a 1x128 block the four
+// warps. Called in a loop over the tile's tokens: the code of all of them
+// unrolled did not fit the instruction cache, and its first fetch took up to
+// 9 us behind the weights' copies.
 template <int KIND>
-__device__ __forceinline__ void store_h(const FewArgs& p, const Walk& s, int c16, float (&g)[16], const float (&u)[16],
-                                        float alpha, int row, float sh, uint32_t (*smax)[4][16],
-                                        uint32_t& tick) {
-  const int nj = min(16, s.n - 16 * c16);
+__device__ __forceinline__ void store_h(const FewArgs& p, const Tile& s, int c0, int nj, float (&g)[4], const float (&u)[4],
+                                        float alpha, int row, float sh, uint32_t (*smax)[4][16], uint32_t& tick) {
   const uint32_t lane = threadIdx.x & 31, wq = row >> 5;
   const int64_t f0 = static_cast<int64_t>(s.m) * 128;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) g[j] = swiglu_f32(g[j] * alpha, u[j] * alpha);
+  for (int j = 0; j < 4; ++j) g[j] = swiglu_f32(g[j] * alpha, u[j] * alpha);
   if (KIND == kBLK) {
     uint32_t mine = 0;     // lane j keeps token j's maximum over this warp's rows
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (j >= nj) break;
+    for (int j = 0; j < 4; ++j) {
       const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(g[j]) & 0x7FFFFFFFu);
       if (lane == j) mine = m;
     }
     // (two buffers in turn: a warp writes one again only after the barrier
     // that every warp reaches when it has read it)
     ++tick;
-    if (lane < 16) smax[tick & 1][wq][lane] = mine;
+    if (lane < 4) smax[tick & 1][wq][lane] = mine;
     epi_sync();
   }
+  // the four tokens side by side, whether real or not, then the stores
+  uint32_t code[4], scale[4];
+  float inv[4];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (j >= nj) break;
-    const int col = 16 * c16 + j;
-    const int64_t r = s.row0 + col;
-    const uint32_t in_chunk = (col & 31) * 16 + (col >> 5) * 4;
+  for (int j = 0; j < 4; ++j) {
+    uint32_t m = __float_as_uint(g[j]) & 0x7FFFFFFFu;
+    scale[j] = 0;
+    inv[j] = 0.0f;
     if (KIND == kMX) {
-      const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(g[j]) & 0x7FFFFFFFu);
-      const int e = mx_exponent(m, 8, true);
-      p.hq[r * p.F + f0 + row] = static_cast<uint8_t>(cvt_e4m3x2(__fmul_rn(g[j], mx_multiplier(e)), 0.0f));
-      if (lane == 0)
-        p.hs[(static_cast<int64_t>(s.slot) * (p.F / 128) + s.m) * 512 + in_chunk + wq] =
-            static_cast<uint8_t>(mx_scale_code(e));
+      const int e = mx_exponent(__reduce_max_sync(0xFFFFFFFFu, m), 8, true);
+      code[j] = cvt_e4m3x2(__fmul_rn(g[j], mx_multiplier(e)), 0.0f);
+      scale[j] = mx_scale_code(e);
     } else if (KIND == kNV) {
-      uint32_t m = __float_as_uint(g[j]) & 0x7FFFFFFFu;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      const uint32_t code = cvt_ue4m3(__fmul_rn(__fdiv_rn(__uint_as_float(m), 6.0f), sh));
-      const float sc = ue4m3_value(code);
+      scale[j] = cvt_ue4m3(__fmul_rn(__fdiv_rn(__uint_as_float(m), 6.0f), sh));
+      const float sc = ue4m3_value(scale[j]);
       const float v = __fmul_rn(g[j], sc == 0.0f ? 0.0f : __fdiv_rn(sh, sc));
-      const float w = __shfl_down_sync(0xFFFFFFFFu, v, 1);
-      if ((lane & 1) == 0) p.hq[(r * p.F + f0 + row) / 2] = static_cast<uint8_t>(cvt_e2m1x2(v, w));
-      if ((lane & 15) == 0)
-        p.hs[(static_cast<int64_t>(s.slot) * (p.F / 64) + 2 * s.m + (row >> 6)) * 512 + in_chunk + ((row >> 4) & 3)] =
-            static_cast<uint8_t>(code);
+      code[j] = cvt_e2m1x2(v, __shfl_down_sync(0xFFFFFFFFu, v, 1));
     } else if (KIND == kBLK) {
-      uint32_t m = 0;
+      m = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) m = max(m, smax[tick & 1][q][j]);
       const float mult = blk_scale_few(m);
-      p.hq[r * p.F + f0 + row] = static_cast<uint8_t>(cvt_e4m3x2(__fmul_rn(g[j], mult), 0.0f));
-      if (row == 0)
-        reinterpret_cast<float*>(p.hs)[(static_cast<int64_t>(s.slot) * (p.F / 128) + s.m) * kTok + col] =
-            __fdiv_rn(1.0f, mult);
+      inv[j] = __fdiv_rn(1.0f, mult);
+      code[j] = cvt_e4m3x2(__fmul_rn(g[j], mult), 0.0f);
     } else {
-      p.hq[r * p.F + f0 + row] = static_cast<uint8_t>(cvt_e4m3x2(__fmul_rn(g[j], sh), 0.0f));
+      code[j] = cvt_e4m3x2(__fmul_rn(g[j], sh), 0.0f);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j >= nj) break;
+    const int col = c0 + j;
+    const int64_t r = s.row0 + col;
+    const uint32_t in_chunk = (col & 31) * 16 + (col >> 5) * 4;
+    if (KIND == kNV) {
+      if ((lane & 1) == 0) p.hq[(r * p.F + f0 + row) / 2] = static_cast<uint8_t>(code[j]);
+      if ((lane & 15) == 0)
+        p.hs[(static_cast<int64_t>(s.slot) * (p.F / 64) + 2 * s.m + (row >> 6)) * 512 + in_chunk + ((row >> 4) & 3)] =
+            static_cast<uint8_t>(scale[j]);
+    } else {
+      p.hq[r * p.F + f0 + row] = static_cast<uint8_t>(code[j]);
+      if (KIND == kMX && lane == 0)
+        p.hs[(static_cast<int64_t>(s.slot) * (p.F / 128) + s.m) * 512 + in_chunk + wq] = static_cast<uint8_t>(scale[j]);
+      if (KIND == kBLK && row == 0)
+        reinterpret_cast<float*>(p.hs)[(static_cast<int64_t>(s.slot) * (p.F / 128) + s.m) * kTok + col] = inv[j];
     }
   }
 }
 
-__device__ __forceinline__ void store_y(const FewArgs& p, const Walk& s, int c16, const float (&a)[16],
-                                        const float (&b)[16], float alpha, int row) {
-  const int nj = min(16, s.n - 16 * c16);
+__device__ __forceinline__ void store_y(const FewArgs& p, const Tile& s, int c0, int nj, const float (&a)[4],
+                                        const float (&b)[4], float alpha, int row) {
   const int64_t m0 = static_cast<int64_t>(s.m) * 256 + row;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < 4; ++j) {
     if (j >= nj) break;
-    float* d = p.y + static_cast<int64_t>(s.row0 + 16 * c16 + j) * p.H + m0;
+    float* d = p.y + static_cast<int64_t>(s.row0 + c0 + j) * p.H + m0;
     d[0] = a[j] * alpha;
     if (m0 + 128 < p.H) d[128] = b[j] * alpha;
   }
@@ -391,13 +418,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(t_empty + 2);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_last = reinterpret_cast<volatile int*>(s_tmem + 2);
-  int* s_at = reinterpret_cast<int*>(s_tmem + 4);      // [8] start of the walk, blocks, rows of the largest group
+  int* s_at = reinterpret_cast<int*>(s_tmem + 6);      // [7] start of the walk, units, rows of the largest group
   uint32_t (*smax)[4][16] = reinterpret_cast<uint32_t (*)[4][16]>(bars + 24);   // [2][4][16]
   int4* s_list = reinterpret_cast<int4*>(bars + 24 + 64);
   int* s_cnt = reinterpret_cast<int*>(s_list + p.list);
 
   const int warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
   grid_launch();
   if (threadIdx.x == 32) {
     for (int s = 0; s < kMost; ++s) {
@@ -450,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int row = sum & 2047, blk = (sum >> 11) & 2047, at = sum >> 22;
     // this CTA's first unit and the expert it falls in
     const int U = static_cast<int>((all >> 11) & 2047) * p.mt * p.kb;
-    const int G = max(1, min(static_cast<int>(gridDim.x), U));
-    const int u0 = min(static_cast<int>(blockIdx.x), G) * (U / G) + min(static_cast<int>(blockIdx.x), U % G);
+    const int G = max(1, min(ctas, U));
+    const int u0 = min(cta, G) * (U / G) + min(cta, U % G);
     const int tile = u0 / p.kb;
     for (int e = lo; e < hi; ++e) {
       const int n = s_cnt[e];
@@ -478,10 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *s_tmem;
   Split sp;
   sp.U = s_at[5];
-  sp.G = max(1, min(static_cast<int>(gridDim.x), sp.U));
+  sp.G = max(1, min(ctas, sp.U));
   sp.base = sp.U / sp.G;
   sp.more = sp.U - sp.base * sp.G;
-  const int units = static_cast<int>(blockIdx.x) < sp.G ? sp.base + (static_cast<int>(blockIdx.x) < sp.more ? 1 : 0) : 0;
+  const int units = cta < sp.G ? sp.base + (cta < sp.more ? 1 : 0) : 0;
   // as many stages as the largest token block of the call leaves room for
   const uint32_t bt = static_cast<uint32_t>((min(s_at[6], kTok) + 15) / 16) * 2048;
   const int STG = min(kMost, static_cast<int>(p.stage_mem / (2 * kATile + bt + SF)));
@@ -620,21 +648,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sh = PHASE == 1 && (KIND == kNV || KIND == kTEN) ? __ldg(p.h_scale) : 1.0f;
     int st = 0;
     uint32_t ph = 0, tc = 0, tick = 0;
+    bool alive = true;
     for (; s.any(); s.next()) {
       const int n16 = (s.n + 15) / 16;
       const bool whole = s.kb1 - s.kb0 == p.kb;
       float alpha = 1.0f;
       if (KIND == kNV || KIND == kTEN) alpha = 1.0f / (sx * __ldg(p.sw + s.e));
-      // the tile's first and last CTA, and this CTA's place for partial sums
-      int ca = 0, cb = 0;
-      float* mine = nullptr;
+      Tile t{s.m, s.row0, s.n, s.slot, 0, 0};
+      // this CTA's place for partial sums: the second for its last tile (and,
+      // before that, 1x128 whole ones), the first for one begun by another CTA
+      float* mine = p.part + (2 * cta + 1) * place;
       if (!whole) {
         const int first = s.tile * p.kb;
-        ca = sp.owner(first);
-        cb = sp.owner(first + p.kb - 1);
-        mine = p.part + (2 * blockIdx.x + (ca == static_cast<int>(blockIdx.x) ? 1 : 0)) * place;
+        t.ca = sp.owner(first);
+        t.cb = sp.owner(first + p.kb - 1);
+        if (t.ca != cta) mine -= place;
       }
-      bool alive = true;
       if (KIND == kBLK) {
         // every stage's product is scaled and added in float32 registers
         float acc[2][kTok / 16][16];
@@ -646,10 +675,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 16; ++j) acc[h][c][j] = 0.0f;
         const int64_t wr = (s.e * p.rows_e + static_cast<int64_t>(s.m) * p.mstep) / 128;
         const bool two = PHASE == 1 || s.m * 256 + 128 < p.rows_end;
+        float w0v = 0.0f, w1v = 0.0f;
         for (int kb = s.kb0; kb < s.kb1; ++kb, ++tc) {
           const uint32_t a = tc & 1;
-          const float w0 = __ldg(p.sw + wr * p.kblk + kb);
-          const float w1 = two ? __ldg(p.sw + (wr + p.half2 / 128) * p.kblk + kb) : 0.0f;
+          if (((kb - s.kb0) & 31) == 0) {      // the weight scales of the next 32 stages, one a lane
+            const int k = min(kb + static_cast<int>(lane), s.kb1 - 1);
+            w0v = __ldg(p.sw + wr * p.kblk + k);
+            w1v = two ? __ldg(p.sw + (wr + p.half2 / 128) * p.kblk + k) : 0.0f;
+          }
+          const float w0 = __shfl_sync(0xFFFFFFFFu, w0v, (kb - s.kb0) & 31);
+          const float w1 = __shfl_sync(0xFFFFFFFFu, w1v, (kb - s.kb0) & 31);
           alive = __all_sync(0xFFFFFFFFu, !*s_abort && ptx::mbar_wait(&full[st], ph, kWaitNs) &&
                                               ptx::mbar_wait(&t_full[a], (tc >> 1) & 1, kWaitNs));
           if (!alive) break;
@@ -680,57 +715,69 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) ptx::mbar_arrive(&empty[st]);
           if (++st == STG) st = 0, ph ^= 1;
         }
+        // the sums go to this CTA's place even for a whole tile, whose threads
+        // read back what they wrote: registers cannot be walked in a loop
+        alive = epi_all(alive);            // (store_h has barriers of its own)
         if (alive) {
 #pragma unroll
           for (int c = 0; c < kTok / 16; ++c) {
             if (c >= n16) break;
-            if (!whole) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if (16 * c + j >= s.n) break;
-                mine[(16 * c + j) * 256 + row] = acc[0][c][j];
-                mine[(16 * c + j) * 256 + 128 + row] = acc[1][c][j];
+            for (int j = 0; j < 16; ++j) {
+              if (16 * c + j >= s.n) break;
+              mine[(16 * c + j) * 256 + row] = acc[0][c][j];
+              mine[(16 * c + j) * 256 + 128 + row] = acc[1][c][j];
+            }
+          }
+          if (whole) {
+#pragma unroll 1
+            for (int c = 0; c < s.n; c += 4) {
+              const int nj = min(4, s.n - c);
+              float g[4], h[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                g[j] = j < nj ? mine[(c + j) * 256 + row] : 0.0f;
+                h[j] = j < nj ? mine[(c + j) * 256 + 128 + row] : 0.0f;
               }
-            } else if (PHASE == 1) {
-              store_h<KIND>(p, s, c, acc[0][c], acc[1][c], alpha, row, sh, smax, tick);
-            } else {
-              store_y(p, s, c, acc[0][c], acc[1][c], alpha, row);
+              if (PHASE == 1) store_h<KIND>(p, t, c, nj, g, h, alpha, row, sh, smax, tick);
+              else store_y(p, t, c, nj, g, h, alpha, row);
             }
           }
         }
       } else {
         const uint32_t a = tc & 1;
-        alive = __all_sync(0xFFFFFFFFu, !*s_abort && ptx::mbar_wait(&t_full[a], (tc >> 1) & 1, kWaitNs));
+        alive = epi_all(!*s_abort && ptx::mbar_wait(&t_full[a], (tc >> 1) & 1, kWaitNs));
         ++tc;
         if (alive) {
           ptx::tc_fence_after();
-          for (int c = 0; c < n16; ++c) {
-            uint32_t v0[16], v1[16];
-            ptx::tmem_ld_32x32b_x16(tmem + tlane + a * 2 * kTok + 16 * c, v0);
-            ptx::tmem_ld_32x32b_x16(tmem + tlane + a * 2 * kTok + kTok + 16 * c, v1);
-            ptx::tmem_ld_wait_regs(v0);
-            ptx::tmem_ld_wait_regs(v1);
-            float g[16], h[16];
+#pragma unroll 1
+          for (int c = 0; c < s.n; c += 4) {
+            const int nj = min(4, s.n - c);
+            uint32_t v0[4], v1[4];
+            ptx::tmem_ld_32x32b_x4(tmem + tlane + a * 2 * kTok + c, v0);
+            ptx::tmem_ld_32x32b_x4(tmem + tlane + a * 2 * kTok + kTok + c, v1);
+            ptx::tmem_ld_wait_regs2(v0, v1);
+            float g[4], h[4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) g[j] = __uint_as_float(v0[j]), h[j] = __uint_as_float(v1[j]);
+            for (int j = 0; j < 4; ++j) g[j] = __uint_as_float(v0[j]), h[j] = __uint_as_float(v1[j]);
             if (!whole) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if (16 * c + j >= s.n) break;
-                mine[(16 * c + j) * 256 + row] = g[j];
-                mine[(16 * c + j) * 256 + 128 + row] = h[j];
+              for (int j = 0; j < 4; ++j) {
+                if (j >= nj) break;
+                mine[(c + j) * 256 + row] = g[j];
+                mine[(c + j) * 256 + 128 + row] = h[j];
               }
             } else if (PHASE == 1) {
-              store_h<KIND>(p, s, c, g, h, alpha, row, sh, smax, tick);
+              store_h<KIND>(p, t, c, nj, g, h, alpha, row, sh, smax, tick);
             } else {
-              store_y(p, s, c, g, h, alpha, row);
+              store_y(p, t, c, nj, g, h, alpha, row);
             }
           }
           ptx::tc_fence_before();
           ptx::mbar_arrive(&t_empty[a]);
         }
       }
-      if (!alive) {
+      if (!alive) {                        // (in all four warps)
         report(p.err, MGQ_ERR_TIMEOUT);
         *s_abort = 1;
         break;
@@ -741,22 +788,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         epi_sync();
         if (threadIdx.x == 64) {
           __threadfence();
-          *s_last = atomicAdd(p.cnt + ca, 1) == cb - ca;
+          *s_last = atomicAdd(p.cnt + t.ca, 1) == t.cb - t.ca;
           __threadfence();
         }
         epi_sync();
         if (*s_last) {
-          for (int c = 0; c < n16; ++c) {
-            float g[16], h[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) g[j] = h[j] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (16 * c + 4 * j < s.n)
-                join4(p.part + (16 * c + 4 * j) * 256 + row, place, ca, cb, s.n - 16 * c - 4 * j, g + 4 * j, h + 4 * j);
-            }
-            if (PHASE == 1) store_h<KIND>(p, s, c, g, h, alpha, row, sh, smax, tick);
-            else store_y(p, s, c, g, h, alpha, row);
+#pragma unroll 1
+          for (int c = 0; c < t.n; c += 4) {
+            const int nj = min(4, t.n - c);
+            float g[4], h[4];
+            join4(p.part + c * 256 + row, place, t.ca, t.cb, nj, g, h);
+            if (PHASE == 1) store_h<KIND>(p, t, c, nj, g, h, alpha, row, sh, smax, tick);
+            else store_y(p, t, c, nj, g, h, alpha, row);
           }
         }
       }
