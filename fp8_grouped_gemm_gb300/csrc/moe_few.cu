@@ -276,10 +276,29 @@ struct Tile {
   int ca, cb;             // its first and last CTA
 };
 
-// The line's U units over G CTAs: the first U % G of them take one more.
+// The line's U units over G CTAs in grains of one unit, or of a whole tile
+// where that makes no stretch more than kWholeSlack units longer than an equal
+// share: whole tiles need no partial sums, whose fence (it waits behind the
+// weights' copies: 13 to 17 us in mid-walk, 2 at its end), counter and join cost
+// more than those units. Slack 0 / 6 / 12 measured 71.8 / 70.0 / 68.9 us on 64
+// tokens of the fine-grained NVFP4 layer and 281 / 280 / 277 us on 33 of the
+// Scout-shaped blockwise one. `more` CTAs have one grain more than the others.
+constexpr int kWholeSlack = 12;
 struct Split {
-  int U, G, base, more;
-  __device__ __forceinline__ int owner(int u) const {     // the CTA that has unit u
+  int U, G, grain, base, more;
+  __device__ __forceinline__ Split(int U_, int kb, int ctas) : U(U_) {
+    const int tiles = U / kb, gt = max(1, min(ctas, tiles)), gu = max(1, min(ctas, U));
+    const int longest = (tiles + gt - 1) / gt * kb, share = (U + gu - 1) / gu;
+    const bool whole = longest <= share + kWholeSlack;
+    G = whole ? gt : gu;
+    grain = whole ? kb : 1;
+    const int n = U / grain;
+    base = n / G;
+    more = n - base * G;
+  }
+  __device__ __forceinline__ int first(int c) const { return grain * (min(c, G) * base + min(c, more)); }
+  __device__ __forceinline__ int units(int c) const { return c < G ? grain * (base + (c < more ? 1 : 0)) : 0; }
+  __device__ __forceinline__ int owner(int u) const {     // the CTA that has unit u (grains of one)
     const int edge = more * (base + 1);
     return u < edge ? u / (base + 1) : more + (u - edge) / base;
   }
@@ -478,8 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int row = sum & 2047, blk = (sum >> 11) & 2047, at = sum >> 22;
     // this CTA's first unit and the expert it falls in
     const int U = static_cast<int>((all >> 11) & 2047) * p.mt * p.kb;
-    const int G = max(1, min(ctas, U));
-    const int u0 = min(cta, G) * (U / G) + min(cta, U % G);
+    const int u0 = Split(U, p.kb, ctas).first(cta);
     const int tile = u0 / p.kb;
     for (int e = lo; e < hi; ++e) {
       const int n = s_cnt[e];
@@ -504,12 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  Split sp;
-  sp.U = s_at[5];
-  sp.G = max(1, min(ctas, sp.U));
-  sp.base = sp.U / sp.G;
-  sp.more = sp.U - sp.base * sp.G;
-  const int units = cta < sp.G ? sp.base + (cta < sp.more ? 1 : 0) : 0;
+  const Split sp(s_at[5], p.kb, ctas);
+  const int units = sp.units(cta);
   // as many stages as the largest token block of the call leaves room for
   const uint32_t bt = static_cast<uint32_t>((min(s_at[6], kTok) + 15) / 16) * 2048;
   const int STG = min(kMost, static_cast<int>(p.stage_mem / (2 * kATile + bt + SF)));
@@ -820,16 +834,22 @@ __global__ void __launch_bounds__(128) few_combine_kernel(const float* y, const 
   grid_wait();
   const int t = blockIdx.y, c = (blockIdx.x * 128 + threadIdx.x) * 4;
   if (c >= H) return;
+  // all rows requested before the first is used; added in the order of j
+  float4 v[kMaxK];
+  float pr[kMaxK];
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    const int r = j < k ? row_of[t * k + j] : -1;
+    pr[j] = r >= 0 ? __ldg(probs + t * k + j) : 0.0f;
+    v[j] = r >= 0 ? *reinterpret_cast<const float4*>(y + static_cast<int64_t>(r) * H + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int j = 0; j < k; ++j) {
-    const int r = row_of[t * k + j];
-    if (r < 0) continue;
-    const float pr = __ldg(probs + t * k + j);
-    const float4 v = *reinterpret_cast<const float4*>(y + static_cast<int64_t>(r) * H + c);
-    o.x = fmaf(pr, v.x, o.x);
-    o.y = fmaf(pr, v.y, o.y);
-    o.z = fmaf(pr, v.z, o.z);
-    o.w = fmaf(pr, v.w, o.w);
+#pragma unroll
+  for (int j = 0; j < kMaxK; ++j) {
+    o.x = fmaf(pr[j], v[j].x, o.x);
+    o.y = fmaf(pr[j], v[j].y, o.y);
+    o.z = fmaf(pr[j], v[j].z, o.z);
+    o.w = fmaf(pr[j], v[j].w, o.w);
   }
   *reinterpret_cast<uint2*>(out + static_cast<int64_t>(t) * H + c) =
       make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
