@@ -70,6 +70,29 @@ int col_gather_dy(const uint16_t* dout, const float* probs, const int32_t* src_r
 int quant_nv2d(const uint16_t* x, int64_t G, int64_t M, int64_t K, uint8_t* row_codes, uint8_t* row_scales,
                uint8_t* col_codes, uint8_t* col_scales, const float* amax, float* s_out, cudaStream_t s);
 
+// A launch that may start while the kernel before it in the stream still runs
+// (programmatic dependent launch): such a kernel reads what others wrote, and
+// writes, only after griddepcontrol.wait. `cluster`: CTAs along x, 1 for none.
+template <typename... P, typename... A>
+bool launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return true;
+  (void)cudaGetLastError();
+  return false;
+}
+
 }  // namespace mgq
 
 #define MGQ_CHECK_ARG(cond)                 \

@@ -40,8 +40,8 @@ __host__ __device__ constexpr uint32_t sf_chunks(int kind) { return kind == kMX 
 // scale bytes of one stage: two weight halves and the tokens (BLK: 64 float32 of the tokens)
 __host__ __device__ constexpr uint32_t sf_bytes(int kind) { return kind == kBLK ? 256u : 3 * 512 * sf_chunks(kind); }
 
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+using ptx::grid_launch;
+using ptx::grid_wait;
 // true in one lane of the (converged) warp. Unlike a test of the lane index it
 // tells the compiler that one thread is left, so that the operands of TMA and
 // MMA instructions are kept in uniform registers.
@@ -104,6 +104,8 @@ struct PrepArgs {
 
 template <int KIND>
 __global__ void __launch_bounds__(128) few_prep_kernel(PrepArgs a) {
+  // (the next launch reads the ids before it waits for this one: they must be there)
+  grid_wait();
   grid_launch();
   const uint32_t lane = threadIdx.x & 31;
   if (blockIdx.x == 0)
@@ -202,6 +204,7 @@ struct FewArgs {
   int list;              // experts that can be active at once
   uint32_t stage_mem;    // shared memory for the stages
   uint32_t idesc0;       // instruction descriptor without N
+  uint64_t inv_ctas;     // ceil(2^40 / grid)
   // phase 1
   uint8_t* hq;
   uint8_t* hs;
@@ -285,15 +288,20 @@ struct Tile {
 // Scout-shaped blockwise one. `more` CTAs have one grain more than the others.
 constexpr int kWholeSlack = 12;
 struct Split {
-  int U, G, grain, base, more;
-  __device__ __forceinline__ Split(int U_, int kb, int ctas) : U(U_) {
-    const int tiles = U / kb, gt = max(1, min(ctas, tiles)), gu = max(1, min(ctas, U));
-    const int longest = (tiles + gt - 1) / gt * kb, share = (U + gu - 1) / gu;
+  int G, grain, base, more;
+  // n / ctas of a launch: the host's ceil(2^40 / ctas), exact for n below 2^28
+  static __device__ __forceinline__ int over(int n, int ctas, uint64_t inv) {
+    return static_cast<int>(static_cast<uint64_t>(n) * inv >> 40);
+  }
+  __device__ __forceinline__ void make(int tiles, int kb, int ctas, uint64_t inv) {
+    const int U = tiles * kb;
+    const int longest = tiles <= ctas ? kb : over(tiles + ctas - 1, ctas, inv) * kb;
+    const int share = U <= ctas ? 1 : over(U + ctas - 1, ctas, inv);
     const bool whole = longest <= share + kWholeSlack;
-    G = whole ? gt : gu;
     grain = whole ? kb : 1;
-    const int n = U / grain;
-    base = n / G;
+    const int n = whole ? tiles : U;
+    G = max(1, min(ctas, n));
+    base = n <= ctas ? min(n, 1) : over(n, ctas, inv);
     more = n - base * G;
   }
   __device__ __forceinline__ int first(int c) const { return grain * (min(c, G) * base + min(c, more)); }
@@ -437,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(t_empty + 2);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_last = reinterpret_cast<volatile int*>(s_tmem + 2);
-  int* s_at = reinterpret_cast<int*>(s_tmem + 6);      // [7] start of the walk, units, rows of the largest group
+  int* s_at = reinterpret_cast<int*>(s_tmem + 4);      // [6] start of the walk, rows of the largest group
+  Split* s_split = reinterpret_cast<Split*>(s_tmem + 10);
   uint32_t (*smax)[4][16] = reinterpret_cast<uint32_t (*)[4][16]>(bars + 24);   // [2][4][16]
   int4* s_list = reinterpret_cast<int4*>(bars + 24 + 64);
   int* s_cnt = reinterpret_cast<int*>(s_list + p.list);
@@ -496,9 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     sum -= mine;
     int row = sum & 2047, blk = (sum >> 11) & 2047, at = sum >> 22;
     // this CTA's first unit and the expert it falls in
-    const int U = static_cast<int>((all >> 11) & 2047) * p.mt * p.kb;
-    const int u0 = Split(U, p.kb, ctas).first(cta);
-    const int tile = u0 / p.kb;
+    Split sp;
+    sp.make(static_cast<int>((all >> 11) & 2047) * p.mt, p.kb, ctas, p.inv_ctas);
+    const int u0 = sp.first(cta);
+    const int tile = sp.grain == 1 ? u0 / p.kb : min(cta, sp.G) * sp.base + min(cta, sp.more);
     for (int e = lo; e < hi; ++e) {
       const int n = s_cnt[e];
       if (n == 0) continue;
@@ -507,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int local = tile - blk * p.mt;
       if (local >= 0 && local < nb * p.mt) {
         s_at[0] = at;
-        s_at[1] = local / nb;
-        s_at[2] = local % nb;
+        s_at[1] = nb == 1 ? local : local / nb;
+        s_at[2] = nb == 1 ? 0 : local % nb;
         s_at[3] = u0 - tile * p.kb;
         s_at[4] = tile;
       }
@@ -516,16 +526,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       blk += nb;
       ++at;
     }
-    if (lane == 0) s_at[5] = U, s_at[6] = static_cast<int>(most);
+    if (lane == 0) {
+      s_at[5] = static_cast<int>(most);
+      *s_split = sp;
+    }
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const Split sp(s_at[5], p.kb, ctas);
+  const Split sp = *s_split;
   const int units = sp.units(cta);
   // as many stages as the largest token block of the call leaves room for
-  const uint32_t bt = static_cast<uint32_t>((min(s_at[6], kTok) + 15) / 16) * 2048;
+  const uint32_t bt = static_cast<uint32_t>((min(s_at[5], kTok) + 15) / 16) * 2048;
   const int STG = min(kMost, static_cast<int>(p.stage_mem / (2 * kATile + bt + SF)));
   uint8_t* sA = smem;
   uint8_t* sB = sA + STG * 2 * kATile;
@@ -831,6 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // out[t] = sum_j probs[t, j] y[row(t, j)] in float32, j ascending, rounded once
 __global__ void __launch_bounds__(128) few_combine_kernel(const float* y, const int32_t* row_of, const float* probs, int T,
                                                           int k, int H, uint16_t* out) {
+  grid_launch();
   grid_wait();
   const int t = blockIdx.y, c = (blockIdx.x * 128 + threadIdx.x) * 4;
   if (c >= H) return;
@@ -907,22 +921,6 @@ Layout layout_of(int T, int k, int E, int64_t H, int64_t F, int kind) {
   return l;
 }
 
-// a launch that may start while the one before it in the stream still runs
-template <typename... P, typename... A>
-bool launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
-}
-
 constexpr size_t kSmemMax = 227 * 1024;
 
 template <int KIND, int PHASE>
@@ -940,11 +938,7 @@ int launch_gemm(const CUtensorMap& tw, const CUtensorMap& tx, FewArgs p, int gri
   // list of active experts, the counts
   const size_t small = 24 * 8 + 128 * 4 + static_cast<size_t>(p.list) * 16 + static_cast<size_t>(p.E) * 4;
   p.stage_mem = static_cast<uint32_t>((kSmemMax - 1024 - small) / 1024 * 1024);
-  if (!launch_after(kern, dim3(grid), kThreads, 1024 + p.stage_mem + small, s, tw, tx, p)) {
-    (void)cudaGetLastError();
-    return MGQ_ERR_CUDA;
-  }
-  return MGQ_OK;
+  return launch_after(kern, dim3(grid), kThreads, 1024 + p.stage_mem + small, 1, s, tw, tx, p) ? MGQ_OK : MGQ_ERR_CUDA;
 }
 
 template <int KIND>
@@ -977,8 +971,7 @@ int few_forward(const void* x, int T, int64_t H, int64_t F, const int32_t* idx, 
   pa.ncnt = 2 * l.grid;
   pa.err = err;
   const int warps = R * static_cast<int>((H + 1023) / 1024);
-  few_prep_kernel<KIND><<<(warps + 3) / 4, 128, 0, s>>>(pa);
-  MGQ_LAUNCH_CHECK();
+  if (!launch_after(few_prep_kernel<KIND>, dim3((warps + 3) / 4), 128, 0, 1, s, pa)) return MGQ_ERR_CUDA;
 
   FewArgs a{};
   a.idx = idx;
@@ -987,6 +980,7 @@ int few_forward(const void* x, int T, int64_t H, int64_t F, const int32_t* idx, 
   a.part = reinterpret_cast<float*>(ws + l.part);
   a.nmax = l.nmax;
   a.list = E < R ? E : R;
+  a.inv_ctas = ((uint64_t(1) << 40) + l.grid - 1) / l.grid;
   a.err = err;
   a.hq = ws + l.hq;
   a.hs = ws + l.hs;
@@ -1028,13 +1022,11 @@ int few_forward(const void* x, int T, int64_t H, int64_t F, const int32_t* idx, 
   weight(W2);
   rc = launch_gemm<KIND, 2>(tw2, th, a, l.grid, s);
   if (rc != MGQ_OK) return rc;
-  if (!launch_after(few_combine_kernel, dim3((H + 511) / 512, T), 128, 0, s, static_cast<const float*>(a.y),
-                    static_cast<const int32_t*>(pa.row_of), probs, T, k, static_cast<int>(H),
-                    static_cast<uint16_t*>(out))) {
-    (void)cudaGetLastError();
-    return MGQ_ERR_CUDA;
-  }
-  return MGQ_OK;
+  return launch_after(few_combine_kernel, dim3((H + 511) / 512, T), 128, 0, 1, s, static_cast<const float*>(a.y),
+                      static_cast<const int32_t*>(pa.row_of), probs, T, k, static_cast<int>(H),
+                      static_cast<uint16_t*>(out))
+             ? MGQ_OK
+             : MGQ_ERR_CUDA;
 }
 
 }  // namespace

@@ -31,8 +31,8 @@ namespace {
 
 constexpr int kSmallThreads = 256, kWarps = 8;
 
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+using ptx::grid_launch;
+using ptx::grid_wait;
 
 // weights are read once: past L1
 __device__ __forceinline__ uint4 ldw16(const uint8_t* p) {
@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_gateup_kernel(SmallArg
   __shared__ __align__(16) uint8_t xsm[kWarps][8 * XUnit<KIND>::kRow];
   __shared__ float xsc[kWarps][KIND == kMX ? 32 : 8];
   __shared__ uint32_t cmax[8];
+  grid_wait();
   grid_launch();
   const int R = a.T * a.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   load_routing(rt, a.idx, R, a.E);
@@ -621,37 +622,13 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
 
 // ---- host side --------------------------------------------------------------------
 
-template <typename K>
-bool launch(K kern, dim3 grid, bool after, int cluster, cudaStream_t s, const SmallArgs& a) {
-  cudaLaunchAttribute at[2];
-  int n = 0;
-  if (after) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    at[n].id = cudaLaunchAttributeClusterDimension;
-    at[n].val.clusterDim.x = cluster;
-    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
-    ++n;
-  }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kSmallThreads);
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = n;
-  if (cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess) return true;
-  (void)cudaGetLastError();
-  return false;
-}
-
 template <int KIND>
 int run_small(const SmallArgs& a, cudaStream_t s) {
   const int R = a.T * a.k;
-  if (!launch(small_gateup_kernel<KIND>, dim3(a.F / ffn_rows(KIND), R < a.E ? R : a.E), false, KIND == kBLK ? 4 : 1, s, a))
+  if (!launch_after(small_gateup_kernel<KIND>, dim3(a.F / ffn_rows(KIND), R < a.E ? R : a.E), kSmallThreads, 0,
+                    KIND == kBLK ? 4 : 1, s, a))
     return MGQ_ERR_CUDA;
-  if (!launch(small_down_kernel<KIND>, dim3(a.H / 16), true, 1, s, a)) return MGQ_ERR_CUDA;
+  if (!launch_after(small_down_kernel<KIND>, dim3(a.H / 16), kSmallThreads, 0, 1, s, a)) return MGQ_ERR_CUDA;
   return MGQ_OK;
 }
 

@@ -223,6 +223,8 @@ __device__ __forceinline__ void zero_scale_rows(const NormArgs& a) {
 template <int SC, int DT, int CH>
 __global__ void __launch_bounds__(512, CH < 4 ? 2 : 1) norm_kernel(NormArgs a) {
   __shared__ float red[2][32];
+  ptx::grid_wait();
+  ptx::grid_launch();
   const int nchunk = a.H >> 3, stride = blockDim.x;
   const uint32_t lane = threadIdx.x & 31;
   const float h = static_cast<float>(a.H), inv_h = 1.0f / h;
@@ -487,11 +489,8 @@ int launch_norm(NormArgs a, cudaStream_t s) {
   row_shape(a.H >> 3, &threads, &ch);
   const int64_t most = static_cast<int64_t>(num_sms()) * (2048 / threads);
   const int grid = static_cast<int>(a.T < most ? a.T : most);
-  if (ch == 1) norm_kernel<SC, DT, 1><<<grid, threads, 0, s>>>(a);
-  else if (ch == 2) norm_kernel<SC, DT, 2><<<grid, threads, 0, s>>>(a);
-  else norm_kernel<SC, DT, 4><<<grid, threads, 0, s>>>(a);
-  MGQ_LAUNCH_CHECK();
-  return MGQ_OK;
+  auto kern = ch == 1 ? norm_kernel<SC, DT, 1> : ch == 2 ? norm_kernel<SC, DT, 2> : norm_kernel<SC, DT, 4>;
+  return launch_after(kern, dim3(grid), threads, 0, 1, s, a) ? MGQ_OK : MGQ_ERR_CUDA;
 }
 
 struct NormBwdArgs {
@@ -514,7 +513,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormBwdArgs a) {
   __shared__ float red[2][32];
   __shared__ uint64_t bars[kMaxSlots];
   extern __shared__ __align__(16) uint8_t ring_mem[];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  ptx::grid_launch();
   const int nchunk = a.H >> 3, stride = blockDim.x;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   RowRing<3> ring;
@@ -599,7 +598,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormBwdArgs a) {
 // Launched while the kernel above drains.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int n, int H, float beta, float* dw) {
   __shared__ float sh[32][33];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  ptx::grid_wait();
   const int l = threadIdx.x & 31, c = blockIdx.x * 32 + l, w = threadIdx.x >> 5;
   float t = 0.0f;
   if (c < H) {
@@ -750,18 +749,8 @@ extern "C" int mgq_add_rmsnorm_bwd(const void* dy_bf16, const void* s_bf16, cons
                                                                           : launch_bwd<4>(a, threads, grid, s);
     if (rc != MGQ_OK) return rc;
   }
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = T > 0 ? 1 : 0;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((a.H + 31) / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, norm_dw_kernel, static_cast<const float*>(a.part), grid, a.H, beta, dw) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return MGQ_ERR_CUDA;
-  }
-  return MGQ_OK;
+  return launch_after(norm_dw_kernel, dim3((a.H + 31) / 32), 1024, 0, 1, s, static_cast<const float*>(a.part), grid, a.H,
+                      beta, dw)
+             ? MGQ_OK
+             : MGQ_ERR_CUDA;
 }

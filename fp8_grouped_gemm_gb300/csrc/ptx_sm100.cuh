@@ -19,6 +19,11 @@ __device__ __forceinline__ uint32_t lane_id() {
   return r;
 }
 
+// programmatic dependent launch: wait until the kernels before this one in the
+// stream have finished and their writes are visible; let the next one start
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));

@@ -17,6 +17,7 @@
 // between the load of the logits and the store of the k results.
 #include "mgq_internal.h"
 #include "device_common.cuh"
+#include "ptx_sm100.cuh"
 
 namespace mgq {
 namespace {
@@ -119,6 +120,8 @@ __device__ __forceinline__ void sort_lane(uint32_t* key, uint32_t& at4) {
 
 template <int V, bool BF16, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
+  ptx::grid_wait();
+  ptx::grid_launch();
   constexpr bool SORTED = V <= 4;     // longer runs: find the next best when the head is taken
   const int lane = threadIdx.x & 31, e0 = lane * V;
   const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
@@ -197,6 +200,8 @@ __device__ __forceinline__ float sum8(float v) {
 // their row's selected logits, then all lanes write the four dense rows.
 template <int V, bool BF16, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(256) router_bwd_kernel(RouterArgs a) {
+  ptx::grid_wait();
+  ptx::grid_launch();
   // a dense row is put together in shared memory: zeros, the selected
   // experts' gradients by id, then V consecutive values a lane
   __shared__ __align__(16) float rows[8][32 * V];
@@ -298,34 +303,28 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(RouterArgs a) {
 }
 
 template <int V, bool BF16>
-void launch_mode(const RouterArgs& a, bool bwd, bool sigmoid, bool renorm, int grid, cudaStream_t s) {
-  if (bwd) {
-    if (sigmoid && renorm) router_bwd_kernel<V, BF16, true, true><<<grid, 256, 0, s>>>(a);
-    else if (sigmoid) router_bwd_kernel<V, BF16, true, false><<<grid, 256, 0, s>>>(a);
-    else if (renorm) router_bwd_kernel<V, BF16, false, true><<<grid, 256, 0, s>>>(a);
-    else router_bwd_kernel<V, BF16, false, false><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (sigmoid && renorm) router_topk_kernel<V, BF16, true, true><<<grid, 256, 0, s>>>(a);
-    else if (sigmoid) router_topk_kernel<V, BF16, true, false><<<grid, 256, 0, s>>>(a);
-    else if (renorm) router_topk_kernel<V, BF16, false, true><<<grid, 256, 0, s>>>(a);
-    else router_topk_kernel<V, BF16, false, false><<<grid, 256, 0, s>>>(a);
-  }
+bool launch_mode(const RouterArgs& a, bool bwd, bool sigmoid, bool renorm, int grid, cudaStream_t s) {
+  void (*kern)(RouterArgs);
+  if (bwd)
+    kern = sigmoid ? (renorm ? router_bwd_kernel<V, BF16, true, true> : router_bwd_kernel<V, BF16, true, false>)
+                   : (renorm ? router_bwd_kernel<V, BF16, false, true> : router_bwd_kernel<V, BF16, false, false>);
+  else
+    kern = sigmoid ? (renorm ? router_topk_kernel<V, BF16, true, true> : router_topk_kernel<V, BF16, true, false>)
+                   : (renorm ? router_topk_kernel<V, BF16, false, true> : router_topk_kernel<V, BF16, false, false>);
+  return launch_after(kern, dim3(grid), 256, 0, 1, s, a);
 }
 
 template <bool BF16>
-void launch_router(RouterArgs a, bool bwd, bool sigmoid, bool renorm, cudaStream_t s) {
+int launch_router(RouterArgs a, bool bwd, bool sigmoid, bool renorm, cudaStream_t s) {
   // vectors of four logits: rows of a multiple of four, aligned bases
   const uintptr_t size = BF16 ? 8 : 16;
   a.vec = a.E % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits)) & (size - 1)) == 0;
   const int64_t per = bwd ? 32 : 8;      // rows of a CTA at a time
   const int64_t ctas = (a.T + per - 1) / per, most = static_cast<int64_t>(num_sms()) * 8;
   const int grid = static_cast<int>(ctas < most ? ctas : most);
-  if (a.E <= 32) launch_mode<1, BF16>(a, bwd, sigmoid, renorm, grid, s);
-  else if (a.E <= 64) launch_mode<2, BF16>(a, bwd, sigmoid, renorm, grid, s);
-  else if (a.E <= 128) launch_mode<4, BF16>(a, bwd, sigmoid, renorm, grid, s);
-  else if (a.E <= 256) launch_mode<8, BF16>(a, bwd, sigmoid, renorm, grid, s);
-  else if (a.E <= 512) launch_mode<16, BF16>(a, bwd, sigmoid, renorm, grid, s);
-  else launch_mode<32, BF16>(a, bwd, sigmoid, renorm, grid, s);
+  auto go = a.E <= 32 ? launch_mode<1, BF16> : a.E <= 64 ? launch_mode<2, BF16> : a.E <= 128 ? launch_mode<4, BF16> :
+            a.E <= 256 ? launch_mode<8, BF16> : a.E <= 512 ? launch_mode<16, BF16> : launch_mode<32, BF16>;
+  return go(a, bwd, sigmoid, renorm, grid, s) ? MGQ_OK : MGQ_ERR_CUDA;
 }
 
 int check_router(const void* logits, int dtype, int64_t T, int E, int k, int score, int renorm) {
@@ -358,12 +357,9 @@ extern "C" int mgq_router_topk(const void* logits, int dtype, int64_t T, int E, 
   a.scale = scale;
   a.idx = topk_idx;
   a.probs = probs;
-  if (dtype == MGQ_OUT_BF16)
-    launch_router<true>(a, false, score == MGQ_SCORE_SIGMOID, renorm != 0, as_stream(stream));
-  else
-    launch_router<false>(a, false, score == MGQ_SCORE_SIGMOID, renorm != 0, as_stream(stream));
-  MGQ_LAUNCH_CHECK();
-  return MGQ_OK;
+  const bool sig = score == MGQ_SCORE_SIGMOID;
+  return dtype == MGQ_OUT_BF16 ? launch_router<true>(a, false, sig, renorm != 0, as_stream(stream))
+                               : launch_router<false>(a, false, sig, renorm != 0, as_stream(stream));
 }
 
 extern "C" int mgq_router_topk_bwd(const void* logits, int dtype, const int32_t* topk_idx, const float* dprobs,
@@ -384,10 +380,7 @@ extern "C" int mgq_router_topk_bwd(const void* logits, int dtype, const int32_t*
   a.dprobs = dprobs;
   a.dlogits = dlogits;
   a.err = error_word();
-  if (dtype == MGQ_OUT_BF16)
-    launch_router<true>(a, true, score == MGQ_SCORE_SIGMOID, renorm != 0, as_stream(stream));
-  else
-    launch_router<false>(a, true, score == MGQ_SCORE_SIGMOID, renorm != 0, as_stream(stream));
-  MGQ_LAUNCH_CHECK();
-  return MGQ_OK;
+  const bool sig = score == MGQ_SCORE_SIGMOID;
+  return dtype == MGQ_OUT_BF16 ? launch_router<true>(a, true, sig, renorm != 0, as_stream(stream))
+                               : launch_router<false>(a, true, sig, renorm != 0, as_stream(stream));
 }
