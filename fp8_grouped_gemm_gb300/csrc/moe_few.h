@@ -15,20 +15,34 @@ int few_small_forward(int kind, const void* x, int T, int64_t H, int64_t F, cons
                       int E, const mgq_operand* W1, const mgq_operand* W2, const float* x_scale, const float* h_scale,
                       void* out, uint8_t* ws, cudaStream_t s);
 
-
-// Whether a call takes that form: few tokens, and weights of the experts they
-// can pick so small that its two launches beat the line's four. The line
-// streams at the memory's rate but starts and joins for about 14 us; the small
-// form needs 6 us and reads at about 2.5 TB/s (its conversions bound it: MX
-// scales every 32 elements, NVFP4 converts to f16). Measured, small / line:
-//   per tensor  38 MB 13.3 / 19.4 us,  75 MB 23.3 / 27.4,  100 MB 33.1 / 27.5
-//   1x128       38 MB 15.0 / 21.2 us,  75 MB 27.2 / 28.9,  151 MB 45.5 / 42.2
-//   MXFP8       26 MB 15.5 / 18.7 us,  39 MB 18.5 / 19.5,   52 MB 25.7 / 23.6
-//   NVFP4       14 MB 12.7 / 16.5 us,  21 MB 13.5 / 19.1,   28 MB 23.9 / 18.9
+// Whether a call takes that form. Its two launches start in less time than the
+// line's four, but a warp of it works through its stretch of H one 128-element
+// unit after another, so its time grows with H and, past one wave of its
+// first launch, with the ffn rows of the experts that the call can pick. The
+// line is near the memory's rate at any size and needs 11 to 16 us to start and
+// to join. Measured at (E, k, H, F) and T tokens, small / line, microseconds:
+//   rows   per tensor                       1x128
+//   4096   (16, 2, 1024, 1024) T2  8.3/11.9  9.4/14.5
+//   8192   (16, 2, 4096, 1024) T4 19.9/23.3 22.9/26.6
+//   9216   (64, 6, 2048, 1536) T1 16.5/18.8 21.4/22.3
+//  12288  (128, 8, 2048,  768) T2 23.0/23.1 27.5/25.1
+//  12288   (32, 4, 1024, 1024) T3 16.7/13.4 20.0/15.8
+//   1024   (32, 2, 8192,  512) T1 20.8/14.7 26.5/16.6
+//   rows   NVFP4 (conversions to f16)
+//   4096   (16, 2, 1024, 1024) T2  8.1/11.7
+//   6144  (128, 8, 2048,  768) T1 13.2/14.3
+//   8192   (16, 2, 1024, 1024) T4 12.7/12.2
+//   9216   (64, 6, 2048, 1536) T1 17.3/15.2
+//   1024   (32, 2, 8192,  512) T1 16.9/15.4
+//   rows   MXFP8 (a scale every 32 elements: twice the work of a unit)
+//   4096   (32, 4, 1024, 1024) T1 10.4/12.9
+//   6144   (32, 4, 1024,  512) T3 13.3/12.1
+//   8192   (16, 2, 1024, 1024) T4 14.2/13.4
+//   1024   (32, 2, 2048,  512) T1 13.2/12.5
 inline bool few_is_small(int kind, int T, int k, int E, int64_t H, int64_t F) {
   const int64_t experts = static_cast<int64_t>(T) * k < E ? static_cast<int64_t>(T) * k : E;
-  const int64_t bytes = experts * 3 * H * F * (kind == kNV ? 9 : 16) / 16;
-  return T <= kSmallT && bytes <= (kind == kNV ? 24 : kind == kMX ? 40 : 72) * int64_t(1000000);
+  const int64_t rows = kind == kMX ? 4864 : kind == kNV ? 7296 : 9728;     // 9728: one wave of 32-row CTAs, two on an SM
+  return T <= kSmallT && H <= (kind == kMX ? 1024 : 4096) && experts * F <= rows;
 }
 
 }  // namespace mgq

@@ -129,6 +129,13 @@ def test_odd_multiples_of_128(recipe, T, E, k, H, F):
 
 
 @pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("T,E,k,H,F", [(2, 2, 2, 4096, 256), (1, 4, 2, 4352, 256), (3, 3, 3, 4352, 512), (8, 2, 1, 4608, 256)])
+def test_few_tokens_with_long_rows(recipe, T, E, k, H, F):
+    """Either side of the length at which few tokens change the form."""
+    test_layer(recipe, T, E, k, H, F)
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
 def test_every_token_on_one_expert(recipe):
     """128 tokens of one expert: two token blocks of the same weights."""
     rng = np.random.default_rng(11)
