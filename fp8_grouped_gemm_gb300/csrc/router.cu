@@ -98,12 +98,12 @@ __device__ __forceinline__ void load_row(const RouterArgs& a, int64_t r, int e0,
 }
 
 // sorts a lane's keys (largest first, equal keys in their order) with their
-// places, a byte each: exchanges of neighbours only
+// experts e0 + i, a byte each: exchanges of neighbours only
 template <int V>
-__device__ __forceinline__ void sort_lane(uint32_t* key, uint32_t& at4) {
+__device__ __forceinline__ void sort_lane(uint32_t* key, int e0, uint32_t& at4) {
   uint32_t at[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) at[i] = i;
+  for (int i = 0; i < V; ++i) at[i] = e0 + i;
 #pragma unroll
   for (int i = 1; i < V; ++i)
 #pragma unroll
@@ -118,12 +118,23 @@ __device__ __forceinline__ void sort_lane(uint32_t* key, uint32_t& at4) {
   for (int i = 0; i < V; ++i) at4 |= at[i] << (8 * i);
 }
 
+// sum over the eight lanes of a row
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
 template <int V, bool BF16, bool SIGMOID, bool RENORM>
 __global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
   ptx::grid_wait();
   ptx::grid_launch();
   constexpr bool SORTED = V <= 4;     // longer runs: find the next best when the head is taken
+  __shared__ uint16_t picked[8][kMaxTopK];
+  uint16_t* pick = picked[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31, e0 = lane * V;
+  uint32_t below;                     // the lanes before this one
+  asm("mov.u32 %0, %%lanemask_lt;" : "=r"(below));
   const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
   for (int64_t r = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5); r < a.T; r += nw) {
     float v[V];
@@ -131,51 +142,52 @@ __global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
     load_row<V, BF16>(a, r, e0, v);
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = e0 + i < a.E ? order_key(v[i]) : 0u;
-    uint32_t head = 0, at4 = 0;       // best key left; its place in the low byte
+    uint32_t head = 0, at4 = 0;       // best key left; its expert in the low byte (or its place in the run)
     if (SORTED) {
-      sort_lane<V>(key, at4);
+      sort_lane<V>(key, e0, at4);
       head = key[0];
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (key[i] > head) head = key[i], at4 = i;
     }
-    uint32_t k_sel = 0;   // lane j: the j-th selected key and its expert
-    int e_sel = 0;
+    uint32_t k_sel = 0;   // lane j: the j-th selected key
     uint32_t top = 0;
+    __syncwarp();         // the last row's picks are read
 #pragma unroll
     for (int j = 0; j < kMaxTopK; ++j) {
       if (j >= a.k) break;
       const uint32_t m = __reduce_max_sync(kFull, head);
       const uint32_t have = __ballot_sync(kFull, head == m);
-      const int w = __ffs(have) - 1;
-      const int e = __shfl_sync(kFull, e0 + static_cast<int>(at4 & 255u), w);
-      if (lane == j) k_sel = m, e_sel = e;
+      if (lane == j) k_sel = m;
       if (j == 0) top = m;
-      const bool mine = lane == w;    // the owner takes it out
-      if (SORTED) {
+      if (head == m && (have & below) == 0) {    // the owner takes it out
+        pick[j] = static_cast<uint16_t>(SORTED ? at4 & 255u : e0 + at4);
+        if (SORTED) {
 #pragma unroll
-        for (int i = 0; i + 1 < V; ++i) key[i] = mine ? key[i + 1] : key[i];
-        key[V - 1] = mine ? 0u : key[V - 1];
-        at4 = mine ? at4 >> 8 : at4;
-        head = key[0];
-      } else if (mine) {
-        head = 0;
-        const int taken = at4;
-        at4 = 0;
+          for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+          key[V - 1] = 0u;
+          at4 >>= 8;
+          head = key[0];
+        } else {
+          head = 0;
+          const int taken = at4;
+          at4 = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (i == taken) key[i] = 0;
-          if (key[i] > head) head = key[i], at4 = i;
+          for (int i = 0; i < V; ++i) {
+            if (i == taken) key[i] = 0;
+            if (key[i] > head) head = key[i], at4 = i;
+          }
         }
       }
     }
+    __syncwarp();
     const bool on = lane < a.k;
     const float mx = from_key(top), l = from_key(k_sel);
     const float s = !on ? 0.0f : SIGMOID ? sigmoid_f32(l) : softmax_term(l, mx);
     float S = 1.0f;
     if (RENORM) {
-      S = warp_sum(s);
+      S = sum8(s);
     } else if (!SIGMOID) {
       S = 0.0f;
 #pragma unroll
@@ -183,17 +195,10 @@ __global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
       S = warp_sum(S);
     }
     if (on) {
-      a.idx[r * a.k + lane] = e_sel;
+      a.idx[r * a.k + lane] = pick[lane];
       a.probs[r * a.k + lane] = S == 0.0f ? 0.0f : a.scale * (s / S);
     }
   }
-}
-
-// sum over the eight lanes of a row
-__device__ __forceinline__ float sum8(float v) {
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  return v;
 }
 
 // A warp takes four rows at a time: eight lanes each work out the gradients of
