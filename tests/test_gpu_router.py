@@ -85,6 +85,43 @@ def test_many_rows_and_a_side_stream():
     assert np.array_equal(idx.cpu().numpy(), OB.router_topk(l.double().numpy(), k)[0])
 
 
+@pytest.mark.parametrize("E,k", [(2, 1), (8, 8), (31, 3), (33, 8), (64, 6), (100, 8), (128, 8), (129, 4), (256, 8),
+                                 (300, 5), (512, 8), (640, 8)])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+@pytest.mark.parametrize("dtype,shift", [(torch.float32, 0), (torch.bfloat16, 0), (torch.float32, 1)])
+def test_a_row_is_the_same_in_any_batch(E, k, score, renorm, dtype, shift):
+    """5003 rows at once (lanes share a warp's rows) and 100 at a time (a warp a
+    row): the same bits, with ties, masked experts and NaN in some rows; rows
+    at odd addresses (shift) as well."""
+    from fp8_grouped_gemm_gb300 import mgq
+    T = 5003
+    g = torch.Generator().manual_seed(E + k)
+    x = torch.randn(T, E, generator=g)
+    x[::3] = (x[::3] * 2).round()                                      # ties
+    x[1::7] = torch.where(torch.rand(x[1::7].shape, generator=g) < 0.5, -torch.inf, x[1::7])
+    x[5::50] = -torch.inf
+    x[6::50] = torch.nan
+    x[7::50] = 0.0
+    x[7::100] *= -1
+    x[8::50, E // 2] = torch.inf
+    flat = torch.empty(T * E + 1, dtype=dtype, device="cuda")
+    logits = flat[shift:shift + T * E].view(T, E)
+    logits.copy_(x.to(dtype))
+    def route(l):
+        i = torch.full((l.shape[0], k), -7, dtype=torch.int32, device="cuda")
+        p = torch.full((l.shape[0], k), 7.0, device="cuda")
+        mgq.router_topk(l, i, p, _mode(score), renorm, 1.5)
+        return i, p
+    i, p = route(logits)
+    parts = [route(logits[t:t + 100]) for t in range(0, T, 100)]
+    assert torch.equal(i, torch.cat([a for a, _ in parts]))
+    assert torch.equal(p.view(torch.int32), torch.cat([b for _, b in parts]).view(torch.int32))
+    clean = torch.nan_to_num(logits[:301].float().cpu(), nan=-torch.inf, posinf=torch.inf, neginf=-torch.inf)
+    with np.errstate(invalid="ignore"):      # a logit of infinity has no softmax; its rank is looked at
+        ri, _ = OB.router_topk(clean.double().numpy(), k, score, renorm, 1.5)
+    assert np.array_equal(i[:301].cpu().numpy(), ri)
+
+
 def test_probabilities_feed_the_unpermute_and_its_gradient_comes_back():
     """dprobs of mgq_moe_unpermute_bwd is what the router's backward takes: shapes and types as they are."""
     from fp8_grouped_gemm_gb300 import mgq
