@@ -374,28 +374,35 @@ __global__ void __launch_bounds__(256) router_topk_rows_kernel(RouterArgs a) {
 
 // ---- backward ------------------------------------------------------------------
 
-// A warp takes four rows at a time: eight lanes each work out the gradients of
-// their row's selected logits, then all lanes write the four dense rows. Bound by
-// three trips to memory one after the other and the write: 32768 rows of 128,
-// renormalised, in 7.2 us, 2.6 TB/s.
-template <int V, bool BF16, bool SIGMOID, bool RENORM>
-__global__ void __launch_bounds__(256) router_bwd_kernel(RouterArgs a) {
+// G lanes a row, 32 / G rows a warp: lane j < k of a row works out the gradient
+// of its j-th selected logit; they meet in shared memory as a dense row, which
+// the G lanes write out in vectors of four. DENSE (softmax over all experts,
+// not renormalised): every expert's score takes part, read the same way. No
+// warp has more than its 32 / G rows to do before T fills the GPU; what is left
+// is three trips to memory, one after the other, and the write. 16 rows of 128:
+// 2.0 us (DENSE 2.8); 32768 rows, float32: 7.2 us at 2.6 TB/s (DENSE 10.3 us at
+// 3.5 TB/s); 32768 rows of 1024: 31 us at 4.4 TB/s.
+template <int G, int V, bool BF16, bool DENSE>
+__global__ void __launch_bounds__(256, DENSE ? 4 : 6) router_bwd_kernel(RouterArgs a) {
   ptx::grid_wait();
   ptx::grid_launch();
-  // a dense row is put together in shared memory: zeros, the selected
-  // experts' gradients by id, then V consecutive values a lane
+  constexpr int ROWS = 32 / G;
   __shared__ __align__(16) float rows[8][32 * V];
-  constexpr bool DENSE = !SIGMOID && !RENORM;      // every expert's score takes part
-  const int lane = threadIdx.x & 31, e0 = lane * V, sub = lane & 7;
-  float* row = rows[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31, sub = lane % G;
+  float* row = rows[threadIdx.x >> 5] + lane / G * (G * V);
 #pragma unroll
-  for (int i = 0; i < V; ++i) row[e0 + i] = 0.0f;
+  for (int i = 0; i < V; ++i) row[sub + G * i] = 0.0f;
+  __syncwarp();
   const int64_t nw = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  for (int64_t r4 = 4 * (blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5)); r4 < a.T; r4 += 4 * nw) {
-    const int64_t r = r4 + (lane >> 3);
+  for (int64_t r0 = ROWS * (blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5)); r0 < a.T;
+       r0 += ROWS * nw) {
+    const int64_t r = r0 + lane / G;
+    const bool live = r < a.T;
+    float v[DENSE ? V : 1];
+    if constexpr (DENSE) load_strided<G, V, BF16>(a, live ? r : r0, sub, v);
     int e = -1;
     float d = 0.0f;
-    if (sub < a.k && r < a.T) {
+    if (sub < a.k && live) {
       e = __ldg(a.sel + r * a.k + sub);
       d = __ldg(a.dprobs + r * a.k + sub);
       if (e < 0 || e >= a.E) {
@@ -404,94 +411,103 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(RouterArgs a) {
       }
     }
     const bool on = e >= 0;
-    const float l = on ? load_logit<BF16>(a.logits, r * a.E + e) : -INFINITY;
-    float g = 0.0f;         // the selected logit's own gradient (DENSE: dprobs times scale, for now)
-    if (SIGMOID) {
+    // loaded by every lane: a branch here costs the row's lanes 0.9 us
+    const float at_e = load_logit<BF16>(a.logits, (live ? r : r0) * a.E + (on ? e : 0));
+    const float l = on ? at_e : -INFINITY;
+    float g = 0.0f, back = 0.0f;
+    if constexpr (DENSE) {
+      float top = v[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) top = fmaxf(top, v[i]);
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      float all = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) all += v[i] = softmax_term(v[i], top);
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
+      const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+      const float s = on ? softmax_term(l, top) * inv : 0.0f;
+      g = s > 0.0f ? a.scale * d * s : 0.0f;
+      back = g;
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) back += __shfl_xor_sync(kFull, back, o);
+      back *= inv;
+    } else if (a.sigmoid) {
       const float s = on ? sigmoid_f32(l) : 0.0f;
-      if (RENORM) {
+      if (a.renorm) {
         const float S = sum8(s);
-        const float q = S == 0.0f ? 0.0f : s / S;
+        const float q = s * (1.0f / (S == 0.0f ? 1.0f : S));
         const float c = sum8(q > 0.0f ? d * q : 0.0f);
         g = q > 0.0f ? a.scale * (d - c) * q * sigmoid_f32(-l) : 0.0f;
       } else {
         g = s > 0.0f ? a.scale * d * s * sigmoid_f32(-l) : 0.0f;
       }
-    } else if (RENORM) {
+    } else {
       float m = l;
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
       const float s = on ? softmax_term(l, m) : 0.0f;
       const float S = sum8(s);
-      const float q = S == 0.0f ? 0.0f : s / S;
+      const float q = s * (1.0f / (S == 0.0f ? 1.0f : S));
       const float c = sum8(q > 0.0f ? d * q : 0.0f);
       g = q > 0.0f ? a.scale * q * (d - c) : 0.0f;
-    } else {
-      g = a.scale * d;
     }
-    const int nr = static_cast<int>(a.T - r4 < 4 ? a.T - r4 : 4);
-    for (int t = 0; t < nr; ++t) {
-      const int64_t rt = r4 + t;
-      const bool own = on && (lane >> 3) == t;
-      float v[V], top = 0.0f, back = 0.0f, gt = g;
-      if (DENSE) {
-        uint32_t km = 0;
-        load_row<V, BF16>(a, rt, e0, v);
+    if (on) atomicAdd(row + e, g);    // (ids of a row are distinct: one addition each)
+    __syncwarp();
+    const int64_t at = r * a.E;
+    if (a.vec) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) km = max(km, order_key(v[i]));
-        top = from_key(__reduce_max_sync(kFull, km));
-        float all = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) all += softmax_term(v[i], top);
-        all = warp_sum(all);
-        const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-        const float s = own ? softmax_term(l, top) * inv : 0.0f;
-        gt = s > 0.0f ? g * s : 0.0f;
-        back = warp_sum(gt) * inv;
+      for (int i = 0; i < V; i += 4) {
+        const int c = 4 * sub + G * i;
+        float4 o = *reinterpret_cast<float4*>(row + c);
+        *reinterpret_cast<float4*>(row + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if constexpr (DENSE)
+          o.x -= v[i] * back, o.y -= v[i + 1] * back, o.z -= v[i + 2] * back, o.w -= v[i + 3] * back;
+        if (live && c < a.E) {
+          if (BF16)
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dlogits) + at + c) =
+                make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+          else
+            *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + at + c) = o;
+        }
       }
-      if (own) atomicAdd(row + e, gt);    // (ids of a row are distinct: one addition each)
-      __syncwarp();
-      float o[V];
+    } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        o[i] = row[e0 + i];
-        row[e0 + i] = 0.0f;
-        if (DENSE) o[i] -= softmax_term(v[i], top) * back;
-      }
-      __syncwarp();
-      const int64_t at = rt * a.E + e0;
-      if (V >= 4 && a.vec) {
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          if (e0 + i >= a.E) continue;
-          if (BF16)
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dlogits) + at + i) =
-                make_uint2(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]));
-          else
-            *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + at + i) =
-                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (e0 + i >= a.E) continue;
-          if (BF16) static_cast<__nv_bfloat16*>(a.dlogits)[at + i] = __float2bfloat16_rn(o[i]);
-          else static_cast<float*>(a.dlogits)[at + i] = o[i];
+        const int c = sub + G * i;
+        float o = row[c];
+        row[c] = 0.0f;
+        if constexpr (DENSE) o -= v[i] * back;
+        if (live && c < a.E) {
+          if (BF16) static_cast<__nv_bfloat16*>(a.dlogits)[at + c] = __float2bfloat16_rn(o);
+          else static_cast<float*>(a.dlogits)[at + c] = o;
         }
       }
     }
+    __syncwarp();
   }
 }
 
+bool launch_grid(void (*kern)(RouterArgs), int64_t rows, const RouterArgs& a, cudaStream_t s) {
+  const int64_t ctas = (a.T + rows - 1) / rows, most = static_cast<int64_t>(num_sms()) * 8;
+  return launch_after(kern, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), 256, 0, 1, s, a);
+}
+
 template <int V, bool BF16>
-bool launch_mode(const RouterArgs& a, bool bwd, bool sigmoid, bool renorm, int grid, cudaStream_t s) {
-  void (*kern)(RouterArgs);
-  if (bwd)
-    kern = sigmoid ? (renorm ? router_bwd_kernel<V, BF16, true, true> : router_bwd_kernel<V, BF16, true, false>)
-                   : (renorm ? router_bwd_kernel<V, BF16, false, true> : router_bwd_kernel<V, BF16, false, false>);
-  else
-    kern = sigmoid ? (renorm ? router_topk_kernel<V, BF16, true, true> : router_topk_kernel<V, BF16, true, false>)
-                   : (renorm ? router_topk_kernel<V, BF16, false, true> : router_topk_kernel<V, BF16, false, false>);
-  return launch_after(kern, dim3(grid), 256, 0, 1, s, a);
+bool launch_topk(const RouterArgs& a, cudaStream_t s) {
+  return launch_grid(a.sigmoid ? (a.renorm ? router_topk_kernel<V, BF16, true, true> : router_topk_kernel<V, BF16, true, false>)
+                               : (a.renorm ? router_topk_kernel<V, BF16, false, true> : router_topk_kernel<V, BF16, false, false>),
+                     8, a, s);
+}
+template <int G, int V, bool BF16>
+bool launch_topk_rows(const RouterArgs& a, cudaStream_t s) {
+  return launch_grid(router_topk_rows_kernel<G, V, BF16>, 8 * (32 / G), a, s);
+}
+template <int G, int V, bool BF16>
+bool launch_bwd(const RouterArgs& a, cudaStream_t s) {
+  return launch_grid(!a.sigmoid && !a.renorm ? router_bwd_kernel<G, V, BF16, true> : router_bwd_kernel<G, V, BF16, false>,
+                     8 * (32 / G), a, s);
 }
 
 // Which kernel takes the forward pass: G lanes a row once that gives every SM
@@ -505,30 +521,30 @@ bool many_rows(int64_t T, int E) {
 }
 
 template <bool BF16>
-int launch_rows(const RouterArgs& a, cudaStream_t s) {
-  const int rows = a.E <= 128 ? 32 : a.E <= 256 ? 16 : 8;        // of a CTA at a time
-  const int64_t ctas = (a.T + rows - 1) / rows, most = static_cast<int64_t>(num_sms()) * 8;
-  void (*kern)(RouterArgs) = a.E <= 32    ? router_topk_rows_kernel<8, 4, BF16>
-                             : a.E <= 64  ? router_topk_rows_kernel<8, 8, BF16>
-                             : a.E <= 128 ? router_topk_rows_kernel<8, 16, BF16>
-                             : a.E <= 256 ? router_topk_rows_kernel<16, 16, BF16>
-                                          : router_topk_rows_kernel<32, 16, BF16>;
-  return launch_after(kern, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), 256, 0, 1, s, a) ? MGQ_OK : MGQ_ERR_CUDA;
-}
-
-template <bool BF16>
 int launch_router(RouterArgs a, bool bwd, bool sigmoid, bool renorm, cudaStream_t s) {
   // vectors of four logits: rows of a multiple of four, aligned bases
   const uintptr_t size = BF16 ? 8 : 16;
   a.vec = a.E % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits)) & (size - 1)) == 0;
   a.sigmoid = sigmoid, a.renorm = renorm;
-  if (!bwd && many_rows(a.T, a.E)) return launch_rows<BF16>(a, s);
-  const int64_t per = bwd ? 32 : 8;      // rows of a CTA at a time
-  const int64_t ctas = (a.T + per - 1) / per, most = static_cast<int64_t>(num_sms()) * 8;
-  const int grid = static_cast<int>(ctas < most ? ctas : most);
-  auto go = a.E <= 32 ? launch_mode<1, BF16> : a.E <= 64 ? launch_mode<2, BF16> : a.E <= 128 ? launch_mode<4, BF16> :
-            a.E <= 256 ? launch_mode<8, BF16> : a.E <= 512 ? launch_mode<16, BF16> : launch_mode<32, BF16>;
-  return go(a, bwd, sigmoid, renorm, grid, s) ? MGQ_OK : MGQ_ERR_CUDA;
+  const int E = a.E;
+  auto go = bwd ? (E <= 32    ? launch_bwd<8, 4, BF16>
+                   : E <= 64  ? launch_bwd<8, 8, BF16>
+                   : E <= 128 ? launch_bwd<8, 16, BF16>
+                   : E <= 256 ? launch_bwd<16, 16, BF16>
+                   : E <= 512 ? launch_bwd<32, 16, BF16>
+                              : launch_bwd<32, 32, BF16>)
+            : many_rows(a.T, E) ? (E <= 32    ? launch_topk_rows<8, 4, BF16>
+                                   : E <= 64  ? launch_topk_rows<8, 8, BF16>
+                                   : E <= 128 ? launch_topk_rows<8, 16, BF16>
+                                   : E <= 256 ? launch_topk_rows<16, 16, BF16>
+                                              : launch_topk_rows<32, 16, BF16>)
+                                : (E <= 32    ? launch_topk<1, BF16>
+                                   : E <= 64  ? launch_topk<2, BF16>
+                                   : E <= 128 ? launch_topk<4, BF16>
+                                   : E <= 256 ? launch_topk<8, BF16>
+                                   : E <= 512 ? launch_topk<16, BF16>
+                                              : launch_topk<32, BF16>);
+  return go(a, s) ? MGQ_OK : MGQ_ERR_CUDA;
 }
 
 int check_router(const void* logits, int dtype, int64_t T, int E, int k, int score, int renorm) {
