@@ -211,11 +211,28 @@ __device__ __forceinline__ float square_sum(const float* v) {
   return sq.x + sq.y;
 }
 
-// the scale bytes of the rows that fill the last 128-row tile are zero
+// The scale bytes of the rows that fill the last 128-row tile are zero. 16 bytes
+// of a tile hold rows r, r + 32, r + 64 and r + 96, a word each.
 __device__ __forceinline__ void zero_scale_rows(const NormArgs& a) {
-  const int kb4 = a.H >> 7, rest = static_cast<int>((128 - (a.T & 127)) & 127) * kb4;
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < rest; i += gridDim.x * blockDim.x)
-    *reinterpret_cast<uint32_t*>(a.scales + tiled_scale_offset(a.T + i / kb4, 4 * (i % kb4), kb4)) = 0;
+  const int kb4 = a.H >> 7, live = static_cast<int>(a.T & 127);
+  if (live == 0) return;
+  uint8_t* tiles = a.scales + (a.T >> 7) * kb4 * 512;
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < kb4 * 32; i += gridDim.x * blockDim.x) {
+    const int r = i & 31;
+    if (r >= live) {
+      *(reinterpret_cast<uint4*>(tiles) + i) = make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int g = 1; g < 4; ++g)
+        if (r + 32 * g >= live) *(reinterpret_cast<uint32_t*>(tiles) + 4 * i + g) = 0;
+    }
+  }
+}
+
+// an atomic only where it raises the value (which never falls)
+__device__ __forceinline__ void raise_amax(const NormArgs& a, uint32_t amax) {
+  unsigned int* const at = reinterpret_cast<unsigned int*>(a.amax);
+  if (amax > *reinterpret_cast<volatile unsigned int*>(at)) atomicMax(at, amax);
 }
 
 // A CTA per row (few rows). SC: the mgq_scaling of the codes or kNoQuant; CH:
@@ -230,6 +247,7 @@ __global__ void __launch_bounds__(512, CH < 4 ? 2 : 1) norm_kernel(NormArgs a) {
   const float h = static_cast<float>(a.H), inv_h = 1.0f / h;
   float ts = 1.0f;
   if (SC == MGQ_TENSOR_F32) ts = __ldg(a.ts);
+  if (SC == MGQ_MX32_E8M0) zero_scale_rows(a);
   uint32_t amax = 0;
   int slot = 0;
   for (int64_t r = blockIdx.x; r < a.T; r += gridDim.x, slot ^= 1) {
@@ -296,10 +314,16 @@ __global__ void __launch_bounds__(512, CH < 4 ? 2 : 1) norm_kernel(NormArgs a) {
     }
   }
   if (SC == MGQ_TENSOR_F32 && a.amax) {
+    // one atomic a CTA
     amax = warp_max_u32(amax);
-    if (lane == 0 && amax) atomicMax(reinterpret_cast<unsigned int*>(a.amax), amax);
+    uint32_t* const all = reinterpret_cast<uint32_t*>(red[slot]);
+    if (lane == 0) all[threadIdx.x >> 5] = amax;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      amax = warp_max_u32(lane < (blockDim.x + 31) >> 5 ? all[lane] : 0u);
+      if (lane == 0) raise_amax(a, amax);
+    }
   }
-  if (SC == MGQ_MX32_E8M0) zero_scale_rows(a);
 }
 
 // 16 bf16 values of a lane, 32 bytes: one store where the row is 32-byte aligned
@@ -431,7 +455,7 @@ __global__ void __launch_bounds__(512) norm_stream_kernel(NormArgs a) {
   }
   if (SC == MGQ_TENSOR_F32 && a.amax) {
     amax = warp_max_u32(amax);
-    if (lane == 0 && amax) atomicMax(reinterpret_cast<unsigned int*>(a.amax), amax);
+    if (lane == 0) raise_amax(a, amax);
   }
   if (SC == MGQ_MX32_E8M0) zero_scale_rows(a);
 }
@@ -442,7 +466,7 @@ void row_shape(int nchunk, int* threads, int* ch) {
   *threads = ((nchunk + *ch - 1) / *ch + 31) / 32 * 32;
 }
 
-constexpr int kNormThreads = 512, kNormBwdThreads = 512;   // streamed: threads of an SM
+constexpr int kNormThreads = 512;            // streamed forward: threads of an SM
 constexpr size_t kRingPerSm = 192 * 1024;    // shared memory for the rings of an SM's CTAs
 
 // CTAs per SM and ring slots of a streamed kernel whose slot takes `slot`
@@ -594,18 +618,33 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormBwdArgs a) {
 }
 
 // dw[c] = beta dw[c] + the sum of the n partial rows, in a fixed order: each of
-// the 32 warps of a CTA sums every 32nd row of 32 columns, four in flight.
-// Launched while the kernel above drains.
+// the 32 warps of a CTA sums every 32nd row of 32 columns, kInFlight of them per
+// trip to memory (measured 4, 8, 16: 1000 rows of 1024 6.4, 6.0, 6.0 us, 333 rows
+// of 2048 5.9, 5.2, 5.5). Launched while the kernel above drains.
+constexpr int kInFlight = 8;
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int n, int H, float beta, float* dw) {
   __shared__ float sh[32][33];
   ptx::grid_wait();
   const int l = threadIdx.x & 31, c = blockIdx.x * 32 + l, w = threadIdx.x >> 5;
   float t = 0.0f;
   if (c < H) {
-    for (int r = w; r < n; r += 128) {
+    const float* p = part + static_cast<int64_t>(w) * H + c;
+    const int64_t step = static_cast<int64_t>(H) * 32;
+    int r = w;
+    for (; r + 32 * (kInFlight - 1) < n; r += 32 * kInFlight, p += kInFlight * step) {
+      float v[kInFlight];
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i) v[i] = __ldcg(p + i * step);
+#pragma unroll
+      for (int o = kInFlight / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) v[i] += v[i + o];
+      t += v[0];
+    }
+    for (; r < n; r += 128, p += 4 * step) {
       float v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = r + 32 * i < n ? part[static_cast<int64_t>(r + 32 * i) * H + c] : 0.0f;
+      for (int i = 0; i < 4; ++i) v[i] = r + 32 * i < n ? __ldcg(p + i * step) : 0.0f;
       t += (v[0] + v[1]) + (v[2] + v[3]);
     }
   }
@@ -621,11 +660,20 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int n,
 
 constexpr int64_t kMaxNormH = 16384;   // four chunks a thread of a 512-thread CTA
 
+// Threads of an SM in the backward. 512, but 192 to 256 threads a row leave two
+// rows to an SM then: four of 192 or three of 256 (9000 rows of 1408 28.6 / 22.4
+// us, of 2048 32.1 / 28.0; more for other lengths costs them: 9000 rows of 4096
+// 48.3 / 55.1, 4000 of 768 10.9 / 12.1).
+int bwd_threads(int threads, int ch) {
+  const int want = 4 * threads < 768 ? 4 * threads : 768;
+  return ch == 1 && want > 512 ? want : 512;
+}
+
 // rows of partial sums of the backward for T rows of H elements: its grid
 int bwd_grid(int64_t T, int64_t H) {
   int threads, ch, ctas, slots;
   row_shape(static_cast<int>(H >> 3), &threads, &ch);
-  ring_shape(threads, kNormBwdThreads, static_cast<size_t>(H) * 6, &ctas, &slots);
+  ring_shape(threads, bwd_threads(threads, ch), static_cast<size_t>(H) * 6, &ctas, &slots);
   const int64_t g = static_cast<int64_t>(num_sms()) * ctas;
   return static_cast<int>(T < g ? T : g);
 }
@@ -634,7 +682,7 @@ template <int CH>
 int launch_bwd(NormBwdArgs a, int threads, int grid, cudaStream_t s) {
   const size_t slot = static_cast<size_t>(a.H) * 6;
   int ctas;
-  ring_shape(threads, kNormBwdThreads, slot, &ctas, &a.slots);
+  ring_shape(threads, bwd_threads(threads, CH), slot, &ctas, &a.slots);
   // (four chunks a thread beside the ring do not fit the registers)
   if constexpr (CH < 4) {
     if (a.T >= 2 * static_cast<int64_t>(grid)) {
