@@ -31,7 +31,8 @@ namespace {
 
 constexpr int kMaxT = 128, kMaxK = 8, kMaxE = 1024;
 constexpr int kTok = 64;                  // tokens of one tile (tensor-memory columns of one half)
-constexpr int kThreads = 192;             // warp 0 TMA, warp 1 MMA, warps 2-5 epilogue
+constexpr int kEpiWarps = 8;              // two groups of four: one thread a weight row each, half of the tokens
+constexpr int kThreads = 64 + 32 * kEpiWarps;   // warp 0 TMA, warp 1 MMA, the others the epilogue
 constexpr uint32_t kATile = 128 * 128;    // bytes of 128 weight rows of one stage
 constexpr int kMaxStages = 6;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -50,16 +51,18 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-// the four epilogue warps
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// the same barrier, true if `ok` is true in all four warps (a wait that ran out
+// the epilogue warps
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory"); }
+// one group of them
+__device__ __forceinline__ void group_sync(int grp) { asm volatile("bar.sync %0, 128;" ::"r"(2 + grp) : "memory"); }
+// the first barrier, true if `ok` is true in all the warps (a wait that ran out
 // in one of them must not leave the others at a barrier that it never reaches)
 __device__ __forceinline__ bool epi_all(bool ok) {
   uint32_t r;
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\t"
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\t"
                "selp.u32 %0, 1, 0, q;\n\t}"
                : "=r"(r)
-               : "r"(static_cast<uint32_t>(ok))
+               : "r"(static_cast<uint32_t>(ok)), "n"(32 * kEpiWarps)
                : "memory");
   return r != 0;
 }
@@ -345,7 +348,7 @@ __device__ __forceinline__ void join4(const float* part, int64_t place, int ca, 
 // 9 us behind the weights' copies.
 template <int KIND>
 __device__ __forceinline__ void store_h(const FewArgs& p, const Tile& s, int c0, int nj, float (&g)[4], const float (&u)[4],
-                                        float alpha, int row, float sh, uint32_t (*smax)[4][16], uint32_t& tick) {
+                                        float alpha, int row, float sh, int grp, uint32_t (*smax)[4][16], uint32_t& tick) {
   const uint32_t lane = threadIdx.x & 31, wq = row >> 5;
   const int64_t f0 = static_cast<int64_t>(s.m) * 128;
 #pragma unroll
@@ -360,8 +363,8 @@ __device__ __forceinline__ void store_h(const FewArgs& p, const Tile& s, int c0,
     // (two buffers in turn: a warp writes one again only after the barrier
     // that every warp reaches when it has read it)
     ++tick;
-    if (lane < 4) smax[tick & 1][wq][lane] = mine;
-    epi_sync();
+    if (lane < 4) smax[tick & 1][wq][4 * grp + lane] = mine;
+    group_sync(grp);
   }
   // the four tokens side by side, whether real or not, then the stores
   uint32_t code[4], scale[4];
@@ -385,7 +388,7 @@ __device__ __forceinline__ void store_h(const FewArgs& p, const Tile& s, int c0,
     } else if (KIND == kBLK) {
       m = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) m = max(m, smax[tick & 1][q][j]);
+      for (int q = 0; q < 4; ++q) m = max(m, smax[tick & 1][q][4 * grp + j]);
       const float mult = blk_scale_few(m);
       inv[j] = __fdiv_rn(1.0f, mult);
       code[j] = cvt_e4m3x2(__fmul_rn(g[j], mult), 0.0f);
@@ -458,11 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 32) {
     for (int s = 0; s < kMost; ++s) {
       ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], KIND == kBLK ? 5 : 1);   // the MMAs; BLK: and the four epilogue warps
+      ptx::mbar_init(&empty[s], KIND == kBLK ? 1 + kEpiWarps : 1);   // the MMAs; BLK: and the epilogue warps
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&t_full[a], 1);
-      ptx::mbar_init(&t_empty[a], 128);
+      ptx::mbar_init(&t_empty[a], kEpiWarps);
     }
     *s_abort = 0;
     ptx::fence_mbar_init();
@@ -666,9 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    // thread = one weight row of each half (tensor-memory lane), all tokens
+    // thread = one weight row of each half (tensor-memory lane) and half of the
+    // tokens: the groups take four columns in turn (1x128: sixteen)
     grid_wait();
-    const int row = (warp & 3) * 32 + lane;
+    const int row = (warp & 3) * 32 + lane, grp = (warp - 2) >> 2;
     const uint32_t tlane = static_cast<uint32_t>(warp & 3) << 21;
     const int64_t place = static_cast<int64_t>(p.nmax) * 256;
     const float sx = KIND == kNV || KIND == kTEN ? __ldg(p.sx) : 1.0f;
@@ -693,11 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (KIND == kBLK) {
         // every stage's product is scaled and added in float32 registers
-        float acc[2][kTok / 16][16];
+        float acc[2][kTok / 32][16];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int c = 0; c < kTok / 16; ++c)
+          for (int c = 0; c < kTok / 32; ++c)
 #pragma unroll
             for (int j = 0; j < 16; ++j) acc[h][c][j] = 0.0f;
         const int64_t wr = (s.e * p.rows_e + static_cast<int64_t>(s.m) * p.mstep) / 128;
@@ -718,16 +722,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           ptx::tc_fence_after();
           const float4* fx = reinterpret_cast<const float4*>(sSF + st * SF);
 #pragma unroll
-          for (int c = 0; c < kTok / 16; ++c) {
-            if (c >= n16) break;
+          for (int c = 0; c < kTok / 32; ++c) {
+            const int c16 = 2 * c + grp;
+            if (c16 >= n16) break;
             uint32_t v0[16], v1[16];
-            ptx::tmem_ld_32x32b_x16(tmem + tlane + a * 2 * kTok + 16 * c, v0);
-            ptx::tmem_ld_32x32b_x16(tmem + tlane + a * 2 * kTok + kTok + 16 * c, v1);
+            ptx::tmem_ld_32x32b_x16(tmem + tlane + a * 2 * kTok + 16 * c16, v0);
+            ptx::tmem_ld_32x32b_x16(tmem + tlane + a * 2 * kTok + kTok + 16 * c16, v1);
             ptx::tmem_ld_wait_regs(v0);
             ptx::tmem_ld_wait_regs(v1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float4 f = fx[4 * c + j];
+              const float4 f = fx[4 * c16 + j];
               const float f4[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -737,9 +742,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           ptx::tc_fence_before();
-          ptx::mbar_arrive(&t_empty[a]);
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&empty[st]);
+          if (lane == 0) {
+            ptx::mbar_arrive(&t_empty[a]);
+            ptx::mbar_arrive(&empty[st]);
+          }
           if (++st == STG) st = 0, ph ^= 1;
         }
         // the sums go to this CTA's place even for a whole tile, whose threads
@@ -747,18 +754,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         alive = epi_all(alive);            // (store_h has barriers of its own)
         if (alive) {
 #pragma unroll
-          for (int c = 0; c < kTok / 16; ++c) {
-            if (c >= n16) break;
+          for (int c = 0; c < kTok / 32; ++c) {
+            const int c0 = 32 * c + 16 * grp;
+            if (c0 >= s.n) break;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              if (16 * c + j >= s.n) break;
-              mine[(16 * c + j) * 256 + row] = acc[0][c][j];
-              mine[(16 * c + j) * 256 + 128 + row] = acc[1][c][j];
+              if (c0 + j >= s.n) break;
+              mine[(c0 + j) * 256 + row] = acc[0][c][j];
+              mine[(c0 + j) * 256 + 128 + row] = acc[1][c][j];
             }
           }
           if (whole) {
 #pragma unroll 1
-            for (int c = 0; c < s.n; c += 4) {
+            for (int c = 16 * grp; c < s.n; c += (c & 12) == 12 ? 20 : 4) {
               const int nj = min(4, s.n - c);
               float g[4], h[4];
 #pragma unroll
@@ -766,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 g[j] = j < nj ? mine[(c + j) * 256 + row] : 0.0f;
                 h[j] = j < nj ? mine[(c + j) * 256 + 128 + row] : 0.0f;
               }
-              if (PHASE == 1) store_h<KIND>(p, t, c, nj, g, h, alpha, row, sh, smax, tick);
+              if (PHASE == 1) store_h<KIND>(p, t, c, nj, g, h, alpha, row, sh, grp, smax, tick);
               else store_y(p, t, c, nj, g, h, alpha, row);
             }
           }
@@ -778,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (alive) {
           ptx::tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < s.n; c += 4) {
+          for (int c = 4 * grp; c < s.n; c += 8) {
             const int nj = min(4, s.n - c);
             uint32_t v0[4], v1[4];
             ptx::tmem_ld_32x32b_x4(tmem + tlane + a * 2 * kTok + c, v0);
@@ -795,22 +803,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mine[(c + j) * 256 + 128 + row] = h[j];
               }
             } else if (PHASE == 1) {
-              store_h<KIND>(p, t, c, nj, g, h, alpha, row, sh, smax, tick);
+              store_h<KIND>(p, t, c, nj, g, h, alpha, row, sh, grp, smax, tick);
             } else {
               store_y(p, t, c, nj, g, h, alpha, row);
             }
           }
           ptx::tc_fence_before();
-          ptx::mbar_arrive(&t_empty[a]);
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&t_empty[a]);
         }
       }
-      if (!alive) {                        // (in all four warps)
+      if (!alive) {                        // (in all the warps)
         report(p.err, MGQ_ERR_TIMEOUT);
         *s_abort = 1;
         break;
       }
       if (!whole) {
-        // the barrier orders the four warps' stores before the fence of the
+        // the barrier orders the warps' stores before the fence of the
         // thread that counts this CTA in
         epi_sync();
         if (threadIdx.x == 64) {
@@ -821,11 +830,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         epi_sync();
         if (*s_last) {
 #pragma unroll 1
-          for (int c = 0; c < t.n; c += 4) {
+          for (int c = 4 * grp; c < t.n; c += 8) {
             const int nj = min(4, t.n - c);
             float g[4], h[4];
             join4(p.part + c * 256 + row, place, t.ca, t.cb, nj, g, h);
-            if (PHASE == 1) store_h<KIND>(p, t, c, nj, g, h, alpha, row, sh, smax, tick);
+            if (PHASE == 1) store_h<KIND>(p, t, c, nj, g, h, alpha, row, sh, grp, smax, tick);
             else store_y(p, t, c, nj, g, h, alpha, row);
           }
         }
