@@ -7,11 +7,18 @@
 // CTAs. Two launches, the second started while the first drains; its weights
 // are requested before it waits for the first.
 //   small_gateup_kernel   a CTA: 32 gate and 32 up rows of one expert (NVFP4: 16
-//                         and 16, one block of its scales), its warps the contraction and quantise their stretch of the
-//                         tokens' x on the way; SwiGLU, h quantised
+//                         and 16, one block of its scales); its warps split the
+//                         contraction and quantise their stretch of the tokens'
+//                         x on the way; SwiGLU, h quantised
 //   small_down_kernel     a CTA: 16 rows of W2 of every picked expert, its warps
 //                         split all of their contractions; out
 // All sums run in an order that only the sizes and the routing decide.
+//
+// Bound by latency: the launch, the ids, the first weights, then a warp's units
+// one after another (two loads deep) and the reduction over the warps. Measured:
+// one token, 2 experts of (1024, 1024), per tensor 6.2 us, NVFP4 6.4, 1x128 7.1,
+// MXFP8 7.4; one token, 8 experts of (2048, 768): per tensor 13.2 us, 2.9 TB/s,
+// NVFP4 13.7 us, 1.5 TB/s (conversions to f16).
 //
 // Lanes: with g = lane / 4 and q = lane % 4, a lane holds 16 bytes of weight
 // rows g and g + 8 per 64-byte chunk and the same bytes of token row g. Which
