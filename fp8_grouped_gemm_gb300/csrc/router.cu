@@ -212,8 +212,10 @@ __global__ void __launch_bounds__(256) router_topk_kernel(RouterArgs a) {
 // and takes the first equal logit, the t-th if the lane gave that
 // value t times before. Sums in the other kernel's order: the same bits.
 //
-// Bound by the integer and compare pipe (189 warp instructions a row of 128):
-// 32768 rows of 128, top 8, in 8.2 us, 18.9 MB at 2.3 TB/s.
+// Bound by the rounds' dependent exchanges at the warps that 48 registers a
+// thread allow (fewer registers spill: six CTAs an SM 8.9 us, seven 11.3); issue
+// and compare pipe are half busy, 148 warp instructions a row of 128. 32768 rows
+// of 128, top 8: 8.2 us, 18.9 MB at 2.3 TB/s.
 
 __device__ __forceinline__ void order2(float& hi, float& lo) {
   const float a = fmaxf(hi, lo), b = fminf(hi, lo);

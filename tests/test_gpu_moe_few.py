@@ -129,9 +129,10 @@ def test_odd_multiples_of_128(recipe, T, E, k, H, F):
 
 
 @pytest.mark.parametrize("recipe", RECIPES)
-@pytest.mark.parametrize("T,E,k,H,F", [(2, 2, 2, 4096, 256), (1, 4, 2, 4352, 256), (3, 3, 3, 4352, 512), (8, 2, 1, 4608, 256)])
+@pytest.mark.parametrize("T,E,k,H,F", [(2, 2, 2, 4096, 256), (1, 4, 2, 4352, 256), (3, 3, 3, 4352, 512), (8, 2, 1, 4608, 256),
+                                       (8, 1, 1, 256, 9728), (1, 1, 1, 256, 9984), (2, 3, 2, 512, 7424)])
 def test_few_tokens_with_long_rows(recipe, T, E, k, H, F):
-    """Either side of the length at which few tokens change the form."""
+    """Either side of the lengths at which few tokens change the form."""
     test_layer(recipe, T, E, k, H, F)
 
 
