@@ -29,10 +29,12 @@ int few_small_forward(int kind, const void* x, int T, int64_t H, int64_t F, cons
 //  12288   (32, 4, 1024, 1024) T3 16.7/13.4 20.0/15.8
 //   1024   (32, 2, 8192,  512) T1 20.8/14.7 26.5/16.6
 //   rows   NVFP4 (conversions to f16)
-//   4096   (16, 2, 1024, 1024) T2  8.1/11.7
-//   6144  (128, 8, 2048,  768) T1 13.2/14.3
-//   8192   (16, 2, 1024, 1024) T4 12.7/12.2
-//   9216   (64, 6, 2048, 1536) T1 17.3/15.2
+//   4096   (16, 2, 4096, 1024) T2 11.7/15.7
+//   6144  (128, 8, 2048,  768) T1 12.0/14.3
+//   6144   (16, 2, 4096, 1024) T3 17.4/16.9
+//   8192   (16, 2, 1024, 1024) T4 10.5/12.2
+//   9216   (64, 6, 2048, 1536) T1 15.1/15.2
+//  12288   (16, 2,  512, 2048) T3 13.7/12.5
 //   1024   (32, 2, 8192,  512) T1 16.9/15.4
 //   rows   MXFP8 (a scale every 32 elements: twice the work of a unit)
 //   4096   (32, 4, 1024, 1024) T1 10.4/12.9
@@ -41,7 +43,8 @@ int few_small_forward(int kind, const void* x, int T, int64_t H, int64_t F, cons
 //   1024   (32, 2, 2048,  512) T1 13.2/12.5
 inline bool few_is_small(int kind, int T, int k, int E, int64_t H, int64_t F) {
   const int64_t experts = static_cast<int64_t>(T) * k < E ? static_cast<int64_t>(T) * k : E;
-  const int64_t rows = kind == kMX ? 4864 : kind == kNV ? 7296 : 9728;     // 9728: one wave of 32-row CTAs, two on an SM
+  // 9728: one wave of 32-row CTAs, two on an SM (NVFP4: of 16-row CTAs, four on an SM)
+  const int64_t rows = kind == kMX || (kind == kNV && H > 2048) ? 4864 : 9728;
   return T <= kSmallT && H <= (kind == kMX ? 1024 : 4096) && experts * F <= rows;
 }
 

@@ -18,7 +18,7 @@
 // one after another (two loads deep) and the reduction over the warps. Measured:
 // one token, 2 experts of (1024, 1024), per tensor 6.2 us, NVFP4 6.4, 1x128 7.1,
 // MXFP8 7.4; one token, 8 experts of (2048, 768): per tensor 13.2 us, 2.9 TB/s,
-// NVFP4 13.7 us, 1.5 TB/s (conversions to f16).
+// NVFP4 12.2 us, 1.7 TB/s (conversions to f16).
 //
 // Lanes: with g = lane / 4 and q = lane % 4, a lane holds 16 bytes of weight
 // rows g and g + 8 per 64-byte chunk and the same bytes of token row g. Which
@@ -407,14 +407,15 @@ __device__ __forceinline__ void unit_mma(float (&acc)[4], const uint32_t (&w0)[8
 // block, one NVFP4 block
 __host__ __device__ constexpr int ffn_rows(int kind) { return kind == kNV ? 16 : 32; }
 
-template <int KIND>
-__global__ void __launch_bounds__(kSmallThreads, 2) small_gateup_kernel(SmallArgs a) {
+// GW: warps of a CTA
+template <int KIND, int GW>
+__global__ void __launch_bounds__(32 * GW, 16 / GW) small_gateup_kernel(SmallArgs a) {
   constexpr int FR = ffn_rows(KIND), TS = FR / 16;     // 16-row tiles of each side
   __shared__ Routing rt;
   __shared__ int sel[3], s_tok[8];
-  __shared__ float red[kWarps][8][2 * FR + 1];
-  __shared__ __align__(16) uint8_t xsm[kWarps][8 * XUnit<KIND>::kRow];
-  __shared__ float xsc[kWarps][KIND == kMX ? 32 : 8];
+  __shared__ float red[GW][8][2 * FR + 1];
+  __shared__ __align__(16) uint8_t xsm[GW][8 * XUnit<KIND>::kRow];
+  __shared__ float xsc[GW][KIND == kMX ? 32 : 8];
   __shared__ uint32_t cmax[8];
   grid_wait();
   grid_launch();
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_gateup_kernel(SmallArg
   __syncthreads();
   const int64_t f0 = static_cast<int64_t>(blockIdx.x) * FR, wrow = static_cast<int64_t>(e) * 2 * a.F + f0;
   const int units = a.H / (KIND == kNV ? 256 : 128);
-  const int u0 = warp * units / kWarps, u1 = (warp + 1) * units / kWarps;
+  const int u0 = warp * units / GW, u1 = (warp + 1) * units / GW;
   const float sx = KIND == kTEN || KIND == kNV ? __ldg(a.x_scale) : 1.0f;
   float acc[2 * TS][4];
 #pragma unroll
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_gateup_kernel(SmallArg
   if (on) {
     float gt = 0.0f, up = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < GW; ++w) {
       gt += red[w][tok][f];
       up += red[w][tok][FR + f];
     }
@@ -632,9 +633,16 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
 template <int KIND>
 int run_small(const SmallArgs& a, cudaStream_t s) {
   const int R = a.T * a.k;
-  if (!launch_after(small_gateup_kernel<KIND>, dim3(a.F / ffn_rows(KIND), R < a.E ? R : a.E), kSmallThreads, 0,
-                    KIND == kBLK ? 4 : 1, s, a))
-    return MGQ_ERR_CUDA;
+  const dim3 grid(a.F / ffn_rows(KIND), R < a.E ? R : a.E);
+  // NVFP4's CTAs of 16 rows: with four warps each, twice as many are on the GPU
+  // at once. Taken where eight warps need a second wave (384 CTAs: 13.7 / 12.2 us
+  // at H 2048; 128 CTAs at H 4096: 10.1 / 13.9).
+  auto gateup = small_gateup_kernel<KIND, 8>;
+  int warps = 8;
+  if constexpr (KIND == kNV) {
+    if (static_cast<int64_t>(grid.x) * grid.y > 2 * num_sms()) gateup = small_gateup_kernel<KIND, 4>, warps = 4;
+  }
+  if (!launch_after(gateup, grid, 32 * warps, 0, KIND == kBLK ? 4 : 1, s, a)) return MGQ_ERR_CUDA;
   if (!launch_after(small_down_kernel<KIND>, dim3(a.H / 16), kSmallThreads, 0, 1, s, a)) return MGQ_ERR_CUDA;
   return MGQ_OK;
 }
