@@ -19,7 +19,7 @@
 //
 // Measured, with residual, sum, y and MXFP8 codes: a row of 4096 in 2.6 us, all
 // of it the launch, one trip to memory and the reduction; 1003 x 5120 (1x128,
-// no residual) in 6.5 us, 4.0 TB/s; 16384 x 4096 in 102 us, 5.9 TB/s of the
+// no residual) in 6.5 us, 4.0 TB/s; 16384 x 4096 in 100 us, 6.0 TB/s of the
 // 6.8 that a plain copy reaches (two streams read, three written). Backward with
 // dsum, 16384 x 4096: 80 us, 6.7 TB/s; 333 x 2048 in 5.0 us, two launches in a row.
 #include "mgq_internal.h"
@@ -473,7 +473,7 @@ void row_shape(int nchunk, int* threads, int* ch) {
   *threads = ((nchunk + *ch - 1) / *ch + 31) / 32 * 32;
 }
 
-constexpr int kNormThreads = 512;            // streamed forward: threads of an SM
+constexpr int kNormThreads = 512;            // streamed forward: threads of an SM (twice that for many rows)
 constexpr size_t kRingPerSm = 192 * 1024;    // shared memory for the rings of an SM's CTAs
 
 // CTAs per SM and ring slots of a streamed kernel whose slot takes `slot`
@@ -501,17 +501,20 @@ int launch_norm_stream(const NormArgs& a, int threads, int grid, size_t smem, cu
 }
 
 // Streamed once every CTA has two rows. Measured, MXFP8, direct / streamed, us:
-// 1300 rows of 4096 9.7 / 8.8, 2500 of 2048 9.6 / 8.3, 5000 of 7168 64.9 / 57.1,
-// 16384 of 4096 105 / 102; with less than two 700 of 2048 3.9 / 3.8, 1300 of
+// 1300 rows of 4096 9.7 / 8.8, 2500 of 2048 9.6 / 8.3, 5000 of 7168 64.9 / 54.4,
+// 16384 of 4096 105 / 100; with less than two 700 of 2048 3.9 / 3.8, 1300 of
 // 1024 3.6 / 4.3. Threads of an SM 256 / 512 / 1024: 5000 of 4096 32.7 / 31.9 /
-// 32.9, 9000 of 1024 18.6 / 15.8 / 16.5.
+// 32.9, 9000 of 1024 18.6 / 15.8 / 16.5; 1024 from nine rows a CTA on: 512 / 1024,
+// 16384 of 4096 103 / 100, 9000 of 7168 100.5 / 96.7, eight rows (5000 of 5120)
+// 40.2 / 41.2.
 template <int SC, int DT>
 int launch_norm(NormArgs a, cudaStream_t s) {
   if (a.H % 128 == 0) {
     const int u = a.H > 1024 ? 2 : 1, st = ((a.H / 16 + u - 1) / u + 31) / 32 * 32;
     const size_t slot = static_cast<size_t>(a.H) * 4;
     int ctas;
-    ring_shape(st, kNormThreads, slot, &ctas, &a.slots);
+    ring_shape(st, 2 * kNormThreads, slot, &ctas, &a.slots);
+    if (a.T < static_cast<int64_t>(9) * num_sms() * ctas) ring_shape(st, kNormThreads, slot, &ctas, &a.slots);
     const int64_t grid = static_cast<int64_t>(num_sms()) * ctas;
     if (a.T >= 2 * grid) {
       a.wide = ((reinterpret_cast<uintptr_t>(a.sum) | reinterpret_cast<uintptr_t>(a.y)) & 31) == 0;
