@@ -556,7 +556,8 @@ int mgq_router_topk_bwd(const void* logits, int dtype, const int32_t* topk_idx, 
  *           grouped GEMMs take them (K-major); scale_image is not used
  *  scaling  MGQ_MX32_E8M0, MGQ_BLK_1x128_F32 (128x128 weight scales, ld the
  *           contraction; x's and h's scale is s = 448 * (1 / amax), two float32
- *           roundings, the last bit of which can differ from the quantisers'), MGQ_TENSOR_F32 (weight scale s per expert) or
+ *           roundings, the last bit of which can differ from the
+ *           quantisers'), MGQ_TENSOR_F32 (weight scale s per expert) or
  *           MGQ_NV16_UE4M3 (global_scale per expert)
  *  x_scale, h_scale  device float32, MGQ_TENSOR_F32: the scale s of x and of
  *           h; MGQ_NV16_UE4M3: their global scale s_g (calibrated beforehand:
