@@ -98,3 +98,37 @@ def test_decode(recipe):
         _rows_close(out, y, idx.cpu().numpy(), probs.cpu().numpy(), v1, v2, recipe, scales=(xs, hs))
         at += n
     assert mgq.get_error() == mgq.OK
+
+
+def _left(ex, recipe):
+    """(W1, W2 values, x scale, h scale) that the layer's codes and scales stand for (delayed, NVFP4)."""
+    E, H, F = ex.w.E, ex.w.H, ex.w.F
+    if recipe == "nvfp4":
+        sg = ex.nv_sg.cpu().numpy()
+        return (_values(ex.w1q, ex.w1s, recipe, E, 2 * F, H, sg[2:2 + E]),
+                _values(ex.w2q, ex.w2s, recipe, E, H, F, sg[2 + E:2 + 2 * E]), sg[0], sg[1])
+    fs = ex.fwd_scale.clone()
+    return (_values(ex.w1q, fs[2:2 + E], recipe, E, 2 * F, H), _values(ex.w2q, fs[2 + E:2 + 2 * E], recipe, E, H, F),
+            fs[0].item(), fs[1].item())
+
+
+def test_decode_after_update_scaling_on_the_same_weights():
+    """A training step ends with update_scaling(), which sets the scales of the
+    next step's weights; the codes are still those of the step's own."""
+    b, x, r = _block("delayed", T=64, train=None)
+    ex = b.experts
+    b.forward(x, r)
+    b.backward(torch.randn(x.shape, generator=torch.Generator().manual_seed(8)).bfloat16().cuda())
+    v1, v2, _, _ = _left(ex, "delayed")
+    old = ex.fwd_scale.clone()
+    ex.update_scaling()
+    assert not torch.equal(old, ex.fwd_scale)
+    xs, hs = ex.fwd_scale[0].item(), ex.fwd_scale[1].item()
+    for n in (5, 20):
+        out, _ = b.decode(x[:n].contiguous(), r[:n].contiguous())
+        y, idx, probs = b.few
+        _rows_close(out, y, idx.cpu().numpy(), probs.cpu().numpy(), v1, v2, "delayed", scales=(xs, hs))
+    # the many-token path on the same codes (bf16 g, u and h on the way: 2e-2, as for the grouped layer)
+    many = bf16_np(b.forward(x, r)[0])[:20]
+    assert np.linalg.norm(bf16_np(out) - many) <= 2e-2 * np.linalg.norm(many)
+    assert mgq.get_error() == mgq.OK
