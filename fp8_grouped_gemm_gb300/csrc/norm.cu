@@ -488,15 +488,25 @@ void ring_shape(int threads, int all, size_t slot, int* ctas, int* slots) {
   *slots = s < 2 ? 2 : s > kMaxSlots ? kMaxSlots : s;
 }
 
+// Allows the largest ring, once per device and kernel (attr_set: the launcher's):
+// the limit is the function's, shared by all host threads, so a call never sets
+// it to its own ring.
 template <typename K>
-bool allow_smem(K kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
+bool allow_rings(K kern, bool (&attr_set)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < 64 && attr_set[dev]) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingPerSm)) != cudaSuccess)
+    return false;
+  if (dev < 64) attr_set[dev] = true;
+  return true;
 }
 
 template <int SC, int DT, int U>
 int launch_norm_stream(const NormArgs& a, int threads, int grid, size_t smem, cudaStream_t s) {
   auto kern = norm_stream_kernel<SC, DT, U>;
-  if (!allow_smem(kern, smem)) return MGQ_ERR_CUDA;
+  static bool attr_set[64] = {false};
+  if (!allow_rings(kern, attr_set)) return MGQ_ERR_CUDA;
   return launch_after(kern, dim3(grid), threads, smem, 1, s, a) ? MGQ_OK : MGQ_ERR_CUDA;
 }
 
@@ -703,9 +713,9 @@ int launch_bwd(NormBwdArgs a, int threads, int grid, cudaStream_t s) {
   if constexpr (CH < 4) {
     if (2 * a.T > 3 * static_cast<int64_t>(grid)) {
       auto kern = norm_bwd_kernel<CH, true>;
-      const size_t smem = slot * a.slots;
-      if (!allow_smem(kern, smem)) return MGQ_ERR_CUDA;
-      return launch_after(kern, dim3(grid), threads, smem, 1, s, a) ? MGQ_OK : MGQ_ERR_CUDA;
+      static bool attr_set[64] = {false};
+      if (!allow_rings(kern, attr_set)) return MGQ_ERR_CUDA;
+      return launch_after(kern, dim3(grid), threads, slot * a.slots, 1, s, a) ? MGQ_OK : MGQ_ERR_CUDA;
     }
   }
   return launch_after(norm_bwd_kernel<CH, false>, dim3(grid), threads, 0, 1, s, a) ? MGQ_OK : MGQ_ERR_CUDA;

@@ -275,3 +275,34 @@ def test_refusals_of_the_binding():
     refused(mgq.ERR_INVALID_ARG, x=x.cpu())                                 # place
     refused(mgq.ERR_UNSUPPORTED, w=w.half())
     refused(mgq.ERR_INVALID_ARG, y=None)                                    # nothing to write
+
+
+def test_two_threads_with_rows_of_different_length():
+    """Two host threads, streams of their own, one kernel and rings of 128 KB and more beside small ones."""
+    import threading
+    from fp8_grouped_gemm_gb300 import mgq
+    failed = []
+
+    def work(T, H):
+        x, w = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda"), torch.ones(H, device="cuda")
+        y, st = torch.empty_like(x), torch.cuda.Stream()
+        dw, ws = torch.empty(H, device="cuda"), torch.empty(mgq.add_rmsnorm_bwd_workspace_size(T, H), dtype=torch.uint8,
+                                                            device="cuda")
+        rstd = torch.ones(T, device="cuda")
+        torch.cuda.synchronize()
+        start.wait()
+        try:
+            for _ in range(3000):
+                mgq.add_rmsnorm_quantize(x, w, EPS, y=y, stream=st)
+                mgq.add_rmsnorm_bwd(x, x, w, rstd, y, dw, ws, stream=st)
+        except mgq.MGQError as e:
+            failed.append((H, e))
+        st.synchronize()
+
+    start = threading.Barrier(2)
+    threads = [threading.Thread(target=work, args=a) for a in ((5000, 2176), (700, 8192))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
