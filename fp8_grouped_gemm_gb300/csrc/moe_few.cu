@@ -914,7 +914,8 @@ struct Layout {
 Layout layout_of(int T, int k, int E, int64_t H, int64_t F, int kind) {
   Layout l{};
   const int64_t R = static_cast<int64_t>(T) * k, slots = R / kTok + E;
-  l.nmax = (T < kTok ? T + 15 : kTok) / 16 * 16;
+  // (a token may name an expert more than once: up to R rows, not T, of one expert)
+  l.nmax = static_cast<int>((R < kTok ? R + 15 : kTok) / 16 * 16);
   l.grid = num_sms();
   const int64_t per = kind == kNV ? 2 : 1;                      // codes per byte
   auto scales = [&](int64_t K) {

@@ -12,7 +12,9 @@
 //                         x on the way; SwiGLU, h quantised
 //   small_down_kernel     a CTA: 16 rows of W2 of every picked expert, its warps
 //                         split all of their contractions; out
-// All sums run in an order that only the sizes and the routing decide.
+// All sums run in an order that only the sizes and the routing decide. An expert
+// that a token names more than once is one row, with the sum of its
+// probabilities: so an expert has at most as many rows as there are tokens.
 //
 // Bound by latency: the launch, the ids, the first weights, then a warp's units
 // one after another (two loads deep) and the reduction over the warps. Measured:
@@ -129,10 +131,36 @@ struct Weight {
 // ---- routing of at most 64 entries ----------------------------------------------
 
 struct Routing {
-  int idx[64], first[64];
+  int idx[64], first[64];   // idx: -1 out of range, -2 named before by the same token
 };
-// entries of lower experts, earlier entries of its own, all entries of its own, and whether
-// entry i is the first of them (thread i < R; -1 in idx: out of range)
+// Thread i < 64: entry i of the table. A token's entries lie side by side, and
+// the few before i are read together with i's own.
+__device__ __forceinline__ void load_routing(Routing& r, const int32_t* idx, int R, int k, int E) {
+  const int i = threadIdx.x;
+  if (i < 64) {
+    int e = -1;
+    if (i < R) {
+      const int j = i % k;
+      e = __ldg(idx + i);
+      bool again = false;
+#pragma unroll
+      for (int d = 1; d < 8; ++d)
+        if (d <= j) again |= __ldg(idx + i - d) == e;
+      e = e < 0 || e >= E ? -1 : again ? -2 : e;
+    }
+    r.idx[i] = e;
+  }
+}
+// the probability of entry i's expert e: its own, and those of later entries of the token that name e again
+__device__ __forceinline__ float prob_of(const int32_t* idx, const float* probs, int i, int k, int e) {
+  const int left = k - 1 - i % k;
+  float p = __ldg(probs + i);
+#pragma unroll
+  for (int d = 1; d < 8; ++d)
+    if (d <= left && __ldg(idx + i + d) == e) p += __ldg(probs + i + d);
+  return p;
+}
+// rows of lower experts, earlier rows of entry i's own, all rows of its own
 __device__ __forceinline__ void place(const Routing& r, int R, int i, int& before, int& same, int& n) {
   const int e = r.idx[i];
   before = same = n = 0;
@@ -141,12 +169,6 @@ __device__ __forceinline__ void place(const Routing& r, int R, int i, int& befor
     before += f >= 0 && f < e;
     n += f == e;
     same += f == e && j < i;
-  }
-}
-__device__ __forceinline__ void load_routing(Routing& r, const int32_t* idx, int R, int E) {
-  if (threadIdx.x < 64) {
-    const int e = static_cast<int>(threadIdx.x) < R ? __ldg(idx + threadIdx.x) : -1;
-    r.idx[threadIdx.x] = e >= 0 && e < E ? e : -1;
   }
 }
 
@@ -420,13 +442,13 @@ __global__ void __launch_bounds__(32 * GW, 16 / GW) small_gateup_kernel(SmallArg
   grid_wait();
   grid_launch();
   const int R = a.T * a.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  load_routing(rt, a.idx, R, a.E);
+  load_routing(rt, a.idx, R, a.k, a.E);
   if (threadIdx.x == 0) sel[0] = -1, sel[2] = 0;
   __syncthreads();
   int before = 0, same = 0, n = 0;
   const bool in = static_cast<int>(threadIdx.x) < R;
   const bool mine = in && rt.idx[threadIdx.x] >= 0;
-  if (in && !mine && blockIdx.x == 0 && blockIdx.y == 0) report(a.err, MGQ_ERR_DEVICE_INDEX);
+  if (in && rt.idx[threadIdx.x] == -1 && blockIdx.x == 0 && blockIdx.y == 0) report(a.err, MGQ_ERR_DEVICE_INDEX);
   if (mine) place(rt, R, threadIdx.x, before, same, n);
   if (threadIdx.x < 64) rt.first[threadIdx.x] = mine && same == 0;
   __syncthreads();
@@ -436,10 +458,10 @@ __global__ void __launch_bounds__(32 * GW, 16 / GW) small_gateup_kernel(SmallArg
     if (rank == static_cast<int>(blockIdx.y)) sel[0] = rt.idx[threadIdx.x], sel[1] = before, sel[2] = n;
   }
   __syncthreads();
-  n = min(sel[2], 8);
+  n = sel[2];                              // (at most T: eight)
   if (n == 0) return;                      // fewer experts picked than the grid allows for
   const int e = sel[0], row0 = sel[1];
-  if (mine && rt.idx[threadIdx.x] == e && same < 8) s_tok[same] = threadIdx.x / a.k;
+  if (mine && rt.idx[threadIdx.x] == e) s_tok[same] = threadIdx.x / a.k;
   __syncthreads();
   const int64_t f0 = static_cast<int64_t>(blockIdx.x) * FR, wrow = static_cast<int64_t>(e) * 2 * a.F + f0;
   const int units = a.H / (KIND == kNV ? 256 : 128);
@@ -546,7 +568,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
   __shared__ float part[kWarps][8][17];
   grid_launch();
   const int R = a.T * a.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  load_routing(rt, a.idx, R, a.E);
+  load_routing(rt, a.idx, R, a.k, a.E);
   for (int i = threadIdx.x; i < kWarps * 8 * 17; i += kSmallThreads) (&part[0][0][0])[i] = 0.0f;
   if (threadIdx.x == 0) s_na = 0;
   __syncthreads();
@@ -555,7 +577,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
   if (mine) {
     place(rt, R, threadIdx.x, before, same, n);
     s_tok[before + same] = threadIdx.x / a.k;
-    s_p[before + same] = __ldg(a.probs + threadIdx.x);
+    s_p[before + same] = prob_of(a.idx, a.probs, threadIdx.x, a.k, rt.idx[threadIdx.x]);
   }
   if (threadIdx.x < 64) rt.first[threadIdx.x] = mine && same == 0;
   __syncthreads();
@@ -576,7 +598,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
   const Operand x{a.hq, a.hs};
   bool waited = false;
   while (u < u1) {
-    const int e = l_e[at], row0 = l_row[at], n = min(l_n[at], 8);
+    const int e = l_e[at], row0 = l_row[at], n = l_n[at];
     const int64_t wrow = static_cast<int64_t>(e) * a.H + h0 + g;
     const int end = min(u1, (at + 1) * units) - at * units;
     int k0 = u - at * units;

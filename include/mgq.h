@@ -549,9 +549,9 @@ int mgq_router_topk_bwd(const void* logits, int dtype, const int32_t* topk_idx, 
  * Q is the recipe's row-wise quantisation (e4m3; NVFP4 e2m1) of the float32
  * values; g, u, h and y stay in float32, out is rounded to bf16 once.
  *  x_bf16   device [T, H] bf16
- *  topk_idx device [T, k] int32, distinct experts per token (an id outside
- *           [0, E) contributes nothing and is reported as
- *           MGQ_ERR_DEVICE_INDEX); probs device [T, k] float32
+ *  topk_idx device [T, k] int32 (an id outside [0, E) contributes nothing and
+ *           is reported as MGQ_ERR_DEVICE_INDEX; an expert that a token names
+ *           again counts again); probs device [T, k] float32
  *  W1       [E, 2F, H] gate rows then up rows, W2 [E, H, F]: operands as the
  *           grouped GEMMs take them (K-major); scale_image is not used
  *  scaling  MGQ_MX32_E8M0, MGQ_BLK_1x128_F32 (128x128 weight scales, ld the

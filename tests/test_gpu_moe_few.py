@@ -276,3 +276,30 @@ def test_refusals_of_the_binding():
         assert e.value.status == mgq.ERR_INVALID_ARG, bad.keys()
     empty = dict(x=x[:0], out=x[:0], topk_idx=a["topk_idx"][:0], probs=a["probs"][:0])
     mgq.moe_few_forward(**{**a, **empty})
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("T,E,k,H,F", [(8, 8, 8, 256, 256), (3, 4, 2, 512, 512), (1, 16, 8, 256, 256), (16, 8, 8, 256, 512),
+                                       (9, 8, 4, 512, 256), (40, 3, 3, 256, 256), (4, 8, 8, 1024, 1280)])
+@pytest.mark.parametrize("rows", ["all", "some"])
+def test_an_expert_named_twice_by_a_token(recipe, T, E, k, H, F, rows):
+    """Padding of a batch names one expert k times (ids all 0): each mention
+    counts with its probability, and nothing is written behind the workspace."""
+    from fp8_grouped_gemm_gb300 import mgq
+    rng = np.random.default_rng(T + k)
+    x = torch.from_numpy(rng.normal(size=(T, H))).bfloat16()
+    idx, p = _routing(T, E, k, rng)
+    if rows == "all":
+        idx[:] = 0
+    else:
+        idx[::2, 1] = idx[::2, 0]
+        idx[T // 2] = E - 1
+    t1, W1, v1 = _weight(E, 2 * F, H, recipe, rng)
+    t2, W2, v2 = _weight(E, H, F, recipe, rng)
+    n, guard = mgq.moe_few_workspace_size(T, k, E, H, F, _scaling(recipe)), 1 << 20
+    ws = torch.full((n + guard,), 0xA5, dtype=torch.uint8, device="cuda")
+    args = (x.cuda(), torch.from_numpy(idx).cuda(), torch.from_numpy(p).cuda(), W1, W2, recipe, E, F)
+    out = _call(*args, ws=ws[:n])
+    assert torch.all(ws[n:] == 0xA5)
+    _rows_close(out, x, idx, p, v1, v2, recipe)
+    assert torch.equal(out, _call(*args, ws=ws[:n]))
