@@ -1661,11 +1661,15 @@ std::atomic<int64_t> g_gemm_opt[MGQ_GEMM_OPT_COUNT];
 
 int64_t gemm_opt(int o) { return g_gemm_opt[o].load(std::memory_order_relaxed); }
 
+}  // namespace
+
 void debug_knobs(int* stall, uint64_t* wait_ns) {
   *stall = gemm_opt(MGQ_GEMM_OPT_DEBUG_STALL) ? 1 : 0;
   const int64_t ms = gemm_opt(MGQ_GEMM_OPT_WAIT_MS);
   *wait_ns = ms > 0 ? (uint64_t)ms * 1000000ull : kWaitNs;
 }
+
+namespace {
 
 bool direct_store_forced() { return gemm_opt(MGQ_GEMM_OPT_DIRECT_STORE) != 0; }
 

@@ -28,6 +28,10 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
+// The failure-detection options (mgq_set_gemm_option): whether producers issue
+// no copies, and the limit of a pipeline wait (gemm.cu).
+void debug_knobs(int* stall, uint64_t* wait_ns);
+
 // Number of SMs of the current device (cached).
 int num_sms();
 

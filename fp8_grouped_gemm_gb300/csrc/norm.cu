@@ -76,17 +76,21 @@ __device__ __forceinline__ void mx_scale(uint32_t amax_bits, int emax, int rceil
 }
 
 // Sum over the CTA; `slot` alternates between two shared arrays from one call
-// to the next, so that one barrier a call is enough.
-__device__ __forceinline__ float block_sum(float v, float (*red)[32], int slot) {
+// to the next, so that one barrier a call is enough. ANY: `any` becomes true in
+// every thread if it is in one.
+template <bool ANY>
+__device__ __forceinline__ float block_sum(float v, float (*red)[32], int slot, bool& any) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   if (nw == 1) {
+    if (ANY) any = __any_sync(0xFFFFFFFFu, any);
     __syncwarp();
     return v;
   }
   if ((threadIdx.x & 31) == 0) red[slot][warp] = v;
-  __syncthreads();
+  if (ANY) any = __syncthreads_or(any);
+  else __syncthreads();
   float t = (threadIdx.x & 31) < nw ? red[slot][threadIdx.x & 31] : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
@@ -94,10 +98,19 @@ __device__ __forceinline__ float block_sum(float v, float (*red)[32], int slot) 
 }
 
 constexpr int kMaxSlots = 8;
-constexpr uint64_t kWaitNs = 2000000000ull;   // limit of a wait for a row's copies
+
+struct RingArgs {
+  int slots;
+  int stall;               // failure-detection test: no row is requested
+  uint64_t wait_ns;        // limit of a wait for a row's copies
+  int* err;
+};
 
 // A ring of row slots filled by bulk copies: NS source rows side by side per
 // slot. Thread 0 requests; the barrier that every reduction passes frees a slot.
+// A wait that runs out in some threads must not leave the others at a barrier
+// or a shuffle: all of them still take part in the row's reduction, whose barrier
+// tells every thread whether one gave up.
 template <int NS>
 struct RowRing {
   uint64_t* full;
@@ -107,16 +120,16 @@ struct RowRing {
   uint32_t ph;
   int64_t next;            // row to request next
 
-  __device__ __forceinline__ void init(uint8_t* base, uint64_t* bars, int n, uint32_t bytes) {
+  __device__ __forceinline__ void init(uint8_t* base, uint64_t* bars, const RingArgs& a, uint32_t bytes) {
     full = bars;
     mem = base;
     row_bytes = bytes;
-    slots = n;
+    slots = a.slots;
     st = ask = 0;
     ph = 0;
-    next = blockIdx.x;
+    next = a.stall ? INT64_MAX : blockIdx.x;
     if (threadIdx.x == 0) {
-      for (int i = 0; i < n; ++i) ptx::mbar_init(&full[i], 1);
+      for (int i = 0; i < slots; ++i) ptx::mbar_init(&full[i], 1);
       ptx::fence_mbar_init();
     }
     __syncthreads();
@@ -136,14 +149,14 @@ struct RowRing {
     next += gridDim.x;
     if (++ask == slots) ask = 0;
   }
-  __device__ __forceinline__ bool wait() { return ptx::mbar_wait(&full[st], ph, kWaitNs); }
+  __device__ __forceinline__ bool wait(uint64_t limit_ns) { return ptx::mbar_wait(&full[st], ph, limit_ns); }
   __device__ __forceinline__ const uint4* row(int i) const {
     return reinterpret_cast<const uint4*>(mem + (static_cast<size_t>(st) * NS + i) * row_bytes);
   }
   // after a wait that ran out: give the copies in flight a last, short chance
-  __device__ __forceinline__ void drain() {
+  __device__ __forceinline__ void drain(uint64_t limit_ns) {
     for (int i = 0; i < slots && threadIdx.x == 0; ++i)
-      ptx::mbar_wait(&full[(st + i) % slots], ph ^ (st + i >= slots ? 1u : 0u), kWaitNs / 100);
+      ptx::mbar_wait(&full[(st + i) % slots], ph ^ (st + i >= slots ? 1u : 0u), limit_ns / 100);
   }
   __device__ __forceinline__ void advance() {
     if (++st == slots) st = 0, ph ^= 1;
@@ -166,9 +179,8 @@ struct NormArgs {
   float* amax;           // per-tensor amax, or null
   int rceil;
   float* rstd;           // or null
-  int slots;             // streamed: ring slots
+  RingArgs ring;         // streamed
   int wide;              // streamed: 32-byte aligned bf16 outputs
-  int* err;
 };
 
 // rstd = 1 / sqrt(ss / H + eps) as a pair rstd + lo, so that y = s (rstd + lo) w
@@ -274,7 +286,8 @@ __global__ void __launch_bounds__(512, CH < 4 ? 2 : 1) norm_kernel(NormArgs a) {
         ss += square_sum<8>(v[i]);
       }
     }
-    ss = block_sum(ss, red, slot);
+    bool none = false;
+    ss = block_sum<false>(ss, red, slot, none);
     float lo;
     const float rstd = root_pair(ss, h, inv_h, a.eps, lo);
     if (a.rstd && threadIdx.x == 0) a.rstd[r] = rstd;
@@ -362,9 +375,9 @@ __global__ void __launch_bounds__(512) norm_stream_kernel(NormArgs a) {
   if (SC == MGQ_TENSOR_F32) ts = __ldg(a.ts);
   RowRing<2> ring;
   const uint16_t* const src[2] = {a.x, a.res};
-  ring.init(ring_mem, bars, a.slots, a.H * 2u);
+  ring.init(ring_mem, bars, a.ring, a.H * 2u);
   if (threadIdx.x == 0)
-    for (int i = 0; i < a.slots; ++i) ring.request(src, a.T);
+    for (int i = 0; i < a.ring.slots; ++i) ring.request(src, a.T);
   float w[U][16];
 #pragma unroll
   for (int i = 0; i < U; ++i) {
@@ -379,11 +392,7 @@ __global__ void __launch_bounds__(512) norm_stream_kernel(NormArgs a) {
   uint32_t amax = 0;
   int slot = 0;
   for (int64_t r = blockIdx.x; r < a.T; r += gridDim.x, slot ^= 1) {
-    if (!ring.wait()) {
-      report(a.err, MGQ_ERR_TIMEOUT);
-      ring.drain();
-      break;
-    }
+    const bool here = ring.wait(a.ring.wait_ns);
     const uint4 *xr = ring.row(0), *rr = ring.row(1);
     const int64_t base = r * a.H;
     float v[U][16];
@@ -406,7 +415,11 @@ __global__ void __launch_bounds__(512) norm_stream_kernel(NormArgs a) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     if (lane == 0) red[slot][threadIdx.x >> 5] = ss;
-    __syncthreads();
+    if (__syncthreads_or(!here)) {
+      report(a.ring.err, MGQ_ERR_TIMEOUT);
+      ring.drain(a.ring.wait_ns);
+      break;
+    }
     ring.advance();                      // every thread has read the slot
     if (threadIdx.x == 0) ring.request(src, a.T);
     const float4* part = reinterpret_cast<const float4*>(red[slot]);
@@ -523,13 +536,13 @@ int launch_norm(NormArgs a, cudaStream_t s) {
     const int u = a.H > 1024 ? 2 : 1, st = ((a.H / 16 + u - 1) / u + 31) / 32 * 32;
     const size_t slot = static_cast<size_t>(a.H) * 4;
     int ctas;
-    ring_shape(st, 2 * kNormThreads, slot, &ctas, &a.slots);
-    if (a.T < static_cast<int64_t>(9) * num_sms() * ctas) ring_shape(st, kNormThreads, slot, &ctas, &a.slots);
+    ring_shape(st, 2 * kNormThreads, slot, &ctas, &a.ring.slots);
+    if (a.T < static_cast<int64_t>(9) * num_sms() * ctas) ring_shape(st, kNormThreads, slot, &ctas, &a.ring.slots);
     const int64_t grid = static_cast<int64_t>(num_sms()) * ctas;
     if (a.T >= 2 * grid) {
       a.wide = ((reinterpret_cast<uintptr_t>(a.sum) | reinterpret_cast<uintptr_t>(a.y)) & 31) == 0;
-      return u == 2 ? launch_norm_stream<SC, DT, 2>(a, st, static_cast<int>(grid), slot * a.slots, s)
-                    : launch_norm_stream<SC, DT, 1>(a, st, static_cast<int>(grid), slot * a.slots, s);
+      return u == 2 ? launch_norm_stream<SC, DT, 2>(a, st, static_cast<int>(grid), slot * a.ring.slots, s)
+                    : launch_norm_stream<SC, DT, 1>(a, st, static_cast<int>(grid), slot * a.ring.slots, s);
     }
   }
   int threads, ch;
@@ -551,8 +564,7 @@ struct NormBwdArgs {
   int H;
   uint16_t* dx;
   float* part;            // [grid, H]
-  int slots;
-  int* err;
+  RingArgs ring;
 };
 
 template <int CH, bool STREAM>
@@ -567,9 +579,9 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormBwdArgs a) {
   RowRing<3> ring;
   const uint16_t* const src[3] = {a.dy, a.s, a.dsum};
   if (STREAM) {
-    ring.init(ring_mem, bars, a.slots, a.H * 2u);
+    ring.init(ring_mem, bars, a.ring, a.H * 2u);
     if (threadIdx.x == 0)
-      for (int i = 0; i < a.slots; ++i) ring.request(src, a.T);
+      for (int i = 0; i < a.ring.slots; ++i) ring.request(src, a.T);
   }
   float dw[CH][8], w[CH][8];
 #pragma unroll
@@ -581,11 +593,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormBwdArgs a) {
   int slot = 0;
   float rstd_next = blockIdx.x < a.T ? __ldg(a.rstd + blockIdx.x) : 0.0f;
   for (int64_t r = blockIdx.x; r < a.T; r += gridDim.x, slot ^= 1) {
-    if (STREAM && !ring.wait()) {
-      report(a.err, MGQ_ERR_TIMEOUT);
-      ring.drain();
-      break;
-    }
+    const bool here = !STREAM || ring.wait(a.ring.wait_ns);
     const float rstd = rstd_next;
     if (r + gridDim.x < a.T) rstd_next = __ldg(a.rstd + r + gridDim.x);
     const uint4* yr = STREAM ? ring.row(0) : reinterpret_cast<const uint4*>(a.dy + r * a.H);
@@ -610,8 +618,14 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormBwdArgs a) {
         }
       }
     }
-    c1 = block_sum(c1, red, slot) * inv_h;
+    bool lost = !here;
+    c1 = block_sum<STREAM>(c1, red, slot, lost) * inv_h;
     if (STREAM) {
+      if (lost) {
+        report(a.ring.err, MGQ_ERR_TIMEOUT);
+        ring.drain(a.ring.wait_ns);
+        break;
+      }
       ring.advance();
       if (threadIdx.x == 0) ring.request(src, a.T);
     }
@@ -706,7 +720,7 @@ template <int CH>
 int launch_bwd(NormBwdArgs a, int threads, int grid, cudaStream_t s) {
   const size_t slot = static_cast<size_t>(a.H) * 6;
   int ctas;
-  ring_shape(threads, bwd_threads(threads, CH), slot, &ctas, &a.slots);
+  ring_shape(threads, bwd_threads(threads, CH), slot, &ctas, &a.ring.slots);
   // Streamed from 1.5 rows a CTA on (direct / streamed, us: 600 rows of 4096 9.9 /
   // 8.9, 16384 of 4096 123 / 80; 600 of 2048, 1.3 a CTA, 6.3 / 6.5). Four chunks a
   // thread beside the ring do not fit the registers.
@@ -715,10 +729,15 @@ int launch_bwd(NormBwdArgs a, int threads, int grid, cudaStream_t s) {
       auto kern = norm_bwd_kernel<CH, true>;
       static bool attr_set[64] = {false};
       if (!allow_rings(kern, attr_set)) return MGQ_ERR_CUDA;
-      return launch_after(kern, dim3(grid), threads, slot * a.slots, 1, s, a) ? MGQ_OK : MGQ_ERR_CUDA;
+      return launch_after(kern, dim3(grid), threads, slot * a.ring.slots, 1, s, a) ? MGQ_OK : MGQ_ERR_CUDA;
     }
   }
   return launch_after(norm_bwd_kernel<CH, false>, dim3(grid), threads, 0, 1, s, a) ? MGQ_OK : MGQ_ERR_CUDA;
+}
+
+void ring_limits(RingArgs& a) {
+  debug_knobs(&a.stall, &a.wait_ns);
+  a.err = error_word();
 }
 
 bool norm_sizes_ok(int64_t T, int64_t H) {
@@ -763,7 +782,7 @@ extern "C" int mgq_add_rmsnorm_quantize(const void* x_bf16, const void* residual
   a.sum = static_cast<uint16_t*>(sum_bf16);
   a.y = static_cast<uint16_t*>(y_bf16);
   a.rstd = rstd;
-  a.err = error_word();
+  ring_limits(a.ring);
   cudaStream_t s = as_stream(stream);
   if (!q) return launch_norm<kNoQuant, MGQ_E4M3>(a, s);
   {
@@ -810,7 +829,7 @@ extern "C" int mgq_add_rmsnorm_bwd(const void* dy_bf16, const void* s_bf16, cons
   a.H = static_cast<int>(H);
   a.dx = static_cast<uint16_t*>(dx_bf16);
   a.part = static_cast<float*>(workspace);
-  a.err = error_word();
+  ring_limits(a.ring);
   const int grid = bwd_grid(T, H);
   if (T > 0) {
     int threads, ch;

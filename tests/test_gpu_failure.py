@@ -64,3 +64,52 @@ def test_gemm_pipeline_timeout_is_reported_and_context_survives():
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert r.returncode == 0, r.stdout + r.stderr
     assert "OK" in r.stdout
+
+
+NORM_SCRIPT = textwrap.dedent("""
+    import sys, time
+    import torch
+    sys.path.insert(0, {root!r})
+    from fp8_grouped_gemm_gb300 import mgq
+    dev = torch.device("cuda:0")
+    g = torch.Generator().manual_seed(1)
+    # one warp a row, a few, the longest rows of the backward's ring
+    for T, H in ((60000, 256), (6000, 2048), (1500, 8192)):
+        x, dy = (torch.randn(T, H, generator=g).bfloat16().to(dev) for _ in range(2))
+        w, rstd = torch.ones(H, device=dev), torch.ones(T, device=dev)
+        ws = torch.empty(mgq.add_rmsnorm_bwd_workspace_size(T, H), dtype=torch.uint8, device=dev)
+        def run():
+            y, dx = (torch.full((T, H), 7.0, dtype=torch.bfloat16, device=dev) for _ in range(2))
+            codes = torch.full((T, H), 0xAB, dtype=torch.uint8, device=dev)
+            sc = torch.empty(mgq.mx_scale_bytes(T, H), dtype=torch.uint8, device=dev)
+            dw = torch.empty(H, device=dev)
+            status = []
+            t0 = time.time()
+            mgq.add_rmsnorm_quantize(x, w, 1e-5, mgq.qdesc(mgq.E4M3, mgq.MX32_E8M0, codes, sc), residual=dy, y=y)
+            torch.cuda.synchronize()
+            status.append(mgq.get_error())
+            mgq.add_rmsnorm_bwd(dy, x, w, rstd, dx, dw, ws, dsum=dy)
+            torch.cuda.synchronize()
+            status.append(mgq.get_error())
+            return y, dx, codes, dw, status, time.time() - t0
+        ref = run()
+        assert ref[4] == [mgq.OK, mgq.OK] and not bool(torch.any(torch.all(ref[0] == 7.0, 1)))
+        mgq.set_gemm_option(mgq.GEMM_OPT_DEBUG_STALL, 1)
+        mgq.set_gemm_option(mgq.GEMM_OPT_WAIT_MS, 50)
+        y, dx, codes, dw, status, dt = run()
+        assert status == [mgq.ERR_TIMEOUT, mgq.ERR_TIMEOUT], status
+        assert bool(torch.all(y == 7.0)) and bool(torch.all(dx == 7.0)) and bool(torch.all(codes == 0xAB))
+        assert dt < 10.0, dt
+        mgq.set_gemm_option(mgq.GEMM_OPT_DEBUG_STALL, 0)
+        mgq.set_gemm_option(mgq.GEMM_OPT_WAIT_MS, 0)
+        again = run()
+        assert again[4] == [mgq.OK, mgq.OK] and all(torch.equal(a, b) for a, b in zip(ref[:4], again[:4]))
+    print("OK")
+""")
+
+
+def test_norm_ring_timeout_is_reported_and_context_survives():
+    r = subprocess.run([sys.executable, "-c", NORM_SCRIPT.format(root=ROOT)], capture_output=True, text=True, timeout=300,
+                       cwd=ROOT)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "OK" in r.stdout
