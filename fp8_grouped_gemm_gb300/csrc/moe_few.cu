@@ -44,7 +44,7 @@ constexpr int kEpiWarps = 8;              // two groups of four: one thread a we
 constexpr int kThreads = 64 + 32 * kEpiWarps;   // warp 0 TMA, warp 1 MMA, the others the epilogue
 constexpr uint32_t kATile = 128 * 128;    // bytes of 128 weight rows of one stage
 constexpr int kMaxStages = 6;
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kBars = 26;                 // 8-byte words of the barriers and flags
 
 __host__ __device__ constexpr uint32_t sf_chunks(int kind) { return kind == kMX ? 1 : kind == kNV ? 4 : 0; }
 // scale bytes of one stage: two weight halves and the tokens (BLK: 64 float32 of the tokens)
@@ -226,6 +226,8 @@ struct FewArgs {
   float* y;
   int H;
   int* err;
+  int stall;             // failure-detection test: no tokens are loaded until the waits have run out
+  uint64_t wait_ns;      // limit of every mbarrier wait
 };
 
 // The line of units, in order: active expert, tile along M, token block of the
@@ -454,13 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = bars + kMaxStages;
   uint64_t* t_full = bars + 2 * kMaxStages;
   uint64_t* t_empty = t_full + 2;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(t_empty + 2);
+  uint64_t* mma_done = t_empty + 2;                    // after a wait that ran out: no MMA in flight
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   volatile int* s_last = reinterpret_cast<volatile int*>(s_tmem + 2);
   int* s_at = reinterpret_cast<int*>(s_tmem + 4);      // [6] start of the walk, rows of the largest group
   Split* s_split = reinterpret_cast<Split*>(s_tmem + 10);
-  uint32_t (*smax)[4][16] = reinterpret_cast<uint32_t (*)[4][16]>(bars + 24);   // [2][4][16]
-  int4* s_list = reinterpret_cast<int4*>(bars + 24 + 64);
+  uint32_t (*smax)[4][16] = reinterpret_cast<uint32_t (*)[4][16]>(bars + kBars);   // [2][4][16]
+  int4* s_list = reinterpret_cast<int4*>(bars + kBars + 64);
   int* s_cnt = reinterpret_cast<int*>(s_list + p.list);
 
   const int warp = threadIdx.x >> 5;
@@ -476,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&t_full[a], 1);
       ptx::mbar_init(&t_empty[a], kEpiWarps);
     }
+    ptx::mbar_init(mma_done, 1);
     *s_abort = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmW);
@@ -594,13 +598,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (Walk v = s; v.any() && early < STG; v.next())
         for (int kb = v.kb0; kb < v.kb1 && early < STG; ++kb, ++early) load_w(v, kb, early);
       grid_wait();
+      if (p.stall)
+        for (const uint64_t t0 = ptx::globaltimer_ns(); !*s_abort && ptx::globaltimer_ns() - t0 < 4 * p.wait_ns;) {
+        }
       int it = 0, st = 0;
       uint32_t ph = 1;                    // (a first pass over the ring waits for nothing)
       for (; s.any(); s.next()) {
         for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
           if (it >= early) {
             if (*s_abort) break;
-            if (!ptx::mbar_wait(&empty[st], ph, kWaitNs)) {
+            if (!ptx::mbar_wait(&empty[st], ph, p.wait_ns)) {
               report(p.err, MGQ_ERR_TIMEOUT);
               *s_abort = 1;
               break;
@@ -610,12 +617,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_x(s, kb, st);
           if (++st == STG) st = 0, ph ^= 1;
         }
-        if (*s_abort) break;
+        if (*s_abort && it >= early) break;
       }
-      // given up: no copy of this CTA may land after it has left
+      // given up: no copy of this CTA may land after it has left (the stages
+      // requested early got their tokens too: their barriers can complete)
       if (*s_abort)
         for (int i = it > STG ? it - STG : 0; i < it; ++i)
-          ptx::mbar_wait(&full[i % STG], (i / STG) & 1, kWaitNs / 100);
+          ptx::mbar_wait(&full[i % STG], (i / STG) & 1, p.wait_ns / 100);
     }
   } else if (warp == 1) {
     if (elect_one()) {
@@ -631,9 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kb = s.kb0; kb < s.kb1; ++kb) {
           if (KIND == kBLK || kb == s.kb0) {
             a = tc & 1;
-            ok = !*s_abort && ptx::mbar_wait(&t_empty[a], ((tc >> 1) & 1) ^ 1, kWaitNs);
+            ok = !*s_abort && ptx::mbar_wait(&t_empty[a], ((tc >> 1) & 1) ^ 1, p.wait_ns);
           }
-          ok = ok && !*s_abort && ptx::mbar_wait(&full[st], ph, kWaitNs);
+          ok = ok && !*s_abort && ptx::mbar_wait(&full[st], ph, p.wait_ns);
           if (!ok) {
             report(p.err, MGQ_ERR_TIMEOUT);
             *s_abort = 1;
@@ -674,6 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (++st == STG) st = 0, ph ^= 1;
         }
+      }
+      if (*s_abort) {
+        ptx::mma_commit(mma_done);
+        ptx::mbar_wait(mma_done, 0, p.wait_ns / 100);
       }
     }
   } else {
@@ -725,8 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float w0 = __shfl_sync(0xFFFFFFFFu, w0v, (kb - s.kb0) & 31);
           const float w1 = __shfl_sync(0xFFFFFFFFu, w1v, (kb - s.kb0) & 31);
-          alive = __all_sync(0xFFFFFFFFu, !*s_abort && ptx::mbar_wait(&full[st], ph, kWaitNs) &&
-                                              ptx::mbar_wait(&t_full[a], (tc >> 1) & 1, kWaitNs));
+          alive = __all_sync(0xFFFFFFFFu, !*s_abort && ptx::mbar_wait(&full[st], ph, p.wait_ns) &&
+                                              ptx::mbar_wait(&t_full[a], (tc >> 1) & 1, p.wait_ns));
           if (!alive) break;
           ptx::tc_fence_after();
           const float4* fx = reinterpret_cast<const float4*>(sSF + st * SF);
@@ -790,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         const uint32_t a = tc & 1;
-        alive = epi_all(!*s_abort && ptx::mbar_wait(&t_full[a], (tc >> 1) & 1, kWaitNs));
+        alive = epi_all(!*s_abort && ptx::mbar_wait(&t_full[a], (tc >> 1) & 1, p.wait_ns));
         ++tc;
         if (alive) {
           ptx::tc_fence_after();
@@ -955,7 +967,7 @@ int launch_gemm(const CUtensorMap& tw, const CUtensorMap& tx, FewArgs p, int gri
   }
   // what is not a stage: alignment, barriers and flags, block maxima, the
   // list of active experts, the counts
-  const size_t small = 24 * 8 + 128 * 4 + static_cast<size_t>(p.list) * 16 + static_cast<size_t>(p.E) * 4;
+  const size_t small = kBars * 8 + 128 * 4 + static_cast<size_t>(p.list) * 16 + static_cast<size_t>(p.E) * 4;
   p.stage_mem = static_cast<uint32_t>((kSmemMax - 1024 - small) / 1024 * 1024);
   return launch_after(kern, dim3(grid), kThreads, 1024 + p.stage_mem + small, 1, s, tw, tx, p) ? MGQ_OK : MGQ_ERR_CUDA;
 }
@@ -1001,6 +1013,7 @@ int few_forward(const void* x, int T, int64_t H, int64_t F, const int32_t* idx, 
   a.list = E < R ? E : R;
   a.inv_ctas = ((uint64_t(1) << 40) + l.grid - 1) / l.grid;
   a.err = err;
+  debug_knobs(&a.stall, &a.wait_ns);
   a.hq = ws + l.hq;
   a.hs = ws + l.hs;
   a.h_scale = h_scale;

@@ -366,7 +366,8 @@ int mgq_nv_scale_image(const void* scale, int64_t rows, int64_t ld, void* image,
  *                             producer issue no loads, so the pipeline waits
  *                             run out and the call reports MGQ_ERR_TIMEOUT
  *                             through mgq_get_error with nothing stored (the
- *                             norm with many rows: no row stored)
+ *                             norm with many rows: no row stored; the layer
+ *                             for a few tokens: its result is undefined)
  *  MGQ_GEMM_OPT_WAIT_MS       limit of every pipeline wait in ms (0: 2000;
  *                             at most 600000)
  * Values outside {0, 1} (WAIT_MS: outside [0, 600000]) or an unknown option

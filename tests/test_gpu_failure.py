@@ -113,3 +113,48 @@ def test_norm_ring_timeout_is_reported_and_context_survives():
                        cwd=ROOT)
     assert r.returncode == 0, r.stdout + r.stderr
     assert "OK" in r.stdout
+
+
+FEW_SCRIPT = textwrap.dedent("""
+    import sys, time
+    import numpy as np, torch
+    sys.path.insert(0, {root!r})
+    from fp8_grouped_gemm_gb300 import mgq
+    from tests.test_gpu_moe_few import RECIPES, XS, HS, _routing, _scaling, _weight
+    rng = np.random.default_rng(3)
+    # more than eight tokens: the form with a ring; several tiles a CTA, and fewer tiles than CTAs
+    for T, E, k, H, F in ((20, 8, 2, 512, 512), (12, 64, 4, 256, 2048)):
+        for recipe in RECIPES:
+            x = torch.from_numpy(rng.normal(size=(T, H))).bfloat16().cuda()
+            idx, p = (torch.from_numpy(a).cuda() for a in _routing(T, E, k, rng))
+            t1, W1, _ = _weight(E, 2 * F, H, recipe, rng)
+            t2, W2, _ = _weight(E, H, F, recipe, rng)
+            ws = torch.zeros(mgq.moe_few_workspace_size(T, k, E, H, F, _scaling(recipe)), dtype=torch.uint8, device="cuda")
+            sc = lambda d: torch.full((1,), d[recipe], device="cuda") if recipe in d else None
+            xs, hs = sc(XS), sc(HS)
+            def run():
+                out = torch.empty_like(x)
+                t0 = time.time()
+                mgq.moe_few_forward(x, idx, p, W1, W2, _scaling(recipe), E, F, out, ws, xs, hs)
+                torch.cuda.synchronize()
+                return out, mgq.get_error(), time.time() - t0
+            ref, status, _ = run()
+            assert status == mgq.OK
+            mgq.set_gemm_option(mgq.GEMM_OPT_DEBUG_STALL, 1)
+            mgq.set_gemm_option(mgq.GEMM_OPT_WAIT_MS, 20)
+            _, status, dt = run()
+            assert status == mgq.ERR_TIMEOUT, (recipe, status)
+            assert dt < 10.0, dt
+            mgq.set_gemm_option(mgq.GEMM_OPT_DEBUG_STALL, 0)
+            mgq.set_gemm_option(mgq.GEMM_OPT_WAIT_MS, 0)
+            out, status, _ = run()
+            assert status == mgq.OK and torch.equal(out, ref), recipe
+    print("OK")
+""")
+
+
+def test_few_token_pipeline_timeout_is_reported_and_context_survives():
+    r = subprocess.run([sys.executable, "-c", FEW_SCRIPT.format(root=ROOT)], capture_output=True, text=True, timeout=300,
+                       cwd=ROOT)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "OK" in r.stdout
