@@ -133,32 +133,33 @@ struct Weight {
 struct Routing {
   int idx[64], first[64];   // idx: -1 out of range, -2 named before by the same token
 };
-// Thread i < 64: entry i of the table. A token's entries lie side by side, and
-// the few before i are read together with i's own.
-__device__ __forceinline__ void load_routing(Routing& r, const int32_t* idx, int R, int k, int E) {
-  const int i = threadIdx.x;
-  if (i < 64) {
-    int e = -1;
-    if (i < R) {
-      const int j = i % k;
-      e = __ldg(idx + i);
-      bool again = false;
+// The ids, and (PROBS) the probability of each: its own and those of the token's
+// later mentions of the expert. Eight lanes take a token's entries, so that
+// mentions meet by shuffles.
+template <bool PROBS>
+__device__ __forceinline__ void load_routing(Routing& r, const int32_t* idx, int T, int k, int E, const float* probs,
+                                             float* prob) {
+  if (threadIdx.x >= 64) return;
+  const int t = threadIdx.x >> 3, j = threadIdx.x & 7, i = t * k + j;
+  const bool live = t < T && j < k;
+  const int e = live ? __ldg(idx + i) : -1;
+  float p = PROBS && live ? __ldg(probs + i) : 0.0f;
+  const float own = p;
+  bool again = false;
 #pragma unroll
-      for (int d = 1; d < 8; ++d)
-        if (d <= j) again |= __ldg(idx + i - d) == e;
-      e = e < 0 || e >= E ? -1 : again ? -2 : e;
+  for (int d = 1; d < 8; ++d) {
+    const int f = __shfl_up_sync(0xFFFFFFFFu, e, d, 8);
+    again |= d <= j && f == e;
+    if (PROBS) {
+      const int g = __shfl_down_sync(0xFFFFFFFFu, e, d, 8);
+      const float q = __shfl_down_sync(0xFFFFFFFFu, own, d, 8);
+      if (d + j < 8 && g == e) p += q;
     }
-    r.idx[i] = e;
   }
-}
-// the probability of entry i's expert e: its own, and those of later entries of the token that name e again
-__device__ __forceinline__ float prob_of(const int32_t* idx, const float* probs, int i, int k, int e) {
-  const int left = k - 1 - i % k;
-  float p = __ldg(probs + i);
-#pragma unroll
-  for (int d = 1; d < 8; ++d)
-    if (d <= left && __ldg(idx + i + d) == e) p += __ldg(probs + i + d);
-  return p;
+  if (live) {
+    r.idx[i] = e < 0 || e >= E ? -1 : again ? -2 : e;
+    if (PROBS) prob[i] = p;
+  }
 }
 // rows of lower experts, earlier rows of entry i's own, all rows of its own
 __device__ __forceinline__ void place(const Routing& r, int R, int i, int& before, int& same, int& n) {
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(32 * GW, 16 / GW) small_gateup_kernel(SmallArg
   grid_wait();
   grid_launch();
   const int R = a.T * a.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  load_routing(rt, a.idx, R, a.k, a.E);
+  load_routing<false>(rt, a.idx, a.T, a.k, a.E, nullptr, nullptr);
   if (threadIdx.x == 0) sel[0] = -1, sel[2] = 0;
   __syncthreads();
   int before = 0, same = 0, n = 0;
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(32 * GW, 16 / GW) small_gateup_kernel(SmallArg
     if (rank == static_cast<int>(blockIdx.y)) sel[0] = rt.idx[threadIdx.x], sel[1] = before, sel[2] = n;
   }
   __syncthreads();
-  n = sel[2];                              // (at most T: eight)
+  n = min(sel[2], 8);                      // (at most T; the bound spares registers)
   if (n == 0) return;                      // fewer experts picked than the grid allows for
   const int e = sel[0], row0 = sel[1];
   if (mine && rt.idx[threadIdx.x] == e) s_tok[same] = threadIdx.x / a.k;
@@ -563,12 +564,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
   constexpr int UN = 4;                    // units in flight
   __shared__ Routing rt;
   __shared__ int l_e[64], l_row[64], l_n[64], s_tok[64];
-  __shared__ float s_p[64];
+  __shared__ float s_p[64], prob[64];
   __shared__ int s_na;
   __shared__ float part[kWarps][8][17];
   grid_launch();
   const int R = a.T * a.k, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  load_routing(rt, a.idx, R, a.k, a.E);
+  load_routing<true>(rt, a.idx, a.T, a.k, a.E, a.probs, prob);
   for (int i = threadIdx.x; i < kWarps * 8 * 17; i += kSmallThreads) (&part[0][0][0])[i] = 0.0f;
   if (threadIdx.x == 0) s_na = 0;
   __syncthreads();
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
   if (mine) {
     place(rt, R, threadIdx.x, before, same, n);
     s_tok[before + same] = threadIdx.x / a.k;
-    s_p[before + same] = prob_of(a.idx, a.probs, threadIdx.x, a.k, rt.idx[threadIdx.x]);
+    s_p[before + same] = prob[threadIdx.x];
   }
   if (threadIdx.x < 64) rt.first[threadIdx.x] = mine && same == 0;
   __syncthreads();
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
   const Operand x{a.hq, a.hs};
   bool waited = false;
   while (u < u1) {
-    const int e = l_e[at], row0 = l_row[at], n = l_n[at];
+    const int e = l_e[at], row0 = l_row[at], n = min(l_n[at], 8);
     const int64_t wrow = static_cast<int64_t>(e) * a.H + h0 + g;
     const int end = min(u1, (at + 1) * units) - at * units;
     int k0 = u - at * units;
