@@ -116,7 +116,10 @@ struct PrepArgs {
 
 template <int KIND>
 __global__ void __launch_bounds__(128) few_prep_kernel(PrepArgs a) {
-  // (the next launch reads the ids before it waits for this one: they must be there)
+  // The next launch reads the ids and the weights before it waits for this one:
+  // they must be there. From here on they and what else the layer was given can
+  // be read through the read-only path; in this kernel, which may start while
+  // they are written, loads are plain.
   grid_wait();
   grid_launch();
   const uint32_t lane = threadIdx.x & 31;
@@ -126,7 +129,7 @@ __global__ void __launch_bounds__(128) few_prep_kernel(PrepArgs a) {
   const int wid = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int i = wid / nchunk, ck = wid - i * nchunk;
   if (i >= a.R) return;
-  const int e = __ldg(a.idx + i);
+  const int e = a.idx[i];
   if (e < 0 || e >= a.E) {
     if (ck == 0 && lane == 0) {
       a.row_of[i] = -1;
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(128) few_prep_kernel(PrepArgs a) {
   }
   int before = 0, same = 0;     // entries of lower experts; earlier entries of this one
   for (int q = lane; q < a.R; q += 32) {
-    const int f = __ldg(a.idx + q);
+    const int f = a.idx[q];
     before += f >= 0 && f < e;
     same += f == e && q < i;
   }
@@ -150,7 +153,13 @@ __global__ void __launch_bounds__(128) few_prep_kernel(PrepArgs a) {
   float v[32];
   const bool in = c < a.H;
   if (in) {
-    load_bf16x32(a.x + static_cast<int64_t>(i / a.k) * a.H + c, v);
+    const uint4* p = reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(i / a.k) * a.H + c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 w = p[j];
+      v[8 * j] = bf16_lo(w.x), v[8 * j + 1] = bf16_hi(w.x), v[8 * j + 2] = bf16_lo(w.y), v[8 * j + 3] = bf16_hi(w.y);
+      v[8 * j + 4] = bf16_lo(w.z), v[8 * j + 5] = bf16_hi(w.z), v[8 * j + 6] = bf16_lo(w.w), v[8 * j + 7] = bf16_hi(w.w);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] = 0.0f;
@@ -158,7 +167,7 @@ __global__ void __launch_bounds__(128) few_prep_kernel(PrepArgs a) {
   const uint32_t in_chunk = (n & 31) * 16 + (n >> 5) * 4;    // the token's place in a 512-byte scale chunk
   if (KIND == kNV) {
     Block32nv b;
-    quantize32_nv(v, __ldg(a.x_scale), b);
+    quantize32_nv(v, *a.x_scale, b);
     if (in) {
       *reinterpret_cast<uint4*>(a.xq + static_cast<int64_t>(row) * (a.H / 2) + c / 2) =
           make_uint4(b.cw[0], b.cw[1], b.cw[2], b.cw[3]);
@@ -177,7 +186,7 @@ __global__ void __launch_bounds__(128) few_prep_kernel(PrepArgs a) {
       for (int j = 0; j < 8; ++j)
         b.cw[j] = cvt_fp8x4_mul<MGQ_E4M3>(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], mult);
     } else {
-      quantize32<SC, MGQ_E4M3>(v, absmax_bits_f32(v, 32), KIND == kTEN ? __ldg(a.x_scale) : 1.0f, true, b);
+      quantize32<SC, MGQ_E4M3>(v, absmax_bits_f32(v, 32), KIND == kTEN ? *a.x_scale : 1.0f, true, b);
     }
     if (in) {
       uint4* dst = reinterpret_cast<uint4*>(a.xq + static_cast<int64_t>(row) * a.H + c);

@@ -43,17 +43,19 @@ constexpr int kSmallThreads = 256, kWarps = 8;
 using ptx::grid_launch;
 using ptx::grid_wait;
 
-// weights are read once: past L1
+// Weights are read once: past L1. (Here as everywhere in this file plain loads,
+// not those of the read-only path: the first launch may start while the one
+// before it still writes what it reads.)
 __device__ __forceinline__ uint4 ldw16(const uint8_t* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p));
   return r;
 }
 __device__ __forceinline__ uint2 ldw8(const uint8_t* p) {
   uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
   return r;
 }
 // d += A (16 x 32, e4m3) B (32 x 8, e4m3)
@@ -142,8 +144,8 @@ __device__ __forceinline__ void load_routing(Routing& r, const int32_t* idx, int
   if (threadIdx.x >= 64) return;
   const int t = threadIdx.x >> 3, j = threadIdx.x & 7, i = t * k + j;
   const bool live = t < T && j < k;
-  const int e = live ? __ldg(idx + i) : -1;
-  float p = PROBS && live ? __ldg(probs + i) : 0.0f;
+  const int e = live ? idx[i] : -1;
+  float p = PROBS && live ? probs[i] : 0.0f;
   const float own = p;
   bool again = false;
 #pragma unroll
@@ -209,11 +211,11 @@ template <int KIND>
 __device__ __forceinline__ void load_sf(const Weight& w, int64_t row, int u, int q, uint32_t (&s)[2]) {
   const uint8_t* t = w.sf + (row >> 7) * w.sf_kb4 * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
   if (KIND == kMX) {
-    s[0] = __ldg(reinterpret_cast<const uint32_t*>(t + static_cast<int64_t>(u) * 512));
+    s[0] = *reinterpret_cast<const uint32_t*>(t + static_cast<int64_t>(u) * 512);
   } else {
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      s[c] = __ldg(reinterpret_cast<const uint32_t*>(t + (static_cast<int64_t>(u) * 4 + 2 * c + (q >> 1)) * 512)) >>
+      s[c] = *reinterpret_cast<const uint32_t*>(t + (static_cast<int64_t>(u) * 4 + 2 * c + (q >> 1)) * 512) >>
              (16 * (q & 1)) & 0xFFFFu;
   }
 }
@@ -288,9 +290,9 @@ struct XUnit {
       if (t >= n) break;
       const uint16_t* p = x + static_cast<int64_t>(tok[t]) * H + u * 32 * kEl + lane * kEl;
       if (KIND == kNV) {
-        raw[t] = __ldg(reinterpret_cast<const uint4*>(p));
+        raw[t] = *reinterpret_cast<const uint4*>(p);
       } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
         raw[t].x = v.x, raw[t].y = v.y;
       }
     }
@@ -467,7 +469,9 @@ __global__ void __launch_bounds__(32 * GW, 16 / GW) small_gateup_kernel(SmallArg
   const int64_t f0 = static_cast<int64_t>(blockIdx.x) * FR, wrow = static_cast<int64_t>(e) * 2 * a.F + f0;
   const int units = a.H / (KIND == kNV ? 256 : 128);
   const int u0 = warp * units / GW, u1 = (warp + 1) * units / GW;
-  const float sx = KIND == kTEN || KIND == kNV ? __ldg(a.x_scale) : 1.0f;
+  // (all scales up front: behind the reduction's barrier their loads would be waited for)
+  const bool scaled = KIND == kTEN || KIND == kNV;
+  const float sx = scaled ? *a.x_scale : 1.0f, sh = scaled ? *a.h_scale : 1.0f, s_w = scaled ? a.w1.s[e] : 1.0f;
   float acc[2 * TS][4];
 #pragma unroll
   for (int i = 0; i < 2 * TS; ++i)
@@ -485,8 +489,8 @@ __global__ void __launch_bounds__(32 * GW, 16 / GW) small_gateup_kernel(SmallArg
         if (KIND == kMX || KIND == kNV) load_sf<KIND>(a.w1, row, u, q, sf[i][h]);
       }
     if (KIND == kBLK) {
-      sw[0] = __ldg(a.w1.s + (wrow >> 7) * (a.H / 128) + u);
-      sw[1] = __ldg(a.w1.s + ((wrow + a.F) >> 7) * (a.H / 128) + u);
+      sw[0] = a.w1.s[(wrow >> 7) * (a.H / 128) + u];
+      sw[1] = a.w1.s[((wrow + a.F) >> 7) * (a.H / 128) + u];
     }
     XUnit<KIND> xu;
     xu.load(a.x, s_tok, n, a.H, u, lane);
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(32 * GW, 16 / GW) small_gateup_kernel(SmallArg
       up += red[w][tok][FR + f];
     }
     float alpha = 1.0f;
-    if (KIND == kTEN || KIND == kNV) alpha = 1.0f / (sx * __ldg(a.w1.s + e));
+    if (scaled) alpha = 1.0f / (sx * s_w);
     h = swiglu_f32(gt * alpha, up * alpha);
   }
   uint32_t m = __float_as_uint(h) & 0x7FFFFFFFu;
@@ -532,7 +536,6 @@ __global__ void __launch_bounds__(32 * GW, 16 / GW) small_gateup_kernel(SmallArg
     ptx::cluster_sync();                   // nobody leaves while its maximum may still be read
   }
   if (KIND == kNV) {
-    const float sh = __ldg(a.h_scale);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     const float sc = ue4m3_value(cvt_ue4m3(__fmul_rn(__fdiv_rn(__uint_as_float(m), 6.0f), sh)));
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(32 * GW, 16 / GW) small_gateup_kernel(SmallArg
       if (f == 0 && (blockIdx.x & 3) == 0)
         static_cast<float*>(a.hs)[r * (a.F / 128) + (blockIdx.x >> 2)] = __fdiv_rn(1.0f, mult);
     } else {
-      mult = __ldg(a.h_scale);
+      mult = sh;
     }
     a.hq[r * a.F + f0 + f] = static_cast<uint8_t>(cvt_e4m3x2(__fmul_rn(h, mult), 0.0f));
   }
@@ -604,7 +607,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
     const int end = min(u1, (at + 1) * units) - at * units;
     int k0 = u - at * units;
     u += end - k0;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, alpha = 1.0f;
+    if (KIND == kTEN || KIND == kNV) alpha = 1.0f / (*a.h_scale * a.w2.s[e]);
     for (; k0 < end; k0 += UN) {
       uint32_t w[UN][2][8], sf[UN][2][2];
       float sw[UN];
@@ -616,7 +620,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
           load_unit<KIND>(a.w2.codes + (wrow + 8 * h) * a.w2.ld + (k0 + i) * 128, q, w[i][h]);
           if (KIND == kMX || KIND == kNV) load_sf<KIND>(a.w2, wrow + 8 * h, k0 + i, q, sf[i][h]);
         }
-        sw[i] = KIND == kBLK ? __ldg(a.w2.s + ((static_cast<int64_t>(e) * a.H + h0) >> 7) * (a.F / 128) + k0 + i) : 1.0f;
+        sw[i] = KIND == kBLK ? a.w2.s[((static_cast<int64_t>(e) * a.H + h0) >> 7) * (a.F / 128) + k0 + i] : 1.0f;
       }
       if (!waited) {
         grid_wait();
@@ -630,8 +634,6 @@ __global__ void __launch_bounds__(kSmallThreads, 2) small_down_kernel(SmallArgs 
         unit_mma<KIND>(acc, w[i][0], w[i][1], sf[i][0], sf[i][1], t, sw[i]);
       }
     }
-    float alpha = 1.0f;
-    if (KIND == kTEN || KIND == kNV) alpha = 1.0f / (__ldg(a.h_scale) * __ldg(a.w2.s + e));
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int c = 2 * q + (j & 1);

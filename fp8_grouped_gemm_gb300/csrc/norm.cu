@@ -43,15 +43,20 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
                     pack_bf16x2(v[6], v[7]));
 }
 
+// (These kernels are launched while the one before them may still run. What that
+// one can have written is read with plain loads: those of the read-only path ask
+// for data that nobody writes while the kernel lives, and nothing but the
+// compiler's order would keep them behind the wait.)
+
 // the weight chunk c (8 values) as float32; wf32 selects float32 storage
 __device__ __forceinline__ void load_w8(const void* w, bool wf32, int c, float* v) {
   if (wf32) {
     const float4* p = reinterpret_cast<const float4*>(w) + 2 * c;
-    const float4 a = __ldg(p), b = __ldg(p + 1);
+    const float4 a = p[0], b = p[1];
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   } else {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(w) + c), v);
+    unpack8(reinterpret_cast<const uint4*>(w)[c], v);
   }
 }
 
@@ -264,7 +269,7 @@ __global__ void __launch_bounds__(512, CH < 4 ? 2 : 1) norm_kernel(NormArgs a) {
   const uint32_t lane = threadIdx.x & 31;
   const float h = static_cast<float>(a.H), inv_h = 1.0f / h;
   float ts = 1.0f;
-  if (SC == MGQ_TENSOR_F32) ts = __ldg(a.ts);
+  if (SC == MGQ_TENSOR_F32) ts = *a.ts;
   if (SC == MGQ_MX32_E8M0) zero_scale_rows(a);
   uint32_t amax = 0;
   int slot = 0;
@@ -372,7 +377,7 @@ __global__ void __launch_bounds__(512) norm_stream_kernel(NormArgs a) {
   const uint32_t lane = threadIdx.x & 31;
   const float h = static_cast<float>(a.H), inv_h = 1.0f / h;
   float ts = 1.0f;
-  if (SC == MGQ_TENSOR_F32) ts = __ldg(a.ts);
+  if (SC == MGQ_TENSOR_F32) ts = *a.ts;
   RowRing<2> ring;
   const uint16_t* const src[2] = {a.x, a.res};
   ring.init(ring_mem, bars, a.ring, a.H * 2u);
@@ -591,11 +596,11 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(NormBwdArgs a) {
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
   int slot = 0;
-  float rstd_next = blockIdx.x < a.T ? __ldg(a.rstd + blockIdx.x) : 0.0f;
+  float rstd_next = blockIdx.x < a.T ? a.rstd[blockIdx.x] : 0.0f;
   for (int64_t r = blockIdx.x; r < a.T; r += gridDim.x, slot ^= 1) {
     const bool here = !STREAM || ring.wait(a.ring.wait_ns);
     const float rstd = rstd_next;
-    if (r + gridDim.x < a.T) rstd_next = __ldg(a.rstd + r + gridDim.x);
+    if (r + gridDim.x < a.T) rstd_next = a.rstd[r + gridDim.x];
     const uint4* yr = STREAM ? ring.row(0) : reinterpret_cast<const uint4*>(a.dy + r * a.H);
     const uint4* sr = STREAM ? ring.row(1) : reinterpret_cast<const uint4*>(a.s + r * a.H);
     const uint4* dr = STREAM ? ring.row(2) : reinterpret_cast<const uint4*>(a.dsum + r * a.H);

@@ -27,10 +27,12 @@ constexpr int kMaxTopK = 8;
 
 // NaN ranks with the masked experts; -0 becomes +0
 __device__ __forceinline__ float clean(float v) { return fmaxf(v, -INFINITY) + 0.0f; }
+// (Plain loads, not those of the read-only path: the launch before may still be
+// writing when these kernels start.)
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
-  return clean(BF16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + i)) << 16)
-                    : __ldg(static_cast<const float*>(p) + i));
+  return clean(BF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16)
+                    : static_cast<const float*>(p)[i]);
 }
 // unsigned key with the order of the floats; 0 is below every float's key
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -78,10 +80,10 @@ __device__ __forceinline__ void load_row(const RouterArgs& a, int64_t r, int e0,
     for (int i = 0; i < V; i += 4) {
       if (e0 + i < a.E) {
         if (BF16) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + at + i));
+          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + at + i);
           v[i] = bf16_lo(w.x), v[i + 1] = bf16_hi(w.x), v[i + 2] = bf16_lo(w.y), v[i + 3] = bf16_hi(w.y);
         } else {
-          const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at + i));
+          const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at + i);
           v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
         }
 #pragma unroll
@@ -405,8 +407,8 @@ __global__ void __launch_bounds__(256, DENSE ? 4 : 6) router_bwd_kernel(RouterAr
     int e = -1;
     float d = 0.0f;
     if (sub < a.k && live) {
-      e = __ldg(a.sel + r * a.k + sub);
-      d = __ldg(a.dprobs + r * a.k + sub);
+      e = a.sel[r * a.k + sub];
+      d = a.dprobs[r * a.k + sub];
       if (e < 0 || e >= a.E) {
         report(a.err, MGQ_ERR_DEVICE_INDEX);
         e = -1;

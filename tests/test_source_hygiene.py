@@ -32,3 +32,18 @@ def test_library_reads_no_environment():
     for p in glob.glob(os.path.join(ROOT, "fp8_grouped_gemm_gb300", "csrc", "*")):
         text = open(p, errors="replace").read()
         assert "getenv" not in text, os.path.relpath(p, ROOT)
+
+
+def test_programmatic_launches_read_with_plain_loads():
+    """A kernel that may start before the one in front of it has finished must not
+    read what that one writes through the read-only path (ld.global.nc), which
+    asks for data that is constant while the kernel lives. (The few-token GEMMs
+    and their combine start behind a launch that has waited: they may.)"""
+    csrc = os.path.join(ROOT, "fp8_grouped_gemm_gb300", "csrc")
+    read = lambda n: open(os.path.join(csrc, n)).read()
+    few = read("moe_few.cu")
+    prep = few[few.index("few_prep_kernel(PrepArgs"):few.index("few_gemm_kernel(const")]
+    for name, text in [(n, read(n)) for n in ("norm.cu", "router.cu", "moe_few_small.cu")] + [("few_prep_kernel", prep)]:
+        assert "griddepcontrol" in read("ptx_sm100.cuh") and "grid_wait()" in text, name
+        for word in ("__ldg(", ".nc.", "load_bf16x32("):
+            assert word not in text, (name, word)
