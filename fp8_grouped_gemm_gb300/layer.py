@@ -44,6 +44,7 @@ ALIGN_NV_TRAIN = 256   # NVFP4 wgrad: a 128-byte stage holds 256 rows of a group
 # more than the image costs; in the fine-grained forward the gate/up GEMM
 # (contraction 2048) gains 6%, the down GEMM (768) less than its image costs
 NV_IMAGE_MIN_K = 2048
+FEW_TOKENS = 128       # the most tokens of a decode batch (mgq_moe_few_forward)
 
 
 class ExpertLayer:
@@ -483,18 +484,24 @@ class ExpertLayer:
         those that the layer holds from its last step. Calls share the layer's
         buffers: one at a time."""
         w, (T, H) = self.w, x.shape
-        k = topk_idx.shape[1]
         if not hasattr(self, "_few"):
             self._few = self._few_operands(), {}
         (W1, W2, xs, hs), spaces = self._few
-        ws = spaces.get((T, k))
-        if ws is None:
-            n = mgq.moe_few_workspace_size(T, k, w.E, H, w.F, self.scaling)
-            ws = spaces[T, k] = torch.empty(max(256, n), dtype=torch.uint8, device=self.dev)
+        ws = self._few_space(spaces, topk_idx.shape[1])
         if out is None:
             out = torch.empty_like(x)
         mgq.moe_few_forward(x, topk_idx, probs, W1, W2, self.scaling, w.E, w.F, out, ws, xs, hs, stream)
         return out
+
+    def _few_space(self, spaces, k):
+        """forward_few's workspace for k experts a token: one for every batch size, and
+        kept (a captured graph holds its address)."""
+        ws = spaces.get(k)
+        if ws is None:
+            w = self.w
+            n = max(mgq.moe_few_workspace_size(T, k, w.E, w.H, w.F, self.scaling) for T in range(1, FEW_TOKENS + 1))
+            ws = spaces[k] = torch.empty(max(256, n), dtype=torch.uint8, device=self.dev)
+        return ws
 
     def _few_operands(self):
         """(W1, W2, x scale, h scale) of forward_few: the forward's own weight operands."""

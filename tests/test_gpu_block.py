@@ -132,3 +132,25 @@ def test_decode_after_update_scaling_on_the_same_weights():
     many = bf16_np(b.forward(x, r)[0])[:20]
     assert np.linalg.norm(bf16_np(out) - many) <= 2e-2 * np.linalg.norm(many)
     assert mgq.get_error() == mgq.OK
+
+
+@pytest.mark.parametrize("recipe", ["mxfp8", "nvfp4"])
+def test_decode_batches_of_every_size_share_one_workspace(recipe):
+    """Nothing is kept per batch size, and a captured step stays valid whatever sizes follow."""
+    b, x, r = _block(recipe, T=128, train=None)
+    b.forward(x, r)
+    ex, y, idx, probs = b.experts, b.y, b.topk_idx, b.probs
+    first = [ex.forward_few(y[:n], idx[:n], probs[:n]) for n in (3, 50)]
+    out = torch.zeros_like(first[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ex.forward_few(y[:3], idx[:3], probs[:3], out)
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    for n in range(1, 129):
+        ex.forward_few(y[:n], idx[:n], probs[:n])
+        assert torch.cuda.memory_allocated() == held, n
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, first[0]) and torch.equal(ex.forward_few(y[:50], idx[:50], probs[:50]), first[1])
+    assert mgq.get_error() == mgq.OK
