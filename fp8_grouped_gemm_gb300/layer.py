@@ -487,9 +487,10 @@ class ExpertLayer:
         if not hasattr(self, "_few"):
             self._few = self._few_operands(), {}
         (W1, W2, xs, hs), spaces = self._few
-        ws = self._few_space(spaces, topk_idx.shape[1])
-        if out is None:
-            out = torch.empty_like(x)
+        with torch.cuda.stream(stream):     # (new memory is the stream's that uses it)
+            ws = self._few_space(spaces, topk_idx.shape[1])
+            if out is None:
+                out = torch.empty_like(x)
         mgq.moe_few_forward(x, topk_idx, probs, W1, W2, self.scaling, w.E, w.F, out, ws, xs, hs, stream)
         return out
 

@@ -154,3 +154,18 @@ def test_decode_batches_of_every_size_share_one_workspace(recipe):
     torch.cuda.synchronize()
     assert torch.equal(out, first[0]) and torch.equal(ex.forward_few(y[:50], idx[:50], probs[:50]), first[1])
     assert mgq.get_error() == mgq.OK
+
+
+def test_decode_on_another_stream_allocates_its_result_there():
+    """Memory of the current stream's pool may still be in use there when the call runs on another."""
+    b, x, r = _block("mxfp8", T=64, train=None)
+    b.forward(x, r)
+    args = (b.y[:9], b.topk_idx[:9], b.probs[:9])
+    ref = b.experts.forward_few(*args)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    out = b.experts.forward_few(*args, stream=st)
+    seg = [s for s in torch.cuda.memory_snapshot() if s["address"] <= out.data_ptr() < s["address"] + s["total_size"]]
+    assert [s["stream"] for s in seg] == [st.cuda_stream]
+    st.synchronize()
+    assert torch.equal(out, ref)
