@@ -483,7 +483,9 @@ class ExpertLayer:
         per-tensor scales of x and h (delayed) and their NVFP4 global scales are
         those that the layer holds from its last step. Calls share the layer's
         buffers: one at a time."""
-        w, (T, H) = self.w, x.shape
+        w = self.w
+        if x.shape[1] != w.H:               # (the call itself sees a row pitch of the weights, not their width)
+            raise mgq.MGQError(mgq.ERR_INVALID_ARG, "ExpertLayer.forward_few")
         if not hasattr(self, "_few"):
             self._few = self._few_operands(), {}
         (W1, W2, xs, hs), spaces = self._few

@@ -169,3 +169,13 @@ def test_decode_on_another_stream_allocates_its_result_there():
     assert [s["stream"] for s in seg] == [st.cuda_stream]
     st.synchronize()
     assert torch.equal(out, ref)
+
+
+
+def test_decode_refuses_rows_of_another_width():
+    b, x, r = _block("mxfp8", T=64, train=None)
+    b.forward(x, r)
+    for H in (b.w.H // 2, 2 * b.w.H):
+        with pytest.raises(mgq.MGQError) as e:
+            b.experts.forward_few(torch.zeros(4, H, dtype=torch.bfloat16, device="cuda"), b.topk_idx[:4], b.probs[:4])
+        assert e.value.status == mgq.ERR_INVALID_ARG
