@@ -86,6 +86,8 @@ class ExpertLayer:
         f32 = dict(dtype=torch.float32, device=d)
         mx = self.scaling == mgq.MX32_E8M0
         blk = self.scaling == mgq.BLK_1x128_F32
+        # forward_few: fixed scales of x and h; whether a step has left some (NVFP4)
+        self.decode_scales, self.stepped = None, False
         # routing
         self.row_id_map = torch.empty(T, k, **i32)
         self.src_row = torch.empty(R, **i32)
@@ -296,6 +298,7 @@ class ExpertLayer:
     def fwd_ops(self, x, topk_idx, probs, stream=None):
         E, H, F, R = self.w.E, self.w.H, self.w.F, self.R_cap
         sc = self.scaling
+        self.stepped = True
         if self.nv:
             a, g = self.nv_amax, self.nv_sg
             dt = mgq.E2M1
@@ -481,20 +484,39 @@ class ExpertLayer:
         workload's T) on the weights that quantize_weights() wrote: one call that
         reads the picked experts' weights once (mgq_moe_few_forward). The
         per-tensor scales of x and h (delayed) and their NVFP4 global scales are
-        those that the layer holds from its last step. Calls share the layer's
-        buffers: one at a time."""
+        those of set_decode_scales(), or else those that the layer holds from its
+        last step. Calls share the layer's buffers: one at a time."""
         w = self.w
         if x.shape[1] != w.H:               # (the call itself sees a row pitch of the weights, not their width)
             raise mgq.MGQError(mgq.ERR_INVALID_ARG, "ExpertLayer.forward_few")
         if not hasattr(self, "_few"):
             self._few = self._few_operands(), {}
         (W1, W2, xs, hs), spaces = self._few
+        if self.decode_scales is not None:
+            xs, hs = self.decode_scales[0:1], self.decode_scales[1:2]
+        elif self.nv and not self.stepped:
+            raise mgq.MGQError(mgq.ERR_INVALID_ARG, "ExpertLayer.forward_few (NVFP4: no scales of x and h yet; run a "
+                               "forward step or set_decode_scales)")
         with torch.cuda.stream(stream):     # (new memory is the stream's that uses it)
             ws = self._few_space(spaces, topk_idx.shape[1])
             if out is None:
                 out = torch.empty_like(x)
         mgq.moe_few_forward(x, topk_idx, probs, W1, W2, self.scaling, w.E, w.F, out, ws, xs, hs, stream)
         return out
+
+    def set_decode_scales(self, x=None, h=None):
+        """Fixes the scales of x and h that forward_few quantises with (delayed: s;
+        NVFP4: s_g = 2688 / amax), so that they depend on no other step: numbers or
+        one-element tensors, or the last step's where None."""
+        if not (self.nv or self.delayed):
+            raise mgq.MGQError(mgq.ERR_UNSUPPORTED, "ExpertLayer.set_decode_scales")
+        if self.nv and not self.stepped and (x is None or h is None):
+            raise mgq.MGQError(mgq.ERR_INVALID_ARG, "ExpertLayer.set_decode_scales (no step has run)")
+        last = self.nv_sg[0:2] if self.nv else self._fs(0, 2)
+        if self.decode_scales is None:
+            self.decode_scales = torch.empty(2, dtype=torch.float32, device=self.dev)
+        for i, v in enumerate((x, h)):
+            self.decode_scales[i] = last[i] if v is None else v
 
     def _few_space(self, spaces, k):
         """forward_few's workspace for k experts a token: one for every batch size, and

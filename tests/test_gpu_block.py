@@ -179,3 +179,45 @@ def test_decode_refuses_rows_of_another_width():
         with pytest.raises(mgq.MGQError) as e:
             b.experts.forward_few(torch.zeros(4, H, dtype=torch.bfloat16, device="cuda"), b.topk_idx[:4], b.probs[:4])
         assert e.value.status == mgq.ERR_INVALID_ARG
+
+
+
+@pytest.mark.parametrize("recipe", ["nvfp4", "delayed"])
+def test_decode_scales_of_its_own(recipe):
+    """Scales of x and h that a program fixes stay, whatever forward runs between; without
+    values they are the last step's."""
+    b, x, r = _block(recipe, T=64, train=None)
+    ex = b.experts
+
+    def decode(xs, hs):
+        out, _ = b.decode(x[:9].contiguous(), r[:9].contiguous())
+        v1, v2, _, _ = _left(ex, recipe)
+        y, idx, probs = b.few
+        _rows_close(out, y, idx.cpu().numpy(), probs.cpu().numpy(), v1, v2, recipe, scales=(xs, hs))
+        return out
+
+    ex.set_decode_scales(11.5, torch.tensor([6.25], device="cuda"))      # no step has run
+    a = decode(11.5, 6.25)
+    b.forward(x * 8, r)
+    assert torch.equal(decode(11.5, 6.25), a)
+    ex.set_decode_scales()
+    _, _, xs, hs = _left(ex, recipe)
+    c = decode(xs, hs)
+    b.forward(x, r * 8)
+    assert torch.equal(decode(xs, hs), c)
+
+
+
+def test_nvfp4_decode_without_scales_is_refused():
+    """Before a step has run or scales were given there is no global scale of x and h."""
+    b, x, r = _block("nvfp4", T=64, train=None)
+    with pytest.raises(mgq.MGQError) as e:
+        b.decode(x[:4].contiguous(), r[:4].contiguous())
+    assert e.value.status == mgq.ERR_INVALID_ARG
+    with pytest.raises(mgq.MGQError):
+        b.experts.set_decode_scales()
+    b.forward(x, r)
+    b.decode(x[:4].contiguous(), r[:4].contiguous())
+    with pytest.raises(mgq.MGQError) as e:
+        _block("mxfp8", T=64, train=None)[0].experts.set_decode_scales(1.0, 1.0)
+    assert e.value.status == mgq.ERR_UNSUPPORTED
