@@ -497,10 +497,14 @@ class ExpertLayer:
         elif self.nv and not self.stepped:
             raise mgq.MGQError(mgq.ERR_INVALID_ARG, "ExpertLayer.forward_few (NVFP4: no scales of x and h yet; run a "
                                "forward step or set_decode_scales)")
-        with torch.cuda.stream(stream):     # (new memory is the stream's that uses it)
-            ws = self._few_space(spaces, topk_idx.shape[1])
-            if out is None:
-                out = torch.empty_like(x)
+        k = topk_idx.shape[1]
+        ws = spaces.get(k)
+        if ws is None or (out is None and stream is not None):
+            with torch.cuda.stream(stream):     # (new memory is the stream's that uses it)
+                ws = self._few_space(spaces, k)
+                out = torch.empty_like(x) if out is None else out
+        elif out is None:
+            out = torch.empty_like(x)
         mgq.moe_few_forward(x, topk_idx, probs, W1, W2, self.scaling, w.E, w.F, out, ws, xs, hs, stream)
         return out
 
