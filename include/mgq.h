@@ -562,14 +562,18 @@ int mgq_router_topk_bwd(const void* logits, int dtype, const int32_t* topk_idx, 
  *           quantisers'), MGQ_TENSOR_F32 (weight scale s per expert) or
  *           MGQ_NV16_UE4M3 (global_scale per expert)
  *  x_scale, h_scale  device float32, MGQ_TENSOR_F32: the scale s of x and of
- *           h; MGQ_NV16_UE4M3: their global scale s_g (calibrated beforehand:
- *           a token's result does not depend on its batch); else unused
+ *           h; MGQ_NV16_UE4M3: their global scale s_g (calibrated beforehand,
+ *           so that a token's scales do not depend on its batch); else unused
  *  workspace  mgq_moe_few_workspace_size() bytes, 256-byte aligned; calls that
  *           can overlap need workspaces of their own
- * The result does not depend on the order in which CTAs run. Requires
- * 0 <= T <= 128, 1 <= k <= 8, k <= E <= 1024, H and F multiples of 128 (NVFP4:
- * of 256) up to 65536, 16-byte aligned pointers. The workspace size is that of
- * the current device, 0 for sizes that are refused. */
+ * The result does not depend on the order in which CTAs run: the same call gives
+ * the same bits. The order of a token's float32 sums does depend on the sizes
+ * and on what the batch picks, and a value of h that such a sum leaves beside a
+ * rounding boundary can take the other code: a token alone and the same token in
+ * a batch agree to that, not to the bit. Requires 0 <= T <= 128, 1 <= k <= 8,
+ * k <= E <= 1024, H and F multiples of 128 (NVFP4: of 256) up to 65536, 16-byte
+ * aligned pointers. The workspace size is that of the current device, 0 for
+ * sizes that are refused. */
 size_t mgq_moe_few_workspace_size(int T, int k, int E, int64_t H, int64_t F, int scaling);
 int mgq_moe_few_forward(const void* x_bf16, int T, int64_t H, int64_t F, const int32_t* topk_idx,
                         const float* probs, int k, int E, const mgq_operand* W1, const mgq_operand* W2,

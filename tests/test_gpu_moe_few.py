@@ -303,3 +303,28 @@ def test_an_expert_named_twice_by_a_token(recipe, T, E, k, H, F, rows):
     assert torch.all(ws[n:] == 0xA5)
     _rows_close(out, x, idx, p, v1, v2, recipe)
     assert torch.equal(out, _call(*args, ws=ws[:n]))
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("H,F", [(512, 512), (1024, 768)])
+def test_a_token_alone_and_in_batches(recipe, H, F):
+    """The same rows in batches of 1, 8, 9 and 128 (both forms, other splits of the
+    sums). The scales of x and the codes of x are the same; sums that differ by
+    1e-6 of themselves move a code of h once in 10^4, and a row has 10^3: most rows
+    differ by the bf16 rounding alone (2^-8 of a value), nine in ten by no more than
+    two answers within the definition's bound can, and any by one step of an element
+    or a block (1/8 of it, e2m1 1/3) that holds half of the row's norm."""
+    rng = np.random.default_rng(H)
+    T, E, k = 128, 8, 2
+    x = torch.from_numpy(rng.normal(size=(T, H))).bfloat16().cuda()
+    idx, p = (torch.from_numpy(a).cuda() for a in _routing(T, E, k, rng))
+    t1, W1, _ = _weight(E, 2 * F, H, recipe, rng)
+    t2, W2, _ = _weight(E, H, F, recipe, rng)
+    run = lambda a, b: bf16_np(_call(x[a:b].contiguous(), idx[a:b].contiguous(), p[a:b].contiguous(), W1, W2, recipe, E, F))
+    whole = run(0, T)
+    for n in (1, 8, 9):
+        part = np.concatenate([run(a, a + n) for a in range(0, 72, n)])
+        err = np.linalg.norm(part - whole[:72], axis=1) / np.linalg.norm(whole[:72], axis=1)
+        assert np.median(err) <= 2.0 ** -8, (n, np.median(err))
+        assert np.quantile(err, 0.9) <= 2 * TOL[recipe], (n, np.quantile(err, 0.9))
+        assert err.max() <= (1 / 6 if recipe == "nvfp4" else 1 / 16), (n, err.max())
