@@ -328,3 +328,46 @@ def test_a_token_alone_and_in_batches(recipe, H, F):
         assert np.median(err) <= 2.0 ** -8, (n, np.median(err))
         assert np.quantile(err, 0.9) <= 2 * TOL[recipe], (n, np.quantile(err, 0.9))
         assert err.max() <= (1 / 6 if recipe == "nvfp4" else 1 / 16), (n, err.max())
+
+
+@pytest.mark.parametrize("recipe", RECIPES)
+@pytest.mark.parametrize("T", [4, 12, 70])
+def test_ids_out_of_range_in_both_forms(recipe, T):
+    """Some ids out of range, then all of them: they contribute nothing and are reported."""
+    from fp8_grouped_gemm_gb300 import mgq
+    rng = np.random.default_rng(T)
+    E, k, H, F = 6, 3, 256, 512
+    x = torch.from_numpy(rng.normal(size=(T, H))).bfloat16()
+    idx, p = _routing(T, E, k, rng)
+    idx[1, 0], idx[2], idx[T - 1, 2] = E, -1, 2 ** 31 - 1
+    t1, W1, v1 = _weight(E, 2 * F, H, recipe, rng)
+    t2, W2, v2 = _weight(E, H, F, recipe, rng)
+    sc = lambda d: torch.full((1,), d[recipe], device="cuda") if recipe in d else None
+    xs, hs = sc(XS), sc(HS)
+    ws = torch.full((mgq.moe_few_workspace_size(T, k, E, H, F, _scaling(recipe)),), 0xFF, dtype=torch.uint8, device="cuda")
+
+    def run(ids):
+        out = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+        mgq.moe_few_forward(x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(p).cuda(), W1, W2, _scaling(recipe), E,
+                            F, out, ws, xs, hs)
+        assert mgq.get_error() == mgq.ERR_DEVICE_INDEX and mgq.get_error() == mgq.OK
+        return out
+
+    out = run(idx)
+    assert torch.all(out[2] == 0)
+    _rows_close(out, x, idx, p, v1, v2, recipe, [t for t in range(T) if t != 2])
+    assert torch.all(run(np.full_like(idx, -3)) == 0)
+
+
+@pytest.mark.parametrize("recipe", ["mxfp8", "delayed", "nvfp4"])
+@pytest.mark.parametrize("T", [3, 20])
+def test_weights_with_a_longer_pitch(recipe, T):
+    """The contraction is the first H (F) elements of longer weight rows (1x128: refused)."""
+    rng = np.random.default_rng(T)
+    E, k, H, F, more = 5, 2, 512, 768, 256
+    x = torch.from_numpy(rng.normal(size=(T, H))).bfloat16()
+    idx, p = _routing(T, E, k, rng)
+    t1, W1, v1 = _weight(E, 2 * F, H + more, recipe, rng)
+    t2, W2, v2 = _weight(E, H, F + 2 * more, recipe, rng)
+    out = _call(x.cuda(), torch.from_numpy(idx).cuda(), torch.from_numpy(p).cuda(), W1, W2, recipe, E, F)
+    _rows_close(out, x, idx, p, v1[:, :, :H], v2[:, :, :F], recipe)

@@ -306,3 +306,84 @@ def test_two_threads_with_rows_of_different_length():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+# ---- enough rows for the streamed form, in every scaling -----------------------------
+
+@pytest.mark.parametrize("T,H", [(20001, 128), (2003, 4096), (1300, 5120), (700, 16384)])
+def test_blockwise_codes_of_many_rows(T, H):
+    test_blockwise_codes(T, H)
+
+
+@pytest.mark.parametrize("T,H,dt", [(20001, 128, 0), (2003, 4096, 1), (1300, 5120, 0), (700, 16384, 1)])
+def test_per_tensor_codes_of_many_rows(T, H, dt):
+    test_per_tensor_codes_and_amax(T, H, dt)
+
+
+@pytest.mark.parametrize("T,H,dt,mode", [(2003, 4096, 1, "floor"), (1300, 5120, 1, "rceil"), (5003, 1024, 0, "floor")])
+def test_mx_codes_of_many_rows_other_formats(T, H, dt, mode):
+    test_mx_codes(T, H, dt, mode)
+
+
+def _codes(T, H, scaling, dt=0):
+    """(QDesc, its output tensors)"""
+    from fp8_grouped_gemm_gb300 import mgq
+    c = torch.full((T, H), 0xAB, dtype=torch.uint8, device="cuda")
+    if scaling == "mx":
+        s = torch.full((mgq.mx_scale_bytes(T, H),), 0xAB, dtype=torch.uint8, device="cuda")
+        return mgq.qdesc(dt, mgq.MX32_E8M0, c, s), (c, s)
+    if scaling == "blk":
+        s = torch.full((H // 128, T), 7.0, device="cuda")
+        return mgq.qdesc(dt, mgq.BLK_1x128_F32, c, s), (c, s)
+    ts, am = torch.full((1,), 3.7, device="cuda"), torch.zeros(1, device="cuda")
+    return mgq.qdesc(dt, mgq.TENSOR_F32, c, tensor_scale=ts, amax_out=am), (c, ts, am)
+
+
+@pytest.mark.parametrize("scaling", ["mx", "blk", "tensor"])
+def test_outputs_at_odd_16_byte_addresses(scaling):
+    """bf16 outputs that are 16-byte but not 32-byte aligned, and sum_out in place of x: the same bits."""
+    T, H = 2003, 1152
+    x, r, w = _inputs(T, H, 21)
+    q, a = _codes(T, H, scaling)
+    ref = _run(x, r, w, q)
+    from fp8_grouped_gemm_gb300 import mgq
+    q, b = _codes(T, H, scaling)
+    at = lambda: torch.full((T * H + 8,), 7.0, dtype=torch.bfloat16, device="cuda")[8:].view(T, H)
+    y, s = at(), at()
+    s.copy_(x)
+    assert y.data_ptr() % 32 == 16
+    mgq.add_rmsnorm_quantize(s, w.cuda(), EPS, q, residual=r.cuda(), sum_out=s, y=y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref["y"]) and torch.equal(s, ref["sum_out"])
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+@pytest.mark.parametrize("T", [9, 2003])
+@pytest.mark.parametrize("scaling", ["mx", "blk", "tensor"])
+def test_nan_and_infinity_with_codes_stay_in_their_row(T, scaling):
+    """A NaN in a row makes all of its codes NaN, an infinity those of its block (the rest of
+    y is 0); the codes and scales of other rows keep their bits."""
+    H = 1152
+    x, r, w = _inputs(T, H, 22)
+    q, a = _codes(T, H, scaling)
+    _run(x, r, w, q)
+    bad = x.clone()
+    bad[2, 5], bad[4, 7] = float("nan"), float("inf")
+    q, b = _codes(T, H, scaling)
+    _run(bad, r, w, q)
+    rest = [t for t in range(T) if t not in (2, 4)]
+    assert torch.equal(a[0][rest], b[0][rest])
+    nan = (b[0] & 0x7F) == 0x7F                      # e4m3
+    assert torch.all(nan[2]) and nan[4, 7]
+    span = {"mx": 32, "blk": 128, "tensor": 1}[scaling]
+    lo = 7 // span * span
+    assert torch.all(nan[4, lo:lo + span])
+    assert torch.all((b[0][4, lo + span:] & 0x7F) == 0)
+    if scaling == "mx":
+        u, v = (untile_mx_scales(u8_np(s), T, H) for s in (a[1], b[1]))
+        assert np.array_equal(u[rest], v[rest]) and np.all(v[2] == 255) and v[4, 0] == 255 and np.all(v[4, 1:] == 0)
+    elif scaling == "blk":
+        assert torch.equal(a[1][:, rest], b[1][:, rest]) and torch.all(torch.isnan(b[1][:, 2]))
+        assert torch.isnan(b[1][0, 4]) and torch.all(b[1][1:, 4] == 1.0)
+    else:
+        assert torch.isnan(b[2][0])

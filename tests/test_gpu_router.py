@@ -181,3 +181,38 @@ def test_refusals_of_the_binding():
         mgq.router_topk(l.half(), idx, p)
     assert e.value.status == mgq.ERR_UNSUPPORTED
     mgq.router_topk(l[:0], idx[:0], p[:0])                 # no rows
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_of_the_unpermute_reaches_the_logits(renorm):
+    """out = sum_j p_j y_j through mgq_moe_unpermute; dprobs from mgq_moe_unpermute_bwd
+    into the router's gradient, against the formula on the same y and dout."""
+    from fp8_grouped_gemm_gb300 import mgq
+    from tests.layer_check import bf16_np
+    T, E, k, H = 40, 8, 2, 256
+    g = torch.Generator().manual_seed(3)
+    l = torch.randn(T, E, generator=g)
+    ld = l.cuda()
+    idx, p = torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")
+    mgq.router_topk(ld, idx, p, renorm=renorm)
+    R = mgq.r_cap(T, k, E, 128)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    rim, src, off, cnt = torch.empty(T, k, **i32), torch.empty(R, **i32), torch.empty(E + 1, **i32), torch.empty(E, **i32)
+    ws = torch.empty(max(16, mgq.permute_workspace_size(T, k, E)), dtype=torch.uint8, device="cuda")
+    mgq.moe_route(idx, E, 128, R, rim, src, off, cnt, ws)
+    y = torch.randn(R, H, generator=g).bfloat16().cuda()
+    dout = torch.randn(T, H, generator=g).bfloat16().cuda()
+    codes, sc = torch.empty(R, H, dtype=torch.uint8, device="cuda"), torch.empty(mgq.mx_scale_bytes(R, H), dtype=torch.uint8,
+                                                                               device="cuda")
+    dp, dl = torch.empty(T, k, device="cuda"), torch.empty(T, E, device="cuda")
+    mgq.moe_unpermute_bwd(dout, y, rim, src, p, R, off, E, mgq.qdesc(mgq.E5M2, mgq.MX32_E8M0, codes, sc), dp)
+    mgq.router_topk_bwd(ld, idx, dp, dl, renorm=renorm)
+    assert mgq.get_error() == mgq.OK
+    y64, d64, rows = bf16_np(y), bf16_np(dout), rim.cpu().numpy()
+    terms = y64[rows] * d64[:, None, :]
+    ref, mag = terms.sum(-1), np.abs(terms).sum(-1)
+    # 256 terms in float32, in any order
+    assert np.all(np.abs(dp.double().cpu().numpy() - ref) <= 256 * U * mag)
+    rl, m = OB.router_topk_bwd(l.double().numpy(), idx.cpu().numpy(), ref, "softmax", renorm, 1.0)
+    _, m2 = OB.router_topk_bwd(l.double().numpy(), idx.cpu().numpy(), mag, "softmax", renorm, 1.0)
+    assert np.all(np.abs(dl.double().cpu().numpy() - rl) <= 96 * U * m + 256 * U * m2 + 1e-37)
