@@ -84,16 +84,6 @@ __device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
   return r & 0xFFu;
 }
 
-// 1x128 scale of a block of x or h: s = 448 (1 / amax) in two float32 roundings,
-// as perf/operators.py defines it (1 for an all-zero block, the largest float32
-// on overflow). The quantisers' IEEE quotient 448 / amax can differ in the last
-// bit, and bf16 inputs do lie on rounding boundaries of their codes: a value in
-// some 500 takes the other neighbour, which requantising h then amplifies.
-__device__ __forceinline__ float blk_scale_few(uint32_t amax_bits) {
-  const float s = amax_bits == 0 ? 1.0f : __fmul_rn(448.0f, __fdiv_rn(1.0f, __uint_as_float(amax_bits)));
-  return isinf(s) ? 3.40282347e38f : s;
-}
-
 // ---------------------------------------------------------------------------
 // Routed rows. Row order: by expert, then by entry i = t k + j. Tokens of an
 // expert fall into blocks of 64; block b of an expert whose rows start at s

@@ -112,12 +112,6 @@ __device__ __forceinline__ float e8m0(uint32_t four, int j) {
   return __uint_as_float((j == 3 ? four >> 1 : four << (23 - 8 * j)) & 0x7F800000u);
 }
 
-// 1x128 scale of the few-token layer (see moe_few.cu)
-__device__ __forceinline__ float blk_scale_few(uint32_t amax_bits) {
-  const float s = amax_bits == 0 ? 1.0f : __fmul_rn(448.0f, __fdiv_rn(1.0f, __uint_as_float(amax_bits)));
-  return isinf(s) ? 3.40282347e38f : s;
-}
-
 struct Operand {          // the tokens' operand: x or h, rows in expert order
   const uint8_t* codes;   // FP8 codes [R][K]; NVFP4: f16 values [R][K]
   const void* scales;     // MX: E8M0 [R][K / 32]; 1x128: float32 [R][K / 128]

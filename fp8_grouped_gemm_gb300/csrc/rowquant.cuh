@@ -28,6 +28,16 @@ __device__ __forceinline__ float blk_scale(uint32_t amax_bits) {
   return isinf(s) ? 3.40282347e38f : s;
 }
 
+// The 1x128 scale that the layer for a few tokens gives x and h (e4m3): s = 448
+// (1 / amax) in two float32 roundings, 1 for an all-zero block, the largest
+// float32 on overflow. That is how the operator is defined (mgq.h), not a cheaper
+// form of blk_scale, whose one quotient can differ in the last bit: a value that
+// then lies on a rounding boundary of its code takes the other neighbour.
+__device__ __forceinline__ float blk_scale_few(uint32_t amax_bits) {
+  const float s = amax_bits == 0 ? 1.0f : __fmul_rn(448.0f, __fdiv_rn(1.0f, __uint_as_float(amax_bits)));
+  return isinf(s) ? 3.40282347e38f : s;
+}
+
 // v: the lane's 32 values; amax_bits: float bits of max |v| of this lane's
 // 32 values; ts: per-tensor scale (MGQ_TENSOR_F32)
 template <int SC, int DT>
