@@ -123,7 +123,7 @@ FEW_SCRIPT = textwrap.dedent("""
     from tests.test_gpu_moe_few import RECIPES, XS, HS, _routing, _scaling, _weight
     rng = np.random.default_rng(3)
     # more than eight tokens: the form with a ring; several tiles a CTA, and fewer tiles than CTAs
-    for T, E, k, H, F in ((20, 8, 2, 512, 512), (12, 64, 4, 256, 2048)):
+    for T, E, k, H, F in ((20, 8, 2, 256, 512), (12, 16, 4, 256, 1024)):
         for recipe in RECIPES:
             x = torch.from_numpy(rng.normal(size=(T, H))).bfloat16().cuda()
             idx, p = (torch.from_numpy(a).cuda() for a in _routing(T, E, k, rng))
