@@ -25,9 +25,9 @@
 //
 // Measured (all four launches; weights / time): one token, 2 experts of (H 4096,
 // F 14336), MXFP8, 363 MB in 65 us, 5.6 TB/s; 16 tokens, all 8 of them, per
-// tensor, 1.41 GB in 196 us, 7.2 TB/s; 64 tokens, 126 of 128 experts of (2048,
-// 768), NVFP4, 335 MB in 65 us, 5.2 TB/s; 33 tokens, 14 of 16 experts of (5120,
-// 8192), 1x128, 1.78 GB in 277 us, 6.4 TB/s. What is not the weights' read is
+// tensor, 1.41 GB in 214 us, 6.6 TB/s; 64 tokens, 126 of 128 experts of (2048,
+// 768), NVFP4, 335 MB in 65 us, 5.2 TB/s; 33 tokens, 14, 14 and 16 of 16 experts of
+// (5120, 8192) in turn, 1x128, 1.85 GB in 277 us, 6.7 TB/s. What is not the weights' read is
 // about 12 us: four starts, the last tiles' epilogues and joins. Small experts
 // with many tokens are bound by the epilogue: 101 tokens on 4 of (512, 768), 14 us
 // per tensor, 21 us NVFP4.

@@ -16,11 +16,12 @@
 // that a token names more than once is one row, with the sum of its
 // probabilities: so an expert has at most as many rows as there are tokens.
 //
-// Bound by latency: the launch, the ids, the first weights, then a warp's units
-// one after another (two loads deep) and the reduction over the warps. Measured:
-// one token, 2 experts of (1024, 1024), per tensor 6.2 us, NVFP4 6.4, 1x128 7.1,
-// MXFP8 7.4; one token, 8 experts of (2048, 768): per tensor 13.2 us, 2.9 TB/s,
-// NVFP4 12.2 us, 1.7 TB/s (conversions to f16).
+// Bound by latency: the launch, the ids, then a warp's units one after another
+// (gate and up: a unit's loads together, the next unit's behind its products;
+// down: four units' loads together) and the reduction over the warps. Measured:
+// one token, 2 experts of (1024, 1024), per tensor 5.9 us, NVFP4 6.5, 1x128 7.0,
+// MXFP8 7.4; one token, 8 experts of (2048, 768): per tensor 13.4 us, 2.8 TB/s,
+// NVFP4 12.1 us, 1.8 TB/s (conversions to f16).
 //
 // Lanes: with g = lane / 4 and q = lane % 4, a lane holds 16 bytes of weight
 // rows g and g + 8 per 64-byte chunk and the same bytes of token row g. Which

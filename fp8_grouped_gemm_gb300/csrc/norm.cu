@@ -19,7 +19,7 @@
 //
 // Measured, with residual, sum, y and MXFP8 codes: a row of 4096 in 2.6 us, all
 // of it the launch, one trip to memory and the reduction; 1003 x 5120 (1x128,
-// no residual) in 6.5 us, 4.0 TB/s; 16384 x 4096 in 100 us, 6.0 TB/s of the
+// no residual) in 6.6 us, 3.9 TB/s; 16384 x 4096 in 101 us, 6.0 TB/s of the
 // 6.8 that a plain copy reaches (two streams read, three written). Backward with
 // dsum, 16384 x 4096: 80 us, 6.7 TB/s; 333 x 2048 in 5.0 us, two launches in a row.
 #include "mgq_internal.h"

@@ -531,7 +531,8 @@ int mgq_add_rmsnorm_bwd(const void* dy_bf16, const void* s_bf16, const void* w, 
  *  probs    device [T, k] float32: scale * s, with renorm 1 divided by the sum
  *           of the k selected s
  * A logit of -infinity masks its expert: it ranks last with probability 0. A
- * NaN logit counts as -infinity. A row with nothing but masked experts gives
+ * NaN logit counts as -infinity. (+infinity ranks first and has no softmax: its
+ * row's probabilities are NaN.) A row with nothing but masked experts gives
  * the k lowest ids with probabilities 0 (and a zero gradient).
  * The gradient dlogits [T, E] (dtype as the logits) is dense: with renorm 1 or
  * sigmoid scores it is 0 outside the selected experts. An id outside [0, E) in
