@@ -92,6 +92,25 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t
   return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_sw128_3d(CUtensorMap* map, const void* base, int elem_bytes, const uint64_t (&dims)[3],
+                          uint64_t pitch1, uint64_t pitch2, const uint32_t (&box)[3]) {
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!load_encode()) return false;
+  }
+  cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+  cuuint64_t strides[2] = {pitch1, pitch2};
+  cuuint32_t b[3] = {box[0], box[1], box[2]};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt = elem_bytes == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUresult r = g_encode(map, dt, 3, const_cast<void*>(base), d, strides, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace mgq
 
 extern "C" {

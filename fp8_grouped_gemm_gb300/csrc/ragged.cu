@@ -1,0 +1,600 @@
+// bf16 products grouped by expert over ragged groups: group e is the rows
+// [offsets[e], offsets[e+1]), any row numbers, no padding.
+//
+//   fwd    Y[r, n]    = sum_k X[r, k] W[e, n, k]
+//   dgrad  dX[r, k]   = sum_n dY[r, n] W[e, n, k]
+//   wgrad  dW[e, n, k] = beta dW[e, n, k] + sum_{r in e} dY[r, n] X[r, k]
+//
+// (The unquantised product that the routed-expert recipes are compared with:
+// `grouped_mm` in "float8 moe training conversion API prototype", pytorch/ao
+// PR #2275, and the BF16 runs of Megatron-LM issue #1152.)
+//
+// Design. Two SMs share a tile (cta_group::2): M = 256 on the weights' side,
+// 128 rows an SM, and up to 256 tokens on the N side, whose extent an MMA takes
+// in steps of 32 from its instruction descriptor: the last tile of a group
+// costs by the rows it has, and a group's first row is any row, because the row
+// coordinate of a TMA box has no alignment. The accumulator then holds channels
+// as lanes and tokens as columns; the epilogue transposes 8 x 8 blocks between
+// lanes and stores 16 bytes of a token at a time, only the group's own rows.
+// The transposed weights of dgrad and both operands of wgrad are read MN-major
+// by the tensor cores. wgrad contracts over the tokens: rows of the last 16-row
+// step that belong to the next group are zeroed in shared memory, in both
+// operands (0 times a NaN of another group is a NaN).
+#include "device_common.cuh"
+#include "mgq_internal.h"
+#include "ptx_sm100.cuh"
+
+namespace mgq {
+namespace {
+
+enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
+
+constexpr int kBK = 64;                            // elements of the contraction a stage (128 bytes)
+constexpr int kTile = 256;                         // M side, and tokens (wgrad: columns) at most
+constexpr int kMaxE = 1024;
+constexpr uint32_t kOpBytes = 128 * 128;           // one operand's share of an SM a stage
+constexpr uint32_t kSmallBox = 32;                 // rows of the token boxes of a group's last tile
+constexpr uint32_t kOutSlot = 32 * 128;            // wgrad: a warp's store staging
+__host__ __device__ constexpr int stages_of(int op) { return op == kWgrad ? 5 : 6; }
+__host__ __device__ constexpr int threads_of(int op) { return op == kWgrad ? 352 : 320; }
+__host__ __device__ constexpr size_t smem_of(int op) {
+  return 1024 + stages_of(op) * 2 * (size_t)kOpBytes + (op == kWgrad ? 8 * kOutSlot : 0) + 256 + 2 * (kMaxE + 8) * 4;
+}
+static_assert(smem_of(kFwd) <= 232448 && smem_of(kWgrad) <= 232448, "shared memory");
+
+struct RaggedArgs {
+  const int32_t* offsets;   // [E + 1], or null: one group of all R rows
+  int E;
+  int64_t R;
+  int64_t M;                // fwd, dgrad: output columns; wgrad: rows of an expert's result
+  int64_t C;                // fwd, dgrad: length of the contraction; wgrad: columns of the result
+  void* out;
+  int64_t ldo;              // fwd, dgrad: row pitch of the result
+  int out_f32;
+  float beta;
+  int stall;                // failure-detection test: no loads are issued
+  uint64_t wait_ns;
+  int* err;
+};
+
+struct RaggedTile {
+  int e, nst;               // group, contraction stages
+  int row0, n;              // fwd, dgrad: first token and tokens of the tile; wgrad: of the group
+  int64_t m0, c0;           // first row on the M side; wgrad: first column
+};
+
+// Order of the tiles of one group: bands of 8 along the M side (wgrad: along the
+// columns), inside a band the band's tiles fastest. A wave of tiles then covers
+// a block of about 8 x 9 and finds both operands' re-reads in L2.
+__device__ __forceinline__ void banded(int64_t local, int64_t slow, int64_t nfast, int64_t& fast, int64_t& s) {
+  constexpr int64_t kBand = 8;
+  const int64_t band = local / (kBand * slow), r = local - band * (kBand * slow);
+  const int64_t w = min(kBand, nfast - band * kBand);
+  s = r / w;
+  fast = band * kBand + (r - s * w);
+}
+
+template <int OP>
+__device__ __forceinline__ bool ragged_tile(const int32_t* s_off, const int32_t* s_cum, const RaggedArgs& p, int64_t t,
+                                            int& ecur, RaggedTile& tl) {
+  const int64_t nM = (p.M + kTile - 1) / kTile;
+  if (OP == kWgrad) {
+    const int64_t nC = (p.C + kTile - 1) / kTile, per = nM * nC;
+    if (t >= per * p.E) return false;
+    const int e = (int)(t / per);
+    int64_t c, m;
+    banded(t - e * per, nM, nC, c, m);
+    tl.e = e;
+    tl.row0 = s_off[e];
+    tl.n = s_off[e + 1] - s_off[e];
+    tl.nst = (tl.n + kBK - 1) / kBK;
+    tl.m0 = m * kTile;
+    tl.c0 = c * kTile;
+  } else {
+    if (t >= s_cum[p.E] * nM) return false;
+    while (ecur < p.E - 1 && s_cum[ecur + 1] * nM <= t) ++ecur;
+    const int e = ecur;
+    int64_t m, tk;
+    banded(t - s_cum[e] * nM, s_cum[e + 1] - s_cum[e], nM, m, tk);
+    tl.e = e;
+    tl.row0 = s_off[e] + (int)tk * kTile;
+    tl.n = min(kTile, s_off[e + 1] - tl.row0);
+    tl.nst = (int)((p.C + kBK - 1) / kBK);
+    tl.m0 = m * kTile;
+    tl.c0 = 0;
+  }
+  return true;
+}
+
+// Offsets into shared memory with the running count of token tiles, by one warp;
+// true if they are a row partition (not negative, not decreasing, within R).
+__device__ __forceinline__ bool load_groups(const RaggedArgs& p, int32_t* s_off, int32_t* s_cum, uint32_t lane) {
+  int cum = 0;
+  bool ok = true;
+  for (int b = 0; b < p.E; b += 32) {
+    const int e = b + (int)lane;
+    const bool in = e < p.E;
+    const int lo = in && p.offsets ? p.offsets[e] : 0;
+    const int hi = !in ? 0 : p.offsets ? p.offsets[e + 1] : (int)p.R;
+    ok &= !in || (lo >= 0 && lo <= hi && hi <= p.R);
+    const int mine = in && lo <= hi ? (hi - lo + kTile - 1) / kTile : 0;
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (in) {
+      s_off[e] = lo;
+      s_cum[e] = cum + inc - mine;
+      if (e == p.E - 1) {
+        s_off[p.E] = hi;
+        s_cum[p.E] = cum + inc;
+      }
+    }
+    cum += __shfl_sync(0xFFFFFFFFu, inc, 31);
+  }
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// 8 x 8 transposition among groups of 8 lanes: v[j] of lane l is (row l, column
+// j); the result is row pairs in words, o[i] = rows 2i, 2i + 1 of column l & 7,
+// rounded to bf16.
+__device__ __forceinline__ uint4 transpose8_bf16(const float* v, uint32_t lane) {
+  const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, b0 ? v[2 * i] : v[2 * i + 1], 1);
+    w[i] = b0 ? pack_bf16x2(other, v[2 * i + 1]) : pack_bf16x2(v[2 * i], other);
+  }
+  uint32_t q[2][2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, b1 ? w[2 * j] : w[2 * j + 1], 2);
+    q[j][0] = b1 ? other : w[2 * j];
+    q[j][1] = b1 ? w[2 * j + 1] : other;
+  }
+  const uint32_t o0 = __shfl_xor_sync(0xFFFFFFFFu, b2 ? q[0][0] : q[1][0], 4);
+  const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, b2 ? q[0][1] : q[1][1], 4);
+  return b2 ? make_uint4(o0, o1, q[1][0], q[1][1]) : make_uint4(q[0][0], q[0][1], o0, o1);
+}
+
+// 32 tokens of a warp's 32 channels: v[j] = (channel chan0 + lane, token tok0 + j).
+// `left` tokens exist.
+__device__ __forceinline__ void store_tokens(void* out, int64_t ldo, int out_f32, const float (&v)[32], int64_t tok0,
+                                             int left, int64_t chan0, int64_t chans, uint32_t lane) {
+  if (out_f32) {
+    float* o = static_cast<float*>(out) + tok0 * ldo + chan0 + lane;
+    const bool in = chan0 + lane < chans;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (in && j < left) o[j * ldo] = v[j];
+  } else {
+    const int64_t c = chan0 + (lane & 24);
+    uint16_t* o = static_cast<uint16_t*>(out) + (tok0 + (lane & 7)) * ldo + c;
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+      if (j >= left) break;                                // the same in the whole warp
+      const uint4 w = transpose8_bf16(v + j, lane);
+      if (j + (int)(lane & 7) < left && c < chans) *reinterpret_cast<uint4*>(o + j * ldo) = w;
+    }
+  }
+}
+
+template <int OP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
+    ragged_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmS, const RaggedArgs p) {
+  constexpr int ST = stages_of(OP);
+  constexpr bool kAmn = OP != kFwd, kBmn = OP == kWgrad;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  uint8_t* sA = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* sB = sA + ST * kOpBytes;
+  uint8_t* sOut = sB + ST * kOpBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + (OP == kWgrad ? 8 * kOutSlot : 0));
+  uint64_t* empty = full + ST;
+  uint64_t* tmem_full = empty + ST;      // [2]
+  uint64_t* tmem_empty = tmem_full + 2;  // [2]
+  uint64_t* mask_go = tmem_empty + 2;    // wgrad: the last stage has landed in both SMs
+  uint64_t* mask_done = mask_go + 1;     // its foreign rows are zero
+  uint64_t* drained = mask_done + 1;     // after a wait ran out: the MMAs issued have finished
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_bad = reinterpret_cast<int*>(s_tmem + 2);
+  int32_t* s_off = reinterpret_cast<int32_t*>(full + 32);
+  int32_t* s_cum = s_off + (kMaxE + 8);
+
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const bool leader = rank == 0;
+  const int64_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&tmem_full[a], 1);
+      ptx::mbar_init(&tmem_empty[a], 2 * 8);      // one arrival per epilogue warp of each CTA
+    }
+    ptx::mbar_init(mask_go, 1);
+    ptx::mbar_init(mask_done, 2);
+    ptx::mbar_init(drained, 1);
+    *s_abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmB);
+    ptx::prefetch_tmap(&tmS);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(s_tmem, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  if (warp == 2) {
+    const bool ok = load_groups(p, s_off, s_cum, lane);
+    if (lane == 0) {
+      *s_bad = ok ? 0 : 1;
+      if (!ok) report(p.err, MGQ_ERR_INVALID_ARG);
+    }
+  }
+  __syncthreads();
+  ptx::tc_fence_before();
+  ptx::cluster_sync();                 // both CTAs' barriers initialised, tensor memory allocated
+  ptx::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const bool run = *s_bad == 0;
+
+  if (run && warp == 0 && lane == 0 && !p.stall) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    int ecur = 0;
+    uint32_t it = 0;
+    RaggedTile tl;
+    for (int64_t t = pair; !*s_abort && ragged_tile<OP>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
+      // this CTA's half of the tokens: one box of 128 rows, or boxes of 32
+      const int half = OP == kWgrad ? 128 : (tl.n + 31) / 32 * 16;
+      const int boxes = half == 128 ? 0 : (half + (int)kSmallBox - 1) / (int)kSmallBox;
+      const uint32_t bytes = 2 * (kOpBytes + (boxes ? boxes * kSmallBox * 128 : kOpBytes));
+      for (int s = 0; s < tl.nst; ++s, ++it) {
+        const uint32_t st = it % ST, ph = (it / ST) & 1;
+        if (*s_abort) break;
+        if (!ptx::mbar_wait(&empty[st], ph ^ 1, p.wait_ns)) {
+          report(p.err, MGQ_ERR_TIMEOUT);
+          *s_abort = 1;
+          break;
+        }
+        if (leader) ptx::mbar_arrive_expect_tx(&full[st], bytes);
+        const uint32_t bar0 = ptx::mapa_shared(ptx::smem_u32(&full[st]), 0);
+        uint8_t* a = sA + st * kOpBytes;
+        uint8_t* b = sB + st * kOpBytes;
+        const int32_t kx = s * kBK;
+        const int32_t am = (int32_t)(tl.m0 + 128 * rank);
+        if (OP == kFwd) {
+          ptx::tma_load_3d_pair(a, &tmA, bar0, kx, am, tl.e);
+        } else {                                     // two chunks of 64 along M
+          const int32_t y = OP == kDgrad ? kx : tl.row0 + kx, z = OP == kDgrad ? tl.e : 0;
+          ptx::tma_load_3d_pair(a, &tmA, bar0, am, y, z);
+          ptx::tma_load_3d_pair(a + kOpBytes / 2, &tmA, bar0, am + 64, y, z);
+        }
+        if (OP == kWgrad) {
+          const int32_t x = (int32_t)(tl.c0 + 128 * rank);
+          ptx::tma_load_3d_pair(b, &tmB, bar0, x, tl.row0 + kx, 0);
+          ptx::tma_load_3d_pair(b + kOpBytes / 2, &tmB, bar0, x + 64, tl.row0 + kx, 0);
+        } else {
+          const int32_t r = tl.row0 + half * (int)rank;
+          if (!boxes) ptx::tma_load_3d_pair(b, &tmB, bar0, kx, r, 0);
+          for (int i = 0; i < boxes; ++i)
+            ptx::tma_load_3d_pair(b + i * kSmallBox * 128, &tmS, bar0, kx, r + i * (int)kSmallBox, 0);
+        }
+      }
+    }
+    // after a wait that ran out: no copy may still be on its way when the CTA
+    // leaves. (The leader's barriers count both CTAs' copies.)
+    if (*s_abort && leader)
+      for (uint32_t i = it > ST ? it - ST : 0; i < it; ++i) ptx::mbar_wait(&full[i % ST], (i / ST) & 1, p.wait_ns);
+  } else if (run && leader && warp == 1 && lane == 0) {
+    // ------------------------------------------------------------ MMA issuer (CTA 0)
+    int ecur = 0;
+    uint32_t it = 0, tc = 0, masks = 0;
+    RaggedTile tl;
+    const uint32_t sA0 = ptx::smem_u32(sA), sB0 = ptx::smem_u32(sB);
+    bool ok = true;
+    for (int64_t t = pair; ok && ragged_tile<OP>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
+      if (tl.nst == 0) continue;
+      const uint32_t a = tc & 1, aph = (tc >> 1) & 1;
+      ok = !*s_abort && ptx::mbar_wait(&tmem_empty[a], aph ^ 1, p.wait_ns);
+      ptx::tc_fence_after();
+      const uint32_t N = OP == kWgrad ? 256u : (uint32_t)(tl.n + 31) / 32 * 32;
+      const uint32_t idesc = ptx::idesc_f16(1, 256, N) | ptx::idesc_mn_major(kAmn, kBmn);
+      for (int s = 0; ok && s < tl.nst; ++s, ++it) {
+        const uint32_t st = it % ST, ph = (it / ST) & 1;
+        ok = !*s_abort && ptx::mbar_wait(&full[st], ph, p.wait_ns);
+        int steps = kBK / 16;
+        if (OP == kWgrad && s == tl.nst - 1 && ok) {
+          const int rows = tl.n - s * kBK;
+          steps = (rows + 15) / 16;
+          if (rows % 16) {
+            ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(mask_go), 0));
+            ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(mask_go), 1));
+            ok = ptx::mbar_wait(mask_done, masks++ & 1, p.wait_ns);
+          }
+        }
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint64_t ad = kAmn ? ptx::sdesc_mnmajor_sw128_chunks(sA0 + st * kOpBytes, kOpBytes / 2)
+                                 : ptx::sdesc_kmajor_sw128(sA0 + st * kOpBytes);
+        const uint64_t bd = kBmn ? ptx::sdesc_mnmajor_sw128_chunks(sB0 + st * kOpBytes, kOpBytes / 2)
+                                 : ptx::sdesc_kmajor_sw128(sB0 + st * kOpBytes);
+        // a K=16 step: 32 bytes along a K-major row, 16 rows (2048 bytes) of an MN-major tile
+        constexpr uint64_t da = kAmn ? 128 : 2, db = kBmn ? 128 : 2;
+        for (int kk = 0; kk < steps; ++kk)
+          ptx::mma_f16_pair(tmem + a * kTile, ad + kk * da, bd + kk * db, idesc, (s > 0 || kk > 0) ? 1u : 0u);
+        ptx::mma_commit_pair(&empty[st], 0x3);        // frees the stage in both CTAs
+      }
+      if (!ok) break;
+      ptx::mma_commit_pair(&tmem_full[a], 0x3);
+      ++tc;
+    }
+    if (!ok) {
+      report(p.err, MGQ_ERR_TIMEOUT);
+      *s_abort = 1;
+      ptx::mma_commit_pair(drained, 0x1);             // the MMAs issued so far finish before the CTA leaves
+      ptx::mbar_wait(drained, 0, p.wait_ns);
+    }
+  } else if (run && warp >= 2 && warp < 10) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const uint32_t q = warp & 3;
+    const uint32_t half = (uint32_t)(warp - 2) >> 2;
+    const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&tmem_empty[0]), 0);
+    const uint32_t empty1 = ptx::mapa_shared(ptx::smem_u32(&tmem_empty[1]), 0);
+    uint8_t* slot = sOut + (warp - 2) * kOutSlot;
+    int ecur = 0;
+    uint32_t tc = 0;
+    RaggedTile tl;
+    for (int64_t t = pair; ragged_tile<OP>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
+      const uint32_t a = tc & 1, aph = (tc >> 1) & 1;
+      const int64_t m0 = tl.m0 + 128 * rank + 32 * q;       // this warp's 32 rows of the M side
+      if (tl.nst > 0) {
+        bool got = *s_abort == 0;
+        got = got && ptx::mbar_wait(&tmem_full[a], aph, p.wait_ns);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          report(p.err, MGQ_ERR_TIMEOUT);
+          *s_abort = 1;
+          break;
+        }
+        ptx::tc_fence_after();
+      }
+      const uint32_t tbase = tmem + a * kTile + ((q * 32) << 16);
+      if (OP != kWgrad) {
+        for (int c = 32 * half; c < tl.n; c += 64) {
+          uint32_t r[32];
+          ptx::tmem_ld_32x32b_x32(tbase + c, r);
+          ptx::tmem_ld_wait();
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          store_tokens(p.out, p.ldo, p.out_f32, v, (int64_t)tl.row0 + c, tl.n - c, m0, p.M, lane);
+        }
+      } else if (m0 < p.M) {
+        const bool row_in = m0 + lane < p.M;
+        const int wide = p.out_f32 ? 32 : 64;               // columns of a 128-byte staging row
+        for (int c = 128 * half; c < 128 * (int)half + 128 && tl.c0 + c < p.C; c += wide) {
+          uint32_t w[32];
+          if (p.out_f32) {
+            if (tl.nst > 0) {
+              ptx::tmem_ld_32x32b_x32(tbase + c, w);
+              ptx::tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) w[j] = 0;
+            }
+            if (p.beta != 0.0f && row_in) {
+              const float* old = static_cast<const float*>(p.out) + ((int64_t)tl.e * p.M + m0 + lane) * p.C + tl.c0 + c;
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                if (tl.c0 + c + j >= p.C) break;            // (C is a multiple of 8)
+                const float4 o = *reinterpret_cast<const float4*>(old + j);
+                w[j] = __float_as_uint(fmaf(p.beta, o.x, __uint_as_float(w[j])));
+                w[j + 1] = __float_as_uint(fmaf(p.beta, o.y, __uint_as_float(w[j + 1])));
+                w[j + 2] = __float_as_uint(fmaf(p.beta, o.z, __uint_as_float(w[j + 2])));
+                w[j + 3] = __float_as_uint(fmaf(p.beta, o.w, __uint_as_float(w[j + 3])));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[32];
+              if (tl.nst > 0) {
+                ptx::tmem_ld_32x32b_x32(tbase + c + 32 * h, r);
+                ptx::tmem_ld_wait();
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = 0;
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                w[16 * h + j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+            }
+          }
+          if (lane == 0) ptx::bulk_wait_read0();            // the store before has read the staging slot
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(slot + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::tma_store_3d(&tmS, slot, (int32_t)(tl.c0 + c), (int32_t)m0, tl.e);
+            ptx::bulk_commit();
+          }
+        }
+      }
+      if (tl.nst > 0) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(a ? empty1 : empty0);
+        ++tc;
+      }
+    }
+    if (OP == kWgrad && lane == 0) ptx::bulk_wait0();       // this warp's stores are complete
+  } else if (OP == kWgrad && run && warp == 10) {
+    // ------------------------------------------------------------ foreign rows of a group's last step
+    int ecur = 0;
+    uint32_t it = 0, masks = 0;
+    RaggedTile tl;
+    const uint32_t done0 = ptx::mapa_shared(ptx::smem_u32(mask_done), 0);
+    for (int64_t t = pair; ragged_tile<OP>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
+      it += tl.nst;
+      const int rows = tl.n - (tl.nst - 1) * kBK;
+      if (tl.nst == 0 || rows % 16 == 0) continue;
+      // (a tile before this one can take long: this wait is for a stage, so it
+      // is repeated until the pipeline itself has given up)
+      bool got = false;
+      while (!got && !*s_abort) got = ptx::mbar_wait(mask_go, masks & 1, 1000000);
+      if (!__all_sync(0xFFFFFFFFu, got)) break;
+      ++masks;
+      const uint32_t st = (it - 1) % ST;
+      for (int r = rows; r < (rows + 15) / 16 * 16; ++r) {
+        // a row is 128 bytes in each of the operands' two chunks
+        uint8_t* base = (lane < 16 ? sA : sB) + st * kOpBytes + (lane & 8 ? kOpBytes / 2 : 0);
+        *reinterpret_cast<uint4*>(base + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(done0);
+    }
+  }
+  __syncthreads();
+  ptx::tc_fence_before();
+  ptx::cluster_sync();                 // the peer's MMAs and reads are finished before freeing
+  ptx::tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int OP>
+int launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ts, const RaggedArgs& p,
+                int64_t max_tiles, cudaStream_t s) {
+  auto kern = ragged_pair_kernel<OP>;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return MGQ_ERR_CUDA;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(OP)) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return MGQ_ERR_CUDA;
+    }
+    attr_set[dev] = true;
+  }
+  const int64_t pairs = min((int64_t)(num_sms() / 2), max_tiles);
+  kern<<<(unsigned)(2 * max(pairs, (int64_t)1)), threads_of(OP), smem_of(OP), s>>>(ta, tb, ts, p);
+  MGQ_LAUNCH_CHECK();
+  return MGQ_OK;
+}
+
+// What every entry point checks: sizes, pitches, alignment.
+int check_ragged(const void* a, int64_t lda, int64_t wa, const void* b, int64_t ldb, int64_t wb, const int32_t* offsets,
+                 int E, int64_t R, int64_t N, int64_t K, const void* out, int out_dtype) {
+  MGQ_CHECK_ARG(E >= 1 && E <= kMaxE && R >= 0 && R < (1ll << 31) - 512 && N > 0 && K > 0);
+  MGQ_CHECK_ARG(N % 8 == 0 && K % 8 == 0 && N < (1ll << 31) - 512 && K < (1ll << 31) - 512);
+  MGQ_CHECK_ARG(offsets || E == 1);
+  MGQ_CHECK_ARG(out_dtype == MGQ_OUT_BF16 || out_dtype == MGQ_OUT_F32);
+  MGQ_CHECK_ARG((reinterpret_cast<uintptr_t>(offsets) & 3u) == 0 && out && aligned16(out));
+  MGQ_CHECK_ARG(lda >= wa && lda % 8 == 0 && ldb >= wb && ldb % 8 == 0 && lda < (1ll << 38) && ldb < (1ll << 38));
+  MGQ_CHECK_ARG(R == 0 || (a && b && aligned16(a) && aligned16(b)));
+  return MGQ_OK;
+}
+
+void fill_knobs(RaggedArgs* p) { debug_knobs(&p->stall, &p->wait_ns); }
+
+// fwd and dgrad: rows of `in` [R, C] by the weights, result columns M.
+template <int OP>
+int run_rows(const void* in, int64_t ldi, const void* w, const int32_t* offsets, int E, int64_t R, int64_t N, int64_t K,
+             void* out, int64_t ldo, int out_dtype, void* stream) {
+  const int64_t M = OP == kFwd ? N : K, C = OP == kFwd ? K : N;
+  int rc = check_ragged(in, ldi, C, w, K, K, offsets, E, R, N, K, out, out_dtype);
+  if (rc != MGQ_OK) return rc;
+  MGQ_CHECK_ARG(ldo >= M && ldo % 8 == 0 && ldo < (1ll << 38));
+  if (R == 0) return MGQ_OK;
+  RaggedArgs p{};
+  p.err = error_word();
+  if (!p.err) return MGQ_ERR_CUDA;
+  p.offsets = offsets;
+  p.E = E;
+  p.R = R;
+  p.M = M;
+  p.C = C;
+  p.out = out;
+  p.ldo = ldo;
+  p.out_f32 = out_dtype == MGQ_OUT_F32;
+  fill_knobs(&p);
+  CUtensorMap ta, tb, ts;
+  const uint64_t u = 2;
+  if (!encode_tmap_sw128_3d(&ta, w, 2, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
+                            {64, OP == kFwd ? 128u : 64u, 1}) ||
+      !encode_tmap_sw128_3d(&tb, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, 128, 1}) ||
+      !encode_tmap_sw128_3d(&ts, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, kSmallBox, 1}))
+    return MGQ_ERR_CUDA;
+  const int64_t tiles = (R / kTile + min((int64_t)E, R)) * ((M + kTile - 1) / kTile);
+  return launch_pair<OP>(ta, tb, ts, p, tiles, as_stream(stream));
+}
+
+}  // namespace
+}  // namespace mgq
+
+using namespace mgq;
+
+extern "C" {
+
+int mgq_ragged_gemm_fwd(const void* x_bf16, int64_t ldx, const void* w_bf16, const int32_t* offsets, int E, int64_t R,
+                        int64_t N, int64_t K, void* y, int64_t ldy, int out_dtype, void* stream) {
+  return run_rows<kFwd>(x_bf16, ldx, w_bf16, offsets, E, R, N, K, y, ldy, out_dtype, stream);
+}
+
+int mgq_ragged_gemm_dgrad(const void* dy_bf16, int64_t lddy, const void* w_bf16, const int32_t* offsets, int E,
+                          int64_t R, int64_t N, int64_t K, void* dx, int64_t lddx, int out_dtype, void* stream) {
+  return run_rows<kDgrad>(dy_bf16, lddy, w_bf16, offsets, E, R, N, K, dx, lddx, out_dtype, stream);
+}
+
+int mgq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void* x_bf16, int64_t ldx, const int32_t* offsets,
+                          int E, int64_t R, int64_t N, int64_t K, float beta, void* dw, int out_dtype, void* stream) {
+  int rc = check_ragged(dy_bf16, lddy, N, x_bf16, ldx, K, offsets, E, R, N, K, dw, out_dtype);
+  if (rc != MGQ_OK) return rc;
+  MGQ_CHECK_ARG(beta == 0.0f || out_dtype == MGQ_OUT_F32);
+  MGQ_CHECK_ARG(beta == beta);
+  const int64_t u = out_dtype == MGQ_OUT_F32 ? 4 : 2;
+  if (R == 0 && beta == 1.0f) return MGQ_OK;
+  RaggedArgs p{};
+  p.err = error_word();
+  if (!p.err) return MGQ_ERR_CUDA;
+  p.offsets = offsets;
+  p.E = E;
+  p.R = R;
+  p.M = N;
+  p.C = K;
+  p.out = dw;
+  p.out_f32 = out_dtype == MGQ_OUT_F32;
+  p.beta = beta;
+  fill_knobs(&p);
+  CUtensorMap ta, tb, to;
+  // (no rows: maps that no load uses, the groups' results are beta times what they were)
+  const uint64_t rows = R > 0 ? R : 1;
+  if (!encode_tmap_sw128_3d(&ta, R > 0 ? dy_bf16 : dw, 2, {(uint64_t)N, rows, 1}, lddy * 2, rows * lddy * 2,
+                            {64, 64, 1}) ||
+      !encode_tmap_sw128_3d(&tb, R > 0 ? x_bf16 : dw, 2, {(uint64_t)K, rows, 1}, ldx * 2, rows * ldx * 2,
+                            {64, 64, 1}) ||
+      !encode_tmap_sw128_3d(&to, dw, (int)u, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
+                            {(uint32_t)(128 / u), 32, 1}))
+    return MGQ_ERR_CUDA;
+  const int64_t tiles = (int64_t)E * ((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile);
+  return launch_pair<kWgrad>(ta, tb, to, p, tiles, as_stream(stream));
+}
+
+}  // extern "C"

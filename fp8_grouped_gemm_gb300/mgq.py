@@ -43,6 +43,7 @@ EXPORTS = (
     "mgq_get_gemm_option", "mgq_nv_scale_image", "mgq_add_rmsnorm_quantize", "mgq_add_rmsnorm_bwd_workspace_size",
     "mgq_add_rmsnorm_bwd", "mgq_router_topk", "mgq_router_topk_bwd",
     "mgq_moe_few_workspace_size", "mgq_moe_few_forward",
+    "mgq_ragged_gemm_fwd", "mgq_ragged_gemm_dgrad", "mgq_ragged_gemm_wgrad",
 )
 
 
@@ -120,6 +121,10 @@ def load() -> ctypes.CDLL:
         lib.mgq_moe_few_workspace_size.argtypes = [i32, i32, i32, i64, i64, i32]
         lib.mgq_moe_few_forward.argtypes = [vp, i32, i64, i64, vp, vp, i32, i32, P(Operand), P(Operand), i32, vp, vp,
                                             vp, vp, sz, vp]
+        rows = [vp, i64, vp, vp, i32, i64, i64, i64, vp, i64, i32, vp]
+        lib.mgq_ragged_gemm_fwd.argtypes = rows
+        lib.mgq_ragged_gemm_dgrad.argtypes = rows
+        lib.mgq_ragged_gemm_wgrad.argtypes = [vp, i64, vp, i64, vp, i32, i64, i64, i64, f32, vp, i32, vp]
         for name in EXPORTS:
             if name != "mgq_status_string" and not name.endswith("_workspace_size"):
                 getattr(lib, name).restype = i32
@@ -469,5 +474,78 @@ def moe_few_forward(x, topk_idx, probs, W1: Operand, W2: Operand, scaling, E, F,
         x.data_ptr(), T, H, F, topk_idx.data_ptr(), probs.data_ptr(), sel[1], E, ctypes.byref(W1), ctypes.byref(W2), scaling,
         None if x_scale is None else x_scale.data_ptr(), None if h_scale is None else h_scale.data_ptr(), out.data_ptr(),
         workspace.data_ptr(), _bytes(workspace), _s(stream))
+    if rc:
+        raise MGQError(rc, fn)
+
+
+def _pitch(t, rows, cols):
+    """Row pitch in elements of a [rows, cols] matrix with contiguous rows, or -1."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        return -1
+    return t.stride(0) if rows > 1 else cols
+
+
+def _ragged(fn, rows_in, wide_in, w, offsets, rows_out, wide_out):
+    """What the ragged products check of their tensors; (offsets pointer, E, pitches)."""
+    E, dev = w.shape[0], torch.cuda.current_device()
+    R = rows_in.shape[0]
+    if w.dim() != 3 or not w.is_contiguous():
+        _refuse(fn)
+    for t in (rows_in, w, rows_out):
+        if not t.is_cuda or t.get_device() != dev:
+            _refuse(fn)
+    if offsets is None:
+        if E != 1:
+            _refuse(fn)
+    elif not (offsets.dtype is _I32 and offsets.shape == (E + 1,) and offsets.is_contiguous() and offsets.is_cuda and
+              offsets.get_device() == dev):
+        _refuse(fn)
+    lda, ldb = _pitch(rows_in, R, wide_in), _pitch(rows_out, R, wide_out)
+    if lda < 0 or ldb < 0:
+        _refuse(fn)
+    return None if offsets is None else offsets.data_ptr(), E, R, lda, ldb
+
+
+def ragged_gemm_fwd(x, w, offsets, y, stream=None):
+    """y[r] = w[e] x[r] for the rows [offsets[e], offsets[e+1]) of group e: x bf16 [R, K],
+    w bf16 [E, N, K], y bf16 or float32 [R, N]; offsets int32 [E+1], or None with E = 1."""
+    fn = "mgq_ragged_gemm_fwd"
+    dt = _OUT_DTYPE.get(y.dtype)
+    if x.dtype is not _BF16 or w.dtype is not _BF16 or dt is None or w.dim() != 3:
+        _refuse(fn, ERR_UNSUPPORTED)
+    _, N, K = w.shape
+    off, E, R, ldx, ldy = _ragged(fn, x, K, w, offsets, y, N)
+    rc = (_lib or load()).mgq_ragged_gemm_fwd(x.data_ptr(), ldx, w.data_ptr(), off, E, R, N, K, y.data_ptr(), ldy, dt,
+                                              _s(stream))
+    if rc:
+        raise MGQError(rc, fn)
+
+
+def ragged_gemm_dgrad(dy, w, offsets, dx, stream=None):
+    """dx[r] = dy[r] w[e] for the rows of group e: dy bf16 [R, N], w bf16 [E, N, K], dx bf16
+    or float32 [R, K]."""
+    fn = "mgq_ragged_gemm_dgrad"
+    dt = _OUT_DTYPE.get(dx.dtype)
+    if dy.dtype is not _BF16 or w.dtype is not _BF16 or dt is None or w.dim() != 3:
+        _refuse(fn, ERR_UNSUPPORTED)
+    _, N, K = w.shape
+    off, E, R, lddy, lddx = _ragged(fn, dy, N, w, offsets, dx, K)
+    rc = (_lib or load()).mgq_ragged_gemm_dgrad(dy.data_ptr(), lddy, w.data_ptr(), off, E, R, N, K, dx.data_ptr(), lddx,
+                                                dt, _s(stream))
+    if rc:
+        raise MGQError(rc, fn)
+
+
+def ragged_gemm_wgrad(dy, x, offsets, dw, beta=0.0, stream=None):
+    """dw[e] = beta dw[e] + dy^T x over the rows of group e: dy bf16 [R, N], x bf16 [R, K],
+    dw float32 (bf16: beta 0) [E, N, K]."""
+    fn = "mgq_ragged_gemm_wgrad"
+    dt = _OUT_DTYPE.get(dw.dtype)
+    if dy.dtype is not _BF16 or x.dtype is not _BF16 or dt is None or dw.dim() != 3:
+        _refuse(fn, ERR_UNSUPPORTED)
+    _, N, K = dw.shape
+    off, E, R, lddy, ldx = _ragged(fn, dy, N, dw, offsets, x, K)
+    rc = (_lib or load()).mgq_ragged_gemm_wgrad(dy.data_ptr(), lddy, x.data_ptr(), ldx, off, E, R, N, K, beta,
+                                                dw.data_ptr(), dt, _s(stream))
     if rc:
         raise MGQError(rc, fn)

@@ -581,6 +581,36 @@ int mgq_moe_few_forward(const void* x_bf16, int T, int64_t H, int64_t F, const i
                         int scaling, const float* x_scale, const float* h_scale, void* out_bf16,
                         void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- bf16 products over ragged groups ---------------------------------------------
+ * The grouped products without quantisation and without padding: group e is the
+ * rows [offsets[e], offsets[e+1]) of the activations, any row numbers (as
+ * mgq_moe_route writes them with align 1), empty groups among them.
+ *   fwd    Y[r, n]     = sum_k X[r, k] W[e, n, k]
+ *   dgrad  dX[r, k]    = sum_n dY[r, n] W[e, n, k]
+ *   wgrad  dW[e, n, k] = beta dW[e, n, k] + sum over the group's rows of dY[r, n] X[r, k]
+ * Float32 accumulation, one rounding to the result's type.
+ *  x, dy    device bf16, [R, K] with row pitch ldx and [R, N] with row pitch lddy (elements)
+ *  w        device bf16 [E, N, K], contiguous
+ *  offsets  device [E+1] int32, 0 <= offsets[e] <= offsets[e+1] <= R (otherwise
+ *           MGQ_ERR_INVALID_ARG in the device error word, nothing written); NULL
+ *           with E = 1: one group of all R rows, a plain product
+ *  y, dx    device, out_dtype (mgq_out_dtype), row pitch ldy, lddx; rows outside
+ *           every group are left as they were. Must not overlap an input.
+ *  dw       device [E, N, K], contiguous; bf16 with beta 0 only. beta 0
+ *           overwrites it whatever it held; an empty group gives beta dW
+ * What lies in rows of no group, or of another group, does not reach a result,
+ * NaN and infinity included. A row's result (wgrad: a group's) does not depend on
+ * the other groups' rows; the same call gives the same bits.
+ * Requires 1 <= E <= 1024, R < 2^31 - 512 (0: fwd and dgrad do nothing), N, K and
+ * the row pitches multiples of 8, 16-byte aligned pointers. */
+int mgq_ragged_gemm_fwd(const void* x_bf16, int64_t ldx, const void* w_bf16, const int32_t* offsets, int E,
+                        int64_t R, int64_t N, int64_t K, void* y, int64_t ldy, int out_dtype, void* stream);
+int mgq_ragged_gemm_dgrad(const void* dy_bf16, int64_t lddy, const void* w_bf16, const int32_t* offsets, int E,
+                          int64_t R, int64_t N, int64_t K, void* dx, int64_t lddx, int out_dtype, void* stream);
+int mgq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void* x_bf16, int64_t ldx,
+                          const int32_t* offsets, int E, int64_t R, int64_t N, int64_t K, float beta, void* dw,
+                          int out_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
