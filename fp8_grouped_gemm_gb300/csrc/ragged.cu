@@ -20,21 +20,20 @@
 // by the tensor cores. wgrad contracts over the tokens: rows of the last 16-row
 // step that belong to the next group are zeroed in shared memory, in both
 // operands (0 times a NaN of another group is a NaN).
-#include "device_common.cuh"
-#include "mgq_internal.h"
-#include "ptx_sm100.cuh"
+#include "ragged.cuh"
 
 namespace mgq {
 namespace {
 
-enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
-
 constexpr int kBK = 64;                            // elements of the contraction a stage (128 bytes)
-constexpr int kTile = 256;                         // M side, and tokens (wgrad: columns) at most
-constexpr int kMaxE = 1024;
 constexpr uint32_t kOpBytes = 128 * 128;           // one operand's share of an SM a stage
-constexpr uint32_t kSmallBox = 32;                 // rows of the token boxes of a group's last tile
 constexpr uint32_t kOutSlot = 32 * 128;            // wgrad: a warp's store staging
+// float32 results: the tensor cores cut each sum off rather than round it, and
+// the error grows with every K=16 step (1.5e-8 a step, relative: 4.4e-6 after a
+// contraction of 4096, which a float32 result shows and a bf16 one does not).
+// So after kPromote stages the partial sum moves to registers of the epilogue,
+// where it is added with rounding, while the other accumulator goes on.
+constexpr int kPromote = 8;
 __host__ __device__ constexpr int stages_of(int op) { return op == kWgrad ? 5 : 6; }
 __host__ __device__ constexpr int threads_of(int op) { return op == kWgrad ? 352 : 320; }
 __host__ __device__ constexpr size_t smem_of(int op) {
@@ -42,147 +41,7 @@ __host__ __device__ constexpr size_t smem_of(int op) {
 }
 static_assert(smem_of(kFwd) <= 232448 && smem_of(kWgrad) <= 232448, "shared memory");
 
-struct RaggedArgs {
-  const int32_t* offsets;   // [E + 1], or null: one group of all R rows
-  int E;
-  int64_t R;
-  int64_t M;                // fwd, dgrad: output columns; wgrad: rows of an expert's result
-  int64_t C;                // fwd, dgrad: length of the contraction; wgrad: columns of the result
-  void* out;
-  int64_t ldo;              // fwd, dgrad: row pitch of the result
-  int out_f32;
-  float beta;
-  int stall;                // failure-detection test: no loads are issued
-  uint64_t wait_ns;
-  int* err;
-};
-
-struct RaggedTile {
-  int e, nst;               // group, contraction stages
-  int row0, n;              // fwd, dgrad: first token and tokens of the tile; wgrad: of the group
-  int64_t m0, c0;           // first row on the M side; wgrad: first column
-};
-
-// Order of the tiles of one group: bands of 8 along the M side (wgrad: along the
-// columns), inside a band the band's tiles fastest. A wave of tiles then covers
-// a block of about 8 x 9 and finds both operands' re-reads in L2.
-__device__ __forceinline__ void banded(int64_t local, int64_t slow, int64_t nfast, int64_t& fast, int64_t& s) {
-  constexpr int64_t kBand = 8;
-  const int64_t band = local / (kBand * slow), r = local - band * (kBand * slow);
-  const int64_t w = min(kBand, nfast - band * kBand);
-  s = r / w;
-  fast = band * kBand + (r - s * w);
-}
-
-template <int OP>
-__device__ __forceinline__ bool ragged_tile(const int32_t* s_off, const int32_t* s_cum, const RaggedArgs& p, int64_t t,
-                                            int& ecur, RaggedTile& tl) {
-  const int64_t nM = (p.M + kTile - 1) / kTile;
-  if (OP == kWgrad) {
-    const int64_t nC = (p.C + kTile - 1) / kTile, per = nM * nC;
-    if (t >= per * p.E) return false;
-    const int e = (int)(t / per);
-    int64_t c, m;
-    banded(t - e * per, nM, nC, c, m);
-    tl.e = e;
-    tl.row0 = s_off[e];
-    tl.n = s_off[e + 1] - s_off[e];
-    tl.nst = (tl.n + kBK - 1) / kBK;
-    tl.m0 = m * kTile;
-    tl.c0 = c * kTile;
-  } else {
-    if (t >= s_cum[p.E] * nM) return false;
-    while (ecur < p.E - 1 && s_cum[ecur + 1] * nM <= t) ++ecur;
-    const int e = ecur;
-    int64_t m, tk;
-    banded(t - s_cum[e] * nM, s_cum[e + 1] - s_cum[e], nM, m, tk);
-    tl.e = e;
-    tl.row0 = s_off[e] + (int)tk * kTile;
-    tl.n = min(kTile, s_off[e + 1] - tl.row0);
-    tl.nst = (int)((p.C + kBK - 1) / kBK);
-    tl.m0 = m * kTile;
-    tl.c0 = 0;
-  }
-  return true;
-}
-
-// Offsets into shared memory with the running count of token tiles, by one warp;
-// true if they are a row partition (not negative, not decreasing, within R).
-__device__ __forceinline__ bool load_groups(const RaggedArgs& p, int32_t* s_off, int32_t* s_cum, uint32_t lane) {
-  int cum = 0;
-  bool ok = true;
-  for (int b = 0; b < p.E; b += 32) {
-    const int e = b + (int)lane;
-    const bool in = e < p.E;
-    const int lo = in && p.offsets ? p.offsets[e] : 0;
-    const int hi = !in ? 0 : p.offsets ? p.offsets[e + 1] : (int)p.R;
-    ok &= !in || (lo >= 0 && lo <= hi && hi <= p.R);
-    const int mine = in && lo <= hi ? (hi - lo + kTile - 1) / kTile : 0;
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (in) {
-      s_off[e] = lo;
-      s_cum[e] = cum + inc - mine;
-      if (e == p.E - 1) {
-        s_off[p.E] = hi;
-        s_cum[p.E] = cum + inc;
-      }
-    }
-    cum += __shfl_sync(0xFFFFFFFFu, inc, 31);
-  }
-  return __all_sync(0xFFFFFFFFu, ok);
-}
-
-// 8 x 8 transposition among groups of 8 lanes: v[j] of lane l is (row l, column
-// j); the result is row pairs in words, o[i] = rows 2i, 2i + 1 of column l & 7,
-// rounded to bf16.
-__device__ __forceinline__ uint4 transpose8_bf16(const float* v, uint32_t lane) {
-  const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float other = __shfl_xor_sync(0xFFFFFFFFu, b0 ? v[2 * i] : v[2 * i + 1], 1);
-    w[i] = b0 ? pack_bf16x2(other, v[2 * i + 1]) : pack_bf16x2(v[2 * i], other);
-  }
-  uint32_t q[2][2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, b1 ? w[2 * j] : w[2 * j + 1], 2);
-    q[j][0] = b1 ? other : w[2 * j];
-    q[j][1] = b1 ? w[2 * j + 1] : other;
-  }
-  const uint32_t o0 = __shfl_xor_sync(0xFFFFFFFFu, b2 ? q[0][0] : q[1][0], 4);
-  const uint32_t o1 = __shfl_xor_sync(0xFFFFFFFFu, b2 ? q[0][1] : q[1][1], 4);
-  return b2 ? make_uint4(o0, o1, q[1][0], q[1][1]) : make_uint4(q[0][0], q[0][1], o0, o1);
-}
-
-// 32 tokens of a warp's 32 channels: v[j] = (channel chan0 + lane, token tok0 + j).
-// `left` tokens exist.
-__device__ __forceinline__ void store_tokens(void* out, int64_t ldo, int out_f32, const float (&v)[32], int64_t tok0,
-                                             int left, int64_t chan0, int64_t chans, uint32_t lane) {
-  if (out_f32) {
-    float* o = static_cast<float*>(out) + tok0 * ldo + chan0 + lane;
-    const bool in = chan0 + lane < chans;
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (in && j < left) o[j * ldo] = v[j];
-  } else {
-    const int64_t c = chan0 + (lane & 24);
-    uint16_t* o = static_cast<uint16_t*>(out) + (tok0 + (lane & 7)) * ldo + c;
-#pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      if (j >= left) break;                                // the same in the whole warp
-      const uint4 w = transpose8_bf16(v + j, lane);
-      if (j + (int)(lane & 7) < left && c < chans) *reinterpret_cast<uint4*>(o + j * ldo) = w;
-    }
-  }
-}
-
-template <int OP>
+template <int OP, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     ragged_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmS, const RaggedArgs p) {
@@ -304,12 +163,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     bool ok = true;
     for (int64_t t = pair; ok && ragged_tile<OP>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
       if (tl.nst == 0) continue;
-      const uint32_t a = tc & 1, aph = (tc >> 1) & 1;
-      ok = !*s_abort && ptx::mbar_wait(&tmem_empty[a], aph ^ 1, p.wait_ns);
-      ptx::tc_fence_after();
       const uint32_t N = OP == kWgrad ? 256u : (uint32_t)(tl.n + 31) / 32 * 32;
       const uint32_t idesc = ptx::idesc_f16(1, 256, N) | ptx::idesc_mn_major(kAmn, kBmn);
-      for (int s = 0; ok && s < tl.nst; ++s, ++it) {
+      uint32_t a = 0;
+      for (int s = 0; s < tl.nst; ++s, ++it) {
+        const bool first = s == 0 || (F32 && s % kPromote == 0);   // of an accumulator
+        if (first) {
+          a = tc & 1;
+          ok = !*s_abort && ptx::mbar_wait(&tmem_empty[a], ((tc >> 1) & 1) ^ 1, p.wait_ns);
+          if (!ok) break;
+        }
         const uint32_t st = it % ST, ph = (it / ST) & 1;
         ok = !*s_abort && ptx::mbar_wait(&full[st], ph, p.wait_ns);
         int steps = kBK / 16;
@@ -331,12 +194,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
         // a K=16 step: 32 bytes along a K-major row, 16 rows (2048 bytes) of an MN-major tile
         constexpr uint64_t da = kAmn ? 128 : 2, db = kBmn ? 128 : 2;
         for (int kk = 0; kk < steps; ++kk)
-          ptx::mma_f16_pair(tmem + a * kTile, ad + kk * da, bd + kk * db, idesc, (s > 0 || kk > 0) ? 1u : 0u);
+          ptx::mma_f16_pair(tmem + a * kTile, ad + kk * da, bd + kk * db, idesc, (!first || kk > 0) ? 1u : 0u);
         ptx::mma_commit_pair(&empty[st], 0x3);        // frees the stage in both CTAs
+        if (s == tl.nst - 1 || (F32 && s % kPromote == kPromote - 1)) {
+          ptx::mma_commit_pair(&tmem_full[a], 0x3);
+          ++tc;
+        }
       }
-      if (!ok) break;
-      ptx::mma_commit_pair(&tmem_full[a], 0x3);
-      ++tc;
     }
     if (!ok) {
       report(p.err, MGQ_ERR_TIMEOUT);
@@ -354,69 +218,100 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     int ecur = 0;
     uint32_t tc = 0;
     RaggedTile tl;
-    for (int64_t t = pair; ragged_tile<OP>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
-      const uint32_t a = tc & 1, aph = (tc >> 1) & 1;
+    bool ok = true;
+    for (int64_t t = pair; ok && ragged_tile<OP>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
       const int64_t m0 = tl.m0 + 128 * rank + 32 * q;       // this warp's 32 rows of the M side
-      if (tl.nst > 0) {
+      // its columns: four runs of 32 (the rows' products: every second run, so that
+      // a short tile's tokens are shared by both warps)
+      const int width = OP == kWgrad ? (int)min((int64_t)kTile, p.C - tl.c0) : tl.n;
+      auto col = [&](int i) { return OP == kWgrad ? 128 * (int)half + 32 * i : 32 * (int)half + 64 * i; };
+      float v[F32 ? 4 : 1][32];
+      const int parts = tl.nst == 0 ? 0 : F32 ? (tl.nst + kPromote - 1) / kPromote : 1;
+      if (F32 && parts == 0) {
+#pragma unroll
+        for (int i = 0; i < (F32 ? 4 : 1); ++i)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[i][j] = 0.0f;
+      }
+      // the next accumulator, and its release once it is read
+      auto wait_acc = [&]() {
         bool got = *s_abort == 0;
-        got = got && ptx::mbar_wait(&tmem_full[a], aph, p.wait_ns);
+        got = got && ptx::mbar_wait(&tmem_full[tc & 1], (tc >> 1) & 1, p.wait_ns);
         if (!__all_sync(0xFFFFFFFFu, got)) {
           report(p.err, MGQ_ERR_TIMEOUT);
           *s_abort = 1;
-          break;
+          return false;
         }
         ptx::tc_fence_after();
-      }
-      const uint32_t tbase = tmem + a * kTile + ((q * 32) << 16);
-      if (OP != kWgrad) {
-        for (int c = 32 * half; c < tl.n; c += 64) {
-          uint32_t r[32];
-          ptx::tmem_ld_32x32b_x32(tbase + c, r);
-          ptx::tmem_ld_wait();
-          float v[32];
+        return true;
+      };
+      auto release_acc = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(tc & 1 ? empty1 : empty0);
+        ++tc;
+      };
+      auto load = [&](int i, float (&d)[32], bool add) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-          store_tokens(p.out, p.ldo, p.out_f32, v, (int64_t)tl.row0 + c, tl.n - c, m0, p.M, lane);
+        for (int h = 0; h < 32; h += 16) {
+          uint32_t r[16];
+          ptx::tmem_ld_32x32b_x16(tmem + (tc & 1) * kTile + ((q * 32) << 16) + col(i) + h, r);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) d[h + j] = add ? d[h + j] + __uint_as_float(r[j]) : __uint_as_float(r[j]);
+        }
+      };
+      if (F32) {
+        for (int part = 0; part < parts; ++part) {
+          if (!(ok = wait_acc())) break;
+#pragma unroll
+          for (int i = 0; i < (F32 ? 4 : 1); ++i)
+            if (col(i) < width) load(i, v[i], part > 0);
+          release_acc();
+        }
+        if (!ok) break;
+      } else if (parts) {
+        if (!(ok = wait_acc())) break;
+      }
+      if (OP != kWgrad) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (col(i) >= width) break;
+          float(&x)[32] = v[F32 ? i : 0];
+          if (!F32) load(i, x, false);
+          store_tokens<F32>(p.out, p.ldo, x, (int64_t)tl.row0 + col(i), width - col(i), m0, p.M, lane);
         }
       } else if (m0 < p.M) {
-        const bool row_in = m0 + lane < p.M;
-        const int wide = p.out_f32 ? 32 : 64;               // columns of a 128-byte staging row
-        for (int c = 128 * half; c < 128 * (int)half + 128 && tl.c0 + c < p.C; c += wide) {
-          uint32_t w[32];
-          if (p.out_f32) {
-            if (tl.nst > 0) {
-              ptx::tmem_ld_32x32b_x32(tbase + c, w);
-              ptx::tmem_ld_wait();
-            } else {
+        // staged rows of 128 bytes: 32 float32 columns, or 64 of bf16
 #pragma unroll
-              for (int j = 0; j < 32; ++j) w[j] = 0;
-            }
-            if (p.beta != 0.0f && row_in) {
+        for (int i = 0; i < 4; i += F32 ? 1 : 2) {
+          const int c = col(i);
+          if (c >= width) break;
+          uint32_t w[32];
+          if (F32) {
+            if (p.beta != 0.0f && m0 + lane < p.M) {
               const float* old = static_cast<const float*>(p.out) + ((int64_t)tl.e * p.M + m0 + lane) * p.C + tl.c0 + c;
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
-                if (tl.c0 + c + j >= p.C) break;            // (C is a multiple of 8)
+                if (c + j >= width) break;                  // (the width is a multiple of 8)
                 const float4 o = *reinterpret_cast<const float4*>(old + j);
-                w[j] = __float_as_uint(fmaf(p.beta, o.x, __uint_as_float(w[j])));
-                w[j + 1] = __float_as_uint(fmaf(p.beta, o.y, __uint_as_float(w[j + 1])));
-                w[j + 2] = __float_as_uint(fmaf(p.beta, o.z, __uint_as_float(w[j + 2])));
-                w[j + 3] = __float_as_uint(fmaf(p.beta, o.w, __uint_as_float(w[j + 3])));
+                float* x = v[F32 ? i : 0] + j;
+                x[0] = fmaf(p.beta, o.x, x[0]);
+                x[1] = fmaf(p.beta, o.y, x[1]);
+                x[2] = fmaf(p.beta, o.z, x[2]);
+                x[3] = fmaf(p.beta, o.w, x[3]);
               }
             }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[F32 ? i : 0][j]);
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              uint32_t r[32];
-              if (tl.nst > 0) {
-                ptx::tmem_ld_32x32b_x32(tbase + c + 32 * h, r);
-                ptx::tmem_ld_wait();
-              } else {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = 0;
-              }
+              for (int j = 0; j < 32; ++j) v[0][j] = 0.0f;
+              if (parts) load(i + h, v[0], false);
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                w[16 * h + j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+              for (int j = 0; j < 16; ++j) w[16 * h + j] = pack_bf16x2(v[0][2 * j], v[0][2 * j + 1]);
             }
           }
           if (lane == 0) ptx::bulk_wait_read0();            // the store before has read the staging slot
@@ -433,12 +328,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
           }
         }
       }
-      if (tl.nst > 0) {
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(a ? empty1 : empty0);
-        ++tc;
-      }
+      if (!F32 && parts) release_acc();
     }
     if (OP == kWgrad && lane == 0) ptx::bulk_wait0();       // this warp's stores are complete
   } else if (OP == kWgrad && run && warp == 10) {
@@ -478,10 +368,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   }
 }
 
-template <int OP>
+template <int OP, bool F32>
 int launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ts, const RaggedArgs& p,
                 int64_t max_tiles, cudaStream_t s) {
-  auto kern = ragged_pair_kernel<OP>;
+  auto kern = ragged_pair_kernel<OP, F32>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -543,7 +433,9 @@ int run_rows(const void* in, int64_t ldi, const void* w, const int32_t* offsets,
       !encode_tmap_sw128_3d(&ts, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, kSmallBox, 1}))
     return MGQ_ERR_CUDA;
   const int64_t tiles = (R / kTile + min((int64_t)E, R)) * ((M + kTile - 1) / kTile);
-  return launch_pair<OP>(ta, tb, ts, p, tiles, as_stream(stream));
+  p.bk = kBK;
+  return p.out_f32 ? launch_pair<OP, true>(ta, tb, ts, p, tiles, as_stream(stream))
+                   : launch_pair<OP, false>(ta, tb, ts, p, tiles, as_stream(stream));
 }
 
 }  // namespace
@@ -594,7 +486,9 @@ int mgq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void* x_bf16,
                             {(uint32_t)(128 / u), 32, 1}))
     return MGQ_ERR_CUDA;
   const int64_t tiles = (int64_t)E * ((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile);
-  return launch_pair<kWgrad>(ta, tb, to, p, tiles, as_stream(stream));
+  p.bk = kBK;
+  return p.out_f32 ? launch_pair<kWgrad, true>(ta, tb, to, p, tiles, as_stream(stream))
+                   : launch_pair<kWgrad, false>(ta, tb, to, p, tiles, as_stream(stream));
 }
 
 }  // extern "C"

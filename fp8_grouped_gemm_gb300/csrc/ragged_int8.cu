@@ -1,0 +1,446 @@
+// int8 products grouped by expert over ragged groups (offsets null: a plain
+// matrix product), and the quantiser that makes their codes.
+//
+//   Y[r, n] = sx[r] sw[e, n] sum_k Xq[r, k] Wq[e, n, k],   r in [offsets[e], offsets[e+1])
+//   s = amax / 127,  q = round(127 x / amax), a half to the even neighbour, per row
+//
+// GB300's tensor cores have no int8 form worth using. Every int8 value is an f16
+// value, though, products of two are exact in f32, and a sum of them is exact
+// while it stays below 2^24: so the codes travel as bytes, half of what bf16
+// would read, and become f16 beside the tensor cores. The tiles are those of the
+// bf16 products: two SMs share 256 output channels by up to 256 tokens.
+//   warp 0        TMA: 128 channels and up to 128 tokens of 128 bytes a stage
+//   warps 2-5     channels: bytes -> f16 -> tensor memory, the MMA's A operand
+//   warps 6-9     tokens: bytes -> f16 -> shared memory, swizzled, the B operand
+//   warp 1        (CTA 0) issues the MMAs of both SMs
+//   warps 10-17   epilogue: scales, transposition, stores
+// A byte b becomes f16 by one permutation and one subtraction for two: 0x6400 |
+// (b ^ 0x80) is 1152 + b as f16. The channels' operand in tensor memory leaves
+// shared memory's bandwidth to the tokens' one; its stages take the columns of a
+// second accumulator, so a tile's MMAs wait for the tile before to be read.
+#include "ragged.cuh"
+
+#include <cuda_fp16.h>
+
+namespace mgq {
+namespace {
+
+constexpr int kBK8 = 128;                          // elements (bytes) of the contraction a stage
+constexpr int kRaw = 3, kConv = 3;                 // stages of bytes, and of f16
+constexpr uint32_t kRawBytes = 128 * 128;          // one operand's bytes of a stage
+constexpr uint32_t kF16Bytes = 128 * 256;          // the tokens' f16 of a stage: two 64-element halves
+constexpr uint32_t kAcol = 256, kAcols = 64;       // tensor memory: the channels' stages
+constexpr int kThreads8 = 18 * 32;
+constexpr size_t kSmem8 = 1024 + kRaw * 2 * (size_t)kRawBytes + kConv * (size_t)kF16Bytes + 8 * 128 + 256 +
+                          2 * (kMaxE + 8) * 4;
+static_assert(kSmem8 <= 232448 && kAcol + kConv * kAcols <= 512, "shared and tensor memory");
+
+// 16 codes -> 16 f16 values in 8 words
+__device__ __forceinline__ void widen16(const uint4& c, uint32_t* o) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = w[i] ^ 0x80808080u;
+    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 base = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
+    __half2 a = __hsub2(*reinterpret_cast<__half2*>(&lo), base), b = __hsub2(*reinterpret_cast<__half2*>(&hi), base);
+    o[2 * i] = *reinterpret_cast<uint32_t*>(&a);
+    o[2 * i + 1] = *reinterpret_cast<uint32_t*>(&b);
+  }
+}
+
+template <bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
+    ragged_int8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmS, const RaggedArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  uint8_t* sA = smem_raw + (((raw + 1023u) & ~1023u) - raw);   // [kRaw] bytes of the channels
+  uint8_t* sB = sA + kRaw * kRawBytes;                         // [kRaw] bytes of the tokens
+  uint8_t* sF = sB + kRaw * kRawBytes;                         // [kConv] f16 of the tokens
+  float* sX = reinterpret_cast<float*>(sF + kConv * kF16Bytes);   // [8 warps][32] token scales
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(sX + 8 * 32);
+  uint64_t* raw_empty = raw_full + kRaw;
+  uint64_t* conv_full = raw_empty + kRaw;
+  uint64_t* conv_empty = conv_full + kConv;
+  uint64_t* acc_full = conv_empty + kConv;
+  uint64_t* acc_empty = acc_full + 1;
+  uint64_t* drained = acc_empty + 1;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_bad = reinterpret_cast<int*>(s_tmem + 2);
+  int32_t* s_off = reinterpret_cast<int32_t*>(raw_full + 32);
+  int32_t* s_cum = s_off + (kMaxE + 8);
+
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const bool leader = rank == 0;
+  const int64_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kRaw; ++s) {
+      ptx::mbar_init(&raw_full[s], 1);
+      ptx::mbar_init(&raw_empty[s], 8);            // one arrival per converting warp
+    }
+    for (int s = 0; s < kConv; ++s) {
+      ptx::mbar_init(&conv_full[s], 2 * 8);        // ... of both CTAs
+      ptx::mbar_init(&conv_empty[s], 1);
+    }
+    ptx::mbar_init(acc_full, 1);
+    ptx::mbar_init(acc_empty, 2 * 8);
+    ptx::mbar_init(drained, 1);
+    *s_abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmB);
+    ptx::prefetch_tmap(&tmS);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(s_tmem, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  if (warp == 2) {
+    const bool ok = load_groups(p, s_off, s_cum, lane);
+    if (lane == 0) {
+      *s_bad = ok ? 0 : 1;
+      if (!ok) report(p.err, MGQ_ERR_INVALID_ARG);
+    }
+  }
+  __syncthreads();
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const bool run = *s_bad == 0;
+  auto timed_out = [&]() {
+    report(p.err, MGQ_ERR_TIMEOUT);
+    *s_abort = 1;
+  };
+
+  if (run && warp == 0 && lane == 0 && !p.stall) {
+    // ------------------------------------------------------------ producer (both CTAs)
+    int ecur = 0;
+    uint32_t it = 0;
+    RaggedTile tl;
+    for (int64_t t = pair; !*s_abort && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
+      const int half = (tl.n + 31) / 32 * 16;      // this CTA's tokens
+      const int boxes = half == 128 ? 0 : (half + (int)kSmallBox - 1) / (int)kSmallBox;
+      const uint32_t bytes = kRawBytes + (boxes ? boxes * kSmallBox * 128 : kRawBytes);
+      for (int s = 0; s < tl.nst; ++s, ++it) {
+        const uint32_t st = it % kRaw;
+        if (*s_abort) break;
+        if (!ptx::mbar_wait(&raw_empty[st], ((it / kRaw) & 1) ^ 1, p.wait_ns)) {
+          timed_out();
+          break;
+        }
+        ptx::mbar_arrive_expect_tx(&raw_full[st], bytes);
+        const int32_t kx = s * kBK8, r = tl.row0 + half * (int)rank;
+        ptx::tma_load_3d(sA + st * kRawBytes, &tmA, &raw_full[st], kx, (int32_t)(tl.m0 + 128 * rank), tl.e);
+        if (!boxes) ptx::tma_load_3d(sB + st * kRawBytes, &tmB, &raw_full[st], kx, r, 0);
+        for (int i = 0; i < boxes; ++i)
+          ptx::tma_load_3d(sB + st * kRawBytes + i * kSmallBox * 128, &tmS, &raw_full[st], kx, r + i * (int)kSmallBox, 0);
+      }
+    }
+    // after a wait that ran out: no copy may still be on its way when the CTA leaves
+    if (*s_abort)
+      for (uint32_t i = it > kRaw ? it - kRaw : 0; i < it; ++i)
+        ptx::mbar_wait(&raw_full[i % kRaw], (i / kRaw) & 1, p.wait_ns);
+  } else if (run && leader && warp == 1 && lane == 0) {
+    // ------------------------------------------------------------ MMA issuer (CTA 0)
+    int ecur = 0;
+    uint32_t it = 0, tc = 0;
+    RaggedTile tl;
+    const uint32_t sF0 = ptx::smem_u32(sF);
+    bool ok = true;
+    for (int64_t t = pair; ok && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs, ++tc) {
+      const uint32_t idesc = ptx::idesc_f16(0, 256, (uint32_t)(tl.n + 31) / 32 * 32);
+      ok = !*s_abort && ptx::mbar_wait(acc_empty, (tc & 1) ^ 1, p.wait_ns);
+      for (int s = 0; ok && s < tl.nst; ++s, ++it) {
+        const uint32_t st = it % kConv;
+        ok = !*s_abort && ptx::mbar_wait(&conv_full[st], (it / kConv) & 1, p.wait_ns);
+        if (!ok) break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kBK8 / 16; ++kk)
+          ptx::mma_f16_ta_pair(tmem, tmem + kAcol + st * kAcols + kk * 8,
+                               ptx::sdesc_kmajor_sw128(sF0 + st * kF16Bytes + (kk >> 2) * (kF16Bytes / 2)) + (kk & 3) * 2,
+                               idesc, (s > 0 || kk > 0) ? 1u : 0u);
+        ptx::mma_commit_pair(&conv_empty[st], 0x3);
+      }
+      if (ok) ptx::mma_commit_pair(acc_full, 0x3);
+    }
+    if (!ok) {
+      timed_out();
+      ptx::mma_commit_pair(drained, 0x1);          // the MMAs issued so far finish before the CTA leaves
+      ptx::mbar_wait(drained, 0, p.wait_ns);
+    }
+  } else if (run && warp >= 2 && warp < 10) {
+    // ------------------------------------------------------------ bytes to f16
+    const bool chan = warp < 6;
+    const uint32_t row = (chan ? (warp & 3) : warp - 6) * 32 + lane;   // channels: the warp's own lanes of tensor memory
+    int ecur = 0;
+    uint32_t it = 0;
+    RaggedTile tl;
+    bool ok = true;
+    for (int64_t t = pair; ok && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
+      const bool mine = chan || (int)row - (int)lane < (tl.n + 31) / 32 * 16;   // tokens: the rows an MMA reads
+      for (int s = 0; s < tl.nst; ++s, ++it) {
+        const uint32_t rs = it % kRaw, cs = it % kConv;
+        ok = *s_abort == 0;
+        ok = ok && ptx::mbar_wait(&raw_full[rs], (it / kRaw) & 1, p.wait_ns);
+        ok = ok && ptx::mbar_wait(&conv_empty[cs], ((it / kConv) & 1) ^ 1, p.wait_ns);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        uint4 c[8];
+        if (mine) {
+          const uint8_t* src = (chan ? sA : sB) + rs * kRawBytes + row * 128;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&raw_empty[rs]);
+        if (chan) {
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) widen16(c[4 * h + j], o + 8 * j);
+            ptx::tmem_st_32x32b_x32(tmem + kAcol + cs * kAcols + 32 * h + ((32u * (warp & 3)) << 16), o);
+          }
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+        } else if (mine) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint32_t o[8];
+            widen16(c[j], o);
+            uint8_t* dst = sF + cs * kF16Bytes + (j >> 2) * (kF16Bytes / 2) + row * 128;
+            *reinterpret_cast<uint4*>(dst + ((((2 * j) & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + ((((2 * j + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          ptx::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&conv_full[cs]), 0));
+      }
+    }
+    if (!ok) timed_out();
+  } else if (run && warp >= 10) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const uint32_t q = warp & 3;
+    const uint32_t half = (uint32_t)(warp - 10) >> 2;
+    const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(acc_empty), 0);
+    float* sx = sX + (warp - 10) * 32;
+    int ecur = 0;
+    uint32_t tc = 0;
+    RaggedTile tl;
+    for (int64_t t = pair; ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs, ++tc) {
+      const int64_t m0 = tl.m0 + 128 * rank + 32 * q;
+      const float sw = m0 + lane < p.M ? p.sw[tl.e * p.M + m0 + lane] : 0.0f;
+      bool got = *s_abort == 0;
+      got = got && ptx::mbar_wait(acc_full, tc & 1, p.wait_ns);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        timed_out();
+        break;
+      }
+      ptx::tc_fence_after();
+      for (int c = 32 * half; c < tl.n; c += 64) {
+        __syncwarp();
+        sx[lane] = c + (int)lane < tl.n ? p.sx[(int64_t)tl.row0 + c + lane] : 0.0f;
+        uint32_t r[32];
+        ptx::tmem_ld_32x32b_x32(tmem + c + ((q * 32) << 16), r);
+        ptx::tmem_ld_wait();
+        __syncwarp();
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * (sx[j] * sw);
+        store_tokens<F32>(p.out, p.ldo, v, (int64_t)tl.row0 + c, tl.n - c, m0, p.M, lane);
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(empty0);
+    }
+  }
+  __syncthreads();
+  ptx::tc_fence_before();
+  ptx::cluster_sync();                 // the peer's MMAs and reads are finished before freeing
+  ptx::tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <bool F32>
+int launch_int8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ts, const RaggedArgs& p,
+                int64_t max_tiles, cudaStream_t s) {
+  auto kern = ragged_int8_kernel<F32>;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return MGQ_ERR_CUDA;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem8) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return MGQ_ERR_CUDA;
+    }
+    attr_set[dev] = true;
+  }
+  const int64_t pairs = min((int64_t)(num_sms() / 2), max_tiles);
+  kern<<<(unsigned)(2 * max(pairs, (int64_t)1)), kThreads8, kSmem8, s>>>(ta, tb, ts, p);
+  MGQ_LAUNCH_CHECK();
+  return MGQ_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Row quantiser. G threads a row, each up to two units of 16 elements in
+// registers (longer rows are read twice). The code is round(127 x / amax) of the
+// exact quotient, decided in float32: with x = a 2^i, amax = b 2^j (8-bit a, b) a
+// quotient that is not halfway between two integers is away from it by at least
+// 1 / (254 * 255) = 2^-16 of its value, and one that is has 9 significant bits; so
+// the product with the rounded 127 / amax (within 2^-22) is rounded to 20 bits
+// first, which puts the halves back in place and moves nothing across one.
+
+struct Quant8Args {
+  const uint16_t* x;
+  int64_t ldx, T;
+  int K;
+  int8_t* codes;
+  float* scale;
+};
+
+__device__ __forceinline__ uint32_t code8(float x, float pre, float inv) {
+  const uint32_t b = __float_as_uint(__fmul_rn(__fmul_rn(x, pre), inv));
+  return __float_as_uint(__fadd_rn(__uint_as_float((b + 8u) & ~15u), 12582912.0f));    // 1.5 2^23: integer in the low bits
+}
+__device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float pre, float inv) {
+  const uint32_t a = __byte_perm(code8(bf16_lo(w0), pre, inv), code8(bf16_hi(w0), pre, inv), 0x0040);
+  const uint32_t b = __byte_perm(code8(bf16_lo(w1), pre, inv), code8(bf16_hi(w1), pre, inv), 0x0040);
+  return __byte_perm(a, b, 0x5410);
+}
+
+template <int G>
+__global__ void __launch_bounds__(G < 128 ? 128 : G) rows_quant8_kernel(Quant8Args a) {
+  constexpr int kRows = G < 128 ? 128 / G : 1;
+  __shared__ uint32_t s_max[G / 32];
+  const int tid = threadIdx.x % G, lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x * (int64_t)kRows + threadIdx.x / G;
+  if (row >= a.T) return;                          // (whole warps; a row of several warps is the CTA)
+  const uint4* x = reinterpret_cast<const uint4*>(a.x + row * a.ldx);
+  const int units = a.K / 16;
+  uint4 w[2][2];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int u = tid + i * G;
+    if (u < units) {
+      w[i][0] = x[2 * u];
+      w[i][1] = x[2 * u + 1];
+    } else {
+      w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      m = absmax_bf16x2(m, w[i][h].x);
+      m = absmax_bf16x2(m, w[i][h].y);
+      m = absmax_bf16x2(m, w[i][h].z);
+      m = absmax_bf16x2(m, w[i][h].w);
+    }
+  for (int u = tid + 2 * G; u < units; u += G)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 v = x[2 * u + h];
+      m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, v.x), v.y), v.z), v.w);
+    }
+  uint32_t bits = fold_bf16x2(m);
+  bits = __reduce_max_sync(0xFFFFFFFFu, bits);
+  if (G > 32) {
+    if (lane == 0) s_max[threadIdx.x >> 5] = bits;
+    __syncthreads();
+    bits = lane < G / 32 ? s_max[lane] : 0u;
+    bits = __reduce_max_sync(0xFFFFFFFFu, bits);
+  }
+  const bool finite = bits < 0x7F800000u;
+  const float amax = __uint_as_float(bits);
+  // (127 / amax overflows below 2^-121: such rows are scaled up first, exactly)
+  const float pre = amax < 0x1p-100f ? 0x1p100f : 1.0f;
+  const float inv = !finite || amax == 0.0f ? 0.0f : __fdiv_rn(127.0f, __fmul_rn(amax, pre));
+  if (tid == 0) a.scale[row] = finite ? __fdiv_rn(amax, 127.0f) : __uint_as_float(0x7FC00000u);
+  uint4* out = reinterpret_cast<uint4*>(a.codes + row * a.K);
+  auto put = [&](int u, const uint4& p, const uint4& q) {
+    out[u] = finite ? make_uint4(codes4(p.x, p.y, pre, inv), codes4(p.z, p.w, pre, inv), codes4(q.x, q.y, pre, inv),
+                                 codes4(q.z, q.w, pre, inv))
+                    : make_uint4(0, 0, 0, 0);
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (tid + i * G < units) put(tid + i * G, w[i][0], w[i][1]);
+  for (int u = tid + 2 * G; u < units; u += G) put(u, x[2 * u], x[2 * u + 1]);
+}
+
+}  // namespace
+}  // namespace mgq
+
+using namespace mgq;
+
+extern "C" {
+
+int mgq_ragged_gemm_int8(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w, const float* w_scale,
+                         const int32_t* offsets, int E, int64_t R, int64_t N, int64_t K, void* y, int64_t ldy,
+                         int out_dtype, void* stream) {
+  MGQ_CHECK_ARG(E >= 1 && E <= kMaxE && R >= 0 && R < (1ll << 31) - 512 && N > 0 && K > 0);
+  MGQ_CHECK_ARG(N % 8 == 0 && K % 16 == 0 && N < (1ll << 31) - 512 && K < (1ll << 31) - 512);
+  MGQ_CHECK_ARG((offsets || E == 1) && (reinterpret_cast<uintptr_t>(offsets) & 3u) == 0);
+  MGQ_CHECK_ARG(out_dtype == MGQ_OUT_BF16 || out_dtype == MGQ_OUT_F32);
+  MGQ_CHECK_ARG(ldx >= K && ldx % 16 == 0 && ldx < (1ll << 39) && ldy >= N && ldy % 8 == 0 && ldy < (1ll << 38));
+  MGQ_CHECK_ARG(R == 0 || (x && x_scale && w && w_scale && y));
+  MGQ_CHECK_ARG(aligned16(x) && aligned16(w) && aligned16(y) && (reinterpret_cast<uintptr_t>(x_scale) & 3u) == 0 &&
+                (reinterpret_cast<uintptr_t>(w_scale) & 3u) == 0);
+  if (R == 0) return MGQ_OK;
+  RaggedArgs p{};
+  p.err = error_word();
+  if (!p.err) return MGQ_ERR_CUDA;
+  p.offsets = offsets;
+  p.E = E;
+  p.R = R;
+  p.M = N;
+  p.C = K;
+  p.out = y;
+  p.ldo = ldy;
+  p.out_f32 = out_dtype == MGQ_OUT_F32;
+  p.bk = kBK8;
+  p.sx = x_scale;
+  p.sw = w_scale;
+  debug_knobs(&p.stall, &p.wait_ns);
+  CUtensorMap ta, tb, ts;
+  if (!encode_tmap_sw128_3d(&ta, w, 1, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K, N * K, {128, 128, 1}) ||
+      !encode_tmap_sw128_3d(&tb, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, 128, 1}) ||
+      !encode_tmap_sw128_3d(&ts, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, kSmallBox, 1}))
+    return MGQ_ERR_CUDA;
+  const int64_t tiles = (R / kTile + min((int64_t)E, R)) * ((N + kTile - 1) / kTile);
+  return p.out_f32 ? launch_int8<true>(ta, tb, ts, p, tiles, as_stream(stream))
+                   : launch_int8<false>(ta, tb, ts, p, tiles, as_stream(stream));
+}
+
+int mgq_rows_quantize_int8(const void* x_bf16, int64_t ldx, int64_t T, int64_t K, int8_t* codes, float* scale,
+                           void* stream) {
+  MGQ_CHECK_ARG(T >= 0 && T < (1ll << 31) && K > 0 && K % 16 == 0 && K < (1ll << 31));
+  MGQ_CHECK_ARG(ldx >= K && ldx % 8 == 0 && (T == 0 || (x_bf16 && codes && scale)));
+  MGQ_CHECK_ARG(aligned16(x_bf16) && aligned16(codes) && (reinterpret_cast<uintptr_t>(scale) & 3u) == 0);
+  if (T == 0) return MGQ_OK;
+  Quant8Args a{static_cast<const uint16_t*>(x_bf16), ldx, T, (int)K, codes, scale};
+  cudaStream_t s = as_stream(stream);
+  const int64_t units = K / 16;
+  if (units <= 64) rows_quant8_kernel<32><<<(unsigned)((T + 3) / 4), 128, 0, s>>>(a);
+  else if (units <= 256) rows_quant8_kernel<128><<<(unsigned)T, 128, 0, s>>>(a);
+  else rows_quant8_kernel<512><<<(unsigned)T, 512, 0, s>>>(a);
+  MGQ_LAUNCH_CHECK();
+  return MGQ_OK;
+}
+
+}  // extern "C"

@@ -44,6 +44,7 @@ EXPORTS = (
     "mgq_add_rmsnorm_bwd", "mgq_router_topk", "mgq_router_topk_bwd",
     "mgq_moe_few_workspace_size", "mgq_moe_few_forward",
     "mgq_ragged_gemm_fwd", "mgq_ragged_gemm_dgrad", "mgq_ragged_gemm_wgrad",
+    "mgq_ragged_gemm_int8", "mgq_rows_quantize_int8",
 )
 
 
@@ -125,6 +126,8 @@ def load() -> ctypes.CDLL:
         lib.mgq_ragged_gemm_fwd.argtypes = rows
         lib.mgq_ragged_gemm_dgrad.argtypes = rows
         lib.mgq_ragged_gemm_wgrad.argtypes = [vp, i64, vp, i64, vp, i32, i64, i64, i64, f32, vp, i32, vp]
+        lib.mgq_ragged_gemm_int8.argtypes = [vp, i64, vp, vp, vp, vp, i32, i64, i64, i64, vp, i64, i32, vp]
+        lib.mgq_rows_quantize_int8.argtypes = [vp, i64, i64, i64, vp, vp, vp]
         for name in EXPORTS:
             if name != "mgq_status_string" and not name.endswith("_workspace_size"):
                 getattr(lib, name).restype = i32
@@ -352,7 +355,7 @@ def amax_history_update(history, head, amax, scale, fmax, stream=None):
 # The calls below check what the C entry points cannot see: place, type, shape
 # and strides of the tensors. A decode step waits for this code, so the checks
 # are written out where they are made: a helper's call costs as much as they do.
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_BF16, _F32, _I32, _I8 = torch.bfloat16, torch.float32, torch.int32, torch.int8
 _OUT_DTYPE = {torch.bfloat16: OUT_BF16, torch.float32: OUT_F32}
 
 
@@ -547,5 +550,43 @@ def ragged_gemm_wgrad(dy, x, offsets, dw, beta=0.0, stream=None):
     off, E, R, lddy, ldx = _ragged(fn, dy, N, dw, offsets, x, K)
     rc = (_lib or load()).mgq_ragged_gemm_wgrad(dy.data_ptr(), lddy, x.data_ptr(), ldx, off, E, R, N, K, beta,
                                                 dw.data_ptr(), dt, _s(stream))
+    if rc:
+        raise MGQError(rc, fn)
+
+
+def ragged_gemm_int8(x, x_scale, w, w_scale, offsets, y, stream=None):
+    """y[r] = x_scale[r] w_scale[e] (w[e] x[r]) for the rows of group e: x int8 [R, K], x_scale
+    float32 [R], w int8 [E, N, K], w_scale float32 [E, N], y bf16 or float32 [R, N]; offsets
+    int32 [E+1], or None with E = 1 (a plain product)."""
+    fn = "mgq_ragged_gemm_int8"
+    dt = _OUT_DTYPE.get(y.dtype)
+    if x.dtype is not _I8 or w.dtype is not _I8 or dt is None or w.dim() != 3:
+        _refuse(fn, ERR_UNSUPPORTED)
+    E, N, K = w.shape
+    off, E, R, ldx, ldy = _ragged(fn, x, K, w, offsets, y, N)
+    if not (x_scale.dtype is _F32 and x_scale.shape == (R,) and x_scale.is_contiguous() and
+            x_scale.get_device() == x.get_device() and w_scale.dtype is _F32 and w_scale.shape == (E, N) and
+            w_scale.is_contiguous() and w_scale.get_device() == x.get_device()):
+        _refuse(fn)
+    rc = (_lib or load()).mgq_ragged_gemm_int8(x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                                               off, E, R, N, K, y.data_ptr(), ldy, dt, _s(stream))
+    if rc:
+        raise MGQError(rc, fn)
+
+
+def rows_quantize_int8(x, codes, scale, stream=None):
+    """scale[t] = amax / 127, codes[t] = round(127 x / amax) for each row of x bf16 [T, K]: codes
+    int8 [T, K], scale float32 [T]."""
+    fn = "mgq_rows_quantize_int8"
+    if x.dtype is not _BF16 or codes.dtype is not _I8 or x.dim() != 2:
+        _refuse(fn, ERR_UNSUPPORTED)
+    T, K = x.shape
+    ldx = _pitch(x, T, K)
+    dev = torch.cuda.current_device()
+    if ldx < 0 or not (codes.shape == x.shape and codes.is_contiguous() and scale.dtype is _F32 and scale.shape == (T,) and
+                       scale.is_contiguous() and x.is_cuda and x.get_device() == dev and codes.is_cuda and
+                       codes.get_device() == dev and scale.is_cuda and scale.get_device() == dev):
+        _refuse(fn)
+    rc = (_lib or load()).mgq_rows_quantize_int8(x.data_ptr(), ldx, T, K, codes.data_ptr(), scale.data_ptr(), _s(stream))
     if rc:
         raise MGQError(rc, fn)

@@ -611,6 +611,35 @@ int mgq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void* x_bf16,
                           const int32_t* offsets, int E, int64_t R, int64_t N, int64_t K, float beta, void* dw,
                           int out_dtype, void* stream);
 
+/* ---- int8 products over ragged groups ----------------------------------------------
+ * The forward product on 8-bit integers with a scale for each token and for each
+ * output channel:
+ *   Y[r, n] = x_scale[r] w_scale[e, n] sum_k X[r, k] W[e, n, k],  r in group e
+ *  x        device int8 [R, K], row pitch ldx (elements); x_scale device float32 [R]
+ *  w        device int8 [E, N, K], contiguous; w_scale device float32 [E, N]
+ *  offsets, y, ldy, out_dtype  as mgq_ragged_gemm_fwd (NULL with E = 1: the plain
+ *           product of all R rows)
+ * Every code from -128 to 127 counts as it stands. The sum is held in float32:
+ * exact while it stays below 2^24 (K up to 1024 whatever the codes), beyond that
+ * within 2^-24 of the running sum for each 16 elements. Its product with
+ * (x_scale w_scale) is rounded to float32, then to the result's type. A NaN scale
+ * makes its row or channel NaN.
+ * Requires N a multiple of 8, K and ldx multiples of 16, ldy of 8; else as above. */
+int mgq_ragged_gemm_int8(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w,
+                         const float* w_scale, const int32_t* offsets, int E, int64_t R, int64_t N, int64_t K,
+                         void* y, int64_t ldy, int out_dtype, void* stream);
+
+/* Such codes and scales from bf16 rows (tokens, or the channels of a weight as
+ * rows of [E N, K]):
+ *   scale[t] = amax_t / 127,  codes[t, k] = the integer nearest to 127 x / amax_t,
+ * of the exact quotient, a half to the even neighbour; a row of zeros has scale 0
+ * and codes 0, a row with a NaN or an infinity scale NaN and codes 0.
+ *  x_bf16   device [T, K], row pitch ldx; codes device int8 [T, K], contiguous;
+ *           scale device float32 [T]
+ * Requires K a multiple of 16, ldx of 8, 0 <= T < 2^31, 16-byte aligned pointers. */
+int mgq_rows_quantize_int8(const void* x_bf16, int64_t ldx, int64_t T, int64_t K, int8_t* codes, float* scale,
+                           void* stream);
+
 #ifdef __cplusplus
 }
 #endif
