@@ -427,6 +427,14 @@ int run_rows(const void* in, int64_t ldi, const void* w, const int32_t* offsets,
   fill_knobs(&p);
   CUtensorMap ta, tb, ts;
   const uint64_t u = 2;
+  p.bk = kBK;
+  if (few_rows(E, R)) {
+    if (!encode_tmap_sw128_3d(&ta, w, 2, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
+                              {64, OP == kFwd ? 128u : 64u, 1}) ||
+        !encode_tmap_sw128_3d(&ts, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, kFewBox, 1}))
+      return MGQ_ERR_CUDA;
+    return run_few(OP, false, ta, ts, p, as_stream(stream));
+  }
   if (!encode_tmap_sw128_3d(&ta, w, 2, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
                             {64, OP == kFwd ? 128u : 64u, 1}) ||
       !encode_tmap_sw128_3d(&tb, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, 128, 1}) ||

@@ -7,13 +7,6 @@
 #include "ptx_sm100.cuh"
 
 namespace mgq {
-namespace {
-
-enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
-
-constexpr int kTile = 256;                         // M side, and tokens (wgrad: columns) at most
-constexpr int kMaxE = 1024;
-constexpr uint32_t kSmallBox = 32;                 // rows of the token boxes of a group's last tile
 
 struct RaggedArgs {
   const int32_t* offsets;   // [E + 1], or null: one group of all R rows
@@ -32,6 +25,14 @@ struct RaggedArgs {
   uint64_t wait_ns;
   int* err;
 };
+
+namespace {
+
+enum { kFwd = 0, kDgrad = 1, kWgrad = 2 };
+
+constexpr int kTile = 256;                         // M side, and tokens (wgrad: columns) at most
+constexpr int kMaxE = 1024;
+constexpr uint32_t kSmallBox = 32;                 // rows of the token boxes of a group's last tile
 
 struct RaggedTile {
   int e, nst;               // group, contraction stages
@@ -136,22 +137,22 @@ __device__ __forceinline__ uint4 transpose8_bf16(const float* v, uint32_t lane) 
   return b2 ? make_uint4(o0, o1, q[1][0], q[1][1]) : make_uint4(q[0][0], q[0][1], o0, o1);
 }
 
-// 32 tokens of a warp's 32 channels: v[j] = (channel chan0 + lane, token tok0 + j).
+// NT tokens of a warp's 32 channels: v[j] = (channel chan0 + lane, token tok0 + j).
 // `left` tokens exist.
-template <bool F32>
-__device__ __forceinline__ void store_tokens(void* out, int64_t ldo, const float (&v)[32], int64_t tok0, int left,
+template <bool F32, int NT>
+__device__ __forceinline__ void store_tokens(void* out, int64_t ldo, const float (&v)[NT], int64_t tok0, int left,
                                              int64_t chan0, int64_t chans, uint32_t lane) {
   if (F32) {
     float* o = static_cast<float*>(out) + tok0 * ldo + chan0 + lane;
     const bool in = chan0 + lane < chans;
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
+    for (int j = 0; j < NT; ++j)
       if (in && j < left) o[j * ldo] = v[j];
   } else {
     const int64_t c = chan0 + (lane & 24);
     uint16_t* o = static_cast<uint16_t*>(out) + (tok0 + (lane & 7)) * ldo + c;
 #pragma unroll
-    for (int j = 0; j < 32; j += 8) {
+    for (int j = 0; j < NT; j += 8) {
       if (j >= left) break;                                // the same in the whole warp
       const uint4 w = transpose8_bf16(v + j, lane);
       if (j + (int)(lane & 7) < left && c < chans) *reinterpret_cast<uint4*>(o + j * ldo) = w;
@@ -160,4 +161,13 @@ __device__ __forceinline__ void store_tokens(void* out, int64_t ldo, const float
 }
 
 }  // namespace
+
+// The form for few rows a group (ragged_few.cu); op kFwd or kDgrad, tensor maps of
+// the weights and of the rows (boxes of kFewBox rows).
+constexpr int kFewBox = 16;
+int run_few(int op, bool i8, const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p, cudaStream_t s);
+
+// Whether a product of R rows over E groups takes that form.
+inline bool few_rows(int E, int64_t R) { return R <= 16 * (int64_t)E || R <= 64; }
+
 }  // namespace mgq

@@ -1,0 +1,411 @@
+// The products over ragged groups for few rows a group (decode batches, short
+// micro-batches): bound by one read of the weights of the groups that have rows.
+//
+// One CTA a tile of 128 output channels by up to 64 tokens of one group, the
+// weights on the tensor cores' M side, tokens on the N side in steps of 16. Two
+// CTAs share an SM, so that one streams weights while the other starts or ends.
+// Where the tiles are too few to keep the memory busy, a cluster of up to 8 CTAs
+// splits the contraction; the parts meet in shared memory over the cluster and
+// are added in the order of the ranks, so the result does not depend on timing.
+// int8 weights become f16 on their way to tensor memory, as in the large form.
+#include "ragged.cuh"
+#include "ragged_int8.cuh"
+
+namespace mgq {
+namespace {
+
+constexpr int kFewTok = 64;                        // tokens of a tile at most
+constexpr uint32_t kFewA = 128 * 128;              // bytes of the weights a stage
+constexpr uint32_t kFewB = kFewTok * 128;          // bytes of the tokens a stage
+constexpr uint32_t kFewF = kFewTok * 256;          // int8: the tokens' f16 of a stage
+__host__ __device__ constexpr int few_stages(bool i8) { return i8 ? 3 : 4; }
+constexpr int kFewConv = 2;                        // int8: stages of f16
+__host__ __device__ constexpr int few_threads(bool i8) { return i8 ? 256 : 192; }
+__host__ __device__ constexpr size_t few_smem(bool i8) {
+  return 1024 + few_stages(i8) * (size_t)(kFewA + kFewB) + (i8 ? kFewConv * (size_t)kFewF : 0) + 256 + (kMaxE + 8) * 4;
+}
+static_assert(2 * (few_smem(true) + 1024) <= 233472 && 2 * (few_smem(false) + 1024) <= 233472, "two CTAs an SM");
+static_assert(few_stages(true) * (kFewA + kFewB) >= kFewTok * 128 * 4, "room for a partial result");
+// tensor memory: int8 one accumulator and the weights' f16; else two accumulators
+constexpr uint32_t kFewAcol = 64, kFewCols8 = 256, kFewCols = 128;
+constexpr int kFewPromote = 8;                     // as kPromote of the large form
+
+struct FewTile {
+  int e, row0, n;
+  int64_t m0;
+};
+
+// Tile t: groups in order, a group's channel tiles, its token tiles fastest (they
+// share the weights). One warp; s_off holds the offsets. False if there is no
+// such tile; `ok` is false for offsets that are no row partition.
+__device__ __forceinline__ bool few_tile(const RaggedArgs& p, const int32_t* s_off, int64_t t, uint32_t lane, FewTile& tl,
+                                         bool& ok) {
+  const int per = (p.E + 31) / 32, e0 = (int)lane * per, e1 = min(e0 + per, p.E);
+  int mine = 0;
+  ok = true;
+  for (int e = e0; e < e1; ++e) {
+    const int lo = s_off[e], hi = s_off[e + 1];
+    ok &= lo >= 0 && lo <= hi && hi <= p.R;
+    mine += (max(hi - lo, 0) + kFewTok - 1) / kFewTok;
+  }
+  ok = __all_sync(0xFFFFFFFFu, ok);
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= (uint32_t)o) inc += v;
+  }
+  const int64_t nM = (p.M + 127) / 128;
+  const uint32_t at = __ballot_sync(0xFFFFFFFFu, inc * nM > t);
+  if (!at) return false;
+  const int src = __ffs(at) - 1;
+  int e = 0, cum = 0, tiles = 0;
+  if ((int)lane == src) {
+    cum = inc - mine;
+    for (e = e0; e < e1; ++e) {
+      tiles = (s_off[e + 1] - s_off[e] + kFewTok - 1) / kFewTok;
+      if ((cum + tiles) * nM > t) break;
+      cum += tiles;
+    }
+  }
+  e = __shfl_sync(0xFFFFFFFFu, e, src);
+  cum = __shfl_sync(0xFFFFFFFFu, cum, src);
+  tiles = max(__shfl_sync(0xFFFFFFFFu, tiles, src), 1);
+  const int64_t local = t - cum * nM, m = local / tiles;
+  tl.e = e;
+  tl.row0 = s_off[e] + (int)(local - m * tiles) * kFewTok;
+  tl.n = min(kFewTok, s_off[e + 1] - tl.row0);
+  tl.m0 = m * 128;
+  return true;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <int OP, bool I8, bool F32>
+__global__ void __launch_bounds__(few_threads(I8), 2)
+    ragged_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const RaggedArgs p, int split) {
+  constexpr int ST = few_stages(I8);
+  constexpr bool kAmn = OP == kDgrad;
+  constexpr bool kParts = F32 && !I8;              // (sums of int8 products are exact to 2^24)
+  constexpr int kElems = I8 ? kBK8 : 64;           // of the contraction a stage
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  uint8_t* sA = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* sB = sA + ST * kFewA;
+  uint8_t* sF = sB + ST * kFewB;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sF + (I8 ? kFewConv * kFewF : 0));
+  uint64_t* empty = full + ST;
+  uint64_t* conv_full = empty + ST;                // [kFewConv]
+  uint64_t* conv_empty = conv_full + kFewConv;
+  uint64_t* acc_full = conv_empty + kFewConv;      // [2]
+  uint64_t* acc_empty = acc_full + 2;              // [2]
+  uint64_t* drained = acc_empty + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_tile = reinterpret_cast<int*>(s_tmem + 2);   // [4]: state, e, row0, n
+  int64_t* s_m0 = reinterpret_cast<int64_t*>(full + 28);
+  int32_t* s_off = reinterpret_cast<int32_t*>(full + 32);
+
+  const int warp = threadIdx.x >> 5;
+  const uint32_t lane = threadIdx.x & 31;
+  const int rank = split > 1 ? (int)ptx::cluster_ctarank() : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], I8 ? 6 : 1);       // int8: one arrival per converting warp
+    }
+    for (int s = 0; s < kFewConv; ++s) {
+      ptx::mbar_init(&conv_full[s], 6);
+      ptx::mbar_init(&conv_empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&acc_full[a], 1);
+      ptx::mbar_init(&acc_empty[a], 4);            // one arrival per epilogue warp
+    }
+    ptx::mbar_init(drained, 1);
+    *s_abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(s_tmem, I8 ? kFewCols8 : kFewCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::grid_wait();                                // from here on: what the launch before wrote
+  ptx::grid_launch();
+  for (int i = threadIdx.x; i <= p.E; i += few_threads(I8)) s_off[i] = p.offsets ? p.offsets[i] : i ? (int)p.R : 0;
+  __syncthreads();
+  if (warp == 2) {
+    FewTile tl;
+    bool ok;
+    const bool any = few_tile(p, s_off, blockIdx.x / split, lane, tl, ok);
+    if (lane == 0) {
+      if (!ok && blockIdx.x == 0) report(p.err, MGQ_ERR_INVALID_ARG);
+      s_tile[0] = ok && any;
+      if (ok && any) {
+        s_tile[1] = tl.e;
+        s_tile[2] = tl.row0;
+        s_tile[3] = tl.n;
+        *s_m0 = tl.m0;
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const bool run = s_tile[0] != 0;                 // the same in the whole cluster
+  const int e = s_tile[1], row0 = s_tile[2], n = s_tile[3];
+  const int64_t m0 = *s_m0;
+  // this rank's stages of the contraction
+  const int nst = (int)((p.C + kElems - 1) / kElems), chunk = (nst + split - 1) / split;
+  const int s0 = min(nst, rank * chunk), ns = min(nst, s0 + chunk) - s0;
+  const int boxes = (n + kFewBox - 1) / kFewBox;
+  auto timed_out = [&]() {
+    report(p.err, MGQ_ERR_TIMEOUT);
+    *s_abort = 1;
+  };
+
+  if (run && warp == 0 && lane == 0 && !p.stall) {
+    // ------------------------------------------------------------ producer
+    int i = 0;
+    for (; i < ns; ++i) {
+      const int st = i % ST;
+      if (*s_abort) break;
+      if (!ptx::mbar_wait(&empty[st], ((i / ST) & 1) ^ 1, p.wait_ns)) {
+        timed_out();
+        break;
+      }
+      ptx::mbar_arrive_expect_tx(&full[st], kFewA + boxes * kFewBox * 128);
+      const int32_t kx = (s0 + i) * kElems;
+      if (kAmn) {                                  // two chunks of 64 channels
+        ptx::tma_load_3d(sA + st * kFewA, &tmA, &full[st], (int32_t)m0, kx, e);
+        ptx::tma_load_3d(sA + st * kFewA + kFewA / 2, &tmA, &full[st], (int32_t)m0 + 64, kx, e);
+      } else {
+        ptx::tma_load_3d(sA + st * kFewA, &tmA, &full[st], kx, (int32_t)m0, e);
+      }
+      for (int b = 0; b < boxes; ++b)
+        ptx::tma_load_3d(sB + st * kFewB + b * kFewBox * 128, &tmB, &full[st], kx, row0 + b * kFewBox, 0);
+    }
+    if (*s_abort)                                  // no copy may be on its way when the CTA leaves
+      for (int j = max(0, i - ST); j < i; ++j) ptx::mbar_wait(&full[j % ST], (j / ST) & 1, p.wait_ns);
+  } else if (run && warp == 1 && lane == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t sA0 = ptx::smem_u32(sA), sB0 = ptx::smem_u32(sB), sF0 = ptx::smem_u32(sF);
+    const uint32_t idesc = ptx::idesc_f16(I8 ? 0 : 1, 128, (uint32_t)boxes * 16) | ptx::idesc_mn_major(kAmn, false);
+    bool ok = true;
+    for (int i = 0; i < ns; ++i) {
+      const bool first = kParts ? i % kFewPromote == 0 : i == 0;
+      const int part = kParts ? i / kFewPromote : 0;
+      const uint32_t acc = tmem + (part & 1) * 64;
+      if (kParts && first) ok = ptx::mbar_wait(&acc_empty[part & 1], ((part >> 1) & 1) ^ 1, p.wait_ns);
+      const int st = I8 ? i % kFewConv : i % ST;
+      ok = ok && !*s_abort &&
+           (I8 ? ptx::mbar_wait(&conv_full[st], (i / kFewConv) & 1, p.wait_ns)
+               : ptx::mbar_wait(&full[st], (i / ST) & 1, p.wait_ns));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      if (I8) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          ptx::mma_f16_ta(acc, tmem + kFewAcol + st * 64 + kk * 8,
+                          ptx::sdesc_kmajor_sw128(sF0 + st * kFewF + (kk >> 2) * (kFewF / 2)) + (kk & 3) * 2, idesc,
+                          (!first || kk > 0) ? 1u : 0u);
+        ptx::mma_commit(&conv_empty[st]);
+      } else {
+        const uint64_t ad = kAmn ? ptx::sdesc_mnmajor_sw128_chunks(sA0 + st * kFewA, kFewA / 2)
+                                 : ptx::sdesc_kmajor_sw128(sA0 + st * kFewA);
+        const uint64_t bd = ptx::sdesc_kmajor_sw128(sB0 + st * kFewB);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          ptx::mma_f16(acc, ad + kk * (kAmn ? 128 : 2), bd + kk * 2, idesc, (!first || kk > 0) ? 1u : 0u);
+        ptx::mma_commit(&empty[st]);
+      }
+      if (i == ns - 1 || (kParts && i % kFewPromote == kFewPromote - 1)) ptx::mma_commit(&acc_full[part & 1]);
+    }
+    if (!ok) {
+      timed_out();
+      ptx::mma_commit(drained);                    // the MMAs issued so far finish before the CTA leaves
+      ptx::mbar_wait(drained, 0, p.wait_ns);
+    }
+  } else if (run && warp >= 2) {
+    if (I8) {
+      // ---------------------------------------------------------- bytes to f16 (warps 2-5 channels, 6-7 tokens)
+      const bool chan = warp < 6;
+      const uint32_t row = (chan ? (warp & 3) : warp - 6) * 32 + lane;
+      const bool mine = chan || (int)(row - lane) < boxes * kFewBox;
+      bool ok = true;
+      for (int i = 0; i < ns; ++i) {
+        const int rs = i % ST, cs = i % kFewConv;
+        ok = *s_abort == 0;
+        ok = ok && ptx::mbar_wait(&full[rs], (i / ST) & 1, p.wait_ns);
+        ok = ok && ptx::mbar_wait(&conv_empty[cs], ((i / kFewConv) & 1) ^ 1, p.wait_ns);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        uint4 c[2][4];
+        if (mine) {
+          const uint8_t* src = chan ? sA + rs * kFewA : sB + rs * kFewB;
+          load_codes(src, row, 0, c[0]);
+          load_codes(src, row, 1, c[1]);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&empty[rs]);
+        if (chan) {
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            codes_to_tmem(c[h], tmem + kFewAcol + cs * 64 + 32 * h + ((32u * (warp & 3)) << 16));
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+        } else if (mine) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) codes_to_smem(c[h], sF + cs * kFewF + h * (kFewF / 2), row);
+          ptx::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&conv_full[cs]);
+      }
+      if (!ok) timed_out();
+    }
+    if (warp < 6) {
+      // ---------------------------------------------------------- the partial result, [token][channel]
+      const uint32_t q = warp & 3;
+      float v[kParts ? kFewTok : 32];
+      const int parts = ns == 0 ? 0 : kParts ? (ns + kFewPromote - 1) / kFewPromote : 1;
+      bool ok = true;
+#pragma unroll
+      for (int j = 0; j < (kParts ? kFewTok : 32); ++j) v[j] = 0.0f;
+      for (int part = 0; part < parts; ++part) {
+        ok = *s_abort == 0;
+        ok = ok && ptx::mbar_wait(&acc_full[part & 1], (part >> 1) & 1, p.wait_ns);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (kParts) {
+#pragma unroll
+          for (int h = 0; h < kFewTok; h += 16) {
+            if (h >= n) break;
+            uint32_t r[16];
+            ptx::tmem_ld_32x32b_x16(tmem + (part & 1) * 64 + h + ((q * 32) << 16), r);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[kParts ? h + j : j] += __uint_as_float(r[j]);
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&acc_empty[part & 1]);
+        }
+      }
+      if (!ok) timed_out();
+      float* part_out = reinterpret_cast<float*>(sA) + q * 32 + lane;
+      if (ok) {
+#pragma unroll
+        for (int h = 0; h < kFewTok; h += 16) {
+          if (h >= n) break;
+          if (!kParts && parts) {
+            uint32_t r[16];
+            ptx::tmem_ld_32x32b_x16(tmem + h + ((q * 32) << 16), r);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part_out[(h + j) * 128] = v[kParts ? h + j : j];
+        }
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tmem_dealloc(tmem, I8 ? kFewCols8 : kFewCols);
+  }
+  if (!run) return;                                // (the whole cluster)
+  if (split > 1) ptx::cluster_sync();              // every part is in place
+  // tokens rank, rank + split, ..: a warp each, four channels a lane
+  const int64_t ch = m0 + 4 * lane;
+  if (ch < p.M && !*s_abort) {
+    const uint32_t mine = ptx::smem_u32(sA) + lane * 16;
+    float4 sw = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (I8) sw = *reinterpret_cast<const float4*>(p.sw + e * p.M + ch);
+    for (int j = rank + split * warp; j < n; j += split * (few_threads(I8) / 32)) {
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int r = 0; r < split; ++r) {
+        const float4 x = split > 1 ? ld_cluster_f32x4(ptx::mapa_shared(mine + j * 512, r))
+                                   : *reinterpret_cast<const float4*>(sA + lane * 16 + j * 512);
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
+      }
+      const int64_t tok = (int64_t)row0 + j;
+      if (I8) {
+        const float sx = p.sx[tok];
+        s.x *= sx * sw.x;
+        s.y *= sx * sw.y;
+        s.z *= sx * sw.z;
+        s.w *= sx * sw.w;
+      }
+      if (F32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + tok * p.ldo + ch) = s;
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + tok * p.ldo + ch) =
+            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+  }
+  if (split > 1) ptx::cluster_sync();              // nobody still reads this CTA's part
+}
+
+template <int OP, bool I8, bool F32>
+int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p, int64_t tiles, int split,
+               cudaStream_t s) {
+  auto kern = ragged_few_kernel<OP, I8, F32>;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return MGQ_ERR_CUDA;
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(I8)) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return MGQ_ERR_CUDA;
+    }
+    attr_set[dev] = true;
+  }
+  return launch_after(kern, dim3((unsigned)(tiles * split)), few_threads(I8), few_smem(I8), split, s, ta, tb, p, split)
+             ? MGQ_OK
+             : MGQ_ERR_CUDA;
+}
+
+}  // namespace
+
+// Rows of the groups with a row at most, and CTAs that split a contraction so
+// that the tiles fill the GPU about twice (two CTAs an SM, and again).
+int64_t few_tiles(int E, int64_t R, int64_t M) {
+  return (R / kFewTok + min((int64_t)E, R)) * ((M + 127) / 128);
+}
+
+int run_few(int op, bool i8, const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p, cudaStream_t s) {
+  const int64_t tiles = few_tiles(p.E, p.R, p.M);
+  const int64_t nst = (p.C + (i8 ? kBK8 : 64) - 1) / (i8 ? kBK8 : 64);
+  int split = 1;
+  while (split < 8 && tiles * split < 2 * num_sms() && nst / (2 * split) >= 4) split *= 2;
+  if (i8) return p.out_f32 ? launch_few<kFwd, true, true>(ta, tb, p, tiles, split, s)
+                           : launch_few<kFwd, true, false>(ta, tb, p, tiles, split, s);
+  if (op == kFwd) return p.out_f32 ? launch_few<kFwd, false, true>(ta, tb, p, tiles, split, s)
+                                   : launch_few<kFwd, false, false>(ta, tb, p, tiles, split, s);
+  return p.out_f32 ? launch_few<kDgrad, false, true>(ta, tb, p, tiles, split, s)
+                   : launch_few<kDgrad, false, false>(ta, tb, p, tiles, split, s);
+}
+
+}  // namespace mgq

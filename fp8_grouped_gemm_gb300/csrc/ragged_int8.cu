@@ -10,44 +10,27 @@
 // would read, and become f16 beside the tensor cores. The tiles are those of the
 // bf16 products: two SMs share 256 output channels by up to 256 tokens.
 //   warp 0        TMA: 128 channels and up to 128 tokens of 128 bytes a stage
-//   warps 2-5     channels: bytes -> f16 -> tensor memory, the MMA's A operand
-//   warps 6-9     tokens: bytes -> f16 -> shared memory, swizzled, the B operand
+//   warps 2-9     channels: bytes -> f16 -> tensor memory, the MMA's A operand
+//   warps 10-17   tokens: bytes -> f16 -> shared memory, swizzled, the B operand
 //   warp 1        (CTA 0) issues the MMAs of both SMs
-//   warps 10-17   epilogue: scales, transposition, stores
-// A byte b becomes f16 by one permutation and one subtraction for two: 0x6400 |
-// (b ^ 0x80) is 1152 + b as f16. The channels' operand in tensor memory leaves
+//   warps 18-25   epilogue: scales, transposition, stores
+// The channels' operand in tensor memory leaves
 // shared memory's bandwidth to the tokens' one; its stages take the columns of a
 // second accumulator, so a tile's MMAs wait for the tile before to be read.
 #include "ragged.cuh"
-
-#include <cuda_fp16.h>
+#include "ragged_int8.cuh"
 
 namespace mgq {
 namespace {
 
-constexpr int kBK8 = 128;                          // elements (bytes) of the contraction a stage
 constexpr int kRaw = 3, kConv = 3;                 // stages of bytes, and of f16
 constexpr uint32_t kRawBytes = 128 * 128;          // one operand's bytes of a stage
 constexpr uint32_t kF16Bytes = 128 * 256;          // the tokens' f16 of a stage: two 64-element halves
 constexpr uint32_t kAcol = 256, kAcols = 64;       // tensor memory: the channels' stages
-constexpr int kThreads8 = 18 * 32;
+constexpr int kThreads8 = 26 * 32;
 constexpr size_t kSmem8 = 1024 + kRaw * 2 * (size_t)kRawBytes + kConv * (size_t)kF16Bytes + 8 * 128 + 256 +
                           2 * (kMaxE + 8) * 4;
 static_assert(kSmem8 <= 232448 && kAcol + kConv * kAcols <= 512, "shared and tensor memory");
-
-// 16 codes -> 16 f16 values in 8 words
-__device__ __forceinline__ void widen16(const uint4& c, uint32_t* o) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t u = w[i] ^ 0x80808080u;
-    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 base = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
-    __half2 a = __hsub2(*reinterpret_cast<__half2*>(&lo), base), b = __hsub2(*reinterpret_cast<__half2*>(&hi), base);
-    o[2 * i] = *reinterpret_cast<uint32_t*>(&a);
-    o[2 * i + 1] = *reinterpret_cast<uint32_t*>(&b);
-  }
-}
 
 template <bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
@@ -81,10 +64,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRaw; ++s) {
       ptx::mbar_init(&raw_full[s], 1);
-      ptx::mbar_init(&raw_empty[s], 8);            // one arrival per converting warp
+      ptx::mbar_init(&raw_empty[s], 16);           // one arrival per converting warp
     }
     for (int s = 0; s < kConv; ++s) {
-      ptx::mbar_init(&conv_full[s], 2 * 8);        // ... of both CTAs
+      ptx::mbar_init(&conv_full[s], 2 * 16);       // ... of both CTAs
       ptx::mbar_init(&conv_empty[s], 1);
     }
     ptx::mbar_init(acc_full, 1);
@@ -175,51 +158,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       ptx::mma_commit_pair(drained, 0x1);          // the MMAs issued so far finish before the CTA leaves
       ptx::mbar_wait(drained, 0, p.wait_ns);
     }
-  } else if (run && warp >= 2 && warp < 10) {
+  } else if (run && warp >= 2 && warp < 18) {
     // ------------------------------------------------------------ bytes to f16
-    const bool chan = warp < 6;
-    const uint32_t row = (chan ? (warp & 3) : warp - 6) * 32 + lane;   // channels: the warp's own lanes of tensor memory
+    // (8 warps an operand: 32 rows, half of a stage's contraction each)
+    const bool chan = warp < 10;
+    const uint32_t quad = chan ? warp & 3 : (warp - 10) & 3;           // channels: the warp's own lanes of tensor memory
+    const int h = (chan ? warp - 2 : warp - 10) >> 2;
+    const uint32_t row = quad * 32 + lane;
     int ecur = 0;
     uint32_t it = 0;
     RaggedTile tl;
     bool ok = true;
     for (int64_t t = pair; ok && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
-      const bool mine = chan || (int)row - (int)lane < (tl.n + 31) / 32 * 16;   // tokens: the rows an MMA reads
+      const bool mine = chan || (int)(quad * 32) < (tl.n + 31) / 32 * 16;   // tokens: the rows an MMA reads
       for (int s = 0; s < tl.nst; ++s, ++it) {
         const uint32_t rs = it % kRaw, cs = it % kConv;
         ok = *s_abort == 0;
         ok = ok && ptx::mbar_wait(&raw_full[rs], (it / kRaw) & 1, p.wait_ns);
+        uint4 c[4];
+        if (ok && mine) load_codes((chan ? sA : sB) + rs * kRawBytes, row, h, c);
         ok = ok && ptx::mbar_wait(&conv_empty[cs], ((it / kConv) & 1) ^ 1, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        uint4 c[8];
-        if (mine) {
-          const uint8_t* src = (chan ? sA : sB) + rs * kRawBytes + row * 128;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
-        }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&raw_empty[rs]);
         if (chan) {
           ptx::tc_fence_after();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t o[32];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) widen16(c[4 * h + j], o + 8 * j);
-            ptx::tmem_st_32x32b_x32(tmem + kAcol + cs * kAcols + 32 * h + ((32u * (warp & 3)) << 16), o);
-          }
+          codes_to_tmem(c, tmem + kAcol + cs * kAcols + 32 * h + ((32u * quad) << 16));
           ptx::tmem_st_wait();
           ptx::tc_fence_before();
         } else if (mine) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t o[8];
-            widen16(c[j], o);
-            uint8_t* dst = sF + cs * kF16Bytes + (j >> 2) * (kF16Bytes / 2) + row * 128;
-            *reinterpret_cast<uint4*>(dst + ((((2 * j) & 7) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + ((((2 * j + 1) & 7) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
+          codes_to_smem(c, sF + cs * kF16Bytes + h * (kF16Bytes / 2), row);
           ptx::fence_proxy_async_smem();
         }
         __syncwarp();
@@ -227,12 +196,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       }
     }
     if (!ok) timed_out();
-  } else if (run && warp >= 10) {
+  } else if (run && warp >= 18) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const uint32_t q = warp & 3;
-    const uint32_t half = (uint32_t)(warp - 10) >> 2;
+    const uint32_t half = (uint32_t)(warp - 18) >> 2;
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(acc_empty), 0);
-    float* sx = sX + (warp - 10) * 32;
+    float* sx = sX + (warp - 18) * 32;
     int ecur = 0;
     uint32_t tc = 0;
     RaggedTile tl;
@@ -246,16 +215,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
         break;
       }
       ptx::tc_fence_after();
-      for (int c = 32 * half; c < tl.n; c += 64) {
+      for (int c = 16 * half; c < tl.n; c += 32) {
         __syncwarp();
-        sx[lane] = c + (int)lane < tl.n ? p.sx[(int64_t)tl.row0 + c + lane] : 0.0f;
-        uint32_t r[32];
-        ptx::tmem_ld_32x32b_x32(tmem + c + ((q * 32) << 16), r);
+        if (lane < 16) sx[lane] = c + (int)lane < tl.n ? p.sx[(int64_t)tl.row0 + c + lane] : 0.0f;
+        uint32_t r[16];
+        ptx::tmem_ld_32x32b_x16(tmem + c + ((q * 32) << 16), r);
         ptx::tmem_ld_wait();
         __syncwarp();
-        float v[32];
+        float v[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * (sx[j] * sw);
+        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]) * (sx[j] * sw);
         store_tokens<F32>(p.out, p.ldo, v, (int64_t)tl.row0 + c, tl.n - c, m0, p.M, lane);
       }
       ptx::tc_fence_before();
@@ -400,7 +369,7 @@ int mgq_ragged_gemm_int8(const int8_t* x, int64_t ldx, const float* x_scale, con
   MGQ_CHECK_ARG(ldx >= K && ldx % 16 == 0 && ldx < (1ll << 39) && ldy >= N && ldy % 8 == 0 && ldy < (1ll << 38));
   MGQ_CHECK_ARG(R == 0 || (x && x_scale && w && w_scale && y));
   MGQ_CHECK_ARG(aligned16(x) && aligned16(w) && aligned16(y) && (reinterpret_cast<uintptr_t>(x_scale) & 3u) == 0 &&
-                (reinterpret_cast<uintptr_t>(w_scale) & 3u) == 0);
+                aligned16(w_scale));
   if (R == 0) return MGQ_OK;
   RaggedArgs p{};
   p.err = error_word();
@@ -417,7 +386,14 @@ int mgq_ragged_gemm_int8(const int8_t* x, int64_t ldx, const float* x_scale, con
   p.sx = x_scale;
   p.sw = w_scale;
   debug_knobs(&p.stall, &p.wait_ns);
+  const bool few = few_rows(E, R);
   CUtensorMap ta, tb, ts;
+  if (few) {
+    if (!encode_tmap_sw128_3d(&ta, w, 1, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K, N * K, {128, 128, 1}) ||
+        !encode_tmap_sw128_3d(&ts, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, kFewBox, 1}))
+      return MGQ_ERR_CUDA;
+    return run_few(kFwd, true, ta, ts, p, as_stream(stream));
+  }
   if (!encode_tmap_sw128_3d(&ta, w, 1, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K, N * K, {128, 128, 1}) ||
       !encode_tmap_sw128_3d(&tb, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, 128, 1}) ||
       !encode_tmap_sw128_3d(&ts, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, kSmallBox, 1}))
