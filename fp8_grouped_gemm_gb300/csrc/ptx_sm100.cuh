@@ -19,6 +19,15 @@ __device__ __forceinline__ uint32_t lane_id() {
   return r;
 }
 
+// one lane of a converged warp. What it issues alone (TMA, MMA) has its operands
+// in uniform registers; under a `lane == 0` branch each of them is moved there
+// lane by lane, which keeps the tensor cores waiting.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // programmatic dependent launch: wait until the kernels before this one in the
 // stream have finished and their writes are visible; let the next one start
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -377,6 +386,13 @@ __device__ __forceinline__ void cluster_sync() {
 // arrive on an mbarrier of any CTA of the cluster (shared::cluster address)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// The same with the default scope: it orders what the arriving thread did in its
+// own CTA (shared memory, tensor memory), which is all that an MMA of the pair
+// reads there, and does not wait for the thread's global stores. The form with
+// cluster scope waits for those: about 1000 cycles an arrival.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // 2D tiled load into this CTA's shared memory whose completion is signalled on
 // an mbarrier of either CTA of the pair (shared::cluster address)

@@ -65,7 +65,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   int32_t* s_off = reinterpret_cast<int32_t*>(full + 32);
   int32_t* s_cum = s_off + (kMaxE + 8);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);   // (known to be uniform)
   const uint32_t lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
   const bool leader = rank == 0;
@@ -107,10 +107,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   const uint32_t tmem = *s_tmem;
   const bool run = *s_bad == 0;
 
-  if (run && warp == 0 && lane == 0 && !p.stall) {
+  if (run && warp == 0 && !p.stall && ptx::elect_one()) {
     // ------------------------------------------------------------ producer (both CTAs)
     int ecur = 0;
-    uint32_t it = 0;
+    uint32_t it = 0, st = 0, ph = 0;
     RaggedTile tl;
     for (int64_t t = pair; !*s_abort && ragged_tile<OP>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
       // this CTA's half of the tokens: one box of 128 rows, or boxes of 32
@@ -118,7 +118,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       const int boxes = half == 128 ? 0 : (half + (int)kSmallBox - 1) / (int)kSmallBox;
       const uint32_t bytes = 2 * (kOpBytes + (boxes ? boxes * kSmallBox * 128 : kOpBytes));
       for (int s = 0; s < tl.nst; ++s, ++it) {
-        const uint32_t st = it % ST, ph = (it / ST) & 1;
         if (*s_abort) break;
         if (!ptx::mbar_wait(&empty[st], ph ^ 1, p.wait_ns)) {
           report(p.err, MGQ_ERR_TIMEOUT);
@@ -148,16 +147,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
           for (int i = 0; i < boxes; ++i)
             ptx::tma_load_3d_pair(b + i * kSmallBox * 128, &tmS, bar0, kx, r + i * (int)kSmallBox, 0);
         }
+        if (++st == ST) st = 0, ph ^= 1;
       }
     }
     // after a wait that ran out: no copy may still be on its way when the CTA
     // leaves. (The leader's barriers count both CTAs' copies.)
     if (*s_abort && leader)
       for (uint32_t i = it > ST ? it - ST : 0; i < it; ++i) ptx::mbar_wait(&full[i % ST], (i / ST) & 1, p.wait_ns);
-  } else if (run && leader && warp == 1 && lane == 0) {
+  } else if (run && leader && warp == 1 && ptx::elect_one()) {
     // ------------------------------------------------------------ MMA issuer (CTA 0)
     int ecur = 0;
-    uint32_t it = 0, tc = 0, masks = 0;
+    uint32_t st = 0, ph = 0, tc = 0, masks = 0;
     RaggedTile tl;
     const uint32_t sA0 = ptx::smem_u32(sA), sB0 = ptx::smem_u32(sB);
     bool ok = true;
@@ -166,22 +166,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       const uint32_t N = OP == kWgrad ? 256u : (uint32_t)(tl.n + 31) / 32 * 32;
       const uint32_t idesc = ptx::idesc_f16(1, 256, N) | ptx::idesc_mn_major(kAmn, kBmn);
       uint32_t a = 0;
-      for (int s = 0; s < tl.nst; ++s, ++it) {
+      for (int s = 0; s < tl.nst; ++s) {
         const bool first = s == 0 || (F32 && s % kPromote == 0);   // of an accumulator
         if (first) {
           a = tc & 1;
           ok = !*s_abort && ptx::mbar_wait(&tmem_empty[a], ((tc >> 1) & 1) ^ 1, p.wait_ns);
           if (!ok) break;
         }
-        const uint32_t st = it % ST, ph = (it / ST) & 1;
         ok = !*s_abort && ptx::mbar_wait(&full[st], ph, p.wait_ns);
         int steps = kBK / 16;
         if (OP == kWgrad && s == tl.nst - 1 && ok) {
           const int rows = tl.n - s * kBK;
           steps = (rows + 15) / 16;
           if (rows % 16) {
-            ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(mask_go), 0));
-            ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(mask_go), 1));
+            ptx::mbar_arrive_pair(ptx::mapa_shared(ptx::smem_u32(mask_go), 0));
+            ptx::mbar_arrive_pair(ptx::mapa_shared(ptx::smem_u32(mask_go), 1));
             ok = ptx::mbar_wait(mask_done, masks++ & 1, p.wait_ns);
           }
         }
@@ -196,6 +195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
         for (int kk = 0; kk < steps; ++kk)
           ptx::mma_f16_pair(tmem + a * kTile, ad + kk * da, bd + kk * db, idesc, (!first || kk > 0) ? 1u : 0u);
         ptx::mma_commit_pair(&empty[st], 0x3);        // frees the stage in both CTAs
+        if (++st == ST) st = 0, ph ^= 1;
         if (s == tl.nst - 1 || (F32 && s % kPromote == kPromote - 1)) {
           ptx::mma_commit_pair(&tmem_full[a], 0x3);
           ++tc;
@@ -248,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       auto release_acc = [&]() {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(tc & 1 ? empty1 : empty0);
+        if (lane == 0) ptx::mbar_arrive_pair(tc & 1 ? empty1 : empty0);
         ++tc;
       };
       auto load = [&](int i, float (&d)[32], bool add) {
@@ -355,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(done0);
+      if (lane == 0) ptx::mbar_arrive_pair(done0);
     }
   }
   __syncthreads();

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
   int64_t* s_m0 = reinterpret_cast<int64_t*>(full + 28);
   int32_t* s_off = reinterpret_cast<int32_t*>(full + 32);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);   // (known to be uniform)
   const uint32_t lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)ptx::cluster_ctarank() : 0;
 
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
     *s_abort = 1;
   };
 
-  if (run && warp == 0 && lane == 0 && !p.stall) {
+  if (run && warp == 0 && !p.stall && ptx::elect_one()) {
     // ------------------------------------------------------------ producer
     int i = 0;
     for (; i < ns; ++i) {
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
     }
     if (*s_abort)                                  // no copy may be on its way when the CTA leaves
       for (int j = max(0, i - ST); j < i; ++j) ptx::mbar_wait(&full[j % ST], (j / ST) & 1, p.wait_ns);
-  } else if (run && warp == 1 && lane == 0) {
+  } else if (run && warp == 1 && ptx::elect_one()) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t sA0 = ptx::smem_u32(sA), sB0 = ptx::smem_u32(sB), sF0 = ptx::smem_u32(sF);
     const uint32_t idesc = ptx::idesc_f16(I8 ? 0 : 1, 128, (uint32_t)boxes * 16) | ptx::idesc_mn_major(kAmn, false);

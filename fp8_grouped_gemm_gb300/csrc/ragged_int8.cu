@@ -23,12 +23,12 @@
 namespace mgq {
 namespace {
 
-constexpr int kRaw = 3, kConv = 3;                 // stages of bytes, and of f16
+constexpr int kRaw = 2, kConv = 8;                 // stages of bytes, and half stages of f16
 constexpr uint32_t kRawBytes = 128 * 128;          // one operand's bytes of a stage
-constexpr uint32_t kF16Bytes = 128 * 256;          // the tokens' f16 of a stage: two 64-element halves
-constexpr uint32_t kAcol = 256, kAcols = 64;       // tensor memory: the channels' stages
+constexpr uint32_t kF16Bytes = 128 * 128;          // the tokens' f16 of half a stage, 64 elements
+constexpr uint32_t kAcol = 256, kAcols = 32;       // tensor memory: the channels' half stages
 constexpr int kThreads8 = 26 * 32;
-constexpr size_t kSmem8 = 1024 + kRaw * 2 * (size_t)kRawBytes + kConv * (size_t)kF16Bytes + 8 * 128 + 256 +
+constexpr size_t kSmem8 = 1024 + kRaw * 2 * (size_t)kRawBytes + kConv * (size_t)kF16Bytes + 8 * 512 + 256 +
                           2 * (kMaxE + 8) * 4;
 static_assert(kSmem8 <= 232448 && kAcol + kConv * kAcols <= 512, "shared and tensor memory");
 
@@ -41,8 +41,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
   uint8_t* sA = smem_raw + (((raw + 1023u) & ~1023u) - raw);   // [kRaw] bytes of the channels
   uint8_t* sB = sA + kRaw * kRawBytes;                         // [kRaw] bytes of the tokens
   uint8_t* sF = sB + kRaw * kRawBytes;                         // [kConv] f16 of the tokens
-  float* sX = reinterpret_cast<float*>(sF + kConv * kF16Bytes);   // [8 warps][32] token scales
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(sX + 8 * 32);
+  float* sX = reinterpret_cast<float*>(sF + kConv * kF16Bytes);   // [8 warps][128] token scales
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(sX + 8 * 128);
   uint64_t* raw_empty = raw_full + kRaw;
   uint64_t* conv_full = raw_empty + kRaw;
   uint64_t* conv_empty = conv_full + kConv;
@@ -55,7 +55,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
   int32_t* s_off = reinterpret_cast<int32_t*>(raw_full + 32);
   int32_t* s_cum = s_off + (kMaxE + 8);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);   // (known to be uniform)
   const uint32_t lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
   const bool leader = rank == 0;
@@ -67,7 +67,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       ptx::mbar_init(&raw_empty[s], 16);           // one arrival per converting warp
     }
     for (int s = 0; s < kConv; ++s) {
-      ptx::mbar_init(&conv_full[s], 2 * 16);       // ... of both CTAs
+      ptx::mbar_init(&conv_full[s], 2 * 8);        // a half stage's warps of both CTAs
       ptx::mbar_init(&conv_empty[s], 1);
     }
     ptx::mbar_init(acc_full, 1);
@@ -101,7 +101,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     *s_abort = 1;
   };
 
-  if (run && warp == 0 && lane == 0 && !p.stall) {
+  if (run && warp == 0 && !p.stall && ptx::elect_one()) {
     // ------------------------------------------------------------ producer (both CTAs)
     int ecur = 0;
     uint32_t it = 0;
@@ -129,7 +129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     if (*s_abort)
       for (uint32_t i = it > kRaw ? it - kRaw : 0; i < it; ++i)
         ptx::mbar_wait(&raw_full[i % kRaw], (i / kRaw) & 1, p.wait_ns);
-  } else if (run && leader && warp == 1 && lane == 0) {
+  } else if (run && leader && warp == 1 && ptx::elect_one()) {
     // ------------------------------------------------------------ MMA issuer (CTA 0)
     int ecur = 0;
     uint32_t it = 0, tc = 0;
@@ -139,16 +139,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     for (int64_t t = pair; ok && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs, ++tc) {
       const uint32_t idesc = ptx::idesc_f16(0, 256, (uint32_t)(tl.n + 31) / 32 * 32);
       ok = !*s_abort && ptx::mbar_wait(acc_empty, (tc & 1) ^ 1, p.wait_ns);
-      for (int s = 0; ok && s < tl.nst; ++s, ++it) {
+      for (int s = 0; ok && s < 2 * tl.nst; ++s, ++it) {
         const uint32_t st = it % kConv;
         ok = !*s_abort && ptx::mbar_wait(&conv_full[st], (it / kConv) & 1, p.wait_ns);
         if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kBK8 / 16; ++kk)
+        for (int kk = 0; kk < 4; ++kk)
           ptx::mma_f16_ta_pair(tmem, tmem + kAcol + st * kAcols + kk * 8,
-                               ptx::sdesc_kmajor_sw128(sF0 + st * kF16Bytes + (kk >> 2) * (kF16Bytes / 2)) + (kk & 3) * 2,
-                               idesc, (s > 0 || kk > 0) ? 1u : 0u);
+                               ptx::sdesc_kmajor_sw128(sF0 + st * kF16Bytes) + kk * 2, idesc,
+                               (s > 0 || kk > 0) ? 1u : 0u);
         ptx::mma_commit_pair(&conv_empty[st], 0x3);
       }
       if (ok) ptx::mma_commit_pair(acc_full, 0x3);
@@ -160,7 +160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     }
   } else if (run && warp >= 2 && warp < 18) {
     // ------------------------------------------------------------ bytes to f16
-    // (8 warps an operand: 32 rows, half of a stage's contraction each)
+    // (8 warps an operand: 32 rows each, 4 warps for each half of a stage)
     const bool chan = warp < 10;
     const uint32_t quad = chan ? warp & 3 : (warp - 10) & 3;           // channels: the warp's own lanes of tensor memory
     const int h = (chan ? warp - 2 : warp - 10) >> 2;
@@ -172,27 +172,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     for (int64_t t = pair; ok && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
       const bool mine = chan || (int)(quad * 32) < (tl.n + 31) / 32 * 16;   // tokens: the rows an MMA reads
       for (int s = 0; s < tl.nst; ++s, ++it) {
-        const uint32_t rs = it % kRaw, cs = it % kConv;
+        const uint32_t rs = it % kRaw, u = 2 * it + h, cs = u % kConv;
         ok = *s_abort == 0;
         ok = ok && ptx::mbar_wait(&raw_full[rs], (it / kRaw) & 1, p.wait_ns);
         uint4 c[4];
         if (ok && mine) load_codes((chan ? sA : sB) + rs * kRawBytes, row, h, c);
-        ok = ok && ptx::mbar_wait(&conv_empty[cs], ((it / kConv) & 1) ^ 1, p.wait_ns);
+        ok = ok && ptx::mbar_wait(&conv_empty[cs], ((u / kConv) & 1) ^ 1, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&raw_empty[rs]);
         if (chan) {
           ptx::tc_fence_after();
-          codes_to_tmem(c, tmem + kAcol + cs * kAcols + 32 * h + ((32u * quad) << 16));
+          codes_to_tmem(c, tmem + kAcol + cs * kAcols + ((32u * quad) << 16));
           ptx::tmem_st_wait();
           ptx::tc_fence_before();
         } else if (mine) {
-          codes_to_smem(c, sF + cs * kF16Bytes + h * (kF16Bytes / 2), row);
+          codes_to_smem(c, sF + cs * kF16Bytes, row);
           ptx::fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&conv_full[cs]), 0));
+        if (lane == 0) ptx::mbar_arrive_pair(ptx::mapa_shared(ptx::smem_u32(&conv_full[cs]), 0));
       }
     }
     if (!ok) timed_out();
@@ -201,13 +201,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     const uint32_t q = warp & 3;
     const uint32_t half = (uint32_t)(warp - 18) >> 2;
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(acc_empty), 0);
-    float* sx = sX + (warp - 18) * 32;
+    float* sx = sX + (warp - 18) * 128;
     int ecur = 0;
     uint32_t tc = 0;
     RaggedTile tl;
     for (int64_t t = pair; ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs, ++tc) {
       const int64_t m0 = tl.m0 + 128 * rank + 32 * q;
       const float sw = m0 + lane < p.M ? p.sw[tl.e * p.M + m0 + lane] : 0.0f;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {                // (in runs of 16 tokens, every second run)
+        const int j = 32 * i + (int)lane, c = 16 * half + (j & 15) + 32 * (j >> 4);
+        sx[j] = c < tl.n ? p.sx[(int64_t)tl.row0 + c] : 0.0f;
+      }
+      __syncwarp();
       bool got = *s_abort == 0;
       got = got && ptx::mbar_wait(acc_full, tc & 1, p.wait_ns);
       if (!__all_sync(0xFFFFFFFFu, got)) {
@@ -216,20 +223,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       }
       ptx::tc_fence_after();
       for (int c = 16 * half; c < tl.n; c += 32) {
-        __syncwarp();
-        if (lane < 16) sx[lane] = c + (int)lane < tl.n ? p.sx[(int64_t)tl.row0 + c + lane] : 0.0f;
         uint32_t r[16];
         ptx::tmem_ld_32x32b_x16(tmem + c + ((q * 32) << 16), r);
         ptx::tmem_ld_wait();
-        __syncwarp();
         float v[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]) * (sx[j] * sw);
+        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]) * (sx[(c >> 5) * 16 + j] * sw);
         store_tokens<F32>(p.out, p.ldo, v, (int64_t)tl.row0 + c, tl.n - c, m0, p.M, lane);
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(empty0);
+      if (lane == 0) ptx::mbar_arrive_pair(empty0);
     }
   }
   __syncthreads();
