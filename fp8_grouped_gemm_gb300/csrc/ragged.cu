@@ -428,7 +428,7 @@ int run_rows(const void* in, int64_t ldi, const void* w, const int32_t* offsets,
   CUtensorMap ta, tb, ts;
   const uint64_t u = 2;
   p.bk = kBK;
-  if (few_rows(E, R)) {
+  if (few_rows(E, R, M)) {
     if (!encode_tmap_sw128_3d(&ta, w, 2, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
                               {64, OP == kFwd ? 128u : 64u, 1}) ||
         !encode_tmap_sw128_3d(&ts, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, kFewBox, 1}))
@@ -440,7 +440,7 @@ int run_rows(const void* in, int64_t ldi, const void* w, const int32_t* offsets,
       !encode_tmap_sw128_3d(&tb, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, 128, 1}) ||
       !encode_tmap_sw128_3d(&ts, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, kSmallBox, 1}))
     return MGQ_ERR_CUDA;
-  const int64_t tiles = (R / kTile + min((int64_t)E, R)) * ((M + kTile - 1) / kTile);
+  const int64_t tiles = token_tiles(E, R, kTile) * ((M + kTile - 1) / kTile);
   p.bk = kBK;
   return p.out_f32 ? launch_pair<OP, true>(ta, tb, ts, p, tiles, as_stream(stream))
                    : launch_pair<OP, false>(ta, tb, ts, p, tiles, as_stream(stream));

@@ -392,14 +392,14 @@ int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p
 // Rows of the groups with a row at most, and CTAs that split a contraction so
 // that the tiles fill the GPU about twice (two CTAs an SM, and again).
 int64_t few_tiles(int E, int64_t R, int64_t M) {
-  return (R / kFewTok + min((int64_t)E, R)) * ((M + 127) / 128);
+  return token_tiles(E, R, kFewTok) * ((M + 127) / 128);
 }
 
 int run_few(int op, bool i8, const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p, cudaStream_t s) {
   const int64_t tiles = few_tiles(p.E, p.R, p.M);
   const int64_t nst = (p.C + (i8 ? kBK8 : 64) - 1) / (i8 ? kBK8 : 64);
   int split = 1;
-  while (split < 8 && tiles * split < 2 * num_sms() && nst / (2 * split) >= 4) split *= 2;
+  while (split < 8 && 2 * tiles * split <= 2 * num_sms() && nst / (2 * split) >= 4) split *= 2;
   if (i8) return p.out_f32 ? launch_few<kFwd, true, true>(ta, tb, p, tiles, split, s)
                            : launch_few<kFwd, true, false>(ta, tb, p, tiles, split, s);
   if (op == kFwd) return p.out_f32 ? launch_few<kFwd, false, true>(ta, tb, p, tiles, split, s)

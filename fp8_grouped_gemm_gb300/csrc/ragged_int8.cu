@@ -10,10 +10,10 @@
 // would read, and become f16 beside the tensor cores. The tiles are those of the
 // bf16 products: two SMs share 256 output channels by up to 256 tokens.
 //   warp 0        TMA: 128 channels and up to 128 tokens of 128 bytes a stage
-//   warps 2-9     channels: bytes -> f16 -> tensor memory, the MMA's A operand
-//   warps 10-17   tokens: bytes -> f16 -> shared memory, swizzled, the B operand
+//   warps 4-11    channels: bytes -> f16 -> tensor memory, the MMA's A operand
+//   warps 12-19   tokens: bytes -> f16 -> shared memory, swizzled, the B operand
 //   warp 1        (CTA 0) issues the MMAs of both SMs
-//   warps 18-25   epilogue: scales, transposition, stores
+//   warps 20-27   epilogue: scales, transposition, stores
 // The channels' operand in tensor memory leaves
 // shared memory's bandwidth to the tokens' one; its stages take the columns of a
 // second accumulator, so a tile's MMAs wait for the tile before to be read.
@@ -23,11 +23,17 @@
 namespace mgq {
 namespace {
 
-constexpr int kRaw = 2, kConv = 8;                 // stages of bytes, and half stages of f16
+constexpr int kRaw = 4, kConv = 4;                 // stages of bytes, and half stages of f16
 constexpr uint32_t kRawBytes = 128 * 128;          // one operand's bytes of a stage
 constexpr uint32_t kF16Bytes = 128 * 128;          // the tokens' f16 of half a stage, 64 elements
 constexpr uint32_t kAcol = 256, kAcols = 32;       // tensor memory: the channels' half stages
-constexpr int kThreads8 = 26 * 32;
+constexpr int kThreads8 = 28 * 32;
+// Registers a thread of the three kinds of warps, out of what the block is
+// launched with: the epilogue holds a tile's 64 words of scaled and transposed
+// bf16 pairs, so that the one accumulator is free before the stores (whose burst
+// takes 3 us a tile when all SMs end one together).
+constexpr int kRegLow = 40, kRegConv = 56, kRegEpi = 120, kRegLaunch = 72;
+static_assert(128 * kRegLow + 512 * kRegConv + 256 * kRegEpi <= kThreads8 * kRegLaunch, "register split");
 constexpr size_t kSmem8 = 1024 + kRaw * 2 * (size_t)kRawBytes + kConv * (size_t)kF16Bytes + 8 * 512 + 256 +
                           2 * (kMaxE + 8) * 4;
 static_assert(kSmem8 <= 232448 && kAcol + kConv * kAcols <= 512, "shared and tensor memory");
@@ -67,7 +73,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       ptx::mbar_init(&raw_empty[s], 16);           // one arrival per converting warp
     }
     for (int s = 0; s < kConv; ++s) {
-      ptx::mbar_init(&conv_full[s], 2 * 8);        // a half stage's warps of both CTAs
+      ptx::mbar_init(&conv_full[s], 2 * 8);        // half of them, of both CTAs
       ptx::mbar_init(&conv_empty[s], 1);
     }
     ptx::mbar_init(acc_full, 1);
@@ -101,19 +107,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     *s_abort = 1;
   };
 
+  if (warp < 4) ptx::setmaxnreg_dec<kRegLow>();
   if (run && warp == 0 && !p.stall && ptx::elect_one()) {
     // ------------------------------------------------------------ producer (both CTAs)
     int ecur = 0;
-    uint32_t it = 0;
+    uint32_t it = 0, st = 0, ph = 0;
     RaggedTile tl;
     for (int64_t t = pair; !*s_abort && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
       const int half = (tl.n + 31) / 32 * 16;      // this CTA's tokens
       const int boxes = half == 128 ? 0 : (half + (int)kSmallBox - 1) / (int)kSmallBox;
       const uint32_t bytes = kRawBytes + (boxes ? boxes * kSmallBox * 128 : kRawBytes);
       for (int s = 0; s < tl.nst; ++s, ++it) {
-        const uint32_t st = it % kRaw;
         if (*s_abort) break;
-        if (!ptx::mbar_wait(&raw_empty[st], ((it / kRaw) & 1) ^ 1, p.wait_ns)) {
+        if (!ptx::mbar_wait(&raw_empty[st], ph ^ 1, p.wait_ns)) {
           timed_out();
           break;
         }
@@ -123,6 +129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
         if (!boxes) ptx::tma_load_3d(sB + st * kRawBytes, &tmB, &raw_full[st], kx, r, 0);
         for (int i = 0; i < boxes; ++i)
           ptx::tma_load_3d(sB + st * kRawBytes + i * kSmallBox * 128, &tmS, &raw_full[st], kx, r + i * (int)kSmallBox, 0);
+        if (++st == kRaw) st = 0, ph ^= 1;
       }
     }
     // after a wait that ran out: no copy may still be on its way when the CTA leaves
@@ -132,16 +139,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
   } else if (run && leader && warp == 1 && ptx::elect_one()) {
     // ------------------------------------------------------------ MMA issuer (CTA 0)
     int ecur = 0;
-    uint32_t it = 0, tc = 0;
+    uint32_t st = 0, ph = 0, tc = 0;
     RaggedTile tl;
     const uint32_t sF0 = ptx::smem_u32(sF);
     bool ok = true;
     for (int64_t t = pair; ok && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs, ++tc) {
       const uint32_t idesc = ptx::idesc_f16(0, 256, (uint32_t)(tl.n + 31) / 32 * 32);
       ok = !*s_abort && ptx::mbar_wait(acc_empty, (tc & 1) ^ 1, p.wait_ns);
-      for (int s = 0; ok && s < 2 * tl.nst; ++s, ++it) {
-        const uint32_t st = it % kConv;
-        ok = !*s_abort && ptx::mbar_wait(&conv_full[st], (it / kConv) & 1, p.wait_ns);
+      for (int s = 0; ok && s < 2 * tl.nst; ++s) {
+        ok = !*s_abort && ptx::mbar_wait(&conv_full[st], ph, p.wait_ns);
         if (!ok) break;
         ptx::tc_fence_after();
 #pragma unroll
@@ -150,6 +156,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
                                ptx::sdesc_kmajor_sw128(sF0 + st * kF16Bytes) + kk * 2, idesc,
                                (s > 0 || kk > 0) ? 1u : 0u);
         ptx::mma_commit_pair(&conv_empty[st], 0x3);
+        if (++st == kConv) st = 0, ph ^= 1;
       }
       if (ok) ptx::mma_commit_pair(acc_full, 0x3);
     }
@@ -158,30 +165,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       ptx::mma_commit_pair(drained, 0x1);          // the MMAs issued so far finish before the CTA leaves
       ptx::mbar_wait(drained, 0, p.wait_ns);
     }
-  } else if (run && warp >= 2 && warp < 18) {
+  } else if (warp >= 4 && warp < 20) {
+    ptx::setmaxnreg_dec<kRegConv>();
     // ------------------------------------------------------------ bytes to f16
     // (8 warps an operand: 32 rows each, 4 warps for each half of a stage)
-    const bool chan = warp < 10;
-    const uint32_t quad = chan ? warp & 3 : (warp - 10) & 3;           // channels: the warp's own lanes of tensor memory
-    const int h = (chan ? warp - 2 : warp - 10) >> 2;
+    const bool chan = warp < 12;
+    const uint32_t quad = warp & 3;                                     // channels: the warp's own lanes of tensor memory
+    const int h = ((warp - 4) >> 2) & 1;
     const uint32_t row = quad * 32 + lane;
     int ecur = 0;
-    uint32_t it = 0;
+    uint32_t rs = 0, rph = 0, cs = h, cph = 0;                          // every second half stage
     RaggedTile tl;
     bool ok = true;
-    for (int64_t t = pair; ok && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
+    for (int64_t t = pair; run && ok && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
       const bool mine = chan || (int)(quad * 32) < (tl.n + 31) / 32 * 16;   // tokens: the rows an MMA reads
-      for (int s = 0; s < tl.nst; ++s, ++it) {
-        const uint32_t rs = it % kRaw, u = 2 * it + h, cs = u % kConv;
+      for (int s = 0; s < tl.nst; ++s) {
         ok = *s_abort == 0;
-        ok = ok && ptx::mbar_wait(&raw_full[rs], (it / kRaw) & 1, p.wait_ns);
+        ok = ok && ptx::mbar_wait(&raw_full[rs], rph, p.wait_ns);
         uint4 c[4];
         if (ok && mine) load_codes((chan ? sA : sB) + rs * kRawBytes, row, h, c);
-        ok = ok && ptx::mbar_wait(&conv_empty[cs], ((u / kConv) & 1) ^ 1, p.wait_ns);
+        __syncwarp();
+        if (ok && lane == 0) ptx::mbar_arrive(&raw_empty[rs]);
+        ok = ok && ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&raw_empty[rs]);
         if (chan) {
           ptx::tc_fence_after();
           codes_to_tmem(c, tmem + kAcol + cs * kAcols + ((32u * quad) << 16));
@@ -193,19 +200,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_pair(ptx::mapa_shared(ptx::smem_u32(&conv_full[cs]), 0));
+        if (++rs == kRaw) rs = 0, rph ^= 1;
+        if ((cs += 2) >= kConv) cs -= kConv, cph ^= 1;
       }
     }
     if (!ok) timed_out();
-  } else if (run && warp >= 18) {
+  } else if (warp >= 20) {
+    ptx::setmaxnreg_inc<kRegEpi>();
     // ------------------------------------------------------------ epilogue (both CTAs)
     const uint32_t q = warp & 3;
-    const uint32_t half = (uint32_t)(warp - 18) >> 2;
+    const uint32_t half = (uint32_t)(warp - 20) >> 2;
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(acc_empty), 0);
-    float* sx = sX + (warp - 18) * 128;
+    float* sx = sX + (warp - 20) * 128;
     int ecur = 0;
     uint32_t tc = 0;
     RaggedTile tl;
-    for (int64_t t = pair; ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs, ++tc) {
+    for (int64_t t = pair; run && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs, ++tc) {
       const int64_t m0 = tl.m0 + 128 * rank + 32 * q;
       const float sw = m0 + lane < p.M ? p.sw[tl.e * p.M + m0 + lane] : 0.0f;
       __syncwarp();
@@ -222,18 +232,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
         break;
       }
       ptx::tc_fence_after();
-      for (int c = 16 * half; c < tl.n; c += 32) {
+      // 16 tokens at a time, every second run
+      auto load = [&](int i, float (&v)[16]) {
         uint32_t r[16];
-        ptx::tmem_ld_32x32b_x16(tmem + c + ((q * 32) << 16), r);
+        ptx::tmem_ld_32x32b_x16(tmem + 16 * half + 32 * i + ((q * 32) << 16), r);
         ptx::tmem_ld_wait();
-        float v[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]) * (sx[(c >> 5) * 16 + j] * sw);
-        store_tokens<F32>(p.out, p.ldo, v, (int64_t)tl.row0 + c, tl.n - c, m0, p.M, lane);
+        for (int j = 0; j < 16; j += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(sx + 16 * i + j);
+          v[j] = __uint_as_float(r[j]) * (x.x * sw);
+          v[j + 1] = __uint_as_float(r[j + 1]) * (x.y * sw);
+          v[j + 2] = __uint_as_float(r[j + 2]) * (x.z * sw);
+          v[j + 3] = __uint_as_float(r[j + 3]) * (x.w * sw);
+        }
+      };
+      auto release = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_pair(empty0);
+      };
+      const int first = 16 * half;
+      float v[16];
+      if (F32) {
+        for (int i = 0; first + 32 * i < tl.n; ++i) {
+          load(i, v);
+          store_tokens<true>(p.out, p.ldo, v, (int64_t)tl.row0 + first + 32 * i, tl.n - first - 32 * i, m0, p.M, lane);
+        }
+        release();
+      } else {
+        uint4 w[8][2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (first + 32 * i >= tl.n) break;
+          load(i, v);
+          w[i][0] = transpose8_bf16(v, lane);
+          w[i][1] = transpose8_bf16(v + 8, lane);
+        }
+        release();
+        const int64_t ch = m0 + (lane & 24);
+        const int left = ch < p.M ? tl.n - first - (int)(lane & 7) : 0;
+        uint16_t* o = static_cast<uint16_t*>(p.out) + ((int64_t)tl.row0 + first + (lane & 7)) * p.ldo + ch;
+#pragma unroll
+        for (int i = 0; i < 8; ++i, o += 32 * p.ldo) {
+          if (32 * i < left) *reinterpret_cast<uint4*>(o) = w[i][0];
+          if (32 * i + 8 < left) *reinterpret_cast<uint4*>(o + 8 * p.ldo) = w[i][1];
+        }
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_pair(empty0);
     }
   }
   __syncthreads();
@@ -256,6 +300,12 @@ int launch_int8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap&
   if (dev < 0 || dev >= 64) return MGQ_ERR_CUDA;
   if (!attr_set[dev]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem8) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return MGQ_ERR_CUDA;
+    }
+    // (a build that launches with fewer registers could not serve the split)
+    cudaFuncAttributes at;
+    if (cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs < kRegLaunch) {
       (void)cudaGetLastError();
       return MGQ_ERR_CUDA;
     }
@@ -390,7 +440,7 @@ int mgq_ragged_gemm_int8(const int8_t* x, int64_t ldx, const float* x_scale, con
   p.sx = x_scale;
   p.sw = w_scale;
   debug_knobs(&p.stall, &p.wait_ns);
-  const bool few = few_rows(E, R);
+  const bool few = few_rows(E, R, N);
   CUtensorMap ta, tb, ts;
   if (few) {
     if (!encode_tmap_sw128_3d(&ta, w, 1, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K, N * K, {128, 128, 1}) ||
@@ -402,7 +452,7 @@ int mgq_ragged_gemm_int8(const int8_t* x, int64_t ldx, const float* x_scale, con
       !encode_tmap_sw128_3d(&tb, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, 128, 1}) ||
       !encode_tmap_sw128_3d(&ts, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, kSmallBox, 1}))
     return MGQ_ERR_CUDA;
-  const int64_t tiles = (R / kTile + min((int64_t)E, R)) * ((N + kTile - 1) / kTile);
+  const int64_t tiles = token_tiles(E, R, kTile) * ((N + kTile - 1) / kTile);
   return p.out_f32 ? launch_int8<true>(ta, tb, ts, p, tiles, as_stream(stream))
                    : launch_int8<false>(ta, tb, ts, p, tiles, as_stream(stream));
 }

@@ -481,45 +481,46 @@ def moe_few_forward(x, topk_idx, probs, W1: Operand, W2: Operand, scaling, E, F,
         raise MGQError(rc, fn)
 
 
-def _pitch(t, rows, cols):
-    """Row pitch in elements of a [rows, cols] matrix with contiguous rows, or -1."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _pitch(t, rows, cols, dev):
+    """Row pitch in elements of a [rows, cols] matrix of device `dev` with contiguous rows, or -1."""
+    if t.shape != (rows, cols) or t.get_device() != dev:
         return -1
-    return t.stride(0) if rows > 1 else cols
+    ld, one = t.stride()
+    return -1 if one != 1 and cols > 1 else ld if rows > 1 else cols
 
 
-def _ragged(fn, rows_in, wide_in, w, offsets, rows_out, wide_out):
-    """What the ragged products check of their tensors; (offsets pointer, E, pitches)."""
-    E, dev = w.shape[0], torch.cuda.current_device()
-    R = rows_in.shape[0]
-    if w.dim() != 3 or not w.is_contiguous():
-        _refuse(fn)
-    for t in (rows_in, w, rows_out):
-        if not t.is_cuda or t.get_device() != dev:
-            _refuse(fn)
+def _offsets(fn, offsets, E, dev):
     if offsets is None:
         if E != 1:
             _refuse(fn)
-    elif not (offsets.dtype is _I32 and offsets.shape == (E + 1,) and offsets.is_contiguous() and offsets.is_cuda and
-              offsets.get_device() == dev):
+        return None
+    if not (offsets.dtype is _I32 and offsets.shape == (E + 1,) and offsets.is_contiguous() and
+            offsets.get_device() == dev):
         _refuse(fn)
-    lda, ldb = _pitch(rows_in, R, wide_in), _pitch(rows_out, R, wide_out)
-    if lda < 0 or ldb < 0:
-        _refuse(fn)
-    return None if offsets is None else offsets.data_ptr(), E, R, lda, ldb
+    return offsets.data_ptr()
 
 
 def ragged_gemm_fwd(x, w, offsets, y, stream=None):
     """y[r] = w[e] x[r] for the rows [offsets[e], offsets[e+1]) of group e: x bf16 [R, K],
     w bf16 [E, N, K], y bf16 or float32 [R, N]; offsets int32 [E+1], or None with E = 1."""
     fn = "mgq_ragged_gemm_fwd"
-    dt = _OUT_DTYPE.get(y.dtype)
-    if x.dtype is not _BF16 or w.dtype is not _BF16 or dt is None or w.dim() != 3:
+    dt, shape = _OUT_DTYPE.get(y.dtype), w.shape
+    if x.dtype is not _BF16 or w.dtype is not _BF16 or dt is None:
         _refuse(fn, ERR_UNSUPPORTED)
-    _, N, K = w.shape
-    off, E, R, ldx, ldy = _ragged(fn, x, K, w, offsets, y, N)
-    rc = (_lib or load()).mgq_ragged_gemm_fwd(x.data_ptr(), ldx, w.data_ptr(), off, E, R, N, K, y.data_ptr(), ldy, dt,
-                                              _s(stream))
+    if len(shape) != 3:
+        _refuse(fn)
+    E, N, K = shape
+    R, dev = x.shape[0], _device()
+    ldx, ldy = _pitch(x, R, K, dev), _pitch(y, R, N, dev)
+    if ldx < 0 or ldy < 0 or w.get_device() != dev or not w.is_contiguous():
+        _refuse(fn)
+    rc = (_lib or load()).mgq_ragged_gemm_fwd(
+        x.data_ptr(), ldx, w.data_ptr(), _offsets(fn, offsets, E, dev), E, R, N, K, y.data_ptr(), ldy, dt,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise MGQError(rc, fn)
 
@@ -528,13 +529,19 @@ def ragged_gemm_dgrad(dy, w, offsets, dx, stream=None):
     """dx[r] = dy[r] w[e] for the rows of group e: dy bf16 [R, N], w bf16 [E, N, K], dx bf16
     or float32 [R, K]."""
     fn = "mgq_ragged_gemm_dgrad"
-    dt = _OUT_DTYPE.get(dx.dtype)
-    if dy.dtype is not _BF16 or w.dtype is not _BF16 or dt is None or w.dim() != 3:
+    dt, shape = _OUT_DTYPE.get(dx.dtype), w.shape
+    if dy.dtype is not _BF16 or w.dtype is not _BF16 or dt is None:
         _refuse(fn, ERR_UNSUPPORTED)
-    _, N, K = w.shape
-    off, E, R, lddy, lddx = _ragged(fn, dy, N, w, offsets, dx, K)
-    rc = (_lib or load()).mgq_ragged_gemm_dgrad(dy.data_ptr(), lddy, w.data_ptr(), off, E, R, N, K, dx.data_ptr(), lddx,
-                                                dt, _s(stream))
+    if len(shape) != 3:
+        _refuse(fn)
+    E, N, K = shape
+    R, dev = dy.shape[0], _device()
+    lddy, lddx = _pitch(dy, R, N, dev), _pitch(dx, R, K, dev)
+    if lddy < 0 or lddx < 0 or w.get_device() != dev or not w.is_contiguous():
+        _refuse(fn)
+    rc = (_lib or load()).mgq_ragged_gemm_dgrad(
+        dy.data_ptr(), lddy, w.data_ptr(), _offsets(fn, offsets, E, dev), E, R, N, K, dx.data_ptr(), lddx, dt,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise MGQError(rc, fn)
 
@@ -543,13 +550,19 @@ def ragged_gemm_wgrad(dy, x, offsets, dw, beta=0.0, stream=None):
     """dw[e] = beta dw[e] + dy^T x over the rows of group e: dy bf16 [R, N], x bf16 [R, K],
     dw float32 (bf16: beta 0) [E, N, K]."""
     fn = "mgq_ragged_gemm_wgrad"
-    dt = _OUT_DTYPE.get(dw.dtype)
-    if dy.dtype is not _BF16 or x.dtype is not _BF16 or dt is None or dw.dim() != 3:
+    dt, shape = _OUT_DTYPE.get(dw.dtype), dw.shape
+    if dy.dtype is not _BF16 or x.dtype is not _BF16 or dt is None:
         _refuse(fn, ERR_UNSUPPORTED)
-    _, N, K = dw.shape
-    off, E, R, lddy, ldx = _ragged(fn, dy, N, dw, offsets, x, K)
-    rc = (_lib or load()).mgq_ragged_gemm_wgrad(dy.data_ptr(), lddy, x.data_ptr(), ldx, off, E, R, N, K, beta,
-                                                dw.data_ptr(), dt, _s(stream))
+    if len(shape) != 3:
+        _refuse(fn)
+    E, N, K = shape
+    R, dev = dy.shape[0], _device()
+    lddy, ldx = _pitch(dy, R, N, dev), _pitch(x, R, K, dev)
+    if lddy < 0 or ldx < 0 or dw.get_device() != dev or not dw.is_contiguous():
+        _refuse(fn)
+    rc = (_lib or load()).mgq_ragged_gemm_wgrad(
+        dy.data_ptr(), lddy, x.data_ptr(), ldx, _offsets(fn, offsets, E, dev), E, R, N, K, beta, dw.data_ptr(), dt,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise MGQError(rc, fn)
 
@@ -559,17 +572,21 @@ def ragged_gemm_int8(x, x_scale, w, w_scale, offsets, y, stream=None):
     float32 [R], w int8 [E, N, K], w_scale float32 [E, N], y bf16 or float32 [R, N]; offsets
     int32 [E+1], or None with E = 1 (a plain product)."""
     fn = "mgq_ragged_gemm_int8"
-    dt = _OUT_DTYPE.get(y.dtype)
-    if x.dtype is not _I8 or w.dtype is not _I8 or dt is None or w.dim() != 3:
+    dt, shape = _OUT_DTYPE.get(y.dtype), w.shape
+    if x.dtype is not _I8 or w.dtype is not _I8 or dt is None:
         _refuse(fn, ERR_UNSUPPORTED)
-    E, N, K = w.shape
-    off, E, R, ldx, ldy = _ragged(fn, x, K, w, offsets, y, N)
-    if not (x_scale.dtype is _F32 and x_scale.shape == (R,) and x_scale.is_contiguous() and
-            x_scale.get_device() == x.get_device() and w_scale.dtype is _F32 and w_scale.shape == (E, N) and
-            w_scale.is_contiguous() and w_scale.get_device() == x.get_device()):
+    if len(shape) != 3:
         _refuse(fn)
-    rc = (_lib or load()).mgq_ragged_gemm_int8(x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
-                                               off, E, R, N, K, y.data_ptr(), ldy, dt, _s(stream))
+    E, N, K = shape
+    R, dev = x.shape[0], _device()
+    ldx, ldy = _pitch(x, R, K, dev), _pitch(y, R, N, dev)
+    if ldx < 0 or ldy < 0 or w.get_device() != dev or not w.is_contiguous() or not (
+            x_scale.dtype is _F32 and x_scale.shape == (R,) and x_scale.is_contiguous() and x_scale.get_device() == dev and
+            w_scale.dtype is _F32 and w_scale.shape == (E, N) and w_scale.is_contiguous() and w_scale.get_device() == dev):
+        _refuse(fn)
+    rc = (_lib or load()).mgq_ragged_gemm_int8(
+        x.data_ptr(), ldx, x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), _offsets(fn, offsets, E, dev), E, R, N, K,
+        y.data_ptr(), ldy, dt, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise MGQError(rc, fn)
 
@@ -578,15 +595,18 @@ def rows_quantize_int8(x, codes, scale, stream=None):
     """scale[t] = amax / 127, codes[t] = round(127 x / amax) for each row of x bf16 [T, K]: codes
     int8 [T, K], scale float32 [T]."""
     fn = "mgq_rows_quantize_int8"
-    if x.dtype is not _BF16 or codes.dtype is not _I8 or x.dim() != 2:
+    shape = x.shape
+    if x.dtype is not _BF16 or codes.dtype is not _I8:
         _refuse(fn, ERR_UNSUPPORTED)
-    T, K = x.shape
-    ldx = _pitch(x, T, K)
-    dev = torch.cuda.current_device()
-    if ldx < 0 or not (codes.shape == x.shape and codes.is_contiguous() and scale.dtype is _F32 and scale.shape == (T,) and
-                       scale.is_contiguous() and x.is_cuda and x.get_device() == dev and codes.is_cuda and
-                       codes.get_device() == dev and scale.is_cuda and scale.get_device() == dev):
+    if len(shape) != 2:
         _refuse(fn)
-    rc = (_lib or load()).mgq_rows_quantize_int8(x.data_ptr(), ldx, T, K, codes.data_ptr(), scale.data_ptr(), _s(stream))
+    T, K = shape
+    dev = _device()
+    ldx = _pitch(x, T, K, dev)
+    if ldx < 0 or not (codes.shape == shape and codes.is_contiguous() and codes.get_device() == dev and
+                       scale.dtype is _F32 and scale.shape == (T,) and scale.is_contiguous() and scale.get_device() == dev):
+        _refuse(fn)
+    rc = (_lib or load()).mgq_rows_quantize_int8(x.data_ptr(), ldx, T, K, codes.data_ptr(), scale.data_ptr(),
+                                                 _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         raise MGQError(rc, fn)
