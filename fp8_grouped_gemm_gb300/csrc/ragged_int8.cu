@@ -32,7 +32,7 @@ constexpr int kThreads8 = 28 * 32;
 // launched with: the epilogue holds a tile's 64 words of scaled and transposed
 // bf16 pairs, so that the one accumulator is free before the stores (whose burst
 // takes 3 us a tile when all SMs end one together).
-constexpr int kRegLow = 40, kRegConv = 56, kRegEpi = 120, kRegLaunch = 72;
+constexpr int kRegLow = 40, kRegConv = 64, kRegEpi = 104, kRegLaunch = 72;
 static_assert(128 * kRegLow + 512 * kRegConv + 256 * kRegEpi <= kThreads8 * kRegLaunch, "register split");
 constexpr size_t kSmem8 = 1024 + kRaw * 2 * (size_t)kRawBytes + kConv * (size_t)kF16Bytes + 8 * 512 + 256 +
                           2 * (kMaxE + 8) * 4;
@@ -58,6 +58,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_bad = reinterpret_cast<int*>(s_tmem + 2);
+  volatile int* s_n = reinterpret_cast<volatile int*>(s_tmem + 3);   // [kRaw] tokens of a stage's tile, -1 after the last one
   int32_t* s_off = reinterpret_cast<int32_t*>(raw_full + 32);
   int32_t* s_cum = s_off + (kMaxE + 8);
 
@@ -123,6 +124,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
           timed_out();
           break;
         }
+        s_n[st] = tl.n;
         ptx::mbar_arrive_expect_tx(&raw_full[st], bytes);
         const int32_t kx = s * kBK8, r = tl.row0 + half * (int)rank;
         ptx::tma_load_3d(sA + st * kRawBytes, &tmA, &raw_full[st], kx, (int32_t)(tl.m0 + 128 * rank), tl.e);
@@ -131,6 +133,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
           ptx::tma_load_3d(sB + st * kRawBytes + i * kSmallBox * 128, &tmS, &raw_full[st], kx, r + i * (int)kSmallBox, 0);
         if (++st == kRaw) st = 0, ph ^= 1;
       }
+    }
+    if (!*s_abort && ptx::mbar_wait(&raw_empty[st], ph ^ 1, p.wait_ns)) {
+      s_n[st] = -1;
+      ptx::mbar_arrive(&raw_full[st]);
     }
     // after a wait that ran out: no copy may still be on its way when the CTA leaves
     if (*s_abort)
@@ -173,38 +179,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     const uint32_t quad = warp & 3;                                     // channels: the warp's own lanes of tensor memory
     const int h = ((warp - 4) >> 2) & 1;
     const uint32_t row = quad * 32 + lane;
-    int ecur = 0;
     uint32_t rs = 0, rph = 0, cs = h, cph = 0;                          // every second half stage
-    RaggedTile tl;
-    bool ok = true;
-    for (int64_t t = pair; run && ok && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
-      const bool mine = chan || (int)(quad * 32) < (tl.n + 31) / 32 * 16;   // tokens: the rows an MMA reads
-      for (int s = 0; s < tl.nst; ++s) {
-        ok = *s_abort == 0;
-        ok = ok && ptx::mbar_wait(&raw_full[rs], rph, p.wait_ns);
-        uint4 c[4];
-        if (ok && mine) load_codes((chan ? sA : sB) + rs * kRawBytes, row, h, c);
-        __syncwarp();
-        if (ok && lane == 0) ptx::mbar_arrive(&raw_empty[rs]);
-        ok = ok && ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        if (chan) {
-          ptx::tc_fence_after();
-          codes_to_tmem(c, tmem + kAcol + cs * kAcols + ((32u * quad) << 16));
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-        } else if (mine) {
-          codes_to_smem(c, sF + cs * kF16Bytes, row);
-          ptx::fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_pair(ptx::mapa_shared(ptx::smem_u32(&conv_full[cs]), 0));
-        if (++rs == kRaw) rs = 0, rph ^= 1;
-        if ((cs += 2) >= kConv) cs -= kConv, cph ^= 1;
+    bool ok = run;
+    while (ok) {
+      ok = *s_abort == 0;
+      ok = ok && ptx::mbar_wait(&raw_full[rs], rph, p.wait_ns);
+      if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+      const int n = s_n[rs];
+      if (n < 0) break;                                                 // no more tiles
+      const bool mine = chan || (int)(quad * 32) < (n + 31) / 32 * 16;  // tokens: the rows an MMA reads
+      uint4 c[4];
+      if (mine) load_codes((chan ? sA : sB) + rs * kRawBytes, row, h, c);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&raw_empty[rs]);
+      ok = ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns);
+      if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+      if (chan) {
+        ptx::tc_fence_after();
+        codes_to_tmem(c, tmem + kAcol + cs * kAcols + ((32u * quad) << 16));
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+      } else if (mine) {
+        codes_to_smem(c, sF + cs * kF16Bytes, row);
+        ptx::fence_proxy_async_smem();
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_pair(ptx::mapa_shared(ptx::smem_u32(&conv_full[cs]), 0));
+      if (++rs == kRaw) rs = 0, rph ^= 1;
+      if ((cs += 2) >= kConv) cs -= kConv, cph ^= 1;
     }
-    if (!ok) timed_out();
+    if (run && !ok) timed_out();
   } else if (warp >= 20) {
     ptx::setmaxnreg_inc<kRegEpi>();
     // ------------------------------------------------------------ epilogue (both CTAs)
@@ -216,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     uint32_t tc = 0;
     RaggedTile tl;
     for (int64_t t = pair; run && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs, ++tc) {
-      const int64_t m0 = tl.m0 + 128 * rank + 32 * q;
+      const int64_t m0 = tl.m0 + (int)(128 * rank + 32 * q);
       const float sw = m0 + lane < p.M ? p.sw[tl.e * p.M + m0 + lane] : 0.0f;
       __syncwarp();
 #pragma unroll
