@@ -396,9 +396,9 @@ int check_ragged(const void* a, int64_t lda, int64_t wa, const void* b, int64_t 
   MGQ_CHECK_ARG(N % 8 == 0 && K % 8 == 0 && N < (1ll << 31) - 512 && K < (1ll << 31) - 512);
   MGQ_CHECK_ARG(offsets || E == 1);
   MGQ_CHECK_ARG(out_dtype == MGQ_OUT_BF16 || out_dtype == MGQ_OUT_F32);
-  MGQ_CHECK_ARG((reinterpret_cast<uintptr_t>(offsets) & 3u) == 0 && out && aligned16(out));
+  MGQ_CHECK_ARG((reinterpret_cast<uintptr_t>(offsets) & 3u) == 0 && aligned16(out));
   MGQ_CHECK_ARG(lda >= wa && lda % 8 == 0 && ldb >= wb && ldb % 8 == 0 && lda < (1ll << 38) && ldb < (1ll << 38));
-  MGQ_CHECK_ARG(R == 0 || (a && b && aligned16(a) && aligned16(b)));
+  MGQ_CHECK_ARG(aligned16(a) && aligned16(b) && (R == 0 || (a && b && out)));
   return MGQ_OK;
 }
 
@@ -468,7 +468,7 @@ int mgq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void* x_bf16,
   int rc = check_ragged(dy_bf16, lddy, N, x_bf16, ldx, K, offsets, E, R, N, K, dw, out_dtype);
   if (rc != MGQ_OK) return rc;
   MGQ_CHECK_ARG(beta == 0.0f || out_dtype == MGQ_OUT_F32);
-  MGQ_CHECK_ARG(beta == beta);
+  MGQ_CHECK_ARG(beta == beta && dw);
   const int64_t u = out_dtype == MGQ_OUT_F32 ? 4 : 2;
   if (R == 0 && beta == 1.0f) return MGQ_OK;
   RaggedArgs p{};

@@ -621,7 +621,7 @@ int mgq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void* x_bf16,
  *           product of all R rows)
  * Every code from -128 to 127 counts as it stands. The sum is held in float32:
  * exact while it stays below 2^24 (K up to 1024 whatever the codes), beyond that
- * within 2^-24 of the running sum for each 16 elements. Its product with
+ * within 2^-23 of the running sum for each 16 elements. Its product with
  * (x_scale w_scale) is rounded to float32, then to the result's type. A NaN scale
  * makes its row or channel NaN.
  * Requires N a multiple of 8, K and ldx multiples of 16, ldy of 8; else as above. */
