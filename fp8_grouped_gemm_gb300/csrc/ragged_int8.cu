@@ -180,31 +180,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     const int h = ((warp - 4) >> 2) & 1;
     const uint32_t row = quad * 32 + lane;
     uint32_t rs = 0, rph = 0, cs = h, cph = 0;                          // every second half stage
+    // (a chain of latencies, which bounds tiles of few tokens: one vote and one
+    // barrier of the warp a round, the codes on their way during the second wait)
+    const uint32_t full0 = ptx::mapa_shared(ptx::smem_u32(conv_full), 0);
     bool ok = run;
     while (ok) {
-      ok = *s_abort == 0;
-      ok = ok && ptx::mbar_wait(&raw_full[rs], rph, p.wait_ns);
-      if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+      ok = ptx::mbar_wait(&raw_full[rs], rph, p.wait_ns);
       const int n = s_n[rs];
-      if (n < 0) break;                                                 // no more tiles
-      const bool mine = chan || (int)(quad * 32) < (n + 31) / 32 * 16;  // tokens: the rows an MMA reads
       uint4 c[4];
-      if (mine) load_codes((chan ? sA : sB) + rs * kRawBytes, row, h, c);
+      load_codes((chan ? sA : sB) + rs * kRawBytes, row, h, c);
+      if (n < 0) break;                                                 // no more tiles
+      ok = ok && ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns);
+      if (!(ok = __all_sync(0xFFFFFFFFu, ok) && !*s_abort)) break;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&raw_empty[rs]);
-      ok = ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns);
-      if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
       if (chan) {
         ptx::tc_fence_after();
         codes_to_tmem(c, tmem + kAcol + cs * kAcols + ((32u * quad) << 16));
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
-      } else if (mine) {
+      } else if ((int)(quad * 32) < (n + 31) / 32 * 16) {               // the rows an MMA reads
         codes_to_smem(c, sF + cs * kF16Bytes, row);
         ptx::fence_proxy_async_smem();
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_pair(ptx::mapa_shared(ptx::smem_u32(&conv_full[cs]), 0));
+      if (lane == 0) ptx::mbar_arrive_pair(full0 + cs * 8);
       if (++rs == kRaw) rs = 0, rph ^= 1;
       if ((cs += 2) >= kConv) cs -= kConv, cph ^= 1;
     }
