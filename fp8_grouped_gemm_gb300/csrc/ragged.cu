@@ -93,6 +93,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     ptx::tmem_alloc_pair(s_tmem, 512);
     ptx::tmem_relinquish_pair();
   }
+  ptx::grid_wait();                    // from here on: what the launch before wrote
+  ptx::grid_launch();
   if (warp == 2) {
     const bool ok = load_groups(p, s_off, s_cum, lane);
     if (lane == 0) {
@@ -384,9 +386,9 @@ int launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap&
     attr_set[dev] = true;
   }
   const int64_t pairs = min((int64_t)(num_sms() / 2), max_tiles);
-  kern<<<(unsigned)(2 * max(pairs, (int64_t)1)), threads_of(OP), smem_of(OP), s>>>(ta, tb, ts, p);
-  MGQ_LAUNCH_CHECK();
-  return MGQ_OK;
+  return launch_after(kern, dim3((unsigned)(2 * max(pairs, (int64_t)1))), threads_of(OP), smem_of(OP), 1, s, ta, tb, ts, p)
+             ? MGQ_OK
+             : MGQ_ERR_CUDA;
 }
 
 // What every entry point checks: sizes, pitches, alignment.

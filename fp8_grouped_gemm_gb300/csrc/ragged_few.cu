@@ -382,6 +382,7 @@ int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p
     }
     attr_set[dev] = true;
   }
+  if (tiles * split >= (1ll << 31)) return MGQ_ERR_INVALID_ARG;
   return launch_after(kern, dim3((unsigned)(tiles * split)), few_threads(I8), few_smem(I8), split, s, ta, tb, p, split)
              ? MGQ_OK
              : MGQ_ERR_CUDA;

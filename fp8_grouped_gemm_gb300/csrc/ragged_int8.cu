@@ -90,6 +90,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     ptx::tmem_alloc_pair(s_tmem, 512);
     ptx::tmem_relinquish_pair();
   }
+  ptx::grid_wait();                    // from here on: what the launch before wrote
+  ptx::grid_launch();
   if (warp == 2) {
     const bool ok = load_groups(p, s_off, s_cum, lane);
     if (lane == 0) {
@@ -316,9 +318,9 @@ int launch_int8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap&
     attr_set[dev] = true;
   }
   const int64_t pairs = min((int64_t)(num_sms() / 2), max_tiles);
-  kern<<<(unsigned)(2 * max(pairs, (int64_t)1)), kThreads8, kSmem8, s>>>(ta, tb, ts, p);
-  MGQ_LAUNCH_CHECK();
-  return MGQ_OK;
+  return launch_after(kern, dim3((unsigned)(2 * max(pairs, (int64_t)1))), kThreads8, kSmem8, 1, s, ta, tb, ts, p)
+             ? MGQ_OK
+             : MGQ_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
@@ -355,6 +357,8 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rows_quant8_kernel(Quant8Ar
   const int tid = threadIdx.x % G, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x * (int64_t)kRows + threadIdx.x / G;
   if (row >= a.T) return;                          // (whole warps; a row of several warps is the CTA)
+  ptx::grid_wait();
+  ptx::grid_launch();
   const uint4* x = reinterpret_cast<const uint4*>(a.x + row * a.ldx);
   const int units = a.K / 16;
   uint4 w[2][2];
@@ -470,11 +474,10 @@ int mgq_rows_quantize_int8(const void* x_bf16, int64_t ldx, int64_t T, int64_t K
   Quant8Args a{static_cast<const uint16_t*>(x_bf16), ldx, T, (int)K, codes, scale};
   cudaStream_t s = as_stream(stream);
   const int64_t units = K / 16;
-  if (units <= 64) rows_quant8_kernel<32><<<(unsigned)((T + 3) / 4), 128, 0, s>>>(a);
-  else if (units <= 256) rows_quant8_kernel<128><<<(unsigned)T, 128, 0, s>>>(a);
-  else rows_quant8_kernel<512><<<(unsigned)T, 512, 0, s>>>(a);
-  MGQ_LAUNCH_CHECK();
-  return MGQ_OK;
+  const bool ok = units <= 64    ? launch_after(rows_quant8_kernel<32>, dim3((unsigned)((T + 3) / 4)), 128, 0, 1, s, a)
+                  : units <= 256 ? launch_after(rows_quant8_kernel<128>, dim3((unsigned)T), 128, 0, 1, s, a)
+                                 : launch_after(rows_quant8_kernel<512>, dim3((unsigned)T), 512, 0, 1, s, a);
+  return ok ? MGQ_OK : MGQ_ERR_CUDA;
 }
 
 }  // extern "C"

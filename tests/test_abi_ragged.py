@@ -117,10 +117,17 @@ def _expect(calls, mgq):
         assert e.value.status == status, i
 
 
-def test_programmatic_launch_of_the_few_row_form_reads_with_plain_loads():
-    """It may start before the launch in front of it has finished: it waits before its
-    first load, and takes nothing through the read-only path."""
-    text = open(os.path.join(ROOT, "fp8_grouped_gemm_gb300", "csrc", "ragged_few.cu")).read()
-    assert "launch_after(" in text and text.index("grid_wait()") < text.index("p.offsets[i]")
+@pytest.mark.parametrize("name", ["ragged.cu", "ragged_int8.cu", "ragged_few.cu"])
+def test_programmatic_launches_read_with_plain_loads(name):
+    """They may start before the launch in front of them has finished: each kernel waits before its first
+    load, and takes nothing through the read-only path."""
+    csrc = os.path.join(ROOT, "fp8_grouped_gemm_gb300", "csrc")
+    text, shared = (open(os.path.join(csrc, n)).read() for n in (name, "ragged.cuh"))
+    kernels = text.split("__global__")[1:]
+    assert kernels and "launch_after(" in text and "<<<" not in text
+    for k in kernels:
+        assert "grid_wait()" in k
+        wait = k.index("grid_wait()")
+        assert all(wait < k.index(w) for w in ("load_groups", "p.offsets[", "tma_load_3d", "x[2 * u]") if w in k)
     for word in ("__ldg(", ".nc.", "__restrict__"):
-        assert word not in text
+        assert word not in text and word not in shared

@@ -146,6 +146,22 @@ def test_wgrad_without_rows(mgq, beta):
     assert torch.equal(dw, beta * old)
 
 
+@pytest.mark.parametrize("R", [5, 4000])
+def test_all_groups_empty(mgq, R):
+    """Rows, but none in a group: nothing is written but the empty groups' zeros."""
+    off, N, K = _off([2, 2, 2]), 1032, 48
+    x, dy, w = (torch.full(s, float("nan"), dtype=BF, device="cuda") for s in ((R, K), (R, N), (2, N, K)))
+    y, dx = torch.full((R, N), 7.0, device="cuda"), torch.full((R, K), 7.0, dtype=BF, device="cuda")
+    dw = torch.full((2, N, K), 7.0, device="cuda")
+    mgq.ragged_gemm_fwd(x, w, off, y)
+    mgq.ragged_gemm_dgrad(dy, w, off, dx)
+    mgq.ragged_gemm_wgrad(dy, x, off, dw)
+    mgq.ragged_gemm_int8(torch.ones(R, K, dtype=I8, device="cuda"), y[:, 0].contiguous(),
+                         torch.ones(2, N, K, dtype=I8, device="cuda"), dw[:, :, 0].contiguous(), off, y)
+    assert mgq.get_error() == mgq.OK
+    assert (y == 7).all() and (dx == 7).all() and (dw == 0).all()
+
+
 @pytest.mark.parametrize("small", [True, False])
 def test_foreign_nan_stays_out(mgq, small):
     """NaN and infinity of one group's rows and weight reach no other group."""
