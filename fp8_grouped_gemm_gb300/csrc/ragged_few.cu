@@ -36,46 +36,47 @@ struct FewTile {
 };
 
 // Tile t: groups in order, a group's channel tiles, its token tiles fastest (they
-// share the weights). One warp; s_off holds the offsets. False if there is no
-// such tile; `ok` is false for offsets that are no row partition.
-__device__ __forceinline__ bool few_tile(const RaggedArgs& p, const int32_t* s_off, int64_t t, uint32_t lane, FewTile& tl,
+// share the weights). A whole warp; s_off holds the offsets. False if there is no
+// such tile; `ok` is false for offsets that are no row partition. (Tile numbers are
+// below 2^31: the launch sees to it.)
+__device__ __forceinline__ bool few_tile(const RaggedArgs& p, const int32_t* s_off, uint32_t t, uint32_t lane, FewTile& tl,
                                          bool& ok) {
-  const int per = (p.E + 31) / 32, e0 = (int)lane * per, e1 = min(e0 + per, p.E);
-  int mine = 0;
+  const int per = (p.E + 31) / 32, e0 = min((int)lane * per, p.E), e1 = min(e0 + per, p.E);
+  const uint32_t nM = (uint32_t)((p.M + 127) / 128);
+  uint32_t mine = 0;
   ok = true;
-  for (int e = e0; e < e1; ++e) {
-    const int lo = s_off[e], hi = s_off[e + 1];
+  for (int e = e0, lo = s_off[e0]; e < e1; ++e) {
+    const int hi = s_off[e + 1];
     ok &= lo >= 0 && lo <= hi && hi <= p.R;
-    mine += (max(hi - lo, 0) + kFewTok - 1) / kFewTok;
+    mine += (uint32_t)(max(hi - lo, 0) + kFewTok - 1) / kFewTok;
+    lo = hi;
   }
   ok = __all_sync(0xFFFFFFFFu, ok);
-  int inc = mine;
+  if (!ok) return false;
+  uint32_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= (uint32_t)o) inc += v;
   }
-  const int64_t nM = (p.M + 127) / 128;
   const uint32_t at = __ballot_sync(0xFFFFFFFFu, inc * nM > t);
   if (!at) return false;
   const int src = __ffs(at) - 1;
-  int e = 0, cum = 0, tiles = 0;
-  if ((int)lane == src) {
-    cum = inc - mine;
-    for (e = e0; e < e1; ++e) {
-      tiles = (s_off[e + 1] - s_off[e] + kFewTok - 1) / kFewTok;
-      if ((cum + tiles) * nM > t) break;
-      cum += tiles;
-    }
+  // every lane walks that lane's groups
+  uint32_t local = t - __shfl_sync(0xFFFFFFFFu, inc - mine, src) * nM, tiles = 1;
+  int e = src * per, lo = s_off[e];
+  for (;; ++e) {
+    const int hi = s_off[e + 1];
+    tiles = (uint32_t)(hi - lo + kFewTok - 1) / kFewTok;
+    if (local < tiles * nM) break;
+    local -= tiles * nM;
+    lo = hi;
   }
-  e = __shfl_sync(0xFFFFFFFFu, e, src);
-  cum = __shfl_sync(0xFFFFFFFFu, cum, src);
-  tiles = max(__shfl_sync(0xFFFFFFFFu, tiles, src), 1);
-  const int64_t local = t - cum * nM, m = local / tiles;
+  const uint32_t m = local / tiles;
   tl.e = e;
-  tl.row0 = s_off[e] + (int)(local - m * tiles) * kFewTok;
+  tl.row0 = lo + (int)(local - m * tiles) * kFewTok;
   tl.n = min(kFewTok, s_off[e + 1] - tl.row0);
-  tl.m0 = m * 128;
+  tl.m0 = (int64_t)m * 128;
   return true;
 }
 
@@ -110,8 +111,6 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
   uint64_t* drained = acc_empty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  int* s_tile = reinterpret_cast<int*>(s_tmem + 2);   // [4]: state, e, row0, n
-  int64_t* s_m0 = reinterpret_cast<int64_t*>(full + 28);
   int32_t* s_off = reinterpret_cast<int32_t*>(full + 32);
 
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);   // (known to be uniform)
@@ -144,29 +143,16 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
   ptx::grid_wait();                                // from here on: what the launch before wrote
   ptx::grid_launch();
   for (int i = threadIdx.x; i <= p.E; i += few_threads(I8)) s_off[i] = p.offsets ? p.offsets[i] : i ? (int)p.R : 0;
-  __syncthreads();
-  if (warp == 2) {
-    FewTile tl;
-    bool ok;
-    const bool any = few_tile(p, s_off, blockIdx.x / split, lane, tl, ok);
-    if (lane == 0) {
-      if (!ok && blockIdx.x == 0) report(p.err, MGQ_ERR_INVALID_ARG);
-      s_tile[0] = ok && any;
-      if (ok && any) {
-        s_tile[1] = tl.e;
-        s_tile[2] = tl.row0;
-        s_tile[3] = tl.n;
-        *s_m0 = tl.m0;
-      }
-    }
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const bool run = s_tile[0] != 0;                 // the same in the whole cluster
-  const int e = s_tile[1], row0 = s_tile[2], n = s_tile[3];
-  const int64_t m0 = *s_m0;
+  FewTile tl{0, 0, 1, 0};
+  bool ok_off;
+  const bool run = few_tile(p, s_off, blockIdx.x / split, lane, tl, ok_off);   // the same in the whole cluster
+  if (!ok_off && blockIdx.x == 0 && threadIdx.x == 0) report(p.err, MGQ_ERR_INVALID_ARG);
+  const int e = tl.e, row0 = tl.row0, n = tl.n;
+  const int64_t m0 = tl.m0;
   // this rank's stages of the contraction
   const int nst = (int)((p.C + kElems - 1) / kElems), chunk = (nst + split - 1) / split;
   const int s0 = min(nst, rank * chunk), ns = min(nst, s0 + chunk) - s0;
@@ -336,35 +322,37 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
   if (split > 1) ptx::cluster_sync();              // every part is in place
   // tokens rank, rank + split, ..: a warp each, four channels a lane
   const int64_t ch = m0 + 4 * lane;
-  if (ch < p.M && !*s_abort) {
-    const uint32_t mine = ptx::smem_u32(sA) + lane * 16;
-    float4 sw = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-    if (I8) sw = *reinterpret_cast<const float4*>(p.sw + e * p.M + ch);
-    for (int j = rank + split * warp; j < n; j += split * (few_threads(I8) / 32)) {
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int r = 0; r < split; ++r) {
-        const float4 x = split > 1 ? ld_cluster_f32x4(ptx::mapa_shared(mine + j * 512, r))
-                                   : *reinterpret_cast<const float4*>(sA + lane * 16 + j * 512);
-        s.x += x.x;
-        s.y += x.y;
-        s.z += x.z;
-        s.w += x.w;
-      }
-      const int64_t tok = (int64_t)row0 + j;
-      if (I8) {
-        const float sx = p.sx[tok];
-        s.x *= sx * sw.x;
-        s.y *= sx * sw.y;
-        s.z *= sx * sw.z;
-        s.w *= sx * sw.w;
-      }
-      if (F32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + tok * p.ldo + ch) = s;
-      else
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + tok * p.ldo + ch) =
-            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  const bool in = ch < p.M && !*s_abort;
+  const uint32_t mine = ptx::smem_u32(sA) + lane * 16;
+  float4 sw = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+  if (I8 && in) sw = *reinterpret_cast<const float4*>(p.sw + e * p.M + ch);
+  constexpr int kWarps = few_threads(I8) / 32;
+  for (int j = rank + split * warp; j < n; j += split * kWarps) {
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int r = 0; r < split; ++r) {
+      const float4 x = split > 1 ? ld_cluster_f32x4(ptx::mapa_shared(mine + j * 512, r))
+                                 : *reinterpret_cast<const float4*>(sA + lane * 16 + j * 512);
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
     }
+    if (!in) continue;
+    const int64_t tok = (int64_t)row0 + j;
+    if (I8) {
+      const float sx = p.sx[tok];
+      s.x *= sx * sw.x;
+      s.y *= sx * sw.y;
+      s.z *= sx * sw.z;
+      s.w *= sx * sw.w;
+    }
+    if (F32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + tok * p.ldo + ch) = s;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + tok * p.ldo + ch) =
+          make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
-  if (split > 1) ptx::cluster_sync();              // nobody still reads this CTA's part
+  __syncwarp();
+  if (split > 1) ptx::cluster_sync_relaxed();      // nobody still reads this CTA's part
 }
 
 template <int OP, bool I8, bool F32>
