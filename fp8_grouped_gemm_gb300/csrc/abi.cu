@@ -92,8 +92,8 @@ bool encode_tmap_2d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t
   return r == CUDA_SUCCESS;
 }
 
-bool encode_tmap_sw128_3d(CUtensorMap* map, const void* base, int elem_bytes, const uint64_t (&dims)[3],
-                          uint64_t pitch1, uint64_t pitch2, const uint32_t (&box)[3]) {
+bool encode_tmap_swz_3d(CUtensorMap* map, const void* base, int elem_bytes, const uint64_t (&dims)[3],
+                        uint64_t pitch1, uint64_t pitch2, const uint32_t (&box)[3]) {
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (!load_encode()) return false;
@@ -106,8 +106,8 @@ bool encode_tmap_sw128_3d(CUtensorMap* map, const void* base, int elem_bytes, co
                                  : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   CUresult r = g_encode(map, dt, 3, const_cast<void*>(base), d, strides, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        box[0] * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

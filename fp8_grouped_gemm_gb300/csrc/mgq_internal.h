@@ -24,12 +24,12 @@ bool encode_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint6
 bool encode_tmap_2d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t inner, uint64_t outer,
                     uint64_t pitch, uint32_t box_inner, uint32_t box_outer, bool sw128 = false);
 
-// 3D tensor map of 8-, 16- or 32-bit elements with the 128-byte swizzle
-// (box[0] * elem_bytes == 128): dims[0] elements contiguous, pitch1 bytes from
+// 3D tensor map of 8-, 16- or 32-bit elements with the 128- or 64-byte swizzle
+// (box[0] * elem_bytes is the one or the other): dims[0] elements contiguous, pitch1 bytes from
 // one dims[1] index to the next, pitch2 bytes from one dims[2] index to the next.
 // What a box covers outside the dims reads as zero and is not stored.
-bool encode_tmap_sw128_3d(CUtensorMap* map, const void* base, int elem_bytes, const uint64_t (&dims)[3],
-                          uint64_t pitch1, uint64_t pitch2, const uint32_t (&box)[3]);
+bool encode_tmap_swz_3d(CUtensorMap* map, const void* base, int elem_bytes, const uint64_t (&dims)[3],
+                        uint64_t pitch1, uint64_t pitch2, const uint32_t (&box)[3]);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

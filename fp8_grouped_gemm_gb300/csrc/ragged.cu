@@ -28,6 +28,7 @@ namespace {
 constexpr int kBK = 64;                            // elements of the contraction a stage (128 bytes)
 constexpr uint32_t kOpBytes = 128 * 128;           // one operand's share of an SM a stage
 constexpr uint32_t kOutSlot = 32 * 128;            // wgrad: a warp's store staging
+__host__ __device__ constexpr uint32_t slot_of(int op) { return op == kWgrad ? kOutSlot : kTokSlot; }
 // float32 results: the tensor cores cut each sum off rather than round it, and
 // the error grows with every K=16 step (1.5e-8 a step, relative: 4.4e-6 after a
 // contraction of 4096, which a float32 result shows and a bf16 one does not).
@@ -37,14 +38,15 @@ constexpr int kPromote = 8;
 __host__ __device__ constexpr int stages_of(int op) { return op == kWgrad ? 5 : 6; }
 __host__ __device__ constexpr int threads_of(int op) { return op == kWgrad ? 352 : 320; }
 __host__ __device__ constexpr size_t smem_of(int op) {
-  return 1024 + stages_of(op) * 2 * (size_t)kOpBytes + (op == kWgrad ? 8 * kOutSlot : 0) + 256 + 2 * (kMaxE + 8) * 4;
+  return 1024 + stages_of(op) * 2 * (size_t)kOpBytes + 8 * slot_of(op) + 256 + 2 * (kMaxE + 8) * 4;
 }
 static_assert(smem_of(kFwd) <= 232448 && smem_of(kWgrad) <= 232448, "shared memory");
 
 template <int OP, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     ragged_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmS, const RaggedArgs p) {
+                       const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmO,
+                       const RaggedArgs p) {
   constexpr int ST = stages_of(OP);
   constexpr bool kAmn = OP != kFwd, kBmn = OP == kWgrad;
   extern __shared__ uint8_t smem_raw[];
@@ -52,7 +54,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
   uint8_t* sA = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint8_t* sB = sA + ST * kOpBytes;
   uint8_t* sOut = sB + ST * kOpBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + (OP == kWgrad ? 8 * kOutSlot : 0));
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + 8 * slot_of(OP));
   uint64_t* empty = full + ST;
   uint64_t* tmem_full = empty + ST;      // [2]
   uint64_t* tmem_empty = tmem_full + 2;  // [2]
@@ -88,6 +90,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     ptx::prefetch_tmap(&tmA);
     ptx::prefetch_tmap(&tmB);
     ptx::prefetch_tmap(&tmS);
+    ptx::prefetch_tmap(&tmO);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(s_tmem, 512);
@@ -216,7 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
     const uint32_t half = (uint32_t)(warp - 2) >> 2;
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(&tmem_empty[0]), 0);
     const uint32_t empty1 = ptx::mapa_shared(ptx::smem_u32(&tmem_empty[1]), 0);
-    uint8_t* slot = sOut + (warp - 2) * kOutSlot;
+    uint8_t* slot = sOut + (warp - 2) * slot_of(OP);
     int ecur = 0;
     uint32_t tc = 0;
     RaggedTile tl;
@@ -281,7 +284,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
           if (col(i) >= width) break;
           float(&x)[32] = v[F32 ? i : 0];
           if (!F32) load(i, x, false);
-          store_tokens<F32>(p.out, p.ldo, x, (int64_t)tl.row0 + col(i), width - col(i), m0, p.M, lane);
+          if (width - col(i) >= 32 && m0 < p.M) send_tokens<F32>(&tmO, slot, x, tl.row0 + col(i), (int32_t)m0, lane);
+          else store_tokens<F32>(p.out, p.ldo, x, (int64_t)tl.row0 + col(i), width - col(i), m0, p.M, lane);
         }
       } else if (m0 < p.M) {
         // staged rows of 128 bytes: 32 float32 columns, or 64 of bf16
@@ -325,14 +329,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            ptx::tma_store_3d(&tmS, slot, (int32_t)(tl.c0 + c), (int32_t)m0, tl.e);
+            ptx::tma_store_3d(&tmO, slot, (int32_t)(tl.c0 + c), (int32_t)m0, tl.e);
             ptx::bulk_commit();
           }
         }
       }
       if (!F32 && parts) release_acc();
     }
-    if (OP == kWgrad && lane == 0) ptx::bulk_wait0();       // this warp's stores are complete
+    if (lane == 0) ptx::bulk_wait0();                       // this warp's stores are complete
   } else if (OP == kWgrad && run && warp == 10) {
     // ------------------------------------------------------------ foreign rows of a group's last step
     int ecur = 0;
@@ -371,8 +375,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(OP), 1)
 }
 
 template <int OP, bool F32>
-int launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ts, const RaggedArgs& p,
-                int64_t max_tiles, cudaStream_t s) {
+int launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ts, const CUtensorMap& to,
+                const RaggedArgs& p, int64_t max_tiles, cudaStream_t s) {
   auto kern = ragged_pair_kernel<OP, F32>;
   static bool attr_set[64] = {false};
   int dev = 0;
@@ -386,7 +390,7 @@ int launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap&
     attr_set[dev] = true;
   }
   const int64_t pairs = min((int64_t)(num_sms() / 2), max_tiles);
-  return launch_after(kern, dim3((unsigned)(2 * max(pairs, (int64_t)1))), threads_of(OP), smem_of(OP), 1, s, ta, tb, ts, p)
+  return launch_after(kern, dim3((unsigned)(2 * max(pairs, (int64_t)1))), threads_of(OP), smem_of(OP), 1, s, ta, tb, ts, to, p)
              ? MGQ_OK
              : MGQ_ERR_CUDA;
 }
@@ -427,25 +431,26 @@ int run_rows(const void* in, int64_t ldi, const void* w, const int32_t* offsets,
   p.ldo = ldo;
   p.out_f32 = out_dtype == MGQ_OUT_F32;
   fill_knobs(&p);
-  CUtensorMap ta, tb, ts;
+  CUtensorMap ta, tb, ts, to;
   const uint64_t u = 2;
   p.bk = kBK;
   if (few_rows(E, R, M)) {
-    if (!encode_tmap_sw128_3d(&ta, w, 2, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
+    if (!encode_tmap_swz_3d(&ta, w, 2, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
                               {64, OP == kFwd ? 128u : 64u, 1}) ||
-        !encode_tmap_sw128_3d(&ts, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, kFewBox, 1}))
+        !encode_tmap_swz_3d(&ts, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, kFewBox, 1}))
       return MGQ_ERR_CUDA;
     return run_few(OP, false, ta, ts, p, as_stream(stream));
   }
-  if (!encode_tmap_sw128_3d(&ta, w, 2, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
+  if (!encode_tmap_swz_3d(&ta, w, 2, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
                             {64, OP == kFwd ? 128u : 64u, 1}) ||
-      !encode_tmap_sw128_3d(&tb, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, 128, 1}) ||
-      !encode_tmap_sw128_3d(&ts, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, kSmallBox, 1}))
+      !encode_tmap_swz_3d(&tb, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, 128, 1}) ||
+      !encode_tmap_swz_3d(&ts, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, kSmallBox, 1}) ||
+      !encode_out(&to, out, R, M, ldo, p.out_f32))
     return MGQ_ERR_CUDA;
   const int64_t tiles = token_tiles(E, R, kTile) * ((M + kTile - 1) / kTile);
   p.bk = kBK;
-  return p.out_f32 ? launch_pair<OP, true>(ta, tb, ts, p, tiles, as_stream(stream))
-                   : launch_pair<OP, false>(ta, tb, ts, p, tiles, as_stream(stream));
+  return p.out_f32 ? launch_pair<OP, true>(ta, tb, ts, to, p, tiles, as_stream(stream))
+                   : launch_pair<OP, false>(ta, tb, ts, to, p, tiles, as_stream(stream));
 }
 
 }  // namespace
@@ -488,17 +493,17 @@ int mgq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void* x_bf16,
   CUtensorMap ta, tb, to;
   // (no rows: maps that no load uses, the groups' results are beta times what they were)
   const uint64_t rows = R > 0 ? R : 1;
-  if (!encode_tmap_sw128_3d(&ta, R > 0 ? dy_bf16 : dw, 2, {(uint64_t)N, rows, 1}, lddy * 2, rows * lddy * 2,
+  if (!encode_tmap_swz_3d(&ta, R > 0 ? dy_bf16 : dw, 2, {(uint64_t)N, rows, 1}, lddy * 2, rows * lddy * 2,
                             {64, 64, 1}) ||
-      !encode_tmap_sw128_3d(&tb, R > 0 ? x_bf16 : dw, 2, {(uint64_t)K, rows, 1}, ldx * 2, rows * ldx * 2,
+      !encode_tmap_swz_3d(&tb, R > 0 ? x_bf16 : dw, 2, {(uint64_t)K, rows, 1}, ldx * 2, rows * ldx * 2,
                             {64, 64, 1}) ||
-      !encode_tmap_sw128_3d(&to, dw, (int)u, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
+      !encode_tmap_swz_3d(&to, dw, (int)u, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
                             {(uint32_t)(128 / u), 32, 1}))
     return MGQ_ERR_CUDA;
   const int64_t tiles = (int64_t)E * ((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile);
   p.bk = kBK;
-  return p.out_f32 ? launch_pair<kWgrad, true>(ta, tb, to, p, tiles, as_stream(stream))
-                   : launch_pair<kWgrad, false>(ta, tb, to, p, tiles, as_stream(stream));
+  return p.out_f32 ? launch_pair<kWgrad, true>(ta, tb, tb, to, p, tiles, as_stream(stream))
+                   : launch_pair<kWgrad, false>(ta, tb, tb, to, p, tiles, as_stream(stream));
 }
 
 }  // extern "C"

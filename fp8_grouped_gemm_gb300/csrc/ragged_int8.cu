@@ -34,20 +34,22 @@ constexpr int kThreads8 = 28 * 32;
 // takes 3 us a tile when all SMs end one together).
 constexpr int kRegLow = 40, kRegConv = 64, kRegEpi = 104, kRegLaunch = 72;
 static_assert(128 * kRegLow + 512 * kRegConv + 256 * kRegEpi <= kThreads8 * kRegLaunch, "register split");
-constexpr size_t kSmem8 = 1024 + kRaw * 2 * (size_t)kRawBytes + kConv * (size_t)kF16Bytes + 8 * 512 + 256 +
+constexpr size_t kSmem8 = 1024 + kRaw * 2 * (size_t)kRawBytes + kConv * (size_t)kF16Bytes + 8 * (512 + kTokSlot) + 256 +
                           2 * (kMaxE + 8) * 4;
 static_assert(kSmem8 <= 232448 && kAcol + kConv * kAcols <= 512, "shared and tensor memory");
 
 template <bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     ragged_int8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmS, const RaggedArgs p) {
+                       const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmO,
+                       const RaggedArgs p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   uint8_t* sA = smem_raw + (((raw + 1023u) & ~1023u) - raw);   // [kRaw] bytes of the channels
   uint8_t* sB = sA + kRaw * kRawBytes;                         // [kRaw] bytes of the tokens
   uint8_t* sF = sB + kRaw * kRawBytes;                         // [kConv] f16 of the tokens
-  float* sX = reinterpret_cast<float*>(sF + kConv * kF16Bytes);   // [8 warps][128] token scales
+  uint8_t* sOut = sF + kConv * kF16Bytes;                      // [8 warps] store staging
+  float* sX = reinterpret_cast<float*>(sOut + 8 * kTokSlot);   // [8 warps][128] token scales
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(sX + 8 * 128);
   uint64_t* raw_empty = raw_full + kRaw;
   uint64_t* conv_full = raw_empty + kRaw;
@@ -85,6 +87,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     ptx::prefetch_tmap(&tmA);
     ptx::prefetch_tmap(&tmB);
     ptx::prefetch_tmap(&tmS);
+    ptx::prefetch_tmap(&tmO);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(s_tmem, 512);
@@ -218,6 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     const uint32_t half = (uint32_t)(warp - 20) >> 2;
     const uint32_t empty0 = ptx::mapa_shared(ptx::smem_u32(acc_empty), 0);
     float* sx = sX + (warp - 20) * 128;
+    uint8_t* slot = sOut + (warp - 20) * kTokSlot;
     int ecur = 0;
     uint32_t tc = 0;
     RaggedTile tl;
@@ -226,9 +230,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       const float sw = m0 + lane < p.M ? p.sw[tl.e * p.M + m0 + lane] : 0.0f;
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {                // (in runs of 16 tokens, every second run)
-        const int j = 32 * i + (int)lane, c = 16 * half + (j & 15) + 32 * (j >> 4);
-        sx[j] = c < tl.n ? p.sx[(int64_t)tl.row0 + c] : 0.0f;
+      for (int i = 0; i < 4; ++i) {                // runs of 32 tokens, every second run
+        const int c = 32 * (int)half + 64 * i + (int)lane;
+        sx[32 * i + lane] = c < tl.n ? p.sx[(int64_t)tl.row0 + c] : 0.0f;
       }
       __syncwarp();
       bool got = *s_abort == 0;
@@ -238,53 +242,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
         break;
       }
       ptx::tc_fence_after();
-      // 16 tokens at a time, every second run
-      auto load = [&](int i, float (&v)[16]) {
-        uint32_t r[16];
-        ptx::tmem_ld_32x32b_x16(tmem + 16 * half + 32 * i + ((q * 32) << 16), r);
-        ptx::tmem_ld_wait();
+      for (int i = 0; 32 * (int)half + 64 * i < tl.n; ++i) {
+        const int c = 32 * (int)half + 64 * i;
+        float v[32];
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(sx + 16 * i + j);
-          v[j] = __uint_as_float(r[j]) * (x.x * sw);
-          v[j + 1] = __uint_as_float(r[j + 1]) * (x.y * sw);
-          v[j + 2] = __uint_as_float(r[j + 2]) * (x.z * sw);
-          v[j + 3] = __uint_as_float(r[j + 3]) * (x.w * sw);
+        for (int h = 0; h < 32; h += 16) {
+          uint32_t r[16];
+          ptx::tmem_ld_32x32b_x16(tmem + c + h + ((q * 32) << 16), r);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(sx + 32 * i + h + j);
+            v[h + j] = __uint_as_float(r[j]) * (x.x * sw);
+            v[h + j + 1] = __uint_as_float(r[j + 1]) * (x.y * sw);
+            v[h + j + 2] = __uint_as_float(r[j + 2]) * (x.z * sw);
+            v[h + j + 3] = __uint_as_float(r[j + 3]) * (x.w * sw);
+          }
         }
-      };
-      auto release = [&]() {
-        ptx::tc_fence_before();
+        if (c + 64 >= tl.n) {                      // the accumulator is read: the next tile may begin
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_pair(empty0);
+        }
+        if (tl.n - c >= 32 && m0 < p.M) send_tokens<F32>(&tmO, slot, v, tl.row0 + c, (int32_t)m0, lane);
+        else store_tokens<F32>(p.out, p.ldo, v, (int64_t)tl.row0 + c, tl.n - c, m0, p.M, lane);
+      }
+      if (32 * (int)half >= tl.n) {                // (no tokens for this warp)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive_pair(empty0);
-      };
-      const int first = 16 * half;
-      float v[16];
-      if (F32) {
-        for (int i = 0; first + 32 * i < tl.n; ++i) {
-          load(i, v);
-          store_tokens<true>(p.out, p.ldo, v, (int64_t)tl.row0 + first + 32 * i, tl.n - first - 32 * i, m0, p.M, lane);
-        }
-        release();
-      } else {
-        uint4 w[8][2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (first + 32 * i >= tl.n) break;
-          load(i, v);
-          w[i][0] = transpose8_bf16(v, lane);
-          w[i][1] = transpose8_bf16(v + 8, lane);
-        }
-        release();
-        const int64_t ch = m0 + (lane & 24);
-        const int left = ch < p.M ? tl.n - first - (int)(lane & 7) : 0;
-        uint16_t* o = static_cast<uint16_t*>(p.out) + ((int64_t)tl.row0 + first + (lane & 7)) * p.ldo + ch;
-#pragma unroll
-        for (int i = 0; i < 8; ++i, o += 32 * p.ldo) {
-          if (32 * i < left) *reinterpret_cast<uint4*>(o) = w[i][0];
-          if (32 * i + 8 < left) *reinterpret_cast<uint4*>(o + 8 * p.ldo) = w[i][1];
-        }
       }
     }
+    if (lane == 0) ptx::bulk_wait0();              // this warp's stores are complete
   }
   __syncthreads();
   ptx::tc_fence_before();
@@ -297,8 +285,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
 }
 
 template <bool F32>
-int launch_int8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ts, const RaggedArgs& p,
-                int64_t max_tiles, cudaStream_t s) {
+int launch_int8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ts, const CUtensorMap& to,
+                const RaggedArgs& p, int64_t max_tiles, cudaStream_t s) {
   auto kern = ragged_int8_kernel<F32>;
   static bool attr_set[64] = {false};
   int dev = 0;
@@ -318,7 +306,7 @@ int launch_int8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap&
     attr_set[dev] = true;
   }
   const int64_t pairs = min((int64_t)(num_sms() / 2), max_tiles);
-  return launch_after(kern, dim3((unsigned)(2 * max(pairs, (int64_t)1))), kThreads8, kSmem8, 1, s, ta, tb, ts, p)
+  return launch_after(kern, dim3((unsigned)(2 * max(pairs, (int64_t)1))), kThreads8, kSmem8, 1, s, ta, tb, ts, to, p)
              ? MGQ_OK
              : MGQ_ERR_CUDA;
 }
@@ -449,20 +437,21 @@ int mgq_ragged_gemm_int8(const int8_t* x, int64_t ldx, const float* x_scale, con
   p.sw = w_scale;
   debug_knobs(&p.stall, &p.wait_ns);
   const bool few = few_rows(E, R, N);
-  CUtensorMap ta, tb, ts;
+  CUtensorMap ta, tb, ts, to;
   if (few) {
-    if (!encode_tmap_sw128_3d(&ta, w, 1, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K, N * K, {128, 128, 1}) ||
-        !encode_tmap_sw128_3d(&ts, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, kFewBox, 1}))
+    if (!encode_tmap_swz_3d(&ta, w, 1, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K, N * K, {128, 128, 1}) ||
+        !encode_tmap_swz_3d(&ts, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, kFewBox, 1}))
       return MGQ_ERR_CUDA;
     return run_few(kFwd, true, ta, ts, p, as_stream(stream));
   }
-  if (!encode_tmap_sw128_3d(&ta, w, 1, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K, N * K, {128, 128, 1}) ||
-      !encode_tmap_sw128_3d(&tb, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, 128, 1}) ||
-      !encode_tmap_sw128_3d(&ts, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, kSmallBox, 1}))
+  if (!encode_tmap_swz_3d(&ta, w, 1, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K, N * K, {128, 128, 1}) ||
+      !encode_tmap_swz_3d(&tb, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, 128, 1}) ||
+      !encode_tmap_swz_3d(&ts, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, kSmallBox, 1}) ||
+      !encode_out(&to, y, R, N, ldy, p.out_f32))
     return MGQ_ERR_CUDA;
   const int64_t tiles = token_tiles(E, R, kTile) * ((N + kTile - 1) / kTile);
-  return p.out_f32 ? launch_int8<true>(ta, tb, ts, p, tiles, as_stream(stream))
-                   : launch_int8<false>(ta, tb, ts, p, tiles, as_stream(stream));
+  return p.out_f32 ? launch_int8<true>(ta, tb, ts, to, p, tiles, as_stream(stream))
+                   : launch_int8<false>(ta, tb, ts, to, p, tiles, as_stream(stream));
 }
 
 int mgq_rows_quantize_int8(const void* x_bf16, int64_t ldx, int64_t T, int64_t K, int8_t* codes, float* scale,
