@@ -355,21 +355,58 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
   if (split > 1) ptx::cluster_sync_relaxed();      // nobody still reads this CTA's part
 }
 
+// Clusters of n CTAs, two CTAs an SM, that are on the GPU at once, n of 1 to 8: they
+// lie within a GPC, and what its SMs leave over differs (304, 152, 97, 74, 58, 46, 38
+// and 36 here). The runtime is asked about a kernel of the same shape that does
+// nothing: for one that allocates tensor memory it counts one CTA an SM.
+struct Resident {
+  int n[9];
+};
+__global__ void __launch_bounds__(few_threads(true), 2) few_shape_kernel() {}
+bool resident_clusters(int threads, size_t smem, Resident* r) {
+  if (cudaFuncSetAttribute(few_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(true)) !=
+      cudaSuccess)
+    return false;
+  for (int c = 1; c <= 8; ++c) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = c;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(c * 1024);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&r->n[c], few_shape_kernel, &cfg) != cudaSuccess) return false;
+  }
+  return true;
+}
+
+// `tiles` tiles; the contraction is split as far as the tiles' clusters still are on
+// the GPU together and each CTA has four stages: a second wave costs more than a
+// larger split gains (60 tiles, 1536 channels, K 4096: 8.2 us by four CTAs a tile,
+// 12.9 by five, whose 58 clusters leave two for later; 96 tiles 13.7 by three, 18.7
+// by two).
 template <int OP, bool I8, bool F32>
-int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p, int64_t tiles, int split,
+int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p, int64_t tiles, int64_t nst,
                cudaStream_t s) {
   auto kern = ragged_few_kernel<OP, I8, F32>;
   static bool attr_set[64] = {false};
+  static Resident resident[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return MGQ_ERR_CUDA;
   if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(I8)) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(I8)) != cudaSuccess ||
+        !resident_clusters(few_threads(I8), few_smem(I8), &resident[dev])) {
       (void)cudaGetLastError();
       return MGQ_ERR_CUDA;
     }
     attr_set[dev] = true;
   }
+  int split = 8;
+  while (split > 1 && (tiles > resident[dev].n[split] || nst / split < 4)) --split;
   if (tiles * split >= (1ll << 31)) return MGQ_ERR_INVALID_ARG;
   return launch_after(kern, dim3((unsigned)(tiles * split)), few_threads(I8), few_smem(I8), split, s, ta, tb, p, split)
              ? MGQ_OK
@@ -378,23 +415,15 @@ int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p
 
 }  // namespace
 
-// Rows of the groups with a row at most, and CTAs that split a contraction so
-// that the tiles fill the GPU about twice (two CTAs an SM, and again).
-int64_t few_tiles(int E, int64_t R, int64_t M) {
-  return token_tiles(E, R, kFewTok) * ((M + 127) / 128);
-}
-
 int run_few(int op, bool i8, const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p, cudaStream_t s) {
-  const int64_t tiles = few_tiles(p.E, p.R, p.M);
+  const int64_t tiles = token_tiles(p.E, p.R, kFewTok) * ((p.M + 127) / 128);
   const int64_t nst = (p.C + (i8 ? kBK8 : 64) - 1) / (i8 ? kBK8 : 64);
-  int split = 1;
-  while (split < 8 && 2 * tiles * split <= 2 * num_sms() && nst / (2 * split) >= 4) split *= 2;
-  if (i8) return p.out_f32 ? launch_few<kFwd, true, true>(ta, tb, p, tiles, split, s)
-                           : launch_few<kFwd, true, false>(ta, tb, p, tiles, split, s);
-  if (op == kFwd) return p.out_f32 ? launch_few<kFwd, false, true>(ta, tb, p, tiles, split, s)
-                                   : launch_few<kFwd, false, false>(ta, tb, p, tiles, split, s);
-  return p.out_f32 ? launch_few<kDgrad, false, true>(ta, tb, p, tiles, split, s)
-                   : launch_few<kDgrad, false, false>(ta, tb, p, tiles, split, s);
+  if (i8) return p.out_f32 ? launch_few<kFwd, true, true>(ta, tb, p, tiles, nst, s)
+                           : launch_few<kFwd, true, false>(ta, tb, p, tiles, nst, s);
+  if (op == kFwd) return p.out_f32 ? launch_few<kFwd, false, true>(ta, tb, p, tiles, nst, s)
+                                   : launch_few<kFwd, false, false>(ta, tb, p, tiles, nst, s);
+  return p.out_f32 ? launch_few<kDgrad, false, true>(ta, tb, p, tiles, nst, s)
+                   : launch_few<kDgrad, false, false>(ta, tb, p, tiles, nst, s);
 }
 
 }  // namespace mgq
