@@ -244,8 +244,6 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
           load_codes(src, row, 0, c[0]);
           load_codes(src, row, 1, c[1]);
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&empty[rs]);
         if (chan) {
           ptx::tc_fence_after();
 #pragma unroll
@@ -259,7 +257,10 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
           ptx::fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&conv_full[cs]);
+        if (lane == 0) {
+          ptx::mbar_arrive(&empty[rs]);            // (only now that the codes are used: a read of them may
+          ptx::mbar_arrive(&conv_full[cs]);        // still be under way after an arrival that follows it)
+        }
       }
       if (!ok) timed_out();
     }

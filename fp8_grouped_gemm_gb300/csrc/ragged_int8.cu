@@ -197,8 +197,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       if (n < 0) break;                                                 // no more tiles
       ok = ok && ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns);
       if (!(ok = __all_sync(0xFFFFFFFFu, ok) && !*s_abort)) break;
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&raw_empty[rs]);
       if (chan) {
         ptx::tc_fence_after();
         codes_to_tmem(c, tmem + kAcol + cs * kAcols + ((32u * quad) << 16));
@@ -209,7 +207,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
         ptx::fence_proxy_async_smem();
       }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_pair(full0 + cs * 8);
+      if (lane == 0) {
+        ptx::mbar_arrive(&raw_empty[rs]);                               // (the codes are used, not only asked for)
+        ptx::mbar_arrive_pair(full0 + cs * 8);
+      }
       if (++rs == kRaw) rs = 0, rph ^= 1;
       if ((cs += 2) >= kConv) cs -= kConv, cph ^= 1;
     }

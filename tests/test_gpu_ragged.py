@@ -240,6 +240,40 @@ def test_int8(mgq, shape, dt):
         _close(y[r], ref, (half + 3 * 2.0 ** -24) * ref.abs() + 1e-38, e)
 
 
+@pytest.mark.parametrize("N,K", [(32, 768), (136, 1040), (32, 4096)])
+@pytest.mark.parametrize("op", ["fwd", "dgrad", "int8"])
+def test_many_groups_of_few_rows(mgq, op, N, K):
+    """More short tiles than the GPU holds at once, and places for tiles that turn out not to exist behind them: a
+    ring's slot is refilled from L2 right after it is given back, so that a read of it that is still under way shows."""
+    E = 1024
+    counts = torch.randint(0, 3, (E,), generator=torch.Generator().manual_seed(3))
+    b = _bounds(counts.tolist(), 0)
+    R, g = b[-1], _gen(23)
+    group = torch.repeat_interleave(torch.arange(E), counts).cuda()
+    if op == "int8":
+        x, w = _int8(g, R, K), _int8(g, E, N, K)
+        ones = (torch.ones(R, device="cuda"), torch.ones(E, N, device="cuda"))
+        run, wt, C = lambda o: mgq.ragged_gemm_int8(x, ones[0], w, ones[1], _off(b), o), w.transpose(1, 2), K
+    elif op == "fwd":
+        x, w = _randn(g, R, K), _randn(g, E, N, K)
+        run, wt, C = lambda o: mgq.ragged_gemm_fwd(x, w, _off(b), o), w.transpose(1, 2), K
+    else:
+        x, w = _randn(g, R, K), _randn(g, E, K, N)
+        run, wt, C = lambda o: mgq.ragged_gemm_dgrad(x, w, _off(b), o), w, K
+    ref, S = torch.empty(R, N, dtype=torch.float64, device="cuda"), torch.empty(R, N, dtype=torch.float64, device="cuda")
+    for r in range(0, R, 128):
+        xr, wr = x[r:r + 128, None].double(), wt[group[r:r + 128]].double()
+        ref[r:r + 128], S[r:r + 128] = torch.bmm(xr, wr)[:, 0], torch.bmm(xr.abs(), wr.abs())[:, 0]
+    for _ in range(4):
+        y = torch.full((R, N), 7.0, device="cuda")
+        run(y)
+        assert mgq.get_error() == mgq.OK
+        if op == "int8":
+            _close(y, ref, torch.where(S < 2 ** 24, 0.0, (K / 16) * 2.0 ** -23 * S), op)
+        else:
+            _close(y, ref, _tol(F32, ref, S, C), op)
+
+
 @pytest.mark.parametrize("R", [2, 40, 5000])
 def test_int8_sums_exact_whatever_the_codes(mgq, R):
     """K of 1024, all codes at the ends of their range: |sum| up to 2^24, every one an integer."""
