@@ -235,15 +235,15 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
         const int rs = i % ST, cs = i % kFewConv;
         ok = *s_abort == 0;
         ok = ok && ptx::mbar_wait(&full[rs], (i / ST) & 1, p.wait_ns);
-        ok = ok && ptx::mbar_wait(&conv_empty[cs], ((i / kFewConv) & 1) ^ 1, p.wait_ns);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        uint4 c[2][4];
+        uint4 c[2][4];                             // (on their way during the second wait)
         if (mine) {
           const uint8_t* src = chan ? sA + rs * kFewA : sB + rs * kFewB;
           load_codes(src, row, 0, c[0]);
           load_codes(src, row, 1, c[1]);
         }
+        ok = ok && ptx::mbar_wait(&conv_empty[cs], ((i / kFewConv) & 1) ^ 1, p.wait_ns);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         if (chan) {
           ptx::tc_fence_after();
 #pragma unroll
