@@ -14,8 +14,9 @@
 // in steps of 32 from its instruction descriptor: the last tile of a group
 // costs by the rows it has, and a group's first row is any row, because the row
 // coordinate of a TMA box has no alignment. The accumulator then holds channels
-// as lanes and tokens as columns; the epilogue transposes 8 x 8 blocks between
-// lanes and stores 16 bytes of a token at a time, only the group's own rows.
+// as lanes and tokens as columns; the epilogue stores only the group's own rows:
+// runs of 32 tokens through shared memory and the TMA, shorter ones from registers
+// (bf16: 8 x 8 blocks transposed between lanes, 16 bytes of a token at a time).
 // The transposed weights of dgrad and both operands of wgrad are read MN-major
 // by the tensor cores. wgrad contracts over the tokens: rows of the last 16-row
 // step that belong to the next group are zeroed in shared memory, in both

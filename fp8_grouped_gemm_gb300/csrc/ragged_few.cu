@@ -8,6 +8,8 @@
 // splits the contraction; the parts meet in shared memory over the cluster and
 // are added in the order of the ranks, so the result does not depend on timing.
 // int8 weights become f16 on their way to tensor memory, as in the large form.
+#include <atomic>
+
 #include "ragged.cuh"
 #include "ragged_int8.cuh"
 
@@ -393,7 +395,7 @@ template <int OP, bool I8, bool F32>
 int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p, int64_t tiles, int64_t nst,
                cudaStream_t s) {
   auto kern = ragged_few_kernel<OP, I8, F32>;
-  static bool attr_set[64] = {false};
+  static std::atomic<bool> attr_set[64];             // set after `resident`, which the first callers fill alike
   static Resident resident[64];
   int dev = 0;
   cudaGetDevice(&dev);

@@ -13,10 +13,10 @@
 //   warps 4-11    channels: bytes -> f16 -> tensor memory, the MMA's A operand
 //   warps 12-19   tokens: bytes -> f16 -> shared memory, swizzled, the B operand
 //   warp 1        (CTA 0) issues the MMAs of both SMs
-//   warps 20-27   epilogue: scales, transposition, stores
-// The channels' operand in tensor memory leaves
-// shared memory's bandwidth to the tokens' one; its stages take the columns of a
-// second accumulator, so a tile's MMAs wait for the tile before to be read.
+//   warps 20-27   epilogue: scales, full runs of 32 tokens to the TMA's stores
+// The channels' operand in tensor memory leaves shared memory's bandwidth to the
+// tokens' one; its stages take the columns of a second accumulator, so a tile's
+// MMAs wait for the tile before to be read.
 #include "ragged.cuh"
 #include "ragged_int8.cuh"
 
@@ -29,9 +29,7 @@ constexpr uint32_t kF16Bytes = 128 * 128;          // the tokens' f16 of half a 
 constexpr uint32_t kAcol = 256, kAcols = 32;       // tensor memory: the channels' half stages
 constexpr int kThreads8 = 28 * 32;
 // Registers a thread of the three kinds of warps, out of what the block is
-// launched with: the epilogue holds a tile's 64 words of scaled and transposed
-// bf16 pairs, so that the one accumulator is free before the stores (whose burst
-// takes 3 us a tile when all SMs end one together).
+// launched with: an epilogue warp holds 32 scaled values beside its addresses.
 constexpr int kRegLow = 40, kRegConv = 64, kRegEpi = 104, kRegLaunch = 72;
 static_assert(128 * kRegLow + 512 * kRegConv + 256 * kRegEpi <= kThreads8 * kRegLaunch, "register split");
 constexpr size_t kSmem8 = 1024 + kRaw * 2 * (size_t)kRawBytes + kConv * (size_t)kF16Bytes + 8 * (512 + kTokSlot) + 256 +
@@ -194,9 +192,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       const int n = s_n[rs];
       uint4 c[4];
       load_codes((chan ? sA : sB) + rs * kRawBytes, row, h, c);
-      if (n < 0) break;                                                 // no more tiles
-      ok = ok && ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns);
-      if (!(ok = __all_sync(0xFFFFFFFFu, ok) && !*s_abort)) break;
+      ok = ok && (n < 0 || ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns));
+      ok = __all_sync(0xFFFFFFFFu, ok && !*s_abort);
+      if (!ok || n < 0) break;                                          // (n < 0: no more tiles)
       if (chan) {
         ptx::tc_fence_after();
         codes_to_tmem(c, tmem + kAcol + cs * kAcols + ((32u * quad) << 16));
