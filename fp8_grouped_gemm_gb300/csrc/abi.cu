@@ -57,6 +57,28 @@ int num_sms() {
   return g_sms[dev];
 }
 
+namespace {
+__global__ void __launch_bounds__(256, 2) shape_kernel() {}
+}  // namespace
+bool resident_clusters(int threads, size_t smem, int* n) {
+  if (threads > 256 || cudaFuncSetAttribute(shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return false;
+  for (int c = 1; c <= 8; ++c) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = c;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(c * 1024);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n[c], shape_kernel, &cfg) != cudaSuccess) return false;
+  }
+  return true;
+}
+
 bool encode_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch,
                        uint32_t box_inner, uint32_t box_outer) {
   {

@@ -81,6 +81,12 @@ int col_gather_dy(const uint16_t* dout, const float* probs, const int32_t* src_r
 int quant_nv2d(const uint16_t* x, int64_t G, int64_t M, int64_t K, uint8_t* row_codes, uint8_t* row_scales,
                uint8_t* col_codes, uint8_t* col_scales, const float* amax, float* s_out, cudaStream_t s);
 
+// n[c], c of 1 to 8: clusters of c CTAs of up to 256 threads and 128 registers that
+// are on the GPU at once. They lie within a GPC, and what its SMs leave over differs
+// (two CTAs an SM: 304, 152, 97, 74, 58, 46, 38 and 36). The runtime is asked about a
+// kernel that does nothing: for one that allocates tensor memory it counts one CTA an SM.
+bool resident_clusters(int threads, size_t smem, int* n);
+
 // A launch that may start while the kernel before it in the stream still runs
 // (programmatic dependent launch): such a kernel reads what others wrote, and
 // writes, only after griddepcontrol.wait. `cluster`: CTAs along x, 1 for none.

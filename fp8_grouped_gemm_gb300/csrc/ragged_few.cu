@@ -358,34 +358,6 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
   if (split > 1) ptx::cluster_sync_relaxed();      // nobody still reads this CTA's part
 }
 
-// Clusters of n CTAs, two CTAs an SM, that are on the GPU at once, n of 1 to 8: they
-// lie within a GPC, and what its SMs leave over differs (304, 152, 97, 74, 58, 46, 38
-// and 36 here). The runtime is asked about a kernel of the same shape that does
-// nothing: for one that allocates tensor memory it counts one CTA an SM.
-struct Resident {
-  int n[9];
-};
-__global__ void __launch_bounds__(few_threads(true), 2) few_shape_kernel() {}
-bool resident_clusters(int threads, size_t smem, Resident* r) {
-  if (cudaFuncSetAttribute(few_shape_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(true)) !=
-      cudaSuccess)
-    return false;
-  for (int c = 1; c <= 8; ++c) {
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = c;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(c * 1024);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&r->n[c], few_shape_kernel, &cfg) != cudaSuccess) return false;
-  }
-  return true;
-}
-
 // `tiles` tiles; the contraction is split as far as the tiles' clusters still are on
 // the GPU together and each CTA has four stages: a second wave costs more than a
 // larger split gains (60 tiles, 1536 channels, K 4096: 8.2 us by four CTAs a tile,
@@ -396,20 +368,20 @@ int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p
                cudaStream_t s) {
   auto kern = ragged_few_kernel<OP, I8, F32>;
   static std::atomic<bool> attr_set[64];             // set after `resident`, which the first callers fill alike
-  static Resident resident[64];
+  static int resident[64][9];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return MGQ_ERR_CUDA;
   if (!attr_set[dev]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(I8)) != cudaSuccess ||
-        !resident_clusters(few_threads(I8), few_smem(I8), &resident[dev])) {
+        !resident_clusters(few_threads(I8), few_smem(I8), resident[dev])) {
       (void)cudaGetLastError();
       return MGQ_ERR_CUDA;
     }
     attr_set[dev] = true;
   }
   int split = 8;
-  while (split > 1 && (tiles > resident[dev].n[split] || nst / split < 4)) --split;
+  while (split > 1 && (tiles > resident[dev][split] || nst / split < 4)) --split;
   if (tiles * split >= (1ll << 31)) return MGQ_ERR_INVALID_ARG;
   return launch_after(kern, dim3((unsigned)(tiles * split)), few_threads(I8), few_smem(I8), split, s, ta, tb, p, split)
              ? MGQ_OK
