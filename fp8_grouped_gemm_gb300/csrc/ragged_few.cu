@@ -7,7 +7,11 @@
 // Where the tiles are too few to keep the memory busy, a cluster of up to 8 CTAs
 // splits the contraction; the parts meet in shared memory over the cluster and
 // are added in the order of the ranks, so the result does not depend on timing.
-// int8 weights become f16 on their way to tensor memory, as in the large form.
+// int8 weights become f16 on their way to tensor memory, as in the large form, and
+// a CTA takes one tile after the other.
+//
+// Measured: 32 rows over 8 x [28672, 4096], bf16 255 us (7.4 TB/s of weights), int8
+// 151-154 (6.1-6.2 TB/s); one row of [4096, 4096] 6.6 and 6.8 us.
 #include <atomic>
 
 #include "ragged.cuh"
@@ -28,8 +32,11 @@ __host__ __device__ constexpr size_t few_smem(bool i8) {
 }
 static_assert(2 * (few_smem(true) + 1024) <= 233472 && 2 * (few_smem(false) + 1024) <= 233472, "two CTAs an SM");
 static_assert(few_stages(true) * (kFewA + kFewB) >= kFewTok * 128 * 4, "room for a partial result");
-// tensor memory: int8 one accumulator and the weights' f16; else two accumulators
+// tensor memory: two accumulators, for int8 with the weights' f16 between them
 constexpr uint32_t kFewAcol = 64, kFewCols8 = 256, kFewCols = 128;
+template <bool I8>
+constexpr uint32_t kFewAcc2 = I8 ? kFewAcol + kFewConv * 64 : 64;
+static_assert(kFewAcc2<true> + 64 <= kFewCols8, "tensor memory");
 constexpr int kFewPromote = 8;                     // as kPromote of the large form
 
 struct FewTile {
@@ -37,41 +44,52 @@ struct FewTile {
   int64_t m0;
 };
 
-// Tile t: groups in order, a group's channel tiles, its token tiles fastest (they
-// share the weights). A whole warp; s_off holds the offsets. False if there is no
-// such tile; `ok` is false for offsets that are no row partition. (Tile numbers are
-// below 2^31: the launch sees to it.)
-__device__ __forceinline__ bool few_tile(const RaggedArgs& p, const int32_t* s_off, uint32_t t, uint32_t lane, FewTile& tl,
-                                         bool& ok) {
-  const int per = (p.E + 31) / 32, e0 = min((int)lane * per, p.E), e1 = min(e0 + per, p.E);
-  const uint32_t nM = (uint32_t)((p.M + 127) / 128);
+// A warp's view of the groups, for the search: each lane has the token tiles of its
+// run of groups, and the sum of those up to and with its own.
+struct FewGroups {
+  uint32_t mine, inc, nM;
+  int per;
+};
+
+// s_off holds the offsets; a whole warp. False for offsets that are no row partition.
+__device__ __forceinline__ bool few_groups(const RaggedArgs& p, const int32_t* s_off, uint32_t lane, FewGroups& g) {
+  g.per = (p.E + 31) / 32;
+  g.nM = (uint32_t)((p.M + 127) / 128);
+  const int e0 = min((int)lane * g.per, p.E), e1 = min(e0 + g.per, p.E);
   uint32_t mine = 0;
-  ok = true;
+  bool ok = true;
   for (int e = e0, lo = s_off[e0]; e < e1; ++e) {
     const int hi = s_off[e + 1];
     ok &= lo >= 0 && lo <= hi && hi <= p.R;
     mine += (uint32_t)(max(hi - lo, 0) + kFewTok - 1) / kFewTok;
     lo = hi;
   }
-  ok = __all_sync(0xFFFFFFFFu, ok);
-  if (!ok) return false;
   uint32_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= (uint32_t)o) inc += v;
   }
-  const uint32_t at = __ballot_sync(0xFFFFFFFFu, inc * nM > t);
+  g.mine = mine;
+  g.inc = inc;
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// Tile t: groups in order, a group's channel tiles, its token tiles fastest (they
+// share the weights). A whole warp. False if there is no such tile. (Tile numbers
+// are below 2^31: the launch sees to it.)
+__device__ __forceinline__ bool few_tile(const FewGroups& g, const int32_t* s_off, uint32_t t, FewTile& tl) {
+  const uint32_t at = __ballot_sync(0xFFFFFFFFu, g.inc * g.nM > t);
   if (!at) return false;
   const int src = __ffs(at) - 1;
   // every lane walks that lane's groups
-  uint32_t local = t - __shfl_sync(0xFFFFFFFFu, inc - mine, src) * nM, tiles = 1;
-  int e = src * per, lo = s_off[e];
+  uint32_t local = t - __shfl_sync(0xFFFFFFFFu, g.inc - g.mine, src) * g.nM, tiles = 1;
+  int e = src * g.per, lo = s_off[e];
   for (;; ++e) {
     const int hi = s_off[e + 1];
     tiles = (uint32_t)(hi - lo + kFewTok - 1) / kFewTok;
-    if (local < tiles * nM) break;
-    local -= tiles * nM;
+    if (local < tiles * g.nM) break;
+    local -= tiles * g.nM;
     lo = hi;
   }
   const uint32_t m = local / tiles;
@@ -149,170 +167,209 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  FewGroups groups;
+  const bool part = few_groups(p, s_off, lane, groups);
+  if (!part && blockIdx.x == 0 && threadIdx.x == 0) report(p.err, MGQ_ERR_INVALID_ARG);
+  // the first tile; int8 without a split takes every gridDim.x-th after it
   FewTile tl{0, 0, 1, 0};
-  bool ok_off;
-  const bool run = few_tile(p, s_off, blockIdx.x / split, lane, tl, ok_off);   // the same in the whole cluster
-  if (!ok_off && blockIdx.x == 0 && threadIdx.x == 0) report(p.err, MGQ_ERR_INVALID_ARG);
-  const int e = tl.e, row0 = tl.row0, n = tl.n;
-  const int64_t m0 = tl.m0;
+  uint32_t tile = blockIdx.x / split;
+  const bool run = part && few_tile(groups, s_off, tile, tl);
+  auto next_tile = [&]() { return I8 && split == 1 && few_tile(groups, s_off, tile += gridDim.x, tl); };
   // this rank's stages of the contraction
   const int nst = (int)((p.C + kElems - 1) / kElems), chunk = (nst + split - 1) / split;
   const int s0 = min(nst, rank * chunk), ns = min(nst, s0 + chunk) - s0;
-  const int boxes = (n + kFewBox - 1) / kFewBox;
   auto timed_out = [&]() {
     report(p.err, MGQ_ERR_TIMEOUT);
     *s_abort = 1;
   };
 
-  if (run && warp == 0 && !p.stall && ptx::elect_one()) {
+  if (run && warp == 0 && !p.stall) {
     // ------------------------------------------------------------ producer
-    int i = 0;
-    for (; i < ns; ++i) {
-      const int st = i % ST;
-      if (*s_abort) break;
-      if (!ptx::mbar_wait(&empty[st], ((i / ST) & 1) ^ 1, p.wait_ns)) {
-        timed_out();
-        break;
+    uint32_t it = 0, st = 0, ph = 0;               // (of the electing lane, the same one throughout)
+    const bool me = ptx::elect_one();
+    do {
+      const int boxes = (tl.n + kFewBox - 1) / kFewBox;
+      for (int i = 0; me && i < ns; ++i, ++it) {
+        if (*s_abort) break;
+        if (!ptx::mbar_wait(&empty[st], ph ^ 1, p.wait_ns)) {
+          timed_out();
+          break;
+        }
+        ptx::mbar_arrive_expect_tx(&full[st], kFewA + boxes * kFewBox * 128);
+        const int32_t kx = (s0 + i) * kElems;
+        if (kAmn) {                                // two chunks of 64 channels
+          ptx::tma_load_3d(sA + st * kFewA, &tmA, &full[st], (int32_t)tl.m0, kx, tl.e);
+          ptx::tma_load_3d(sA + st * kFewA + kFewA / 2, &tmA, &full[st], (int32_t)tl.m0 + 64, kx, tl.e);
+        } else {
+          ptx::tma_load_3d(sA + st * kFewA, &tmA, &full[st], kx, (int32_t)tl.m0, tl.e);
+        }
+        for (int b = 0; b < boxes; ++b)
+          ptx::tma_load_3d(sB + st * kFewB + b * kFewBox * 128, &tmB, &full[st], kx, tl.row0 + b * kFewBox, 0);
+        if (++st == ST) st = 0, ph ^= 1;
       }
-      ptx::mbar_arrive_expect_tx(&full[st], kFewA + boxes * kFewBox * 128);
-      const int32_t kx = (s0 + i) * kElems;
-      if (kAmn) {                                  // two chunks of 64 channels
-        ptx::tma_load_3d(sA + st * kFewA, &tmA, &full[st], (int32_t)m0, kx, e);
-        ptx::tma_load_3d(sA + st * kFewA + kFewA / 2, &tmA, &full[st], (int32_t)m0 + 64, kx, e);
-      } else {
-        ptx::tma_load_3d(sA + st * kFewA, &tmA, &full[st], kx, (int32_t)m0, e);
-      }
-      for (int b = 0; b < boxes; ++b)
-        ptx::tma_load_3d(sB + st * kFewB + b * kFewBox * 128, &tmB, &full[st], kx, row0 + b * kFewBox, 0);
-    }
-    if (*s_abort)                                  // no copy may be on its way when the CTA leaves
-      for (int j = max(0, i - ST); j < i; ++j) ptx::mbar_wait(&full[j % ST], (j / ST) & 1, p.wait_ns);
-  } else if (run && warp == 1 && ptx::elect_one()) {
+      __syncwarp();
+    } while (!__any_sync(0xFFFFFFFFu, *s_abort != 0) && next_tile());
+    if (me && *s_abort)                            // no copy may be on its way when the CTA leaves
+      for (uint32_t j = it > ST ? it - ST : 0; j < it; ++j) ptx::mbar_wait(&full[j % ST], (j / ST) & 1, p.wait_ns);
+    __syncwarp();
+  } else if (run && warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const uint32_t sA0 = ptx::smem_u32(sA), sB0 = ptx::smem_u32(sB), sF0 = ptx::smem_u32(sF);
-    const uint32_t idesc = ptx::idesc_f16(I8 ? 0 : 1, 128, (uint32_t)boxes * 16) | ptx::idesc_mn_major(kAmn, false);
+    uint32_t st = 0, ph = 0, pc = 0;               // stage of its operands, accumulator
     bool ok = true;
-    for (int i = 0; i < ns; ++i) {
-      const bool first = kParts ? i % kFewPromote == 0 : i == 0;
-      const int part = kParts ? i / kFewPromote : 0;
-      const uint32_t acc = tmem + (part & 1) * 64;
-      if (kParts && first) ok = ptx::mbar_wait(&acc_empty[part & 1], ((part >> 1) & 1) ^ 1, p.wait_ns);
-      const int st = I8 ? i % kFewConv : i % ST;
-      ok = ok && !*s_abort &&
-           (I8 ? ptx::mbar_wait(&conv_full[st], (i / kFewConv) & 1, p.wait_ns)
-               : ptx::mbar_wait(&full[st], (i / ST) & 1, p.wait_ns));
-      if (!ok) break;
-      ptx::tc_fence_after();
-      if (I8) {
+    const bool me = ptx::elect_one();
+    do {
+      const uint32_t idesc = ptx::idesc_f16(I8 ? 0 : 1, 128, (uint32_t)(tl.n + kFewBox - 1) / kFewBox * kFewBox) |
+                             ptx::idesc_mn_major(kAmn, false);
+      for (int i = 0; me && i < ns; ++i) {
+        const bool first = kParts ? i % kFewPromote == 0 : i == 0;
+        const uint32_t acc = tmem + (pc & 1) * kFewAcc2<I8>;
+        if (first) ok = ptx::mbar_wait(&acc_empty[pc & 1], ((pc >> 1) & 1) ^ 1, p.wait_ns);
+        ok = ok && !*s_abort && ptx::mbar_wait(I8 ? &conv_full[st] : &full[st], ph, p.wait_ns);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (I8) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          ptx::mma_f16_ta(acc, tmem + kFewAcol + st * 64 + kk * 8,
-                          ptx::sdesc_kmajor_sw128(sF0 + st * kFewF + (kk >> 2) * (kFewF / 2)) + (kk & 3) * 2, idesc,
-                          (!first || kk > 0) ? 1u : 0u);
-        ptx::mma_commit(&conv_empty[st]);
-      } else {
-        const uint64_t ad = kAmn ? ptx::sdesc_mnmajor_sw128_chunks(sA0 + st * kFewA, kFewA / 2)
-                                 : ptx::sdesc_kmajor_sw128(sA0 + st * kFewA);
-        const uint64_t bd = ptx::sdesc_kmajor_sw128(sB0 + st * kFewB);
+          for (int kk = 0; kk < 8; ++kk)
+            ptx::mma_f16_ta(acc, tmem + kFewAcol + st * 64 + kk * 8,
+                            ptx::sdesc_kmajor_sw128(sF0 + st * kFewF + (kk >> 2) * (kFewF / 2)) + (kk & 3) * 2, idesc,
+                            (!first || kk > 0) ? 1u : 0u);
+          ptx::mma_commit(&conv_empty[st]);
+        } else {
+          const uint64_t ad = kAmn ? ptx::sdesc_mnmajor_sw128_chunks(sA0 + st * kFewA, kFewA / 2)
+                                   : ptx::sdesc_kmajor_sw128(sA0 + st * kFewA);
+          const uint64_t bd = ptx::sdesc_kmajor_sw128(sB0 + st * kFewB);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          ptx::mma_f16(acc, ad + kk * (kAmn ? 128 : 2), bd + kk * 2, idesc, (!first || kk > 0) ? 1u : 0u);
-        ptx::mma_commit(&empty[st]);
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_f16(acc, ad + kk * (kAmn ? 128 : 2), bd + kk * 2, idesc, (!first || kk > 0) ? 1u : 0u);
+          ptx::mma_commit(&empty[st]);
+        }
+        if (++st == (I8 ? kFewConv : ST)) st = 0, ph ^= 1;
+        if (i == ns - 1 || (kParts && i % kFewPromote == kFewPromote - 1)) ptx::mma_commit(&acc_full[pc++ & 1]);
       }
-      if (i == ns - 1 || (kParts && i % kFewPromote == kFewPromote - 1)) ptx::mma_commit(&acc_full[part & 1]);
-    }
-    if (!ok) {
+      __syncwarp();
+    } while (__all_sync(0xFFFFFFFFu, ok) && next_tile());
+    if (!ok) {                                     // (the electing lane)
       timed_out();
       ptx::mma_commit(drained);                    // the MMAs issued so far finish before the CTA leaves
       ptx::mbar_wait(drained, 0, p.wait_ns);
     }
+    __syncwarp();
   } else if (run && warp >= 2) {
-    if (I8) {
-      // ---------------------------------------------------------- bytes to f16 (warps 2-5 channels, 6-7 tokens)
-      const bool chan = warp < 6;
-      const uint32_t row = (chan ? (warp & 3) : warp - 6) * 32 + lane;
-      const bool mine = chan || (int)(row - lane) < boxes * kFewBox;
-      bool ok = true;
-      for (int i = 0; i < ns; ++i) {
-        const int rs = i % ST, cs = i % kFewConv;
-        ok = *s_abort == 0;
-        ok = ok && ptx::mbar_wait(&full[rs], (i / ST) & 1, p.wait_ns);
-        uint4 c[2][4];                             // (on their way during the second wait)
-        if (mine) {
-          const uint8_t* src = chan ? sA + rs * kFewA : sB + rs * kFewB;
-          load_codes(src, row, 0, c[0]);
-          load_codes(src, row, 1, c[1]);
-        }
-        ok = ok && ptx::mbar_wait(&conv_empty[cs], ((i / kFewConv) & 1) ^ 1, p.wait_ns);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        if (chan) {
-          ptx::tc_fence_after();
+    // int8: which rows this warp converts (warps 2-5 channels, 6-7 tokens)
+    const bool chan = warp < 6;
+    const uint32_t q = warp & 3, row = (chan ? q : warp - 6) * 32 + lane;
+    uint32_t rs = 0, rph = 0, cs = 0, cph = 0, pc = 0;
+    bool ok = true;
+    do {
+      const int n = tl.n;
+      if (I8) {
+        // -------------------------------------------------------- bytes to f16
+        const bool mine = chan || (int)(row - lane) < (n + kFewBox - 1) / kFewBox * kFewBox;
+        for (int i = 0; i < ns; ++i) {
+          ok = *s_abort == 0;
+          ok = ok && ptx::mbar_wait(&full[rs], rph, p.wait_ns);
+          uint4 c[2][4];                           // (on their way during the second wait)
+          if (mine) {
+            const uint8_t* src = chan ? sA + rs * kFewA : sB + rs * kFewB;
+            load_codes(src, row, 0, c[0]);
+            load_codes(src, row, 1, c[1]);
+          }
+          ok = ok && ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          if (chan) {
+            ptx::tc_fence_after();
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            codes_to_tmem(c[h], tmem + kFewAcol + cs * 64 + 32 * h + ((32u * (warp & 3)) << 16));
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-        } else if (mine) {
+            for (int h = 0; h < 2; ++h)
+              codes_to_tmem(c[h], tmem + kFewAcol + cs * 64 + 32 * h + ((32u * q) << 16));
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+          } else if (mine) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) codes_to_smem(c[h], sF + cs * kFewF + h * (kFewF / 2), row);
-          ptx::fence_proxy_async_smem();
+            for (int h = 0; h < 2; ++h) codes_to_smem(c[h], sF + cs * kFewF + h * (kFewF / 2), row);
+            ptx::fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(&empty[rs]);          // (only now that the codes are used: a read of them may
+            ptx::mbar_arrive(&conv_full[cs]);      // still be under way after an arrival that follows it)
+          }
+          if (++rs == ST) rs = 0, rph ^= 1;
+          if (++cs == kFewConv) cs = 0, cph ^= 1;
         }
-        __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&empty[rs]);            // (only now that the codes are used: a read of them may
-          ptx::mbar_arrive(&conv_full[cs]);        // still be under way after an arrival that follows it)
-        }
+        if (!ok) timed_out();
       }
-      if (!ok) timed_out();
-    }
-    if (warp < 6) {
-      // ---------------------------------------------------------- the partial result, [token][channel]
-      const uint32_t q = warp & 3;
-      float v[kParts ? kFewTok : 32];
+      if (!chan || !ok) continue;
+      // ---------------------------------------------------------- the result, channels as lanes
+      const int64_t ch = tl.m0 + 32 * q + lane;
+      const float sw = I8 && split == 1 && ch < p.M ? p.sw[tl.e * p.M + ch] : 0.0f;
+      float v[kParts ? kFewTok : 16];
       const int parts = ns == 0 ? 0 : kParts ? (ns + kFewPromote - 1) / kFewPromote : 1;
-      bool ok = true;
 #pragma unroll
-      for (int j = 0; j < (kParts ? kFewTok : 32); ++j) v[j] = 0.0f;
-      for (int part = 0; part < parts; ++part) {
-        ok = *s_abort == 0;
-        ok = ok && ptx::mbar_wait(&acc_full[part & 1], (part >> 1) & 1, p.wait_ns);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+      for (int j = 0; j < (kParts ? kFewTok : 16); ++j) v[j] = 0.0f;
+      auto wait_acc = [&]() {
+        bool got = *s_abort == 0;
+        got = got && ptx::mbar_wait(&acc_full[pc & 1], (pc >> 1) & 1, p.wait_ns);
+        got = __all_sync(0xFFFFFFFFu, got);
+        if (!got) timed_out();
         ptx::tc_fence_after();
-        if (kParts) {
+        return got;
+      };
+      auto release_acc = [&]() {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&acc_empty[pc & 1]);
+        ++pc;
+      };
+      const uint32_t lanes = tmem + ((q * 32) << 16);
+      if (kParts) {
+        for (int part = 0; part < parts; ++part) {
+          if (!(ok = wait_acc())) break;
 #pragma unroll
           for (int h = 0; h < kFewTok; h += 16) {
             if (h >= n) break;
             uint32_t r[16];
-            ptx::tmem_ld_32x32b_x16(tmem + (part & 1) * 64 + h + ((q * 32) << 16), r);
+            ptx::tmem_ld_32x32b_x16(lanes + (pc & 1) * kFewAcc2<I8> + h, r);
             ptx::tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[kParts ? h + j : j] += __uint_as_float(r[j]);
           }
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&acc_empty[part & 1]);
+          release_acc();
         }
+      } else if (parts) {
+        ok = wait_acc();
       }
-      if (!ok) timed_out();
-      float* part_out = reinterpret_cast<float*>(sA) + q * 32 + lane;
-      if (ok) {
+      if (!ok) break;
 #pragma unroll
-        for (int h = 0; h < kFewTok; h += 16) {
-          if (h >= n) break;
-          if (!kParts && parts) {
-            uint32_t r[16];
-            ptx::tmem_ld_32x32b_x16(tmem + h + ((q * 32) << 16), r);
-            ptx::tmem_ld_wait();
+      for (int h = 0; h < kFewTok; h += 16) {
+        if (h >= n) break;
+        float x[16];
+        if (!kParts && parts) {
+          uint32_t r[16];
+          ptx::tmem_ld_32x32b_x16(lanes + (pc & 1) * kFewAcc2<I8> + h, r);
+          ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+          for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(r[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) x[j] = v[kParts ? h + j : j];
+        }
+        if (split > 1) {                           // [token][channel], for the sum at the end
+          float* part_out = reinterpret_cast<float*>(sA) + q * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) part_out[(h + j) * 128] = x[j];
+        } else {
+          if (I8) {
+            const float sx = (int)lane < min(16, n - h) ? p.sx[(int64_t)tl.row0 + h + lane] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] *= __shfl_sync(0xFFFFFFFFu, sx, j) * sw;
           }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) part_out[(h + j) * 128] = v[kParts ? h + j : j];
+          store_tokens<F32>(p.out, p.ldo, x, (int64_t)tl.row0 + h, n - h, tl.m0 + 32 * q, p.M, lane);
         }
       }
-    }
+      if (!kParts && parts) release_acc();
+    } while (ok && next_tile());
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -321,8 +378,10 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
     __syncwarp();
     ptx::tmem_dealloc(tmem, I8 ? kFewCols8 : kFewCols);
   }
-  if (!run) return;                                // (the whole cluster)
-  if (split > 1) ptx::cluster_sync();              // every part is in place
+  if (split == 1 || !run) return;                  // (the whole cluster)
+  const int e = tl.e, row0 = tl.row0, n = tl.n;
+  const int64_t m0 = tl.m0;
+  ptx::cluster_sync();                             // every part is in place
   // tokens rank, rank + split, ..: a warp each, four channels a lane
   const int64_t ch = m0 + 4 * lane;
   const bool in = ch < p.M && !*s_abort;
@@ -333,8 +392,7 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
   for (int j = rank + split * warp; j < n; j += split * kWarps) {
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int r = 0; r < split; ++r) {
-      const float4 x = split > 1 ? ld_cluster_f32x4(ptx::mapa_shared(mine + j * 512, r))
-                                 : *reinterpret_cast<const float4*>(sA + lane * 16 + j * 512);
+      const float4 x = ld_cluster_f32x4(ptx::mapa_shared(mine + j * 512, r));
       s.x += x.x;
       s.y += x.y;
       s.z += x.z;
@@ -355,7 +413,7 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
           make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
   __syncwarp();
-  if (split > 1) ptx::cluster_sync_relaxed();      // nobody still reads this CTA's part
+  ptx::cluster_sync_relaxed();                     // nobody still reads this CTA's part
 }
 
 // `tiles` tiles; the contraction is split as far as the tiles' clusters still are on
@@ -382,8 +440,13 @@ int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p
   }
   int split = 8;
   while (split > 1 && (tiles > resident[dev][split] || nst / split < 4)) --split;
-  if (tiles * split >= (1ll << 31)) return MGQ_ERR_INVALID_ARG;
-  return launch_after(kern, dim3((unsigned)(tiles * split)), few_threads(I8), few_smem(I8), split, s, ta, tb, p, split)
+  if (tiles >= (1ll << 31)) return MGQ_ERR_INVALID_ARG;
+  // int8: as many CTAs as are on the GPU at once take the tiles in turn, so that the
+  // ring goes on over a tile's end (16 rows over 8 x [28672, 4096] 164 -> 154 us, 256 x
+  // [512, 2048] 74 -> 64). bf16 tiles have twice the bytes, and the GPU's own order of
+  // handing out CTAs serves them better (259 us against 263).
+  const int64_t ctas = split > 1 ? tiles * split : I8 ? min(tiles, (int64_t)resident[dev][1]) : tiles;
+  return launch_after(kern, dim3((unsigned)ctas), few_threads(I8), few_smem(I8), split, s, ta, tb, p, split)
              ? MGQ_OK
              : MGQ_ERR_CUDA;
 }
