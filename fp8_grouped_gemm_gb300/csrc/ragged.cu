@@ -435,7 +435,7 @@ int run_rows(const void* in, int64_t ldi, const void* w, const int32_t* offsets,
   CUtensorMap ta, tb, ts, to;
   const uint64_t u = 2;
   p.bk = kBK;
-  if (few_rows(E, R, M)) {
+  if (few_rows(E, R, M, false)) {
     if (!encode_tmap_swz_3d(&ta, w, 2, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K * u, N * K * u,
                               {64, OP == kFwd ? 128u : 64u, 1}) ||
         !encode_tmap_swz_3d(&ts, in, 2, {(uint64_t)C, (uint64_t)R, 1}, ldi * u, R * ldi * u, {64, kFewBox, 1}))

@@ -214,16 +214,25 @@ inline int64_t token_tiles(int E, int64_t R, int64_t per) {
   return (R - g) / per + g;
 }
 
-// Whether a product of R rows over E groups, M output channels, takes that form:
-// up to 32 rows a group on average, where the weights' bytes count and two CTAs an
-// SM with one tile each stream them best, or so few tiles that they fit the GPU at
-// once, where its smaller tiles and the split contraction use more SMs. Measured
-// both ways (replayed graphs): 2 rows of 8 experts 4096 x 14336, 39 us against 48;
-// 512 rows over 8 x [512, 4096] 8 against 24; 64 experts x [4096, 4096], 2048 rows
-// 318 against 330 but 4096 rows 348 against 337, 16384 rows 694 against 437. Over a
-// grid of 200 sizes the rule's choice takes 0.5% more than the better one's.
-inline bool few_rows(int E, int64_t R, int64_t M) {
-  return R <= 32 * (R < E ? R : (int64_t)E) || token_tiles(E, R, 64) * ((M + 127) / 128) <= 2 * num_sms();
+// Whether a product of R rows over E groups, M output channels, takes that form: up
+// to 32 rows a group on average (40 in the GPU's first three waves of tiles), where
+// the weights' bytes count and two CTAs an SM stream them best, or so few tiles that
+// they fit the GPU at once, where its smaller tiles and the split contraction use
+// more SMs. Measured both ways (replayed graphs): 2 rows of 8 experts 4096 x 14336,
+// 39 us against 48; 512 rows over 8 x [512, 4096] 8 against 24; 64 x [4096, 4096] with
+// 24, 40, 64 and 128 rows each 315, 320, 327 and 396 against 327, 330, 335 and 347; 40
+// rows each within three waves 0.78 (contraction of 512) to 1.01 (14336) of the large
+// form's time. Over a grid of 638 such sizes the choice takes 2% (int8 1%) more than
+// the better one's.
+// int8: the conversion makes a tile of 64 tokens dear, and the large form shares it
+// over 256 channels. 64 x [4096, 4096] with 24, 40, 64 (uneven) and 80 rows each 176,
+// 209, 280 and 376 us against 235, 236, 241 and 242; one wave without a split, K 4096:
+// 0.72 of the large form's time with 12 rows a group, 0.94 with 24, 1.15 with 32, 1.36
+// with 40; with a split 0.4 to 0.9.
+inline bool few_rows(int E, int64_t R, int64_t M, bool i8) {
+  const int64_t groups = R < E ? R : E, tiles = token_tiles(E, R, 64) * ((M + 127) / 128);
+  if (i8) return tiles <= num_sms() || R <= (tiles <= 2 * num_sms() ? 24 : 48) * groups;
+  return tiles <= 2 * num_sms() || R <= (tiles <= 6 * num_sms() ? 40 : 32) * groups;
 }
 
 }  // namespace mgq

@@ -435,7 +435,7 @@ int mgq_ragged_gemm_int8(const int8_t* x, int64_t ldx, const float* x_scale, con
   p.sx = x_scale;
   p.sw = w_scale;
   debug_knobs(&p.stall, &p.wait_ns);
-  const bool few = few_rows(E, R, N);
+  const bool few = few_rows(E, R, N, true);
   CUtensorMap ta, tb, ts, to;
   if (few) {
     if (!encode_tmap_swz_3d(&ta, w, 1, {(uint64_t)K, (uint64_t)N, (uint64_t)E}, K, N * K, {128, 128, 1}) ||
