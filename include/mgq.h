@@ -601,7 +601,8 @@ int mgq_moe_few_forward(const void* x_bf16, int T, int64_t H, int64_t F, const i
  *           overwrites it whatever it held; an empty group gives beta dW
  * What lies in rows of no group, or of another group, does not reach a result,
  * NaN and infinity included. A row's result (wgrad: a group's) does not depend on
- * the other groups' rows; the same call gives the same bits.
+ * what the other groups' rows hold (the sizes, R and E among them, choose how its sum
+ * is split); the same call gives the same bits.
  * Requires 1 <= E <= 1024, R < 2^31 - 512 (0: fwd and dgrad do nothing), N, K and
  * the row pitches multiples of 8, 16-byte aligned pointers. */
 int mgq_ragged_gemm_fwd(const void* x_bf16, int64_t ldx, const void* w_bf16, const int32_t* offsets, int E,

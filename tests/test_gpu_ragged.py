@@ -13,6 +13,10 @@ int8: sums are exact below 2^24; the scales' product and its product with the su
 once each (2^-24): half * |exact| + 3 * 2^-24 * |exact|.
 """
 import math
+import os
+import subprocess
+import sys
+import threading
 
 import pytest
 import torch
@@ -542,6 +546,72 @@ def test_streams_graphs_and_repeats(mgq):
         assert all(torch.equal(a, c) for a, c in zip(again, held)) and not torch.equal(first[0], held[0])
         x.copy_(old)
         assert mgq.get_error() == mgq.OK
+
+
+@pytest.mark.parametrize("R", [24, 3000])
+def test_first_calls_inside_a_capture(R):
+    """A process whose first call of each operator is captured; the replay gives the bits of a later call."""
+    code = f"""
+import torch
+from fp8_grouped_gemm_gb300 import mgq
+R, N, K, E = {R}, 264, 1040, 3
+x, dy, w = (torch.randn(s, device="cuda").bfloat16() for s in ((R, K), (R, N), (E, N, K)))
+x8, w8 = (torch.randint(-128, 128, s, device="cuda", dtype=torch.int8) for s in ((R, K), (E, N, K)))
+xs, ws, off = torch.rand(R, device="cuda"), torch.rand(E, N, device="cuda"), torch.tensor([0, R // 3, R // 2, R]).int().cuda()
+new = lambda: [torch.zeros(s, device="cuda", dtype=d) for s, d in (((R, N), torch.bfloat16), ((R, K), torch.float32),
+               ((E, N, K), torch.float32), ((R, N), torch.float32), ((R, K), torch.int8), ((R,), torch.float32))]
+def run(o):
+    mgq.ragged_gemm_int8(x8, xs, w8, ws, off, o[3])
+    mgq.rows_quantize_int8(x, o[4], o[5])
+    mgq.ragged_gemm_fwd(x, w, off, o[0])
+    mgq.ragged_gemm_dgrad(dy, w, off, o[1])
+    mgq.ragged_gemm_wgrad(dy, x, off, o[2])
+a, b, g = new(), new(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    run(a)
+g.replay()
+run(b)
+torch.cuda.synchronize()
+assert mgq.get_error() == mgq.OK and all(t.any() for t in a) and all(torch.equal(s, t) for s, t in zip(a, b))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_host_threads(mgq):
+    """Four host threads on streams of their own, sizes of both forms: the bits of calls one after the other."""
+    g = _gen(24)
+    N, K = 520, 1040
+    w, w8, ws = _randn(g, 4, N, K), _int8(g, 4, N, K), torch.rand(4, N, device="cuda")
+    sets = []
+    for R in (6, 40, 900, 2500):
+        off = _off([0, R // 2, R // 2, R - 1, R])
+        sets.append((_randn(g, R, K), _int8(g, R, K), torch.rand(R, device="cuda"), off, R))
+
+    def run(i, out):
+        x, x8, xs, off, R = sets[i]
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for y, y8 in out:
+                mgq.ragged_gemm_fwd(x, w, off, y)
+                mgq.ragged_gemm_int8(x8, xs, w8, ws, off, y8)
+        s.synchronize()
+
+    def new(n):
+        return [[(torch.zeros(q[4], N, device="cuda"), torch.zeros(q[4], N, device="cuda")) for _ in range(n)] for q in sets]
+
+    outs, one = new(20), new(1)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(i, outs[i])) for i in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    for i in range(4):
+        run(i, one[i])
+        for y, y8 in outs[i]:
+            assert torch.equal(y, one[i][0][0]) and torch.equal(y8, one[i][0][1])
+    assert mgq.get_error() == mgq.OK
 
 
 def test_rows_do_not_depend_on_other_groups(mgq):
