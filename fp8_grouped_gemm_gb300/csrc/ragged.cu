@@ -21,6 +21,11 @@
 // by the tensor cores. wgrad contracts over the tokens: rows of the last 16-row
 // step that belong to the next group are zeroed in shared memory, in both
 // operands (0 times a NaN of another group is a NaN).
+//
+// Bound by the tensor cores (active 97% of the time at 8192 rows of 4 x [8192, 4096])
+// and, for long calls, by the power cap. Measured: 8192^3 forward 572 us (1920
+// TFLOP/s), dgrad 574, wgrad 588; 8024 rows over 128 x [1536, 2048] dgrad 131 us
+// (6.6 TB/s), wgrad into 128 x [2048, 768] float32 136 us (6.3 TB/s, the writes).
 #include "ragged.cuh"
 
 namespace mgq {
