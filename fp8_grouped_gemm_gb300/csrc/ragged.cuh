@@ -51,7 +51,7 @@ __device__ __forceinline__ void banded(int64_t local, int64_t slow, int64_t nfas
   fast = band * kBand + (r - s * w);
 }
 
-template <int OP>
+template <int OP, int TOK = kTile>
 __device__ __forceinline__ bool ragged_tile(const int32_t* s_off, const int32_t* s_cum, const RaggedArgs& p, int64_t t,
                                             int& ecur, RaggedTile& tl) {
   const int64_t nM = (p.M + kTile - 1) / kTile;
@@ -74,8 +74,8 @@ __device__ __forceinline__ bool ragged_tile(const int32_t* s_off, const int32_t*
     int64_t m, tk;
     banded(t - s_cum[e] * nM, s_cum[e + 1] - s_cum[e], nM, m, tk);
     tl.e = e;
-    tl.row0 = s_off[e] + (int)tk * kTile;
-    tl.n = min(kTile, s_off[e + 1] - tl.row0);
+    tl.row0 = s_off[e] + (int)tk * TOK;
+    tl.n = min(TOK, s_off[e + 1] - tl.row0);
     tl.nst = (int)((p.C + p.bk - 1) / p.bk);
     tl.m0 = m * kTile;
     tl.c0 = 0;
@@ -83,8 +83,9 @@ __device__ __forceinline__ bool ragged_tile(const int32_t* s_off, const int32_t*
   return true;
 }
 
-// Offsets into shared memory with the running count of token tiles, by one warp;
-// true if they are a row partition (not negative, not decreasing, within R).
+// Offsets into shared memory with the running count of token tiles (of TOK tokens), by
+// one warp; true if they are a row partition (not negative, not decreasing, within R).
+template <int TOK = kTile>
 __device__ __forceinline__ bool load_groups(const RaggedArgs& p, int32_t* s_off, int32_t* s_cum, uint32_t lane) {
   int cum = 0;
   bool ok = true;
@@ -94,7 +95,7 @@ __device__ __forceinline__ bool load_groups(const RaggedArgs& p, int32_t* s_off,
     const int lo = in && p.offsets ? p.offsets[e] : 0;
     const int hi = !in ? 0 : p.offsets ? p.offsets[e + 1] : (int)p.R;
     ok &= !in || (lo >= 0 && lo <= hi && hi <= p.R);
-    const int mine = in && lo <= hi ? (hi - lo + kTile - 1) / kTile : 0;
+    const int mine = in && lo <= hi ? (hi - lo + TOK - 1) / TOK : 0;
     int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -37,7 +37,11 @@ constexpr uint32_t kFewAcol = 64, kFewCols8 = 256, kFewCols = 128;
 template <bool I8>
 constexpr uint32_t kFewAcc2 = I8 ? kFewAcol + kFewConv * 64 : 64;
 static_assert(kFewAcc2<true> + 64 <= kFewCols8, "tensor memory");
-constexpr int kFewPromote = 8;                     // as kPromote of the large form
+// Stages after which a float32 result's sum moves to registers, where it is added with
+// rounding: 512 elements of bf16 as in the large form; int8: 1024, whose sum is exact
+// whatever the codes (128 * 128 * 1024 = 2^24; beyond that the tensor cores cut off).
+// (int8 without it: 32 rows over 8 x [28672, 4096], float32 148 us against 153.)
+constexpr int kFewPromote = 8;
 
 struct FewTile {
   int e, row0, n;
@@ -115,7 +119,7 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
                       const RaggedArgs p, int split) {
   constexpr int ST = few_stages(I8);
   constexpr bool kAmn = OP == kDgrad;
-  constexpr bool kParts = F32 && !I8;              // (sums of int8 products are exact to 2^24)
+  constexpr bool kParts = F32;
   constexpr int kElems = I8 ? kBK8 : 64;           // of the contraction a stage
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
@@ -263,51 +267,11 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
     const uint32_t q = warp & 3, row = (chan ? q : warp - 6) * 32 + lane;
     uint32_t rs = 0, rph = 0, cs = 0, cph = 0, pc = 0;
     bool ok = true;
+    const uint32_t lanes = tmem + ((q * 32) << 16);
     do {
       const int n = tl.n;
-      if (I8) {
-        // -------------------------------------------------------- bytes to f16
-        const bool mine = chan || (int)(row - lane) < (n + kFewBox - 1) / kFewBox * kFewBox;
-        for (int i = 0; i < ns; ++i) {
-          ok = *s_abort == 0;
-          ok = ok && ptx::mbar_wait(&full[rs], rph, p.wait_ns);
-          uint4 c[2][4];                           // (on their way during the second wait)
-          if (mine) {
-            const uint8_t* src = chan ? sA + rs * kFewA : sB + rs * kFewB;
-            load_codes(src, row, 0, c[0]);
-            load_codes(src, row, 1, c[1]);
-          }
-          ok = ok && ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          if (chan) {
-            ptx::tc_fence_after();
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              codes_to_tmem(c[h], tmem + kFewAcol + cs * 64 + 32 * h + ((32u * q) << 16));
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-          } else if (mine) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) codes_to_smem(c[h], sF + cs * kFewF + h * (kFewF / 2), row);
-            ptx::fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) {
-            ptx::mbar_arrive(&empty[rs]);          // (only now that the codes are used: a read of them may
-            ptx::mbar_arrive(&conv_full[cs]);      // still be under way after an arrival that follows it)
-          }
-          if (++rs == ST) rs = 0, rph ^= 1;
-          if (++cs == kFewConv) cs = 0, cph ^= 1;
-        }
-        if (!ok) timed_out();
-      }
-      if (!chan || !ok) continue;
-      // ---------------------------------------------------------- the result, channels as lanes
-      const int64_t ch = tl.m0 + 32 * q + lane;
-      const float sw = I8 && split == 1 && ch < p.M ? p.sw[tl.e * p.M + ch] : 0.0f;
       float v[kParts ? kFewTok : 16];
-      const int parts = ns == 0 ? 0 : kParts ? (ns + kFewPromote - 1) / kFewPromote : 1;
+      int parts = ns == 0 ? 0 : kParts ? (ns + kFewPromote - 1) / kFewPromote : 1;   // still to be taken
 #pragma unroll
       for (int j = 0; j < (kParts ? kFewTok : 16); ++j) v[j] = 0.0f;
       auto wait_acc = [&]() {
@@ -324,21 +288,78 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
         if (lane == 0) ptx::mbar_arrive(&acc_empty[pc & 1]);
         ++pc;
       };
-      const uint32_t lanes = tmem + ((q * 32) << 16);
-      if (kParts) {
-        for (int part = 0; part < parts; ++part) {
-          if (!(ok = wait_acc())) break;
+      auto take_part = [&]() {                     // the next accumulator's values into the sums
+        if (!wait_acc()) return false;
 #pragma unroll
-          for (int h = 0; h < kFewTok; h += 16) {
-            if (h >= n) break;
-            uint32_t r[16];
-            ptx::tmem_ld_32x32b_x16(lanes + (pc & 1) * kFewAcc2<I8> + h, r);
-            ptx::tmem_ld_wait();
+        for (int h = 0; h < kFewTok; h += 16) {
+          if (h >= n) break;
+          uint32_t r[16];
+          ptx::tmem_ld_32x32b_x16(lanes + (pc & 1) * kFewAcc2<I8> + h, r);
+          ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[kParts ? h + j : j] += __uint_as_float(r[j]);
-          }
-          release_acc();
+          for (int j = 0; j < 16; ++j) v[kParts ? h + j : j] += __uint_as_float(r[j]);
         }
+        release_acc();
+        --parts;
+        return true;
+      };
+      if (I8) {
+        // -------------------------------------------------------- bytes to f16
+        const bool mine = chan || (int)(row - lane) < (n + kFewBox - 1) / kFewBox * kFewBox;
+        for (int i = 0; i < ns; ++i) {
+          ok = *s_abort == 0;
+          ok = ok && ptx::mbar_wait(&full[rs], rph, p.wait_ns);
+          // On their way during the second wait: all the codes, or half of them where the
+          // registers hold sums (both halves: 32 rows over 8 x [28672, 4096] 153 -> 160 us).
+          uint4 c[kParts ? 1 : 2][4];
+          const uint8_t* src = chan ? sA + rs * kFewA : sB + rs * kFewB;
+          if (mine) {
+            load_codes(src, row, 0, c[0]);
+            if (!kParts) load_codes(src, row, 1, c[kParts ? 0 : 1]);
+          }
+          ok = ok && ptx::mbar_wait(&conv_empty[cs], cph ^ 1, p.wait_ns);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          if (chan) {
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (kParts && h) load_codes(src, row, 1, c[0]);
+              const uint32_t at = tmem + kFewAcol + cs * 64 + 32 * h + ((32u * q) << 16);
+              if (kParts) codes_to_tmem_halves(c[0], at);
+              else codes_to_tmem(c[kParts ? 0 : h], at);
+            }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+          } else if (mine) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (kParts && h) load_codes(src, row, 1, c[0]);
+              codes_to_smem(c[kParts ? 0 : h], sF + cs * kFewF + h * (kFewF / 2), row);
+            }
+            ptx::fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(&empty[rs]);          // (only now that the codes are used: a read of them may
+            ptx::mbar_arrive(&conv_full[cs]);      // still be under way after an arrival that follows it)
+          }
+          if (++rs == ST) rs = 0, rph ^= 1;
+          if (++cs == kFewConv) cs = 0, cph ^= 1;
+          // A part is taken two stages after its last one: its MMAs have then finished
+          // (this stage's place in the ring had waited for them), and the accumulator is
+          // free again before it is needed.
+          if (kParts && chan && i > kFewPromote && i % kFewPromote == 1 && !(ok = take_part())) break;
+        }
+        if (!ok) timed_out();
+      }
+      if (!chan || !ok) continue;
+      // ---------------------------------------------------------- the result, channels as lanes
+      const int64_t ch = tl.m0 + 32 * q + lane;
+      const float sw = I8 && split == 1 && ch < p.M ? p.sw[tl.e * p.M + ch] : 0.0f;
+      const bool summed = parts > 0;
+      if (kParts) {
+        while (ok && parts > 0) ok = take_part();
       } else if (parts) {
         ok = wait_acc();
       }
@@ -347,7 +368,7 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
       for (int h = 0; h < kFewTok; h += 16) {
         if (h >= n) break;
         float x[16];
-        if (!kParts && parts) {
+        if (!kParts && summed) {
           uint32_t r[16];
           ptx::tmem_ld_32x32b_x16(lanes + (pc & 1) * kFewAcc2<I8> + h, r);
           ptx::tmem_ld_wait();
@@ -370,7 +391,7 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
           store_tokens<F32>(p.out, p.ldo, x, (int64_t)tl.row0 + h, n - h, tl.m0 + 32 * q, p.M, lane);
         }
       }
-      if (!kParts && parts) release_acc();
+      if (!kParts && summed) release_acc();
     } while (ok && next_tile());
   }
   ptx::tc_fence_before();

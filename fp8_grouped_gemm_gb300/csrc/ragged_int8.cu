@@ -6,9 +6,10 @@
 //
 // GB300's tensor cores have no int8 form worth using. Every int8 value is an f16
 // value, though, products of two are exact in f32, and a sum of them is exact
-// while it stays below 2^24: so the codes travel as bytes, half of what bf16
-// would read, and become f16 beside the tensor cores. The tiles are those of the
-// bf16 products: two SMs share 256 output channels by up to 256 tokens.
+// while it stays below 2^24 (kPartHalves: what becomes of longer ones). So the codes
+// travel as bytes, half of what bf16 would read, and become f16 beside the tensor
+// cores. The tiles are those of the bf16 products: two SMs share 256 output channels
+// by up to 256 tokens.
 //   warp 0        TMA: 128 channels and up to 128 tokens of 128 bytes a stage
 //   warps 4-11    channels: bytes -> f16 -> tensor memory, the MMA's A operand
 //   warps 12-19   tokens: bytes -> f16 -> shared memory, swizzled, the B operand
@@ -31,21 +32,38 @@ namespace {
 constexpr int kRaw = 4, kConv = 4;                 // stages of bytes, and half stages of f16
 constexpr uint32_t kRawBytes = 128 * 128;          // one operand's bytes of a stage
 constexpr uint32_t kF16Bytes = 128 * 128;          // the tokens' f16 of half a stage, 64 elements
-constexpr uint32_t kAcol = 256, kAcols = 32;       // tensor memory: the channels' half stages
+constexpr uint32_t kAcols = 32;                    // tensor memory: columns of one of the channels' half stages
 constexpr int kThreads8 = 28 * 32;
-// Registers a thread of the three kinds of warps, out of what the block is
-// launched with: an epilogue warp holds 32 scaled values beside its addresses.
-constexpr int kRegLow = 40, kRegConv = 64, kRegEpi = 104, kRegLaunch = 72;
-static_assert(128 * kRegLow + 512 * kRegConv + 256 * kRegEpi <= kThreads8 * kRegLaunch, "register split");
+// A sum of 1024 products is exact in float32 whatever the codes (128 * 128 * 1024 =
+// 2^24); beyond 2^24 the tensor cores cut bits off at every step, always towards
+// zero. So for float32 results of longer contractions (PARTS) the sum moves to
+// registers of the epilogue every 1024 elements and is added there with rounding.
+// Those registers hold 192 tokens of a tile, not 256, which leaves the tensor memory
+// room for two accumulators. It costs conversions (8192^3 587 -> 675 us, 32768 rows
+// over 8 x [4096, 14336] 1975 -> 2300, 1003 rows of [16384, 5120] 107 -> 130), and
+// bf16 results go without: what they lose is far below their own rounding.
+constexpr int kPartHalves = 1024 / 64;
+__host__ __device__ constexpr int tokens_of(bool parts) { return parts ? 192 : 256; }
+__host__ __device__ constexpr uint32_t acol_of(bool parts) { return parts ? 384u : 256u; }
+// Registers a thread of the three kinds of warps, out of what the block is launched
+// with: an epilogue warp holds 32 scaled values (96 sums) beside its addresses.
+constexpr int kRegLow = 40, kRegLaunch = 72;
+__host__ __device__ constexpr int reg_conv(bool parts) { return parts ? 48 : 64; }
+__host__ __device__ constexpr int reg_epi(bool parts) { return parts ? 136 : 104; }
+static_assert(128 * kRegLow + 512 * reg_conv(true) + 256 * reg_epi(true) <= kThreads8 * kRegLaunch, "register split");
+static_assert(128 * kRegLow + 512 * reg_conv(false) + 256 * reg_epi(false) <= kThreads8 * kRegLaunch, "register split");
 constexpr size_t kSmem8 = 1024 + kRaw * 2 * (size_t)kRawBytes + kConv * (size_t)kF16Bytes + 8 * (512 + kTokSlot) + 256 +
                           2 * (kMaxE + 8) * 4;
-static_assert(kSmem8 <= 232448 && kAcol + kConv * kAcols <= 512, "shared and tensor memory");
+static_assert(kSmem8 <= 232448 && acol_of(true) + kConv * kAcols <= 512 && 2 * tokens_of(true) <= acol_of(true),
+              "shared and tensor memory");
 
-template <bool F32>
+template <bool F32, bool PARTS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     ragged_int8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmO,
                        const RaggedArgs p) {
+  constexpr int TOK = tokens_of(PARTS), NACC = PARTS ? 2 : 1;
+  constexpr uint32_t kAcol = acol_of(PARTS);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_u32(smem_raw);
   uint8_t* sA = smem_raw + (((raw + 1023u) & ~1023u) - raw);   // [kRaw] bytes of the channels
@@ -57,9 +75,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
   uint64_t* raw_empty = raw_full + kRaw;
   uint64_t* conv_full = raw_empty + kRaw;
   uint64_t* conv_empty = conv_full + kConv;
-  uint64_t* acc_full = conv_empty + kConv;
-  uint64_t* acc_empty = acc_full + 1;
-  uint64_t* drained = acc_empty + 1;
+  uint64_t* acc_full = conv_empty + kConv;                     // [NACC]
+  uint64_t* acc_empty = acc_full + NACC;
+  uint64_t* drained = acc_empty + NACC;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_bad = reinterpret_cast<int*>(s_tmem + 2);
@@ -82,8 +100,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       ptx::mbar_init(&conv_full[s], 2 * 8);        // half of them, of both CTAs
       ptx::mbar_init(&conv_empty[s], 1);
     }
-    ptx::mbar_init(acc_full, 1);
-    ptx::mbar_init(acc_empty, 2 * 8);
+    for (int a = 0; a < NACC; ++a) {
+      ptx::mbar_init(&acc_full[a], 1);
+      ptx::mbar_init(&acc_empty[a], 2 * 8);        // one arrival per epilogue warp of each CTA
+    }
     ptx::mbar_init(drained, 1);
     *s_abort = 0;
     ptx::fence_mbar_init();
@@ -99,7 +119,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
   ptx::grid_wait();                    // from here on: what the launch before wrote
   ptx::grid_launch();
   if (warp == 2) {
-    const bool ok = load_groups(p, s_off, s_cum, lane);
+    const bool ok = load_groups<TOK>(p, s_off, s_cum, lane);
     if (lane == 0) {
       *s_bad = ok ? 0 : 1;
       if (!ok) report(p.err, MGQ_ERR_INVALID_ARG);
@@ -122,7 +142,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     int ecur = 0;
     uint32_t it = 0, st = 0, ph = 0;
     RaggedTile tl;
-    for (int64_t t = pair; !*s_abort && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
+    for (int64_t t = pair; !*s_abort && ragged_tile<kFwd, TOK>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
       const int half = (tl.n + 31) / 32 * 16;      // this CTA's tokens
       const int boxes = half == 128 ? 0 : (half + (int)kSmallBox - 1) / (int)kSmallBox;
       const uint32_t bytes = kRawBytes + (boxes ? boxes * kSmallBox * 128 : kRawBytes);
@@ -157,22 +177,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     RaggedTile tl;
     const uint32_t sF0 = ptx::smem_u32(sF);
     bool ok = true;
-    for (int64_t t = pair; ok && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs, ++tc) {
+    for (int64_t t = pair; ok && ragged_tile<kFwd, TOK>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
       const uint32_t idesc = ptx::idesc_f16(0, 256, (uint32_t)(tl.n + 31) / 32 * 32);
-      ok = !*s_abort && ptx::mbar_wait(acc_empty, (tc & 1) ^ 1, p.wait_ns);
-      for (int s = 0; ok && s < 2 * tl.nst; ++s) {
-        ok = !*s_abort && ptx::mbar_wait(&conv_full[st], ph, p.wait_ns);
-        if (!ok) break;
-        ptx::tc_fence_after();
+      // an accumulator a part (one loop over all half stages with a question for the
+      // part's ends in it: 64 x [4096, 4096] of 80 rows, bf16, 242 -> 255 us)
+      for (int s0 = 0, s1; ok && s0 < 2 * tl.nst; s0 = s1, ++tc) {
+        s1 = PARTS ? min(s0 + kPartHalves, 2 * tl.nst) : 2 * tl.nst;
+        const uint32_t acc = tmem + tc % NACC * TOK;
+        ok = !*s_abort && ptx::mbar_wait(&acc_empty[tc % NACC], ((tc / NACC) & 1) ^ 1, p.wait_ns);
+        for (int s = s0; ok && s < s1; ++s) {
+          ok = !*s_abort && ptx::mbar_wait(&conv_full[st], ph, p.wait_ns);
+          if (!ok) break;
+          ptx::tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          ptx::mma_f16_ta_pair(tmem, tmem + kAcol + st * kAcols + kk * 8,
-                               ptx::sdesc_kmajor_sw128(sF0 + st * kF16Bytes) + kk * 2, idesc,
-                               (s > 0 || kk > 0) ? 1u : 0u);
-        ptx::mma_commit_pair(&conv_empty[st], 0x3);
-        if (++st == kConv) st = 0, ph ^= 1;
+          for (int kk = 0; kk < 4; ++kk)
+            ptx::mma_f16_ta_pair(acc, tmem + kAcol + st * kAcols + kk * 8,
+                                 ptx::sdesc_kmajor_sw128(sF0 + st * kF16Bytes) + kk * 2, idesc,
+                                 (s > s0 || kk > 0) ? 1u : 0u);
+          ptx::mma_commit_pair(&conv_empty[st], 0x3);
+          if (++st == kConv) st = 0, ph ^= 1;
+        }
+        if (ok) ptx::mma_commit_pair(&acc_full[tc % NACC], 0x3);
       }
-      if (ok) ptx::mma_commit_pair(acc_full, 0x3);
     }
     if (!ok) {
       timed_out();
@@ -180,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       ptx::mbar_wait(drained, 0, p.wait_ns);
     }
   } else if (warp >= 4 && warp < 20) {
-    ptx::setmaxnreg_dec<kRegConv>();
+    ptx::setmaxnreg_dec<reg_conv(PARTS)>();
     // ------------------------------------------------------------ bytes to f16
     // (8 warps an operand: 32 rows each, 4 warps for each half of a stage)
     const bool chan = warp < 12;
@@ -202,7 +228,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
       if (!ok || n < 0) break;                                          // (n < 0: no more tiles)
       if (chan) {
         ptx::tc_fence_after();
-        codes_to_tmem(c, tmem + kAcol + cs * kAcols + ((32u * quad) << 16));
+        if (PARTS) codes_to_tmem_halves(c, tmem + kAcol + cs * kAcols + ((32u * quad) << 16));
+        else codes_to_tmem(c, tmem + kAcol + cs * kAcols + ((32u * quad) << 16));
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
       } else if ((int)(quad * 32) < (n + 31) / 32 * 16) {               // the rows an MMA reads
@@ -219,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     }
     if (run && !ok) timed_out();
   } else if (warp >= 20) {
-    ptx::setmaxnreg_inc<kRegEpi>();
+    ptx::setmaxnreg_inc<reg_epi(PARTS)>();
     // ------------------------------------------------------------ epilogue (both CTAs)
     const uint32_t q = warp & 3;
     const uint32_t half = (uint32_t)(warp - 20) >> 2;
@@ -229,51 +256,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
     int ecur = 0;
     uint32_t tc = 0;
     RaggedTile tl;
-    for (int64_t t = pair; run && ragged_tile<kFwd>(s_off, s_cum, p, t, ecur, tl); t += npairs, ++tc) {
+    // the next accumulator, and its release once it is read
+    auto wait_acc = [&]() {
+      bool got = *s_abort == 0;
+      got = got && ptx::mbar_wait(&acc_full[tc % NACC], (tc / NACC) & 1, p.wait_ns);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        timed_out();
+        return false;
+      }
+      ptx::tc_fence_after();
+      return true;
+    };
+    auto release_acc = [&]() {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_pair(empty0 + tc % NACC * 8);
+      ++tc;
+    };
+    for (int64_t t = pair; run && ragged_tile<kFwd, TOK>(s_off, s_cum, p, t, ecur, tl); t += npairs) {
       const int64_t m0 = tl.m0 + (int)(128 * rank + 32 * q);
       const float sw = m0 + lane < p.M ? p.sw[tl.e * p.M + m0 + lane] : 0.0f;
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {                // runs of 32 tokens, every second run
+      for (int i = 0; i < TOK / 64; ++i) {         // runs of 32 tokens, every second run
         const int c = 32 * (int)half + 64 * i + (int)lane;
         sx[32 * i + lane] = c < tl.n ? p.sx[(int64_t)tl.row0 + c] : 0.0f;
       }
       __syncwarp();
-      bool got = *s_abort == 0;
-      got = got && ptx::mbar_wait(acc_full, tc & 1, p.wait_ns);
-      if (!__all_sync(0xFFFFFFFFu, got)) {
-        timed_out();
-        break;
-      }
-      ptx::tc_fence_after();
-      for (int i = 0; 32 * (int)half + 64 * i < tl.n; ++i) {
+      auto scale_and_store = [&](int i, float (&v)[32]) {
         const int c = 32 * (int)half + 64 * i;
-        float v[32];
 #pragma unroll
-        for (int h = 0; h < 32; h += 16) {
-          uint32_t r[16];
-          ptx::tmem_ld_32x32b_x16(tmem + c + h + ((q * 32) << 16), r);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(sx + 32 * i + h + j);
-            v[h + j] = __uint_as_float(r[j]) * (x.x * sw);
-            v[h + j + 1] = __uint_as_float(r[j + 1]) * (x.y * sw);
-            v[h + j + 2] = __uint_as_float(r[j + 2]) * (x.z * sw);
-            v[h + j + 3] = __uint_as_float(r[j + 3]) * (x.w * sw);
-          }
-        }
-        if (c + 64 >= tl.n) {                      // the accumulator is read: the next tile may begin
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_pair(empty0);
+        for (int j = 0; j < 32; j += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(sx + 32 * i + j);
+          v[j] *= x.x * sw;
+          v[j + 1] *= x.y * sw;
+          v[j + 2] *= x.z * sw;
+          v[j + 3] *= x.w * sw;
         }
         if (tl.n - c >= 32 && m0 < p.M) send_tokens<F32>(&tmO, slot, v, tl.row0 + c, (int32_t)m0, lane);
         else store_tokens<F32>(p.out, p.ldo, v, (int64_t)tl.row0 + c, tl.n - c, m0, p.M, lane);
-      }
-      if (32 * (int)half >= tl.n) {                // (no tokens for this warp)
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_pair(empty0);
+      };
+      auto load = [&](int i, float (&v)[32], bool add) {
+#pragma unroll
+        for (int h = 0; h < 32; h += 16) {
+          uint32_t r[16];
+          ptx::tmem_ld_32x32b_x16(tmem + tc % NACC * TOK + 32 * half + 64 * i + h + ((q * 32) << 16), r);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[h + j] = add ? v[h + j] + __uint_as_float(r[j]) : __uint_as_float(r[j]);
+        }
+      };
+      if (PARTS) {
+        float v[TOK / 64][32];
+        bool got = true;
+        const int parts = (2 * tl.nst + kPartHalves - 1) / kPartHalves;
+        for (int part = 0; part < parts; ++part) {
+          if (!(got = wait_acc())) break;
+#pragma unroll
+          for (int i = 0; i < TOK / 64; ++i)
+            if (32 * (int)half + 64 * i < tl.n) load(i, v[i], part > 0);
+          release_acc();
+        }
+        if (!got) break;
+#pragma unroll
+        for (int i = 0; i < TOK / 64; ++i)
+          if (32 * (int)half + 64 * i < tl.n) scale_and_store(i, v[i]);
+      } else {
+        if (!wait_acc()) break;
+        for (int i = 0; 32 * (int)half + 64 * i < tl.n; ++i) {
+          float v[32];
+          load(i, v, false);
+          if (32 * (int)half + 64 * (i + 1) >= tl.n) release_acc();   // it is read: the next tile may begin
+          scale_and_store(i, v);
+        }
+        if (32 * (int)half >= tl.n) release_acc(); // (no tokens for this warp)
       }
     }
     if (lane == 0) ptx::bulk_wait0();              // this warp's stores are complete
@@ -288,10 +344,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1)
   }
 }
 
-template <bool F32>
+template <bool F32, bool PARTS>
 int launch_int8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ts, const CUtensorMap& to,
                 const RaggedArgs& p, int64_t max_tiles, cudaStream_t s) {
-  auto kern = ragged_int8_kernel<F32>;
+  auto kern = ragged_int8_kernel<F32, PARTS>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -454,9 +510,11 @@ int mgq_ragged_gemm_int8(const int8_t* x, int64_t ldx, const float* x_scale, con
       !encode_tmap_swz_3d(&ts, x, 1, {(uint64_t)K, (uint64_t)R, 1}, ldx, R * ldx, {128, kSmallBox, 1}) ||
       !encode_out(&to, y, R, N, ldy, p.out_f32))
     return MGQ_ERR_CUDA;
-  const int64_t tiles = token_tiles(E, R, kTile) * ((N + kTile - 1) / kTile);
-  return p.out_f32 ? launch_int8<true>(ta, tb, ts, to, p, tiles, as_stream(stream))
-                   : launch_int8<false>(ta, tb, ts, to, p, tiles, as_stream(stream));
+  const bool parts = p.out_f32 && K > 1024;
+  const int64_t tiles = token_tiles(E, R, tokens_of(parts)) * ((N + kTile - 1) / kTile);
+  return parts       ? launch_int8<true, true>(ta, tb, ts, to, p, tiles, as_stream(stream))
+         : p.out_f32 ? launch_int8<true, false>(ta, tb, ts, to, p, tiles, as_stream(stream))
+                     : launch_int8<false, false>(ta, tb, ts, to, p, tiles, as_stream(stream));
 }
 
 int mgq_rows_quantize_int8(const void* x_bf16, int64_t ldx, int64_t T, int64_t K, int8_t* codes, float* scale,

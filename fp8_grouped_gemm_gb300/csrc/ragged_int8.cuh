@@ -37,6 +37,16 @@ __device__ __forceinline__ void codes_to_tmem(const uint4 (&c)[4], uint32_t tadd
   for (int j = 0; j < 4; ++j) widen16(c[j], o + 8 * j);
   ptx::tmem_st_32x32b_x32(taddr, o);
 }
+// the same in two pieces, for warps with few registers
+__device__ __forceinline__ void codes_to_tmem_halves(const uint4 (&c)[4], uint32_t taddr) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t o[16];
+    widen16(c[2 * h], o);
+    widen16(c[2 * h + 1], o + 8);
+    ptx::tmem_st_32x32b_x16(taddr + 16 * h, o);
+  }
+}
 // ... as a K-major operand in shared memory: rows of 64 elements, 128-byte swizzle
 __device__ __forceinline__ void codes_to_smem(const uint4 (&c)[4], uint8_t* tile, uint32_t row) {
 #pragma unroll

@@ -621,11 +621,15 @@ int mgq_ragged_gemm_wgrad(const void* dy_bf16, int64_t lddy, const void* x_bf16,
  *  w        device int8 [E, N, K], contiguous; w_scale device float32 [E, N]
  *  offsets, y, ldy, out_dtype  as mgq_ragged_gemm_fwd (NULL with E = 1: the plain
  *           product of all R rows)
- * Every code from -128 to 127 counts as it stands. The sum is held in float32:
- * exact while it stays below 2^24 (K up to 1024 whatever the codes), beyond that
- * within 2^-23 of the running sum for each 16 elements. Its product with
- * (x_scale w_scale) is rounded to float32, then to the result's type. A NaN scale
- * makes its row or channel NaN.
+ * Every code from -128 to 127 counts as it stands. The sum is held in float32 and
+ * exact while it stays below 2^24 (K up to 1024 whatever the codes). Longer sums:
+ *   float32 results: the sum of each 1024 elements is exact, and these are added in
+ *   float32, rounded to nearest (2^-24 of the sum an addition);
+ *   bf16 results: beyond 2^24 each step of 16 elements can lose up to 5 * 2^-23 of the
+ *   running sum, towards zero (14336 elements of one sign: 1e-4 of it measured, 5.4e-4
+ *   at most; the rounding to bf16 is 3.9e-3).
+ * Its product with (x_scale w_scale) is rounded to float32, then to the result's
+ * type. A NaN scale makes its row or channel NaN.
  * Requires N a multiple of 8, K and ldx multiples of 16, ldy of 8; else as above. */
 int mgq_ragged_gemm_int8(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w,
                          const float* w_scale, const int32_t* offsets, int E, int64_t R, int64_t N, int64_t K,

@@ -302,6 +302,42 @@ def test_int8_long_sums(mgq):
         assert ((y.double() - ref).abs() <= (K / 16 + 4) * 2.0 ** -23 * ref).all()
 
 
+# R, E, N of the few-row form with a split contraction, without a split, and of the large form
+LONG_SUMS = [(13, 1, 520), (37, 2, 10240), (1307, 1, 1544), (1307, 2, 1544)]
+
+
+@pytest.mark.parametrize("K", [1040, 2048, 14352])
+@pytest.mark.parametrize("R,E,N", LONG_SUMS)
+def test_int8_float32_sums_of_any_codes(mgq, R, E, N, K):
+    """Codes of one sign, so that sums pass 2^24 and their last bits count: parts of 1024 elements are integers up to
+    2^24, exact; each part is added with one rounding (at most one more a part where a cluster splits the contraction),
+    and the scales take two roundings, so every one is at most 2^-24 of the final sum."""
+    g = _gen(26)
+    b = _bounds([R] if E == 1 else [R // 3, R - R // 3], 0)
+    x = torch.randint(64, 128, (R, K), device="cuda", generator=g).to(I8)
+    w = torch.randint(64, 128, (E, N, K), device="cuda", generator=g).to(I8)
+    # products of 97 to 127 in every place: each step of 16 then cuts off the same
+    x[::2] = (97 + torch.arange(R, device="cuda") % 31).to(I8)[::2, None]
+    w[:, ::2] = (97 + torch.arange(N, device="cuda") % 31).to(I8)[None, ::2, None]
+    x[R // 2:] = -x[R // 2:]
+    xs = torch.rand(R, device="cuda", generator=g) + 0.5
+    ws = torch.rand(E, N, device="cuda", generator=g) + 0.5
+    y = torch.empty(R, N, device="cuda")
+    mgq.ragged_gemm_int8(x, xs, w, ws, _off(b), y)
+    assert mgq.get_error() == mgq.OK
+    for e in range(E):
+        r = slice(b[e], b[e + 1])
+        ref = (x[r].double() @ w[e].double().t()) * xs[r, None].double() * ws[e].double()
+        _close(y[r], ref, (2 * math.ceil(K / 1024) + 2) * 2.0 ** -24 * ref.abs(), e)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=IDS)
+def test_int8_float32_in_parts(mgq, shape):
+    """Contractions of more than 1024 elements, whose sums leave the accumulator in parts: every group and tile."""
+    counts, lead, tail, N, _ = shape
+    test_int8(mgq, (counts, lead, tail, N, 2576), F32)
+
+
 def test_int8_nan_scale(mgq):
     g = _gen(8)
     for R in (6, 3000):
