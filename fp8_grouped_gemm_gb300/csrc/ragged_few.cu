@@ -412,7 +412,9 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
   float4 sw = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
   if (I8 && in) sw = *reinterpret_cast<const float4*>(p.sw + e * p.M + ch);
   constexpr int kWarps = few_threads(I8) / 32;
-  for (int j = rank + split * warp; j < n; j += split * kWarps) {
+  // (only lanes that use what they read: the last barrier does not wait for a load whose
+  // value nobody needs, and the peer's shared memory may be gone after it)
+  for (int j = rank + split * warp; in && j < n; j += split * kWarps) {
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int r = 0; r < split; ++r) {
       const float4 x = ld_cluster_f32x4(ptx::mapa_shared(mine + j * 512, r));
@@ -421,7 +423,6 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
       s.z += x.z;
       s.w += x.w;
     }
-    if (!in) continue;
     const int64_t tok = (int64_t)row0 + j;
     if (I8) {
       const float sx = p.sx[tok];
@@ -440,8 +441,9 @@ __global__ void __launch_bounds__(few_threads(I8), 2)
 }
 
 // `tiles` tiles; the contraction is split as far as the tiles' clusters still are on
-// the GPU together and each CTA has four stages: a second wave costs more than a
-// larger split gains (60 tiles, 1536 channels, K 4096: 8.2 us by four CTAs a tile,
+// the GPU together and a CTA has four stages on average (they go out in equal runs,
+// the last ranks' are shorter or empty): a second wave costs more than a larger split
+// gains (60 tiles, 1536 channels, K 4096: 8.2 us by four CTAs a tile,
 // 12.9 by five, whose 58 clusters leave two for later; 96 tiles 13.7 by three, 18.7
 // by two).
 template <int OP, bool I8, bool F32>

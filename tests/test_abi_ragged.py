@@ -131,3 +131,12 @@ def test_programmatic_launches_read_with_plain_loads(name):
         assert all(wait < k.index(w) for w in ("load_groups", "p.offsets[", "tma_load_3d", "x[2 * u]") if w in k)
     for word in ("__ldg(", ".nc.", "__restrict__"):
         assert word not in text and word not in shared
+
+
+def test_split_parts_are_read_by_lanes_that_use_them():
+    """The few-row form's last cluster barrier lets the peers leave and waits for no load by itself. So every
+    load from a peer's shared memory has its value stored before it: a lane that stores nothing reads nothing."""
+    text = open(os.path.join(ROOT, "fp8_grouped_gemm_gb300", "csrc", "ragged_few.cu")).read()
+    body = text[text.index("const bool in = "):text.index("ptx::cluster_sync_relaxed()")]
+    assert body.count("ld_cluster_f32x4(") == 1 and "continue" not in body and "break" not in body
+    assert "; in && j < n; " in body[:body.index("ld_cluster_f32x4(")]

@@ -691,6 +691,30 @@ def test_waits_run_out(mgq, R):
         assert mgq.get_error() == mgq.OK and torch.equal(out, good)
 
 
+@pytest.mark.parametrize("R", [20, 4000])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_waits_run_out_over_long_contractions(mgq, R, dt):
+    """The same where a cluster splits the contraction (R 20) and where the sum leaves in parts (R 4000, float32)."""
+    g = _gen(27)
+    N, K = 1544, 4112
+    b = _off([0, 5, R])
+    x, w = _randn(g, R, K), _randn(g, 2, N, K)
+    x8, w8, s, t = _int8(g, R, K), _int8(g, 2, N, K), torch.ones(R, device="cuda"), torch.ones(2, N, device="cuda")
+    for run in (lambda o: mgq.ragged_gemm_fwd(x, w, b, o), lambda o: mgq.ragged_gemm_int8(x8, s, w8, t, b, o)):
+        good, out = (torch.empty(R, N, dtype=dt, device="cuda") for _ in range(2))
+        run(good)
+        mgq.set_gemm_option(mgq.GEMM_OPT_WAIT_MS, 20)
+        mgq.set_gemm_option(mgq.GEMM_OPT_DEBUG_STALL, 1)
+        try:
+            run(out)
+            assert mgq.get_error() == mgq.ERR_TIMEOUT
+        finally:
+            mgq.set_gemm_option(mgq.GEMM_OPT_DEBUG_STALL, 0)
+            mgq.set_gemm_option(mgq.GEMM_OPT_WAIT_MS, 0)
+        run(out)
+        assert mgq.get_error() == mgq.OK and torch.equal(out, good)
+
+
 # ---------------------------------------------------------------------------
 # together: the routed experts' layer over unpadded groups
 
