@@ -4,6 +4,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "mgq.h"
 
 namespace mgq {
@@ -86,6 +89,32 @@ int quant_nv2d(const uint16_t* x, int64_t G, int64_t M, int64_t K, uint8_t* row_
 // (two CTAs an SM: 304, 152, 97, 74, 58, 46, 38 and 36). The runtime is asked about a
 // kernel that does nothing: for one that allocates tensor memory it counts one CTA an SM.
 bool resident_clusters(int threads, size_t smem, int* n);
+
+// What a launcher sets and asks once per device (a static one for each kernel). run()
+// calls prepare(dev) for the current device until it has returned true; one host thread
+// at a time, and a caller that gets true sees all that prepare wrote.
+class OncePerDevice {
+ public:
+  template <typename F>
+  bool run(F prepare) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return false;
+    if (done_[dev].load(std::memory_order_acquire)) return true;
+    std::lock_guard<std::mutex> lk(mu_);
+    if (done_[dev].load(std::memory_order_relaxed)) return true;
+    if (!prepare(dev)) {
+      (void)cudaGetLastError();
+      return false;
+    }
+    done_[dev].store(true, std::memory_order_release);
+    return true;
+  }
+  static constexpr int kDevices = 64;
+
+ private:
+  std::mutex mu_;
+  std::atomic<bool> done_[kDevices]{};
+};
 
 // A launch that may start while the kernel before it in the stream still runs
 // (programmatic dependent launch): such a kernel reads what others wrote, and

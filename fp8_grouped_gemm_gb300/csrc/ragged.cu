@@ -384,17 +384,11 @@ template <int OP, bool F32>
 int launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ts, const CUtensorMap& to,
                 const RaggedArgs& p, int64_t max_tiles, cudaStream_t s) {
   auto kern = ragged_pair_kernel<OP, F32>;
-  static bool attr_set[64] = {false};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return MGQ_ERR_CUDA;
-  if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(OP)) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return MGQ_ERR_CUDA;
-    }
-    attr_set[dev] = true;
-  }
+  static OncePerDevice once;
+  if (!once.run([&](int) {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(OP)) == cudaSuccess;
+      }))
+    return MGQ_ERR_CUDA;
   const int64_t pairs = min((int64_t)(num_sms() / 2), max_tiles);
   return launch_after(kern, dim3((unsigned)(2 * max(pairs, (int64_t)1))), threads_of(OP), smem_of(OP), 1, s, ta, tb, ts, to, p)
              ? MGQ_OK

@@ -12,8 +12,6 @@
 //
 // Measured: 32 rows over 8 x [28672, 4096], bf16 255 us (7.4 TB/s of weights), int8
 // 151-154 (6.1-6.2 TB/s); one row of [4096, 4096] 6.6 and 6.8 us.
-#include <atomic>
-
 #include "ragged.cuh"
 #include "ragged_int8.cuh"
 
@@ -450,27 +448,24 @@ template <int OP, bool I8, bool F32>
 int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p, int64_t tiles, int64_t nst,
                cudaStream_t s) {
   auto kern = ragged_few_kernel<OP, I8, F32>;
-  static std::atomic<bool> attr_set[64];             // set after `resident`, which the first callers fill alike
-  static int resident[64][9];
+  static OncePerDevice once;
+  static int residents[OncePerDevice::kDevices][9];  // by device and CTAs a cluster
+  if (!once.run([&](int dev) {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(I8)) == cudaSuccess &&
+               resident_clusters(few_threads(I8), few_smem(I8), residents[dev]);
+      }))
+    return MGQ_ERR_CUDA;
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return MGQ_ERR_CUDA;
-  if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(I8)) != cudaSuccess ||
-        !resident_clusters(few_threads(I8), few_smem(I8), resident[dev])) {
-      (void)cudaGetLastError();
-      return MGQ_ERR_CUDA;
-    }
-    attr_set[dev] = true;
-  }
+  const int* resident = residents[dev];
   int split = 8;
-  while (split > 1 && (tiles > resident[dev][split] || nst / split < 4)) --split;
+  while (split > 1 && (tiles > resident[split] || nst / split < 4)) --split;
   if (tiles >= (1ll << 31)) return MGQ_ERR_INVALID_ARG;
   // int8: as many CTAs as are on the GPU at once take the tiles in turn, so that the
   // ring goes on over a tile's end (16 rows over 8 x [28672, 4096] 164 -> 154 us, 256 x
   // [512, 2048] 74 -> 64). bf16 tiles have twice the bytes, and the GPU's own order of
   // handing out CTAs serves them better (259 us against 263).
-  const int64_t ctas = split > 1 ? tiles * split : I8 ? min(tiles, (int64_t)resident[dev][1]) : tiles;
+  const int64_t ctas = split > 1 ? tiles * split : I8 ? min(tiles, (int64_t)resident[1]) : tiles;
   return launch_after(kern, dim3((unsigned)ctas), few_threads(I8), few_smem(I8), split, s, ta, tb, p, split)
              ? MGQ_OK
              : MGQ_ERR_CUDA;

@@ -348,23 +348,14 @@ template <bool F32, bool PARTS>
 int launch_int8(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& ts, const CUtensorMap& to,
                 const RaggedArgs& p, int64_t max_tiles, cudaStream_t s) {
   auto kern = ragged_int8_kernel<F32, PARTS>;
-  static bool attr_set[64] = {false};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return MGQ_ERR_CUDA;
-  if (!attr_set[dev]) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem8) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return MGQ_ERR_CUDA;
-    }
-    // (a build that launches with fewer registers could not serve the split)
-    cudaFuncAttributes at;
-    if (cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs < kRegLaunch) {
-      (void)cudaGetLastError();
-      return MGQ_ERR_CUDA;
-    }
-    attr_set[dev] = true;
-  }
+  static OncePerDevice once;
+  if (!once.run([&](int) {
+        // (a build that launches with fewer registers could not serve the split)
+        cudaFuncAttributes at;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem8) == cudaSuccess &&
+               cudaFuncGetAttributes(&at, kern) == cudaSuccess && at.numRegs >= kRegLaunch;
+      }))
+    return MGQ_ERR_CUDA;
   const int64_t pairs = min((int64_t)(num_sms() / 2), max_tiles);
   return launch_after(kern, dim3((unsigned)(2 * max(pairs, (int64_t)1))), kThreads8, kSmem8, 1, s, ta, tb, ts, to, p)
              ? MGQ_OK

@@ -140,3 +140,13 @@ def test_split_parts_are_read_by_lanes_that_use_them():
     body = text[text.index("const bool in = "):text.index("ptx::cluster_sync_relaxed()")]
     assert body.count("ld_cluster_f32x4(") == 1 and "continue" not in body and "break" not in body
     assert "; in && j < n; " in body[:body.index("ld_cluster_f32x4(")]
+
+
+@pytest.mark.parametrize("name", ["ragged.cu", "ragged_int8.cu", "ragged_few.cu"])
+def test_first_calls_prepare_their_kernel_once(name):
+    """What a launcher keeps per device is filled by one host thread, and read after it is whole: no flag or table
+    that a second first caller could read or write meanwhile."""
+    text = open(os.path.join(ROOT, "fp8_grouped_gemm_gb300", "csrc", name)).read()
+    launchers = text.count("launch_after(kern")
+    assert launchers and text.count("static OncePerDevice once;") == text.count("once.run(") == launchers
+    assert "attr_set" not in text and "static bool" not in text

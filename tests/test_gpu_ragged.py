@@ -650,6 +650,54 @@ def test_host_threads(mgq):
     assert mgq.get_error() == mgq.OK
 
 
+def test_first_calls_from_host_threads():
+    """A process whose first call of each operator comes from several threads at once, each thread's first CUDA call
+    at all being the library's (raw entry points, no stream of its own): the bits of later calls."""
+    code = """
+import ctypes, threading, torch
+from fp8_grouped_gemm_gb300 import mgq
+E, N, K = 4, 520, 2064
+lib, work = mgq.load(), []
+for R in (6, 900, 2500):
+    x, dy, w = (torch.randn(s, device="cuda").bfloat16() for s in ((R, K), (R, N), (E, N, K)))
+    x8, w8 = (torch.randint(-128, 128, s, device="cuda", dtype=torch.int8) for s in ((R, K), (E, N, K)))
+    xs, ws, off = torch.rand(R, device="cuda"), torch.rand(E, N, device="cuda"), torch.tensor([0, R // 2, R // 2, R - 1, R]).int().cuda()
+    p = lambda t: t.data_ptr()
+    for f32 in (0, 1):
+        dt = torch.float32 if f32 else torch.bfloat16
+        new = lambda *s, dt=dt: torch.zeros(s, device="cuda", dtype=dt)
+        hold = (x, dy, w, x8, w8, xs, ws, off)
+        calls = [
+            (lambda o, x=x, w=w, off=off, R=R, f32=f32: lib.mgq_ragged_gemm_fwd(p(x), K, p(w), p(off), E, R, N, K, p(o), N, f32, None), new, (R, N)),
+            (lambda o, dy=dy, w=w, off=off, R=R, f32=f32: lib.mgq_ragged_gemm_dgrad(p(dy), N, p(w), p(off), E, R, N, K, p(o), K, f32, None), new, (R, K)),
+            (lambda o, dy=dy, x=x, off=off, R=R, f32=f32: lib.mgq_ragged_gemm_wgrad(p(dy), N, p(x), K, p(off), E, R, N, K, 0.0, p(o), f32, None), new, (E, N, K)),
+            (lambda o, x8=x8, xs=xs, w8=w8, ws=ws, off=off, R=R, f32=f32: lib.mgq_ragged_gemm_int8(p(x8), K, p(xs), p(w8), p(ws), p(off), E, R, N, K, p(o), N, f32, None), new, (R, N))]
+        for call, new, shape in calls:
+            work.append((call, [new(*shape) for _ in range(3)], hold))
+torch.cuda.synchronize()
+bad = []
+def run(call, out, gate):
+    gate.wait()
+    rc = call(out)
+    if rc:
+        bad.append(rc)
+for call, outs, _ in work:                       # two threads for every kernel, new ones each time
+    gate = threading.Barrier(2)
+    ts = [threading.Thread(target=run, args=(call, o, gate)) for o in outs[:2]]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+for call, outs, _ in work:
+    assert call(outs[2]) == 0
+torch.cuda.synchronize()
+assert not bad and mgq.get_error() == mgq.OK, bad
+for call, (a, b, c), _ in work:
+    assert c.any() and torch.equal(a, c) and torch.equal(b, c)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_rows_do_not_depend_on_other_groups(mgq):
     """A group's results with other groups around it, where both calls take the same form."""
     g = _gen(17)
