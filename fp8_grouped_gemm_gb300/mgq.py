@@ -481,8 +481,9 @@ def moe_few_forward(x, topk_idx, probs, W1: Operand, W2: Operand, scaling, E, F,
         raise MGQError(rc, fn)
 
 
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (looked up once; a PyTorch without CUDA has neither, and imports this module all the same)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _pitch(t, rows, cols, dev):

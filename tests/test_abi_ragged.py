@@ -1,6 +1,8 @@
 """Host-side argument validation of the products over ragged groups and of the
 int8 row quantiser: each refusal comes back before anything is launched (CPU only)."""
 import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -150,3 +152,23 @@ def test_first_calls_prepare_their_kernel_once(name):
     launchers = text.count("launch_after(kern")
     assert launchers and text.count("static OncePerDevice once;") == text.count("once.run(") == launchers
     assert "attr_set" not in text and "static bool" not in text
+
+
+def test_binding_imports_without_cuda_in_torch():
+    """A PyTorch built without CUDA lacks the bindings that the calls use: the module and the library load, and what
+    needs no device (versions, sizes, refusals by type) works."""
+    code = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, name)
+from fp8_grouped_gemm_gb300 import mgq
+assert mgq.load().mgq_version() == mgq.INTERFACE_VERSION and mgq.permute_workspace_size(64, 2, 8) > 0
+try:
+    mgq.ragged_gemm_fwd(torch.zeros(4, 16), torch.zeros(2, 8, 16), None, torch.zeros(4, 8))
+except mgq.MGQError as e:
+    assert e.status == mgq.ERR_UNSUPPORTED
+else:
+    raise AssertionError("not refused")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
