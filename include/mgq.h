@@ -589,7 +589,11 @@ int mgq_moe_few_forward(const void* x_bf16, int T, int64_t H, int64_t F, const i
  *   fwd    Y[r, n]     = sum_k X[r, k] W[e, n, k]
  *   dgrad  dX[r, k]    = sum_n dY[r, n] W[e, n, k]
  *   wgrad  dW[e, n, k] = beta dW[e, n, k] + sum over the group's rows of dY[r, n] X[r, k]
- * Float32 accumulation, one rounding to the result's type.
+ * Sums are held in float32: the tensor cores add 16 products a step and keep 24 bits,
+ * cut off towards zero (at most 5 * 2^-23 of the running sum a step; 4.4e-6 of the
+ * result's norm after 4096 elements of random sign). A float32 result's sum moves to
+ * registers every 512 elements and is added there with rounding (4.7e-7); a bf16
+ * result's stays, far below its one rounding to bf16 (1.7e-3).
  *  x, dy    device bf16, [R, K] with row pitch ldx and [R, N] with row pitch lddy (elements)
  *  w        device bf16 [E, N, K], contiguous
  *  offsets  device [E+1] int32, 0 <= offsets[e] <= offsets[e+1] <= R (otherwise

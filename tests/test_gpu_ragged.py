@@ -123,6 +123,30 @@ def test_wgrad(mgq, shape, dt):
         _close(dw[e], ref, _tol(dt, ref, S, max(1, counts[e])), e)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("R,C,M", [(13, 14344, 520), (290, 4104, 5128), (1307, 4104, 2568)])
+@pytest.mark.parametrize("op", ["fwd", "dgrad", "wgrad"])
+def test_sums_of_one_sign(mgq, op, R, C, M, dt):
+    """Operands of one sign, for which every bit that is cut off counts the same way. A step aligns its 16 products
+    and the running sum to the largest of them, cuts each off two bits below its 24 (16 * 2^-25 of it) and the sum
+    to 24 bits (2^-23): at most 5 * 2^-23 of the sum a step, float32 results 32 steps of a part of it and then a
+    rounding for each part (2^-24)."""
+    g = _gen(28)
+    pos = lambda *s: (torch.rand(s, device="cuda", generator=g) + 1).to(BF)
+    if op == "wgrad":                                     # contraction over C rows, R of them another group's
+        a, c, out = pos(C + R, 264), pos(C + R, 136), torch.empty(2, 264, 136, dtype=dt, device="cuda")
+        mgq.ragged_gemm_wgrad(a, c, _off([0, R, R + C]), out)
+        out, ref = out[1], a[R:].double().t() @ c[R:].double()
+    else:
+        x, w = pos(R, C), pos(1, *((M, C) if op == "fwd" else (C, M)))
+        out = torch.empty(R, M, dtype=dt, device="cuda")
+        (mgq.ragged_gemm_fwd if op == "fwd" else mgq.ragged_gemm_dgrad)(x, w, None, out)
+        ref = x.double() @ (w[0].double().t() if op == "fwd" else w[0].double())
+    steps, parts = (32, math.ceil(C / 512)) if dt is F32 else (math.ceil(C / 16), 0)
+    half = 2.0 ** -24 if dt is F32 else 2.0 ** -8
+    _close(out, ref, (half + 5 * steps * 2.0 ** -23 + parts * 2.0 ** -24) * ref, op)
+
+
 @pytest.mark.parametrize("beta", [1.0, 0.5, -2.0])
 def test_wgrad_accumulates(mgq, beta):
     g = _gen(3)
