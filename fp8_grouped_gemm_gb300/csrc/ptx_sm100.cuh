@@ -401,10 +401,12 @@ __device__ __forceinline__ void cluster_sync_relaxed() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// The same with the default scope: it orders what the arriving thread did in its
-// own CTA (shared memory, tensor memory), which is all that an MMA of the pair
-// reads there, and does not wait for the thread's global stores. The form with
-// cluster scope waits for those: about 1000 cycles an arrival.
+// The same with the default scope, the CTA's: it orders what the arriving thread did
+// in its own CTA (shared memory, tensor memory) and does not wait for the thread's
+// global stores. The form with cluster scope waits for those: about 1000 cycles an
+// arrival. Where the barrier is the peer's, whose MMA then reads this CTA's memory, the
+// scope does not formally cover the reader: that the pair's MMA sees what was in place
+// before such an arrival is an assumption about the hardware, which the tests bear out.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

@@ -23,9 +23,13 @@
 // operands (0 times a NaN of another group is a NaN).
 //
 // Bound by the tensor cores (active 97% of the time at 8192 rows of 4 x [8192, 4096])
-// and, for long calls, by the power cap. Measured: 8192^3 forward 572 us (1920
-// TFLOP/s), dgrad 574, wgrad 588; 8024 rows over 128 x [1536, 2048] dgrad 131 us
-// (6.6 TB/s), wgrad into 128 x [2048, 768] float32 136 us (6.3 TB/s, the writes).
+// and, for long calls, by the power cap. Measured: 8192^3 forward 572-587 us (1870-1920
+// TFLOP/s), dgrad 574-603, wgrad 588-610 on a card that was idle before, 6 to 9% more on
+// one that was not; 8024 rows over 128 x [1536, 2048] dgrad 131 us (6.6 TB/s), wgrad into
+// 128 x [2048, 768] float32 133-136 us (6.3 TB/s, the writes). With beta that call takes
+// 637 us: the old result comes by loads of 16 bytes a lane, each in its own row, after
+// the sums are complete. wgrad gives a tile all of its group's rows, so few tiles leave
+// most of the GPU idle (one expert of [1024, 1024], 32768 rows: 16 tiles, 149 us).
 #include "ragged.cuh"
 
 namespace mgq {
@@ -39,7 +43,9 @@ __host__ __device__ constexpr uint32_t slot_of(int op) { return op == kWgrad ? k
 // the error grows with every K=16 step (1.5e-8 a step, relative: 4.4e-6 after a
 // contraction of 4096, which a float32 result shows and a bf16 one does not).
 // So after kPromote stages the partial sum moves to registers of the epilogue,
-// where it is added with rounding, while the other accumulator goes on.
+// where it is added with rounding, while the other accumulator goes on. (168 registers
+// a thread, and a few spilled: 20 bytes stored and 52 loaded, wgrad 44 and 196. 8192^3
+// 587 -> 700 us, wgrad 610 -> 672.)
 constexpr int kPromote = 8;
 __host__ __device__ constexpr int stages_of(int op) { return op == kWgrad ? 5 : 6; }
 __host__ __device__ constexpr int threads_of(int op) { return op == kWgrad ? 352 : 320; }

@@ -221,13 +221,18 @@ inline int64_t token_tiles(int E, int64_t R, int64_t per) {
 // they fit the GPU at once, where its smaller tiles and the split contraction use
 // more SMs. Measured both ways (replayed graphs): 2 rows of 8 experts 4096 x 14336,
 // 39 us against 48; 512 rows over 8 x [512, 4096] 8 against 24; 64 x [4096, 4096] with
-// 24, 40, 64 and 128 rows each 315, 320, 327 and 396 against 327, 330, 335 and 347; 40
+// 24, 40, 64 and 128 rows each 315, 319, 326 and 399 against 328, 331, 335 and 345; 40
 // rows each within three waves 0.78 (contraction of 512) to 1.01 (14336) of the large
-// form's time. Over a grid of 638 such sizes the choice takes 2% (int8 1%) more than
-// the better one's.
+// form's time. The limit lies below where the forms meet on even groups (64 rows a
+// group, where it gives away 3 to 4%) because uneven ones meet earlier: 40 and 64 rows
+// on average 328 and 348 against 331 and 335, and over 16 x [4096, 14336] 312 to 328 and
+// 299 to 316 against 306 to 309 and 311 to 321. Over a grid of 638 sizes, even and uneven, the
+// choice takes 2% (int8 1%) more than the better one's. (That compares the two forms;
+// just past the limit of tiles the large one fills half of the GPU: 2560 rows of
+// [1024, 4096] 23 us, which the tensor cores could do in 11.)
 // int8: the conversion makes a tile of 64 tokens dear, and the large form shares it
-// over 256 channels. 64 x [4096, 4096] with 24, 40, 64 (uneven) and 80 rows each 176,
-// 209, 280 and 376 us against 235, 236, 241 and 242; one wave without a split, K 4096:
+// over 256 channels. 64 x [4096, 4096], bf16 results, with 24, 40, 64 (uneven) and 80
+// rows each 175, 191, 276 and 381 us against 233, 232, 241 and 240; one wave without a split, K 4096:
 // 0.72 of the large form's time with 12 rows a group, 0.94 with 24, 1.15 with 32, 1.36
 // with 40; with a split 0.4 to 0.9.
 inline bool few_rows(int E, int64_t R, int64_t M, bool i8) {

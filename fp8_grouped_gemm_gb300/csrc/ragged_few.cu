@@ -11,7 +11,7 @@
 // a CTA takes one tile after the other.
 //
 // Measured: 32 rows over 8 x [28672, 4096], bf16 255 us (7.4 TB/s of weights), int8
-// 151-154 (6.1-6.2 TB/s); one row of [4096, 4096] 6.6 and 6.8 us.
+// 147 (6.4 TB/s; float32 153); one row of [4096, 4096] 6.6 and 6.8 us (float32 7.1).
 #include "ragged.cuh"
 #include "ragged_int8.cuh"
 
@@ -462,8 +462,8 @@ int launch_few(const CUtensorMap& ta, const CUtensorMap& tb, const RaggedArgs& p
   while (split > 1 && (tiles > resident[split] || nst / split < 4)) --split;
   if (tiles >= (1ll << 31)) return MGQ_ERR_INVALID_ARG;
   // int8: as many CTAs as are on the GPU at once take the tiles in turn, so that the
-  // ring goes on over a tile's end (16 rows over 8 x [28672, 4096] 164 -> 154 us, 256 x
-  // [512, 2048] 74 -> 64). bf16 tiles have twice the bytes, and the GPU's own order of
+  // ring goes on over a tile's end (32 rows over 8 x [28672, 4096] 162 -> 151-154 us, 1000
+  // rows over 256 x [512, 2048] 74 -> 64). bf16 tiles have twice the bytes, and the GPU's own order of
   // handing out CTAs serves them better (259 us against 263).
   const int64_t ctas = split > 1 ? tiles * split : I8 ? min(tiles, (int64_t)resident[1]) : tiles;
   return launch_after(kern, dim3((unsigned)ctas), few_threads(I8), few_smem(I8), split, s, ta, tb, p, split)

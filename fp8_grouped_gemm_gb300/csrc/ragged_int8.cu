@@ -21,8 +21,9 @@
 //
 // Bound by the tensor cores at their f16 rate (active 87% of the time at 8192 rows
 // of 4 x [8192, 4096]), short contractions by the wait between tiles, long calls by
-// the power cap. Measured: 8192^3 529 us (2080 TFLOP/s), 32768 rows over 8 x [4096,
-// 14336] 1840-1860, float32.
+// the power cap; float32 results of long contractions by the conversion (kPartHalves:
+// tensor cores 71%, issue slots 65%). Measured: 8192^3 539-580 us (1900-2040 TFLOP/s),
+// float32 668; 32768 rows over 8 x [4096, 14336] 1890, float32 2140.
 #include "ragged.cuh"
 #include "ragged_int8.cuh"
 
